@@ -1,4 +1,4 @@
-"""ctypes declarations of the libdeformagg C ABI (include/deformagg.h, include/dcn.h).
+"""ctypes declarations of the libdeformagg C ABI (include/*.h).
 
 Only marshalling lives here.  Loading fails loudly when the library has not
 been built: there is no CPU fallback.
@@ -13,10 +13,12 @@ from typing import List
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libdeformagg.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "deformagg.h")
-HEADER_PATHS = [HEADER_PATH, os.path.join(os.path.dirname(PKG_DIR), "include", "dcn.h")]
+HEADER_PATHS = [os.path.join(os.path.dirname(HEADER_PATH), f)
+                for f in ("deformagg.h", "dcn.h", "group_norm.h", "int8.h")]
 
 DA_OK, DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED, DA_ERR_HIP = 0, 1, 2, 3
 DA_F32, DA_BF16, DA_F16 = 0, 1, 2
+DA_ACT_NONE, DA_ACT_RELU, DA_ACT_SILU, DA_ACT_GELU = 0, 1, 2, 3
 DA_FLAG_SLICES_ALWAYS, DA_FLAG_SLICES_NEVER, DA_FLAG_BWD_REGATHER, DA_FLAG_BWD_ROW_ORDER = \
     1, 2, 4, 8
 DA_FLAG_DETERMINISTIC = 16
@@ -55,6 +57,33 @@ class DCNProblem(ctypes.Structure):
         ("out_dtype", ctypes.c_int32),
         ("flags", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class GNProblem(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("channels", ctypes.c_int64),
+        ("groups", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("activation", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class I8Problem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("in_channels", ctypes.c_int64),
+        ("out_channels", ctypes.c_int64),
+        ("activation", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
     ]
 
 
@@ -120,6 +149,24 @@ def load() -> ctypes.CDLL:
     lib.dcn_backward.argtypes = [dprob, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     for name in ("dcn_out_size", "dcn_forward", "dcn_backward_workspace_size", "dcn_backward"):
         getattr(lib, name).restype = ctypes.c_int
+    gprob, iprob, i64 = ctypes.POINTER(GNProblem), ctypes.POINTER(I8Problem), ctypes.c_int64
+    size_t = ctypes.c_size_t
+    lib.gn_forward_workspace_size.argtypes = [gprob, szp]
+    lib.gn_forward.argtypes = [gprob] + [vp] * 7 + [size_t, vp]
+    lib.gn_backward_workspace_size.argtypes = [gprob, szp]
+    lib.gn_backward.argtypes = [gprob] + [vp] * 10 + [size_t, vp]
+    lib.i8_quantize_rows.argtypes = [i64, i64, ctypes.c_int32, vp, vp, vp, vp]
+    lib.i8_matmul_workspace_size.argtypes = [iprob, szp]
+    lib.i8_matmul.argtypes = [iprob] + [vp] * 7 + [size_t, vp]
+    lib.i8_linear_workspace_size.argtypes = [iprob, szp]
+    lib.i8_linear.argtypes = [iprob] + [vp] * 6 + [size_t, vp]
+    lib.i8_norm_linear_workspace_size.argtypes = [gprob, i64, szp]
+    lib.i8_norm_linear.argtypes = [gprob, i64] + [vp] * 8 + [size_t, vp]
+    for name in ("gn_forward_workspace_size", "gn_forward", "gn_backward_workspace_size",
+                 "gn_backward", "i8_quantize_rows", "i8_matmul_workspace_size", "i8_matmul",
+                 "i8_linear_workspace_size", "i8_linear", "i8_norm_linear_workspace_size",
+                 "i8_norm_linear"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.da_status_string.argtypes = [ctypes.c_int]
     lib.da_status_string.restype = ctypes.c_char_p
     lib.da_last_error.argtypes = []
@@ -143,5 +190,5 @@ def declared_functions() -> List[str]:
         with open(path) as f:
             text = f.read()
         text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-        names += re.findall(r"\b((?:da|dcn)_[a-z_]+)\s*\(", text)
+        names += re.findall(r"\b((?:da|dcn|gn|i8)_[a-z0-9_]+)\s*\(", text)
     return names

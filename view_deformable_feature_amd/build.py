@@ -19,10 +19,12 @@ PROBE_PATH = os.path.join(PKG_DIR, "libbwprobe.so")
 PROBE_SOURCE = os.path.join(PKG_DIR, "csrc", "bw_probe.hip")
 SOURCES = [os.path.join(CSRC, f)
            for f in ("da_forward.hip", "da_backward.hip", "da_pack.hip", "da_api.cpp", "dcn.hip",
-                     "dcn_api.cpp", "da_noalloc.hip")]
-HEADERS = [os.path.join(INCLUDE, "deformagg.h"), os.path.join(INCLUDE, "dcn.h")] + [
+                     "dcn_api.cpp", "da_noalloc.hip", "gn.hip", "gn_api.cpp", "i8.hip",
+                     "i8_api.cpp")]
+HEADERS = [os.path.join(INCLUDE, f) for f in ("deformagg.h", "dcn.h", "group_norm.h", "int8.h")] + [
     os.path.join(CSRC, f) for f in ("da_internal.h", "da_device.h", "da_pack.h", "dcn_internal.h",
-                                    "host_errors.h")]
+                                    "host_errors.h", "act_device.h", "gn_internal.h",
+                                    "i8_internal.h")]
 EXPORTS = os.path.join(CSRC, "exports.map")   # the C ABI is the only export
 ARCH = "gfx950"
 

@@ -1,0 +1,141 @@
+// Activations and 16-byte vector access shared by the group norm (gn.hip) and the
+// 8-bit products (i8.hip).  Device code.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "da_internal.h"
+#include "group_norm.h"
+
+namespace da {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// sigmoid(z) by the hardware's exponential and reciprocal (one unit in the last place
+// each): exp(-z) is off by 2^-23 + |z| 2^-24 of itself, so the result is off by that
+// share of 1 - sigmoid(z) at most.
+__device__ __forceinline__ float sigmoid_f(float z) {
+    return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
+template <int V>
+__device__ __forceinline__ void activate(float (&z)[V], int act) {
+    if (act == DA_ACT_RELU) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) z[e] = z[e] < 0.0f ? 0.0f : z[e];   // a NaN stays one
+    } else if (act == DA_ACT_SILU) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) z[e] *= sigmoid_f(z[e]);
+    } else if (act == DA_ACT_GELU) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) z[e] *= 0.5f * (1.0f + erff(z[e] * 0.70710678f));
+    }
+}
+
+// d[e] *= act'(z[e])
+template <int V>
+__device__ __forceinline__ void activate_grad(float (&d)[V], const float (&z)[V], int act) {
+    if (act == DA_ACT_RELU) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[e] = z[e] <= 0.0f ? 0.0f : d[e];
+    } else if (act == DA_ACT_SILU) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float s = sigmoid_f(z[e]);
+            d[e] *= s * (1.0f + z[e] * (1.0f - s));
+        }
+    } else if (act == DA_ACT_GELU) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float phi = 0.39894228f * __expf(-0.5f * z[e] * z[e]);
+            d[e] *= 0.5f * (1.0f + erff(z[e] * 0.70710678f)) + z[e] * phi;
+        }
+    }
+}
+
+// Raw storage of V elements of T, moved in one access: V = 16 bytes' worth, or 1.
+template <typename T, int V>
+struct Raw {
+    u32x4 q;
+    static __device__ __forceinline__ Raw load(const T* p) {
+        return {*reinterpret_cast<const u32x4*>(p)};
+    }
+    static __device__ __forceinline__ Raw zero() { return {u32x4{0, 0, 0, 0}}; }
+    __device__ __forceinline__ void unpack(float (&v)[V]) const {
+        typedef T vec __attribute__((ext_vector_type(V)));
+        const vec t = __builtin_bit_cast(vec, q);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = (float)t[e];
+    }
+};
+template <typename T>
+struct Raw<T, 1> {
+    T t;
+    static __device__ __forceinline__ Raw load(const T* p) { return {*p}; }
+    static __device__ __forceinline__ Raw zero() { return {(T)0.0f}; }
+    __device__ __forceinline__ void unpack(float (&v)[1]) const { v[0] = (float)t; }
+};
+
+// Store V floats as elements of D at p (aligned to min(16, V * sizeof(D)) bytes), each
+// rounded once to nearest even.
+template <typename D, int V>
+__device__ __forceinline__ void store_as(D* p, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        *p = (D)v[0];
+    } else {
+        constexpr int kPer = V * (int)sizeof(D) <= 16 ? V : 16 / (int)sizeof(D);
+        typedef D vec __attribute__((ext_vector_type(kPer)));
+#pragma unroll
+        for (int b = 0; b < V; b += kPer) {
+            vec t;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) t[e] = (D)v[b + e];
+            *reinterpret_cast<vec*>(p + b) = t;
+        }
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_vec(void* base, int64_t i, const float (&v)[V], int dtype) {
+    if (dtype == DA_BF16)
+        store_as(static_cast<__bf16*>(base) + i, v);
+    else if (dtype == DA_F16)
+        store_as(static_cast<_Float16*>(base) + i, v);
+    else
+        store_as(static_cast<float*>(base) + i, v);
+}
+
+template <typename D, int V>
+__device__ __forceinline__ void load_as(const D* p, float (&v)[V]) {
+    if constexpr (V == 1) {
+        v[0] = (float)*p;
+    } else {
+        constexpr int kPer = V * (int)sizeof(D) <= 16 ? V : 16 / (int)sizeof(D);
+        typedef D vec __attribute__((ext_vector_type(kPer)));
+#pragma unroll
+        for (int b = 0; b < V; b += kPer) {
+            const vec t = *reinterpret_cast<const vec*>(p + b);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) v[b + e] = (float)t[e];
+        }
+    }
+}
+template <int V>
+__device__ __forceinline__ void load_vec(const void* base, int64_t i, float (&v)[V], int dtype) {
+    if (dtype == DA_BF16)
+        load_as(static_cast<const __bf16*>(base) + i, v);
+    else if (dtype == DA_F16)
+        load_as(static_cast<const _Float16*>(base) + i, v);
+    else
+        load_as(static_cast<const float*>(base) + i, v);
+}
+
+__device__ __forceinline__ float load_elem(const void* base, int64_t i, int dtype) {
+    float v[1];
+    load_vec(base, i, v, dtype);
+    return v[0];
+}
+
+}  // namespace da

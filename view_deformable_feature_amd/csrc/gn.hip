@@ -1,0 +1,512 @@
+// Group norm with an activation on channels-last maps, forward and backward.
+// Contract and formulas: include/group_norm.h.
+//
+// Lanes lie along the channels of a row, so every access is a run of whole 16-byte
+// vectors, and a thread stays with one vector of channels: its weights, its groups'
+// statistics and the backward's per-channel sums sit in registers.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "act_device.h"
+#include "gn_internal.h"
+
+namespace da {
+namespace {
+
+// Where a workgroup works: its slab of channels, and its threads' places in it.
+struct Slab {
+    int ch0, width;        // channels
+    int unit0, nunits;     // statistics units
+    int g0;                // first group
+    int cols, R;           // vectors per row, rows at a time
+    int r, v;              // this thread's row and vector; r >= R: none
+};
+
+template <int V>
+__device__ __forceinline__ Slab slab_of(const GnArgs& a, int s, int threads) {
+    Slab b;
+    if (a.upg == 1) {
+        b.ch0 = s * a.slab_ch;
+        b.width = min(a.slab_ch, a.C - b.ch0);
+        b.g0 = b.unit0 = b.ch0 / a.cpg;
+        b.nunits = b.width / a.cpg;
+    } else {
+        const int g = s / a.upg, u = s - g * a.upg;
+        b.ch0 = g * a.cpg + u * a.cpu;
+        b.width = min(a.cpu, a.cpg - u * a.cpu);
+        b.g0 = g;
+        b.unit0 = s;
+        b.nunits = 1;
+    }
+    b.cols = b.width / V;
+    b.R = threads / b.cols;
+    b.r = threadIdx.x / b.cols;
+    b.v = threadIdx.x - b.r * b.cols;
+    return b;
+}
+
+// out[u] = sum of red[r * cols + j] over r < R and the `per` columns of unit u, by one
+// wave per unit.  Every thread of the workgroup calls it; red is complete on entry, out
+// on return.
+__device__ __forceinline__ void unit_sums(const float* red, int R, int cols, int per, int nunits,
+                                          float* out) {
+    const int lane = threadIdx.x & (kWave - 1), nw = blockDim.x / kWave;
+    for (int u = threadIdx.x / kWave; u < nunits; u += nw) {
+        float t = 0.0f;
+        for (int e = lane; e < R * per; e += kWave) {
+            const int r = e / per, j = e - r * per;
+            t += red[r * cols + u * per + j];
+        }
+        for (int m = kWave / 2; m; m >>= 1) t += __shfl_xor(t, m);
+        if (lane == 0) out[u] = t;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ double wave_sum(double t) {
+    for (int m = kWave / 2; m; m >>= 1) t += __shfl_xor(t, m);
+    return t;
+}
+
+// The group's first value in image n: all of the group's means are formed and kept as
+// differences from it, so that a large common offset cancels before anything is rounded.
+__device__ __forceinline__ float origin_of(const GnArgs& a, int n, int g) {
+    return load_elem(a.x, (int64_t)n * a.S * a.C + (int64_t)g * a.cpg, a.x_dtype);
+}
+
+// One chunk: (mean less the group's origin, M2) of each unit, where M2 is the sum of
+// squared deviations from that mean.  Each thread takes its squares about its first row,
+// then moves them to the unit's mean.
+template <typename T, int V>
+__global__ __launch_bounds__(kGnThreads) void gn_stats_kernel(GnArgs a) {
+    __shared__ float red[kGnThreads * V];
+    __shared__ float um[kGnThreads * V], uq[kGnThreads * V];
+    const int s = blockIdx.x % a.slabs;
+    const int chunk = (blockIdx.x / a.slabs) % a.chunks;
+    const int n = blockIdx.x / a.slabs / a.chunks;
+    const Slab b = slab_of<V>(a, s, kGnThreads);
+    const int64_t r0 = chunk * a.rows_per_chunk, r1 = min(r0 + a.rows_per_chunk, a.S);
+    const T* p = static_cast<const T*>(a.x) + ((int64_t)n * a.S) * a.C + b.ch0 + b.v * V;
+
+    float first[V], sum[V], sq[V];
+    int cnt = 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) first[e] = sum[e] = sq[e] = 0.0f;
+    if (b.r < b.R) {
+        int64_t row = r0 + b.r;
+        if (row < r1) Raw<T, V>::load(p + row * a.C).unpack(first);
+        constexpr int U = 4;
+        for (; row < r1; row += U * b.R) {
+            Raw<T, V> q[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (row + i * b.R < r1) q[i] = Raw<T, V>::load(p + (row + i * b.R) * a.C);
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (row + i * b.R < r1) {
+                    float x[V];
+                    q[i].unpack(x);
+                    ++cnt;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float d = x[e] - first[e];
+                        sum[e] += d;
+                        sq[e] = fmaf(d, d, sq[e]);
+                    }
+                }
+        }
+    }
+    // one value per thread where a vector lies in one unit, else one per channel
+    const int per_ch = a.upg == 1 ? a.cpg : b.width;
+    const bool whole = per_ch % V == 0;
+    const int cols = whole ? b.cols : b.width, per = whole ? per_ch / V : per_ch;
+    const float rc = cnt ? 1.0f / cnt : 0.0f;
+    float m[V];   // this thread's channel means, less the origin
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        m[e] = (first[e] - origin_of(a, n, b.g0 + (b.v * V + e) / per_ch)) + sum[e] * rc;
+    if (b.r < b.R) {
+        if (whole) {
+            float t = 0.0f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) t += m[e];
+            red[b.r * cols + b.v] = t * cnt;
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) red[b.r * cols + b.v * V + e] = m[e] * cnt;
+        }
+    }
+    __syncthreads();
+    unit_sums(red, b.R, cols, per, b.nunits, um);
+    const float total = (float)(r1 - r0) * per_ch;
+    float dev[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const float d = m[e] - um[(b.v * V + e) / per_ch] / total;
+        // sum of squares about m is sq - sum^2 / cnt, below zero by rounding alone; a NaN stays
+        const float t = sq[e] - sum[e] * sum[e] * rc;
+        dev[e] = cnt ? (t < 0.0f ? 0.0f : t) + cnt * d * d : 0.0f;
+    }
+    if (b.r < b.R) {
+        if (whole) {
+            float t = 0.0f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) t += dev[e];
+            red[b.r * cols + b.v] = t;
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) red[b.r * cols + b.v * V + e] = dev[e];
+        }
+    }
+    __syncthreads();
+    unit_sums(red, b.R, cols, per, b.nunits, uq);
+    float2* part = a.unit_part + ((int64_t)n * a.chunks + chunk) * a.units + b.unit0;
+    for (int u = threadIdx.x; u < b.nunits; u += kGnThreads)
+        part[u] = make_float2(um[u] / total, uq[u]);
+}
+
+// The chunks' statistics of groups g0 .. g0 + ngroups - 1 joined in binary64, one wave
+// per group: mean and rstd into LDS.  Every thread of the workgroup calls it.
+__device__ __forceinline__ void join_stats(const GnArgs& a, int n, int g0, int ngroups, float* gm,
+                                           float* gr) {
+    const int lane = threadIdx.x & (kWave - 1), nw = blockDim.x / kWave;
+    const double total = (double)a.S * a.cpg;
+    for (int j = threadIdx.x / kWave; j < ngroups; j += nw) {
+        const int g = g0 + j;
+        const float2* part = a.unit_part + (int64_t)n * a.chunks * a.units + (int64_t)g * a.upg;
+        const int entries = a.chunks * a.upg;
+        double sum = 0.0, m2 = 0.0;
+        for (int e = lane; e < entries; e += kWave) {
+            const int c = e / a.upg, u = e - c * a.upg;
+            const int64_t r0 = c * a.rows_per_chunk;
+            const double cnt = (double)(min(r0 + a.rows_per_chunk, a.S) - r0) *
+                               min(a.cpu, a.cpg - u * a.cpu);
+            sum += cnt * part[(int64_t)c * a.units + u].x;
+        }
+        const double mean = wave_sum(sum) / total;
+        for (int e = lane; e < entries; e += kWave) {
+            const int c = e / a.upg, u = e - c * a.upg;
+            const int64_t r0 = c * a.rows_per_chunk;
+            const double cnt = (double)(min(r0 + a.rows_per_chunk, a.S) - r0) *
+                               min(a.cpu, a.cpg - u * a.cpu);
+            const float2 q = part[(int64_t)c * a.units + u];
+            m2 += q.y + cnt * (q.x - mean) * (q.x - mean);
+        }
+        const double var = wave_sum(m2) / total;
+        if (lane == 0) {
+            gm[j] = (float)(mean + (double)origin_of(a, n, g));
+            // squares past binary32: no number
+            gr[j] = var < 0x1p1000 ? (float)(1.0 / sqrt(var + (double)a.eps))
+                                   : __uint_as_float(0x7fc00000u);
+        }
+    }
+    __syncthreads();
+}
+
+// mean and rstd alone: 4 groups to a workgroup.
+constexpr int kGnJoin = kGnThreads / kWave;
+__global__ __launch_bounds__(kGnThreads) void gn_join_kernel(GnArgs a) {
+    __shared__ float gm[kGnJoin], gr[kGnJoin];
+    const int blocks = (a.G + kGnJoin - 1) / kGnJoin;
+    const int n = blockIdx.x / blocks, g0 = (blockIdx.x - n * blocks) * kGnJoin;
+    const int ngroups = min(kGnJoin, a.G - g0);
+    join_stats(a, n, g0, ngroups, gm, gr);
+    if ((int)threadIdx.x < ngroups) {
+        a.mean[(int64_t)n * a.G + g0 + threadIdx.x] = gm[threadIdx.x];
+        a.rstd[(int64_t)n * a.G + g0 + threadIdx.x] = gr[threadIdx.x];
+    }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kGnThreads) void gn_apply_kernel(GnArgs a) {
+    __shared__ float gm[kGnThreads * V], gr[kGnThreads * V];
+    const int s = blockIdx.x % a.slabs;
+    const int chunk = (blockIdx.x / a.slabs) % a.chunks;
+    const int n = blockIdx.x / a.slabs / a.chunks;
+    const Slab b = slab_of<V>(a, s, kGnThreads);
+    const int ngroups = a.upg == 1 ? b.nunits : 1;
+    join_stats(a, n, b.g0, ngroups, gm, gr);
+    if (chunk == 0 && (a.upg == 1 || s % a.upg == 0)) {
+        for (int j = threadIdx.x; j < ngroups; j += kGnThreads) {
+            if (a.mean) a.mean[(int64_t)n * a.G + b.g0 + j] = gm[j];
+            if (a.rstd) a.rstd[(int64_t)n * a.G + b.g0 + j] = gr[j];
+        }
+    }
+    if (b.r >= b.R) return;
+    float mu[V], sc[V], bi[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const int c = b.v * V + e, j = a.upg == 1 ? c / a.cpg : 0;
+        mu[e] = gm[j];
+        sc[e] = gr[j] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
+        bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
+    }
+    const int64_t r0 = chunk * a.rows_per_chunk, r1 = min(r0 + a.rows_per_chunk, a.S);
+    const int64_t base = ((int64_t)n * a.S) * a.C + b.ch0 + b.v * V;
+    const T* p = static_cast<const T*>(a.x) + base;
+    constexpr int U = 4;
+    for (int64_t row = r0 + b.r; row < r1; row += U * b.R) {
+        Raw<T, V> q[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (row + i * b.R < r1) q[i] = Raw<T, V>::load(p + (row + i * b.R) * a.C);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (row + i * b.R < r1) {
+                float z[V];
+                q[i].unpack(z);
+#pragma unroll
+                for (int e = 0; e < V; ++e) z[e] = fmaf(z[e] - mu[e], sc[e], bi[e]);
+                activate(z, a.act);
+                store_vec(a.out, base + (row + i * b.R) * a.C, z, a.out_dtype);
+            }
+    }
+}
+
+// Sums of dz and dz * xhat: per channel (for grad_weight and grad_bias) and, weighted,
+// per unit (for grad_x), of one chunk.
+template <typename T, int V>
+__global__ __launch_bounds__(kGnThreads) void gn_bwd_stats_kernel(GnArgs a) {
+    __shared__ float ra[kGnThreads * V], rb[kGnThreads * V];
+    __shared__ float ua[kGnThreads * V], ub[kGnThreads * V];
+    const int s = blockIdx.x % a.slabs;
+    const int chunk = (blockIdx.x / a.slabs) % a.chunks;
+    const int n = blockIdx.x / a.slabs / a.chunks;
+    const Slab b = slab_of<V>(a, s, kGnThreads);
+    const int64_t r0 = chunk * a.rows_per_chunk, r1 = min(r0 + a.rows_per_chunk, a.S);
+    const int64_t base = ((int64_t)n * a.S) * a.C + b.ch0 + b.v * V;
+    const T* p = static_cast<const T*>(a.x) + base;
+
+    float A[V], B[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) A[e] = B[e] = 0.0f;
+    if (b.r < b.R) {
+        float mu[V], rs[V], w[V], bi[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const int c = b.v * V + e, j = a.upg == 1 ? c / a.cpg : 0;
+            mu[e] = a.mean[(int64_t)n * a.G + b.g0 + j];
+            rs[e] = a.rstd[(int64_t)n * a.G + b.g0 + j];
+            w[e] = a.weight ? a.weight[b.ch0 + c] : 1.0f;
+            bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
+        }
+        constexpr int U = 2;
+        for (int64_t row = r0 + b.r; row < r1; row += U * b.R) {
+            Raw<T, V> q[U];
+            float d[U][V];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (row + i * b.R < r1) {
+                    q[i] = Raw<T, V>::load(p + (row + i * b.R) * a.C);
+                    load_vec(a.grad_out, base + (row + i * b.R) * a.C, d[i], a.out_dtype);
+                }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (row + i * b.R < r1) {
+                    float x[V], z[V];
+                    q[i].unpack(x);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        x[e] = (x[e] - mu[e]) * rs[e];
+                        z[e] = fmaf(x[e], w[e], bi[e]);
+                    }
+                    activate_grad(d[i], z, a.act);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        A[e] += d[i][e];
+                        B[e] = fmaf(d[i][e], x[e], B[e]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            ra[b.r * b.width + b.v * V + e] = A[e];
+            rb[b.r * b.width + b.v * V + e] = B[e];
+        }
+    }
+    __syncthreads();
+    // rows folded in halves: R -> ceil(R / 2) -> ... -> 1
+    for (int R = b.R; R > 1;) {
+        const int half = (R + 1) / 2, n2 = (R - half) * b.width;
+        for (int e = threadIdx.x; e < n2; e += kGnThreads) {
+            ra[e] += ra[e + half * b.width];
+            rb[e] += rb[e + half * b.width];
+        }
+        R = half;
+        __syncthreads();
+    }
+    float2* cp = a.chan_part + ((int64_t)n * a.chunks + chunk) * a.C + b.ch0;
+    for (int c = threadIdx.x; c < b.width; c += kGnThreads) {
+        cp[c] = make_float2(ra[c], rb[c]);
+        const float w = a.weight ? a.weight[b.ch0 + c] : 1.0f;
+        ra[c] *= w;
+        rb[c] *= w;
+    }
+    __syncthreads();
+    const int per = a.upg == 1 ? a.cpg : b.width;
+    unit_sums(ra, 1, b.width, per, b.nunits, ua);
+    unit_sums(rb, 1, b.width, per, b.nunits, ub);
+    float2* up = a.unit_part + ((int64_t)n * a.chunks + chunk) * a.units + b.unit0;
+    for (int u = threadIdx.x; u < b.nunits; u += kGnThreads) up[u] = make_float2(ua[u], ub[u]);
+}
+
+// grad_weight and grad_bias of 16 channels from the chunks' sums.
+constexpr int kGnChanBlock = 16;
+__device__ __forceinline__ void channel_sums(const GnArgs& a, int block) {
+    __shared__ float2 red[kGnThreads];
+    const int c = block * kGnChanBlock + threadIdx.x % kGnChanBlock;
+    float2 t = make_float2(0.0f, 0.0f);
+    const int64_t parts = (int64_t)a.N * a.chunks;
+    if (c < a.C)
+        for (int64_t e = threadIdx.x / kGnChanBlock; e < parts; e += kGnThreads / kGnChanBlock) {
+            const float2 q = a.chan_part[e * a.C + c];
+            t.x += q.x;
+            t.y += q.y;
+        }
+    red[threadIdx.x] = t;
+    __syncthreads();
+    if (threadIdx.x < kGnChanBlock && c < a.C) {
+        for (int e = threadIdx.x + kGnChanBlock; e < kGnThreads; e += kGnChanBlock) {
+            t.x += red[e].x;
+            t.y += red[e].y;
+        }
+        if (a.grad_bias) a.grad_bias[c] = t.x;
+        if (a.grad_weight) a.grad_weight[c] = t.y;
+    }
+}
+
+// grad_x of one chunk; the workgroups after the last chunk's form grad_weight and
+// grad_bias.
+template <typename T, int V>
+__global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int64_t chunk_blocks) {
+    if (blockIdx.x >= chunk_blocks) {
+        channel_sums(a, blockIdx.x - chunk_blocks);
+        return;
+    }
+    __shared__ float m1[kGnThreads * V], m2[kGnThreads * V];
+    const int s = blockIdx.x % a.slabs;
+    const int chunk = (blockIdx.x / a.slabs) % a.chunks;
+    const int n = blockIdx.x / a.slabs / a.chunks;
+    const Slab b = slab_of<V>(a, s, kGnThreads);
+    const int ngroups = a.upg == 1 ? b.nunits : 1;
+    {
+        const int lane = threadIdx.x & (kWave - 1), nw = kGnThreads / kWave;
+        const double inv = 1.0 / ((double)a.S * a.cpg);
+        for (int j = threadIdx.x / kWave; j < ngroups; j += nw) {
+            const float2* part = a.unit_part + (int64_t)n * a.chunks * a.units +
+                                 (int64_t)(b.g0 + j) * a.upg;
+            double t1 = 0.0, t2 = 0.0;
+            for (int e = lane; e < a.chunks * a.upg; e += kWave) {
+                const int c = e / a.upg, u = e - c * a.upg;
+                const float2 q = part[(int64_t)c * a.units + u];
+                t1 += q.x;
+                t2 += q.y;
+            }
+            t1 = wave_sum(t1);
+            t2 = wave_sum(t2);
+            if (lane == 0) {
+                m1[j] = (float)(t1 * inv);
+                m2[j] = (float)(t2 * inv);
+            }
+        }
+        __syncthreads();
+    }
+    if (b.r >= b.R) return;
+    float mu[V], rs[V], w[V], bi[V], c1[V], c2[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const int c = b.v * V + e, j = a.upg == 1 ? c / a.cpg : 0;
+        mu[e] = a.mean[(int64_t)n * a.G + b.g0 + j];
+        rs[e] = a.rstd[(int64_t)n * a.G + b.g0 + j];
+        w[e] = a.weight ? a.weight[b.ch0 + c] : 1.0f;
+        bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
+        c1[e] = m1[j];
+        c2[e] = m2[j];
+    }
+    const int64_t r0 = chunk * a.rows_per_chunk, r1 = min(r0 + a.rows_per_chunk, a.S);
+    const int64_t base = ((int64_t)n * a.S) * a.C + b.ch0 + b.v * V;
+    const T* p = static_cast<const T*>(a.x) + base;
+    constexpr int U = 2;
+    for (int64_t row = r0 + b.r; row < r1; row += U * b.R) {
+        Raw<T, V> q[U];
+        float d[U][V];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (row + i * b.R < r1) {
+                q[i] = Raw<T, V>::load(p + (row + i * b.R) * a.C);
+                load_vec(a.grad_out, base + (row + i * b.R) * a.C, d[i], a.out_dtype);
+            }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (row + i * b.R < r1) {
+                float x[V], z[V];
+                q[i].unpack(x);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    x[e] = (x[e] - mu[e]) * rs[e];
+                    z[e] = fmaf(x[e], w[e], bi[e]);
+                }
+                activate_grad(d[i], z, a.act);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    z[e] = rs[e] * (fmaf(w[e], d[i][e], -c1[e]) - x[e] * c2[e]);
+                store_as(static_cast<T*>(a.grad_x) + base + (row + i * b.R) * a.C, z);
+            }
+    }
+}
+
+template <typename T, int V>
+hipError_t forward(const GnArgs& a, hipStream_t stream) {
+    const uint32_t blocks = (uint32_t)((int64_t)a.N * a.chunks * a.slabs);
+    gn_stats_kernel<T, V><<<blocks, kGnThreads, 0, stream>>>(a);
+    gn_apply_kernel<T, V><<<blocks, kGnThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t backward(const GnArgs& a, hipStream_t stream) {
+    const int64_t blocks = (int64_t)a.N * a.chunks * a.slabs;
+    if (blocks) gn_bwd_stats_kernel<T, V><<<(uint32_t)blocks, kGnThreads, 0, stream>>>(a);
+    const int64_t dx = a.grad_x ? blocks : 0;
+    const int64_t ch = a.grad_weight || a.grad_bias ? (a.C + kGnChanBlock - 1) / kGnChanBlock : 0;
+    if (dx + ch)
+        gn_bwd_apply_kernel<T, V><<<(uint32_t)(dx + ch), kGnThreads, 0, stream>>>(a, dx);
+    return hipGetLastError();
+}
+
+template <typename F>
+hipError_t by_type(int dtype, bool vec, F&& f) {
+    switch (dtype) {
+        case DA_BF16: return vec ? f(__bf16{}, std::integral_constant<int, 8>{})
+                                 : f(__bf16{}, std::integral_constant<int, 1>{});
+        case DA_F16: return vec ? f(_Float16{}, std::integral_constant<int, 8>{})
+                                : f(_Float16{}, std::integral_constant<int, 1>{});
+        default: return vec ? f(float{}, std::integral_constant<int, 4>{})
+                            : f(float{}, std::integral_constant<int, 1>{});
+    }
+}
+
+}  // namespace
+
+hipError_t launch_gn_stats(const GnArgs& a, bool vec, hipStream_t stream) {
+    return by_type(a.x_dtype, vec, [&](auto t, auto v) {
+        const uint32_t blocks = (uint32_t)((int64_t)a.N * a.chunks * a.slabs);
+        gn_stats_kernel<decltype(t), decltype(v)::value><<<blocks, kGnThreads, 0, stream>>>(a);
+        gn_join_kernel<<<a.N * ((a.G + kGnJoin - 1) / kGnJoin), kGnThreads, 0, stream>>>(a);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_gn_forward(const GnArgs& a, bool vec, hipStream_t stream) {
+    return by_type(a.x_dtype, vec, [&](auto t, auto v) {
+        return forward<decltype(t), decltype(v)::value>(a, stream);
+    });
+}
+
+hipError_t launch_gn_backward(const GnArgs& a, bool vec, hipStream_t stream) {
+    return by_type(a.x_dtype, vec, [&](auto t, auto v) {
+        return backward<decltype(t), decltype(v)::value>(a, stream);
+    });
+}
+
+}  // namespace da

@@ -1,0 +1,56 @@
+// Internal launch description of the group-norm kernels (gn.hip), filled by the host
+// API (gn_api.cpp).  Not part of the public ABI.
+//
+// A workgroup covers a slab: slab_ch consecutive channels (whole groups, and whole
+// vectors of VEC channels) of some rows of one image.  Its threads form R rows of
+// slab_ch / VEC vectors; a thread keeps its vector of channels and walks the rows.  A
+// group wider than kGnThreads vectors is cut into upg units of cpu channels (the last
+// one shorter), one to a slab; otherwise a unit is a group.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime_api.h>
+
+#include "group_norm.h"
+
+namespace da {
+
+constexpr int kGnThreads = 256;
+
+struct GnArgs {
+    const void* x;            // [N, S, C] of x_dtype
+    const float* weight;      // [C] or NULL
+    const float* bias;        // [C] or NULL
+    void* out;                // [N, S, C] of out_dtype
+    float* mean;              // [N, G] or NULL (read in the backward)
+    float* rstd;              // [N, G] or NULL
+    const void* grad_out;     // [N, S, C] of out_dtype
+    void* grad_x;             // [N, S, C] of x_dtype, or NULL
+    float* grad_weight;       // [C] or NULL
+    float* grad_bias;         // [C] or NULL
+    float2* unit_part;        // [N, chunks, units]: (mean, sum of squared deviations), or the
+                              // backward's sums of weight * dz and weight * dz * xhat
+    float2* chan_part;        // backward: [N, chunks, C] sums of dz and dz * xhat
+    int64_t S;
+    int64_t rows_per_chunk;
+    int32_t N, C, G, cpg;
+    int32_t slab_ch, slabs;
+    int32_t upg, cpu, units;
+    int32_t chunks;           // row chunks of an image (statistics and apply alike)
+    int32_t act, x_dtype, out_dtype;
+    float eps;
+};
+
+// Statistics alone, for a kernel that normalises as it reads: workspace bytes (and the
+// problem's checks), then mean and rstd [N, G] in that workspace (256-byte aligned).
+da_status gn_stats_bytes(const gn_problem* p, uint64_t& bytes);
+hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace,
+                            const float** mean, const float** rstd, hipStream_t stream);
+
+hipError_t launch_gn_stats(const GnArgs& a, bool vec, hipStream_t stream);
+hipError_t launch_gn_forward(const GnArgs& a, bool vec, hipStream_t stream);
+hipError_t launch_gn_backward(const GnArgs& a, bool vec, hipStream_t stream);
+
+}  // namespace da

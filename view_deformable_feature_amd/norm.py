@@ -1,0 +1,184 @@
+"""PyTorch binding of the group norm with an activation in libdeformagg
+(include/group_norm.h).
+
+Maps are channels last, [N, ..., C] with any number of dimensions between (they are the
+rows of an image): the layout ``dcn_forward`` and the aggregation work in, so a
+normalisation between two of them copies nothing.  Activations go by name: "none", "relu",
+"silu", "gelu" (by the error function).
+
+Only metadata checks and pointer passing happen here; every step runs in the HIP
+kernels of libdeformagg.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from .api import _DTYPES, _FLOATS, _need, _ptr, _stream
+
+__all__ = ["gn_forward", "gn_backward", "gn_workspace_size", "gn_backward_workspace_size",
+           "GroupNormActFunction", "group_norm_act"]
+
+_ACTIVATIONS = {"none": _lib.DA_ACT_NONE, "relu": _lib.DA_ACT_RELU, "silu": _lib.DA_ACT_SILU,
+                "gelu": _lib.DA_ACT_GELU}
+
+
+def _activation(name: str) -> int:
+    code = _ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {name!r}")
+    return code
+
+
+def _gn_problem(x: torch.Tensor, groups: int, eps: float, activation: str,
+                out_dtype: torch.dtype) -> _lib.GNProblem:
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x must be a [N, ..., C] tensor")
+    if x.dtype not in _DTYPES or out_dtype not in _DTYPES:
+        raise TypeError(f"input / output dtypes must be among {_FLOATS}")
+    shape = x.shape
+    return _lib.GNProblem(shape[0], math.prod(shape[1:-1]), shape[-1], int(groups), float(eps),
+                          _activation(activation), _DTYPES[x.dtype], _DTYPES[out_dtype], 0, 0)
+
+
+def _params(weight, bias, dev, C):
+    if weight is not None:
+        _need(weight, "weight", torch.float32, dev, (C,))
+    if bias is not None:
+        _need(bias, "bias", torch.float32, dev, (C,))
+
+
+def _size(func: str, *args) -> int:
+    n = ctypes.c_size_t(0)
+    _lib.check(getattr(_lib.load(), func)(*args, ctypes.byref(n)), func)
+    return n.value
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, dev) -> Optional[torch.Tensor]:
+    if workspace is None:
+        return torch.empty(need, device=dev, dtype=torch.uint8) if need else None
+    _need(workspace, "workspace", torch.uint8, dev)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace has {workspace.numel()} bytes, {need} needed")
+    return workspace
+
+
+def _ws_args(workspace: Optional[torch.Tensor]):
+    return (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
+
+
+def gn_workspace_size(x: torch.Tensor, groups: int) -> int:
+    """Bytes of ``workspace`` that ``gn_forward`` uses for x."""
+    prob = _gn_problem(x, groups, 0.0, "none", x.dtype)
+    return _size("gn_forward_workspace_size", ctypes.byref(prob))
+
+
+def gn_backward_workspace_size(x: torch.Tensor, groups: int) -> int:
+    """Bytes of ``workspace`` that ``gn_backward`` uses for x."""
+    prob = _gn_problem(x, groups, 0.0, "none", x.dtype)
+    return _size("gn_backward_workspace_size", ctypes.byref(prob))
+
+
+def gn_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, eps: float = 1e-5, activation: str = "none",
+               out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+               workspace: Optional[torch.Tensor] = None
+               ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(out [N, ..., C], mean [N, G] float32, rstd [N, G] float32): act of the normalised,
+    scaled and shifted x.  out has x's type unless ``out`` / ``out_dtype`` says otherwise;
+    ``out`` may be x itself."""
+    lib = _lib.load()
+    odt = out.dtype if out is not None else (out_dtype or x.dtype)
+    prob = _gn_problem(x, groups, eps, activation, odt)
+    dev = x.device
+    _need(x, "x", _FLOATS, dev)
+    _params(weight, bias, dev, x.shape[-1])
+    if out is None:
+        out = torch.empty(x.shape, device=dev, dtype=odt)
+    else:
+        _need(out, "out", _FLOATS, dev, x.shape)
+    need = _size("gn_forward_workspace_size", ctypes.byref(prob))
+    mean = torch.empty((x.shape[0], int(groups)), device=dev, dtype=torch.float32)
+    rstd = torch.empty((x.shape[0], int(groups)), device=dev, dtype=torch.float32)
+    workspace = _workspace(workspace, need, dev)
+    with torch.cuda.device(dev):
+        st = lib.gn_forward(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out),
+                            _ptr(mean), _ptr(rstd), *_ws_args(workspace), _stream(dev))
+    _lib.check(st, "gn_forward")
+    return out, mean, rstd
+
+
+def gn_backward(x: torch.Tensor, grad_out: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                groups: int, weight: Optional[torch.Tensor] = None,
+                bias: Optional[torch.Tensor] = None, activation: str = "none",
+                grad_x: Optional[torch.Tensor] = None, need_x: bool = True,
+                need_params: bool = True, workspace: Optional[torch.Tensor] = None
+                ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(grad_x of x's type, grad_weight [C] float32, grad_bias [C] float32), from what
+    ``gn_forward`` was given and returned.  ``grad_x`` may be grad_out itself; ``need_x`` and
+    ``need_params`` false leave out that part (None in its place)."""
+    lib = _lib.load()
+    if not isinstance(grad_out, torch.Tensor) or grad_out.dtype not in _DTYPES:
+        raise TypeError(f"grad_out must be a tensor of one of {_FLOATS}")
+    prob = _gn_problem(x, groups, 0.0, activation, grad_out.dtype)
+    dev, C = x.device, x.shape[-1]
+    _need(x, "x", _FLOATS, dev)
+    _need(grad_out, "grad_out", _FLOATS, dev, x.shape)
+    stats = (x.shape[0], int(groups))
+    _need(mean, "mean", torch.float32, dev, stats)
+    _need(rstd, "rstd", torch.float32, dev, stats)
+    _params(weight, bias, dev, C)
+    if grad_x is not None:
+        _need(grad_x, "grad_x", x.dtype, dev, x.shape)
+    elif need_x:
+        grad_x = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    need = _size("gn_backward_workspace_size", ctypes.byref(prob))
+    gw = torch.empty((C,), device=dev, dtype=torch.float32) if need_params else None
+    gb = torch.empty((C,), device=dev, dtype=torch.float32) if need_params else None
+    workspace = _workspace(workspace, need, dev)
+    with torch.cuda.device(dev):
+        st = lib.gn_backward(ctypes.byref(prob), _ptr(x), _ptr(grad_out), _ptr(mean), _ptr(rstd),
+                             _ptr(weight), _ptr(bias), _ptr(grad_x), _ptr(gw), _ptr(gb),
+                             *_ws_args(workspace), _stream(dev))
+    _lib.check(st, "gn_backward")
+    return grad_x, gw, gb
+
+
+class GroupNormActFunction(torch.autograd.Function):
+    """Autograd wrapper: gradients for x, weight and bias, each in its own type (the
+    parameters' sums are formed in float32)."""
+
+    @staticmethod
+    def forward(ctx, x, groups, weight=None, bias=None, eps=1e-5, activation="none",
+                out_dtype=None):
+        x = x.contiguous()
+        w = None if weight is None else weight.contiguous().float()
+        b = None if bias is None else bias.contiguous().float()
+        out, mean, rstd = gn_forward(x, groups, w, b, eps, activation, out_dtype=out_dtype)
+        ctx.save_for_backward(x, w, b, mean, rstd)
+        ctx.conf = (groups, activation)
+        ctx.param_dtypes = tuple(None if p is None else p.dtype for p in (weight, bias))
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out):
+        x, w, b, mean, rstd = ctx.saved_tensors
+        groups, activation = ctx.conf
+        if grad_out.dtype not in _DTYPES:
+            grad_out = grad_out.float()
+        need_x, _, need_w, need_b = ctx.needs_input_grad[:4]
+        gx, gw, gb = gn_backward(x, grad_out.contiguous(), mean, rstd, groups, w, b, activation,
+                                 need_x=need_x, need_params=need_w or need_b)
+        wt, bt = ctx.param_dtypes
+        return (gx, None, gw.to(wt) if need_w else None, gb.to(bt) if need_b else None,
+                None, None, None)
+
+
+def group_norm_act(x, groups, weight=None, bias=None, eps=1e-5, activation="none", out_dtype=None):
+    """act(group norm of x [N, ..., C]), differentiable in x, weight and bias."""
+    return GroupNormActFunction.apply(x, groups, weight, bias, eps, activation, out_dtype)

@@ -8,7 +8,7 @@
 #include <stdint.h>
 
 #include "act_device.h"
-#include "gn_internal.h"
+#include "gn_device.h"
 
 namespace da {
 namespace {
@@ -61,17 +61,6 @@ __device__ __forceinline__ void unit_sums(const float* red, int R, int cols, int
         if (lane == 0) out[u] = t;
     }
     __syncthreads();
-}
-
-__device__ __forceinline__ double wave_sum(double t) {
-    for (int m = kWave / 2; m; m >>= 1) t += __shfl_xor(t, m);
-    return t;
-}
-
-// The group's first value in image n: all of the group's means are formed and kept as
-// differences from it, so that a large common offset cancels before anything is rounded.
-__device__ __forceinline__ float origin_of(const GnArgs& a, int n, int g) {
-    return load_elem(a.x, (int64_t)n * a.S * a.C + (int64_t)g * a.cpg, a.x_dtype);
 }
 
 // One chunk: (mean less the group's origin, M2) of each unit, where M2 is the sum of
@@ -163,44 +152,6 @@ __global__ __launch_bounds__(kGnThreads) void gn_stats_kernel(GnArgs a) {
     float2* part = a.unit_part + ((int64_t)n * a.chunks + chunk) * a.units + b.unit0;
     for (int u = threadIdx.x; u < b.nunits; u += kGnThreads)
         part[u] = make_float2(um[u] / total, uq[u]);
-}
-
-// The chunks' statistics of groups g0 .. g0 + ngroups - 1 joined in binary64, one wave
-// per group: mean and rstd into LDS.  Every thread of the workgroup calls it.
-__device__ __forceinline__ void join_stats(const GnArgs& a, int n, int g0, int ngroups, float* gm,
-                                           float* gr) {
-    const int lane = threadIdx.x & (kWave - 1), nw = blockDim.x / kWave;
-    const double total = (double)a.S * a.cpg;
-    for (int j = threadIdx.x / kWave; j < ngroups; j += nw) {
-        const int g = g0 + j;
-        const float2* part = a.unit_part + (int64_t)n * a.chunks * a.units + (int64_t)g * a.upg;
-        const int entries = a.chunks * a.upg;
-        double sum = 0.0, m2 = 0.0;
-        for (int e = lane; e < entries; e += kWave) {
-            const int c = e / a.upg, u = e - c * a.upg;
-            const int64_t r0 = c * a.rows_per_chunk;
-            const double cnt = (double)(min(r0 + a.rows_per_chunk, a.S) - r0) *
-                               min(a.cpu, a.cpg - u * a.cpu);
-            sum += cnt * part[(int64_t)c * a.units + u].x;
-        }
-        const double mean = wave_sum(sum) / total;
-        for (int e = lane; e < entries; e += kWave) {
-            const int c = e / a.upg, u = e - c * a.upg;
-            const int64_t r0 = c * a.rows_per_chunk;
-            const double cnt = (double)(min(r0 + a.rows_per_chunk, a.S) - r0) *
-                               min(a.cpu, a.cpg - u * a.cpu);
-            const float2 q = part[(int64_t)c * a.units + u];
-            m2 += q.y + cnt * (q.x - mean) * (q.x - mean);
-        }
-        const double var = wave_sum(m2) / total;
-        if (lane == 0) {
-            gm[j] = (float)(mean + (double)origin_of(a, n, g));
-            // squares past binary32: no number
-            gr[j] = var < 0x1p1000 ? (float)(1.0 / sqrt(var + (double)a.eps))
-                                   : __uint_as_float(0x7fc00000u);
-        }
-    }
-    __syncthreads();
 }
 
 // mean and rstd alone: 4 groups to a workgroup.
@@ -488,11 +439,12 @@ hipError_t by_type(int dtype, bool vec, F&& f) {
 
 }  // namespace
 
-hipError_t launch_gn_stats(const GnArgs& a, bool vec, hipStream_t stream) {
+hipError_t launch_gn_stats(const GnArgs& a, bool vec, bool joined, hipStream_t stream) {
     return by_type(a.x_dtype, vec, [&](auto t, auto v) {
         const uint32_t blocks = (uint32_t)((int64_t)a.N * a.chunks * a.slabs);
         gn_stats_kernel<decltype(t), decltype(v)::value><<<blocks, kGnThreads, 0, stream>>>(a);
-        gn_join_kernel<<<a.N * ((a.G + kGnJoin - 1) / kGnJoin), kGnThreads, 0, stream>>>(a);
+        if (joined)
+            gn_join_kernel<<<a.N * ((a.G + kGnJoin - 1) / kGnJoin), kGnThreads, 0, stream>>>(a);
         return hipGetLastError();
     });
 }

@@ -156,10 +156,9 @@ da_status gn_stats_bytes(const gn_problem* p, uint64_t& bytes) {
     return DA_OK;
 }
 
-hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace,
-                            const float** mean, const float** rstd, hipStream_t stream) {
+hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace, bool joined,
+                            GnArgs& a, hipStream_t stream) {
     const bool vec = vectors_fit(p) && aligned(x, 16);
-    GnArgs a;
     lay_out(p, vec ? 16 / elem_bytes(p->x_dtype) : 1, a);
     unsigned char* base = static_cast<unsigned char*>(workspace);
     a.x = x;
@@ -168,9 +167,7 @@ hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace,
     a.rstd = reinterpret_cast<float*>(base);
     base += part_bytes((uint64_t)p->batch * p->groups * 4);
     a.unit_part = reinterpret_cast<float2*>(base);
-    *mean = a.mean;
-    *rstd = a.rstd;
-    return launch_gn_stats(a, vec, stream);
+    return launch_gn_stats(a, vec, joined, stream);
 }
 
 }  // namespace da

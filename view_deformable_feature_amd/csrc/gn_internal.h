@@ -44,12 +44,13 @@ struct GnArgs {
 };
 
 // Statistics alone, for a kernel that normalises as it reads: workspace bytes (and the
-// problem's checks), then mean and rstd [N, G] in that workspace (256-byte aligned).
+// problem's checks); then a filled in and the chunks' statistics enqueued, and where
+// `joined`, mean and rstd [N, G] in that workspace (256-byte aligned) as well.
 da_status gn_stats_bytes(const gn_problem* p, uint64_t& bytes);
-hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace,
-                            const float** mean, const float** rstd, hipStream_t stream);
+hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace, bool joined,
+                            GnArgs& a, hipStream_t stream);
 
-hipError_t launch_gn_stats(const GnArgs& a, bool vec, hipStream_t stream);
+hipError_t launch_gn_stats(const GnArgs& a, bool vec, bool joined, hipStream_t stream);
 hipError_t launch_gn_forward(const GnArgs& a, bool vec, hipStream_t stream);
 hipError_t launch_gn_backward(const GnArgs& a, bool vec, hipStream_t stream);
 

@@ -1,9 +1,21 @@
 // Products of 8-bit codes with a scale per row and output channel, and the quantisation
 // of rows to such codes.  Contract and formulas: include/int8.h.
+//
+// The matrix instruction v_mfma_i32_16x16x64_i8 takes 16 rows of 64 consecutive codes of
+// either operand, 16 bytes of row l % 16 at byte 16 * (l / 16) in lane l, and leaves in
+// lane l four sums: rows 4 * (l / 16) .. + 3 of the first operand with row l % 16 of the
+// second.  The weights are the first operand throughout, so a lane ends up with four
+// consecutive output channels of one row and stores them at once.
+//
+// Columns past K: the rows' codes are zero there, so the weights may be anything that is
+// in memory; only the last bytes of the whole weight matrix are fetched one by one.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "act_device.h"
+#include "gn_device.h"
 #include "i8_internal.h"
 
 namespace da {
@@ -11,101 +23,770 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+__device__ __forceinline__ i32x4 mfma(i32x4 w, i32x4 x, i32x4 acc) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, acc, 0, 0, 0);
+}
+
+// ---- quantisation ------------------------------------------------------------------------
+
 // A row's scale and the factor its codes are formed with, from the largest magnitude's
-// bits (magnitudes order as their bits do, infinities and NaNs last).
-__device__ __forceinline__ void row_scale(uint32_t big_bits, float& scale, float& inverse) {
-    const float big = __uint_as_float(big_bits);
-    if (big_bits >= 0x7f800000u) {
-        scale = __uint_as_float(0x7fc00000u);
-        inverse = 0.0f;
-    } else if (big < 0x1p-100f) {
-        scale = inverse = 0.0f;
-    } else {
-        scale = big / 127.0f;
-        inverse = 127.0f / big;
-    }
-}
-
-__device__ __forceinline__ int code_of(float x, float inverse) {
-    // a row with a NaN or an infinity has inverse 0 and its codes are 0 whatever x is
-    const float q = rintf(x * inverse);
-    return inverse == 0.0f ? 0 : (int)q;
-}
-
-// One wave per row, read twice (the second time from cache).
-constexpr int kQuantThreads = 256;
-__global__ __launch_bounds__(kQuantThreads) void i8_quantize_kernel(I8Args a) {
-    const int64_t m = (int64_t)blockIdx.x * (kQuantThreads / kWave) + threadIdx.x / kWave;
-    const int lane = threadIdx.x & (kWave - 1);
-    if (m >= a.M) return;
-    const auto value = [&](int k) {
-        float v[1] = {load_elem(a.x, m * a.K + k, a.x_dtype)};
-        if (a.mean) {
-            const int64_t j = m / a.S * a.G + k / a.cpg;
-            const float w = a.norm_weight ? a.norm_weight[k] : 1.0f;
-            v[0] = fmaf(v[0] - a.mean[j], a.rstd[j] * w, a.norm_bias ? a.norm_bias[k] : 0.0f);
-            activate(v, a.norm_act);
-        }
-        return v[0];
-    };
-    uint32_t big = 0;
-    for (int k = lane; k < a.K; k += kWave) big = max(big, __float_as_uint(value(k)) & 0x7fffffffu);
-    for (int s = kWave / 2; s; s >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, s));
+// bits (magnitudes order as their bits do, infinities and NaNs last).  Both quotients are
+// the correctly rounded ones.
+struct RowScale {
     float scale, inverse;
-    row_scale(big, scale, inverse);
-    for (int k = lane; k < a.K; k += kWave) a.a[m * a.K + k] = (int8_t)code_of(value(k), inverse);
-    if (lane == 0) a.a_scale[m] = scale;
+    uint32_t mask;   // 0 where every code is 0 whatever x * inverse is
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t big_bits) {
+    const float big = __uint_as_float(big_bits);
+    if (big_bits >= 0x7f800000u) return {__uint_as_float(0x7fc00000u), 0.0f, 0u};
+    if (big < 0x1p-100f) return {0.0f, 0.0f, 0u};
+    return {big / 127.0f, 127.0f / big, ~0u};
 }
 
-// 16 bytes of row `row` from column k on, zeros outside the matrix.
-__device__ __forceinline__ i32x4 piece(const int8_t* p, int64_t row, int64_t rows, int k, int K) {
-    i32x4 q = {0, 0, 0, 0};
-    if (row < rows)
-        for (int i = 0; i < 16; ++i)
-            if (k + i < K) q[i / 4] |= (int)((uint32_t)(uint8_t)p[row * K + k + i] << (8 * (i % 4)));
-    return q;
+// Four codes.  Adding 1.5 * 2^23 to the rounded product rounds it once more, to the nearest
+// whole number, ties to even, and leaves it in the low byte in two's complement; the two
+// steps must not become one multiply-add, which would round once.
+__device__ __forceinline__ uint32_t pack_codes(const float* x, const RowScale& s) {
+#pragma clang fp contract(off)
+    constexpr float kMagic = 12582912.0f;
+    const uint32_t q0 = __float_as_uint(x[0] * s.inverse + kMagic);
+    const uint32_t q1 = __float_as_uint(x[1] * s.inverse + kMagic);
+    const uint32_t q2 = __float_as_uint(x[2] * s.inverse + kMagic);
+    const uint32_t q3 = __float_as_uint(x[3] * s.inverse + kMagic);
+    const uint32_t lo = __builtin_amdgcn_perm(q1, q0, 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(q3, q2, 0x0c0c0400u);
+    return __builtin_amdgcn_perm(hi, lo, 0x05040100u) & s.mask;
 }
 
-// A wave forms 16 rows x 64 columns.
-__global__ __launch_bounds__(256) void i8_matmul_kernel(I8Args a) {
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int tiles = (a.N + 63) / 64;
-    const int64_t m0 = (int64_t)(blockIdx.x / tiles) * 64 + wave * 16;
-    const int n0 = (int)(blockIdx.x % tiles) * 64;
-    i32x4 acc[4] = {};
-    for (int k = 0; k < a.K; k += 64) {
-        const i32x4 fa = piece(a.a, m0 + lane % 16, a.M, k + lane / 16 * 16, a.K);
-        for (int j = 0; j < 4; ++j) {
-            const i32x4 fb = piece(a.w, n0 + j * 16 + lane % 16, a.N, k + lane / 16 * 16, a.K);
-            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa, fb, acc[j], 0, 0, 0);
+// Eight numbers of a row from column c on, XB bytes each; zeros past column K.  Any
+// alignment.
+template <int XB>
+struct Eight {
+    u32x4 q[XB / 2];
+    __device__ __forceinline__ void load(const void* x, int64_t row, int c, int K) {
+        const char* p = static_cast<const char*>(x) + (row * K + c) * XB;
+        if (c + 8 <= K) {
+            __builtin_memcpy(q, p, 8 * XB);
+        } else {
+            uint32_t w[2 * XB];
+#pragma unroll
+            for (int e = 0; e < 2 * XB; ++e) w[e] = 0;
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (c + e < K) {
+                    if constexpr (XB == 4) {
+                        __builtin_memcpy(&w[e], p + 4 * e, 4);
+                    } else {
+                        uint16_t h;
+                        __builtin_memcpy(&h, p + 2 * e, 2);
+                        w[e / 2] |= (uint32_t)h << (16 * (e & 1));
+                    }
+                }
+            __builtin_memcpy(q, w, 8 * XB);
         }
     }
-    for (int j = 0; j < 4; ++j) {
-        const int n = n0 + j * 16 + lane % 16;
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + lane / 16 * 4 + i;
-            if (m < a.M && n < a.N) {
-                float y[1] = {(float)acc[j][i] * a.a_scale[m] * a.w_scale[n]};
-                if (a.bias) y[0] += a.bias[n];
-                activate(y, a.act);
-                store_vec(a.out, m * a.N + n, y, a.out_dtype);
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < XB / 2; ++i) q[i] = u32x4{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ void unpack(float (&v)[8], bool bf16) const {
+        if constexpr (XB == 4) {
+            __builtin_memcpy(v, q, 32);
+        } else if (bf16) {
+            typedef __bf16 vec __attribute__((ext_vector_type(8)));
+            const vec t = __builtin_bit_cast(vec, q[0]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (float)t[e];
+        } else {
+            typedef _Float16 vec __attribute__((ext_vector_type(8)));
+            const vec t = __builtin_bit_cast(vec, q[0]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (float)t[e];
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t magnitude(const float (&v)[8]) {
+    uint32_t big = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(v[e]) & 0x7fffffffu);
+    return big;
+}
+
+// The normalisation of eight channels of a row, which a lane keeps for all its rows, and the
+// activation behind it; columns past K give 0.
+struct NormCoef {
+    float mu[8], sc[8], bi[8];
+    __device__ __forceinline__ void apply(float (&v)[8], int act) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e] - mu[e], sc[e], bi[e]);
+        activate(v, act);
+    }
+    // of channels c .. c + 7: mean_of and rstd_of give a group's
+    template <typename F, typename G>
+    __device__ __forceinline__ void load(const I8Args& a, int cpg, int c, F&& mean_of, G&& rstd_of) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            mu[e] = sc[e] = bi[e] = 0.0f;   // a column past K holds 0
+            if (c + e < a.K) {
+                const int j = (c + e) / cpg;
+                mu[e] = mean_of(j);
+                sc[e] = rstd_of(j) * (a.norm_weight ? a.norm_weight[c + e] : 1.0f);
+                if (a.norm_bias) bi[e] = a.norm_bias[c + e];
             }
         }
     }
+};
+
+// One wave per row; a row's first 2048 numbers stay in registers, what is past them is read
+// again.
+constexpr int kQuantThreads = 256;
+template <int XB>
+__global__ __launch_bounds__(kQuantThreads) void i8_quantize_kernel(I8Args a) {
+    constexpr int kHold = 4;
+    const int64_t m = (int64_t)blockIdx.x * (kQuantThreads / kWave) + threadIdx.x / kWave;
+    const int lane = threadIdx.x & (kWave - 1);
+    if (m >= a.M) return;
+    const bool bf16 = a.x_dtype == DA_BF16;
+    Eight<XB> hold[kHold];
+    float v[8];
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        const int c = (i * kWave + lane) * 8;
+        if (c < a.K) hold[i].load(a.x, m, c, a.K);
+        else hold[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        hold[i].unpack(v, bf16);
+        big = max(big, magnitude(v));
+    }
+    for (int c = (kHold * kWave + lane) * 8; c < a.K; c += kWave * 8) {
+        Eight<XB> t;
+        t.load(a.x, m, c, a.K);
+        t.unpack(v, bf16);
+        big = max(big, magnitude(v));
+    }
+    for (int s = kWave / 2; s; s >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, s));
+    const RowScale s = row_scale(big);
+    const auto put = [&](const Eight<XB>& t, int c) {
+        t.unpack(v, bf16);
+        const u32x2 q = {pack_codes(v, s), pack_codes(v + 4, s)};
+        int8_t* p = a.a + m * a.K + c;
+        if (c + 8 <= a.K) {
+            __builtin_memcpy(p, &q, 8);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (c + e < a.K) p[e] = (int8_t)(q[e / 4] >> (8 * (e & 3)));
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+        if ((i * kWave + lane) * 8 < a.K) put(hold[i], (i * kWave + lane) * 8);
+    for (int c = (kHold * kWave + lane) * 8; c < a.K; c += kWave * 8) {
+        Eight<XB> t;
+        t.load(a.x, m, c, a.K);
+        put(t, c);
+    }
+    if (lane == 0) a.a_scale[m] = s.scale;
+}
+
+// The same behind a group norm whose means and rstds are in memory: rows past the rows
+// kernel's depth, read twice.
+template <int XB>
+__global__ __launch_bounds__(kQuantThreads) void i8_norm_quantize_kernel(I8Args a, GnArgs g) {
+    const int64_t m = (int64_t)blockIdx.x * (kQuantThreads / kWave) + threadIdx.x / kWave;
+    const int lane = threadIdx.x & (kWave - 1);
+    if (m >= a.M) return;
+    const bool bf16 = a.x_dtype == DA_BF16;
+    const float* mean = g.mean + m / g.S * g.G;
+    const float* rstd = g.rstd + m / g.S * g.G;
+    const auto value = [&](int c, float (&v)[8]) {
+        Eight<XB> q;
+        q.load(a.x, m, c, a.K);
+        q.unpack(v, bf16);
+        NormCoef f;
+        f.load(a, g.cpg, c, [&](int j) { return mean[j]; }, [&](int j) { return rstd[j]; });
+        f.apply(v, g.act);
+    };
+    float v[8];
+    uint32_t big = 0;
+    for (int c = lane * 8; c < a.K; c += kWave * 8) {
+        value(c, v);
+        big = max(big, magnitude(v));
+    }
+    for (int s = kWave / 2; s; s >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, s));
+    const RowScale s = row_scale(big);
+    for (int c = lane * 8; c < a.K; c += kWave * 8) {
+        value(c, v);
+        const u32x2 q = {pack_codes(v, s), pack_codes(v + 4, s)};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < a.K) a.a[m * a.K + c + e] = (int8_t)(q[e / 4] >> (8 * (e & 3)));
+    }
+    if (lane == 0) a.a_scale[m] = s.scale;
+}
+
+// ---- pieces of the operands --------------------------------------------------------------
+
+// 16 codes of weight row n from column k on; columns past K hold what follows in memory.
+__device__ __forceinline__ i32x4 weight_piece(const I8Args& a, int n, int k) {
+    const int64_t at = (int64_t)n * a.K + k, end = (int64_t)a.N * a.K;
+    i32x4 q = {0, 0, 0, 0};
+    if (at + 16 <= end) {
+        __builtin_memcpy(&q, a.w + at, 16);
+    } else {
+        for (int i = 0; i < 15; ++i)
+            if (at + i < end) q[i / 4] |= (int)((uint32_t)(uint8_t)a.w[at + i] << (8 * (i & 3)));
+    }
+    return q;
+}
+
+// 16 codes of row m from column k on, zeros past K.
+__device__ __forceinline__ i32x4 code_piece(const I8Args& a, int64_t m, int k) {
+    const int8_t* p = a.a + m * a.K + k;
+    i32x4 q = {0, 0, 0, 0};
+    if (k + 16 <= a.K) {
+        __builtin_memcpy(&q, p, 16);
+    } else {
+        for (int i = 0; i < 15; ++i)
+            if (k + i < a.K) q[i / 4] |= (int)((uint32_t)(uint8_t)p[i] << (8 * (i & 3)));
+    }
+    return q;
+}
+
+// ---- results -----------------------------------------------------------------------------
+
+// Scales and bias of the four output channels from n on (0 past N).
+struct ColumnScale {
+    float s[4], b[4];
+};
+__device__ __forceinline__ ColumnScale column_scale(const I8Args& a, int n) {
+    ColumnScale c;
+    if (n + 4 <= a.N) {
+        __builtin_memcpy(c.s, a.w_scale + n, 16);
+        if (a.bias) {
+            __builtin_memcpy(c.b, a.bias + n, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c.b[i] = 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c.s[i] = n + i < a.N ? a.w_scale[n + i] : 0.0f;
+            c.b[i] = n + i < a.N && a.bias ? a.bias[n + i] : 0.0f;
+        }
+    }
+    return c;
+}
+
+template <typename D>
+__device__ __forceinline__ void store_four(D* p, const float (&y)[4], int count) {
+    typedef D vec __attribute__((ext_vector_type(4)));
+    const vec t = {(D)y[0], (D)y[1], (D)y[2], (D)y[3]};
+    if (count >= 4) {
+        __builtin_memcpy(p, &t, sizeof t);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < count) p[i] = t[i];
+    }
+}
+
+// out[m, n .. n + 3] from the sums: conversion, row scale, column scale and bias round once
+// each, then the activation and the rounding to the stored type.
+__device__ __forceinline__ void finish(const I8Args& a, int64_t m, int n, const i32x4& acc,
+                                       float row, const ColumnScale& c) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = fmaf((float)acc[i] * row, c.s[i], c.b[i]);
+    activate(y, a.act);
+    const int64_t at = m * a.N + n;
+    if (a.out_dtype == DA_BF16)
+        store_four(static_cast<__bf16*>(a.out) + at, y, a.N - n);
+    else if (a.out_dtype == DA_F16)
+        store_four(static_cast<_Float16*>(a.out) + at, y, a.N - n);
+    else
+        store_four(static_cast<float*>(a.out) + at, y, a.N - n);
+}
+
+// ---- rows kernel -------------------------------------------------------------------------
+//
+// A workgroup brings 16 * MT rows of at most 64 * KT columns into LDS as codes (copied, or
+// quantised from x, or normalised and quantised), each wave keeps all of them as operands
+// in registers, and the waves deal the 16-column tiles of the output among them, the
+// weights coming straight from L2: x is read once, out written once, and no codes go
+// through memory.
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsWaves = kRowsThreads / kWave;
+
+template <int XB, bool NORM, int KT, int MT>
+__global__ __launch_bounds__(kRowsThreads) void i8_rows_kernel(I8Args a, GnArgs g) {
+    constexpr int kBM = 16 * MT, kKp = 64 * KT, kStride = kKp + 16;   // odd 16-byte units
+    __shared__ __align__(16) unsigned char codes[kBM * kStride];
+    __shared__ float scales[kBM];
+    __shared__ float gm[NORM ? kKp : 1], gr[NORM ? kKp : 1];   // at most K groups
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int nb = blockIdx.x % a.n_blocks;
+    int64_t m0 = blockIdx.x / a.n_blocks, mend = a.M;
+    if constexpr (NORM) {   // a block stays in one image
+        const int n = (int)(m0 / a.m_blocks);
+        m0 = n * g.S + (m0 - (int64_t)n * a.m_blocks) * kBM;
+        mend = (n + 1) * g.S;
+        join_stats(g, n, 0, g.G, gm, gr);
+    } else {
+        m0 *= kBM;
+    }
+
+    if constexpr (XB == 0) {
+        for (int i = threadIdx.x; i < kBM * KT * 4; i += kRowsThreads) {
+            const int r = i / (KT * 4), c = i % (KT * 4) * 16;
+            i32x4 q = {0, 0, 0, 0};
+            if (m0 + r < mend && c < a.K) q = code_piece(a, m0 + r, c);
+            *reinterpret_cast<i32x4*>(codes + r * kStride + c) = q;
+        }
+        if (threadIdx.x < kBM)
+            scales[threadIdx.x] = m0 + threadIdx.x < mend ? a.a_scale[m0 + threadIdx.x] : 0.0f;
+    } else {
+        // L lanes to a row, NV vectors of eight to a lane; a wave has 4 * MT rows
+        constexpr int L = KT * 8 < kWave ? KT * 8 : kWave, NV = KT * 8 / L, RPI = kWave / L;
+        constexpr int kIters = 4 * MT / RPI;
+        constexpr int kBatch = kIters < 8 / NV ? kIters : 8 / NV;
+        const bool bf16 = a.x_dtype == DA_BF16;
+        const int c0 = lane % L * 8;
+        NormCoef f[NORM ? NV : 1];
+        if constexpr (NORM) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                f[j].load(a, g.cpg, c0 + j * L * 8, [&](int k) { return gm[k]; },
+                          [&](int k) { return gr[k]; });
+        }
+#pragma unroll 1
+        for (int b = 0; b < kIters; b += kBatch) {
+            Eight<XB> q[kBatch][NV];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t m = m0 + wave * 4 * MT + (b + i) * RPI + lane / L;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = c0 + j * L * 8;
+                    if (m < mend && c < a.K) q[i][j].load(a.x, m, c, a.K);
+                    else q[i][j].zero();
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = wave * 4 * MT + (b + i) * RPI + lane / L;
+                float v[NV][8];
+                uint32_t big = 0;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    q[i][j].unpack(v[j], bf16);
+                    if constexpr (NORM) f[j].apply(v[j], g.act);
+                    big = max(big, magnitude(v[j]));
+                }
+#pragma unroll
+                for (int s = L / 2; s; s >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, s));
+                const RowScale s = row_scale(big);
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    *reinterpret_cast<u32x2*>(codes + r * kStride + c0 + j * L * 8) =
+                        u32x2{pack_codes(v[j], s), pack_codes(v[j] + 4, s)};
+                if (lane % L == 0) scales[r] = s.scale;
+            }
+        }
+    }
+    __syncthreads();
+
+    const int col = lane % 16, part = lane / 16;
+    const auto row_operand = [&](int mt, int kc) {
+        return *reinterpret_cast<const i32x4*>(codes + (mt * 16 + col) * kStride + kc * 64 +
+                                               part * 16);
+    };
+    constexpr bool kHeld = KT * MT <= 32;   // at most 128 registers
+    i32x4 held[kHeld ? MT : 1][kHeld ? KT : 1];
+    if constexpr (kHeld) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int kc = 0; kc < KT; ++kc) held[mt][kc] = row_operand(mt, kc);
+    }
+    float rs[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) rs[mt] = scales[mt * 16 + col];
+
+    const int tiles = (a.N + 15) / 16;
+    const int t1 = min(tiles, (nb + 1) * a.tiles_per_block);
+    const auto weights = [&](int t, i32x4 (&wf)[KT]) {
+        const int n = min(t * 16 + col, a.N - 1);
+#pragma unroll
+        for (int kc = 0; kc < KT; ++kc) {
+            const int k = kc * 64 + part * 16;
+            wf[kc] = k < a.K ? weight_piece(a, n, k) : i32x4{0, 0, 0, 0};
+        }
+    };
+    int t = nb * a.tiles_per_block + wave;
+    i32x4 wf[KT];
+    if (t < t1) weights(t, wf);
+    for (; t < t1; t += kRowsWaves) {
+        i32x4 next[KT];
+        if (t + kRowsWaves < t1) weights(t + kRowsWaves, next);
+        i32x4 acc[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) acc[mt] = i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kc = 0; kc < KT; ++kc)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                acc[mt] = mfma(wf[kc], kHeld ? held[kHeld ? mt : 0][kHeld ? kc : 0]
+                                             : row_operand(mt, kc), acc[mt]);
+        const int n = t * 16 + part * 4;
+        if (n < a.N) {
+            const ColumnScale c = column_scale(a, n);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                if (m0 + mt * 16 + col < mend) finish(a, m0 + mt * 16 + col, n, acc[mt], rs[mt], c);
+        }
+#pragma unroll
+        for (int kc = 0; kc < KT; ++kc) wf[kc] = next[kc];
+    }
+}
+
+// ---- streaming kernel --------------------------------------------------------------------
+//
+// At most 16 * MT rows: a wave takes 16 output channels and every KW-th run of 64 columns,
+// the weights going from memory into operand registers, several runs in flight; the KW
+// waves' sums meet in LDS.  The rows' codes come from memory (XB 0), or the workgroup
+// quantises up to 16 rows of x into LDS first.
+
+constexpr int kSkinnyThreads = 512;
+constexpr int kSkinnyWaves = kSkinnyThreads / kWave;
+constexpr int kSkinnyRuns = 8;                 // weight runs of a wave in flight
+constexpr size_t kSkinnyLds = 48 * 1024;       // of codes
+
+template <int XB, int MT>
+__global__ __launch_bounds__(kSkinnyThreads) void i8_skinny_kernel(I8Args a, int kw_count) {
+    extern __shared__ __align__(16) unsigned char codes[];   // [M][stride], XB != 0
+    __shared__ __align__(16) i32x4 meet[kSkinnyWaves][MT][kWave];
+    __shared__ uint32_t bigs[16][kSkinnyWaves];
+    __shared__ float scales[16];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int col = lane % 16, part = lane / 16;
+    const int kw = wave % kw_count;
+    const int tile = blockIdx.x * (kSkinnyWaves / kw_count) + wave / kw_count;
+    const int tiles = (a.N + 15) / 16, runs = (a.K + 63) / 64;
+    const int stride = runs * 64 + 16;
+    const int n = min(tile * 16 + col, a.N - 1);
+    const bool live = tile < tiles;
+
+    i32x4 wf[kSkinnyRuns];
+    const auto fetch = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < kSkinnyRuns; ++i) {
+            const int k = (c + i * kw_count) * 64 + part * 16;
+            wf[i] = live && k < a.K ? weight_piece(a, n, k) : i32x4{0, 0, 0, 0};
+        }
+    };
+    fetch(kw);   // on its way while the rows are quantised
+
+    if constexpr (XB != 0) {
+        // 8 / 2^j waves to a row
+        const bool bf16 = a.x_dtype == DA_BF16;
+        int share = 1;
+        while (share < kSkinnyWaves && kSkinnyWaves / (2 * share) >= (int)a.M) share *= 2;
+        const int part_of = wave % share;
+        for (int m = wave / share; m < (int)a.M; m += kSkinnyWaves / share) {
+            uint32_t big = 0;
+            for (int c = (part_of * kWave + lane) * 8; c < a.K; c += share * kWave * 8) {
+                Eight<XB> q;
+                float v[8];
+                q.load(a.x, m, c, a.K);
+                q.unpack(v, bf16);
+                big = max(big, magnitude(v));
+            }
+            for (int s = kWave / 2; s; s >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, s));
+            if (lane == 0) bigs[m][part_of] = big;
+        }
+        __syncthreads();
+        for (int m = wave / share; m < (int)a.M; m += kSkinnyWaves / share) {
+            uint32_t big = 0;
+            for (int i = 0; i < share; ++i) big = max(big, bigs[m][i]);
+            const RowScale s = row_scale(big);
+            for (int c = (part_of * kWave + lane) * 8; c < runs * 64; c += share * kWave * 8) {
+                Eight<XB> q;
+                float v[8];
+                if (c < a.K) q.load(a.x, m, c, a.K);
+                else q.zero();
+                q.unpack(v, bf16);
+                *reinterpret_cast<u32x2*>(codes + m * stride + c) =
+                    u32x2{pack_codes(v, s), pack_codes(v + 4, s)};
+            }
+            if (part_of == 0 && lane == 0) scales[m] = s.scale;
+        }
+        __syncthreads();
+    }
+
+    i32x4 acc[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc[mt] = i32x4{0, 0, 0, 0};
+    for (int c = kw; c < runs;) {
+        i32x4 now[kSkinnyRuns];
+#pragma unroll
+        for (int i = 0; i < kSkinnyRuns; ++i) now[i] = wf[i];
+        const int at = c;
+        c += kSkinnyRuns * kw_count;
+        if (c < runs) fetch(c);
+#pragma unroll
+        for (int i = 0; i < kSkinnyRuns; ++i) {
+            const int k = (at + i * kw_count) * 64 + part * 16;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                i32x4 x = {0, 0, 0, 0};
+                const int m = mt * 16 + col;
+                if constexpr (XB != 0) {
+                    if (m < (int)a.M && k < runs * 64)
+                        x = *reinterpret_cast<const i32x4*>(codes + m * stride + k);
+                } else {
+                    if (m < (int)a.M && k < a.K) x = code_piece(a, m, k);
+                }
+                acc[mt] = mfma(now[i], x, acc[mt]);
+            }
+        }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) meet[wave][mt][lane] = acc[mt];
+    __syncthreads();
+    // the waves of a tile deal its row tiles
+    const int nn = tile * 16 + part * 4;
+    if (!live || nn >= a.N) return;
+    const ColumnScale cs = column_scale(a, nn);
+    for (int mt = kw; mt < MT; mt += kw_count) {
+        i32x4 t = meet[wave - kw][mt][lane];
+        for (int i = 1; i < kw_count; ++i) t += meet[wave - kw + i][mt][lane];
+        const int m = mt * 16 + col;
+        if (m < (int)a.M) finish(a, m, nn, t, XB != 0 ? scales[m] : a.a_scale[m], cs);
+    }
+}
+
+// ---- tiled product -----------------------------------------------------------------------
+//
+// BM rows by BN output channels to a workgroup, 128 columns at a time through LDS, each
+// wave WM x WN of it; the next 128 columns are on their way to registers while the matrix
+// cores work.  A 16-byte piece p of an LDS row r sits at place p ^ f(r), so that the 16 rows
+// an operand is read from fall into different banks.
+
+constexpr int kTileK = 128;
+
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(BM / WM * (BN / WN) * kWave) void i8_tile_kernel(I8Args a) {
+    constexpr int kThreads = BM / WM * (BN / WN) * kWave;
+    constexpr int kPieces = kTileK / 16;                       // of a row
+    constexpr int kXLoads = BM * kPieces / kThreads, kWLoads = BN * kPieces / kThreads;
+    static_assert(BM * kPieces % kThreads == 0 && BN * kPieces % kThreads == 0, "whole loads");
+    __shared__ __align__(16) i32x4 xs[2][BM * kPieces], ws[2][BN * kPieces];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int col = lane % 16, part = lane / 16;
+    const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
+
+    // Workgroups go round the 8 XCDs: each gets a run of consecutive tiles, and runs go down
+    // 8 row tiles before the next column tile, so that an XCD's L2 sees few operands.
+    const int mt = (int)((a.M + BM - 1) / BM), nt = (a.N + BN - 1) / BN;
+    int id = blockIdx.x;
+    {
+        const int total = mt * nt, per = total / 8, extra = total % 8;
+        const int x = id % 8, i = id / 8;
+        id = x * per + min(x, extra) + i;
+    }
+    const int band = id / (8 * nt), in_band = id - band * 8 * nt;
+    const int rows = min(8, mt - band * 8);
+    const int64_t m0 = (int64_t)(band * 8 + in_band % rows) * BM;
+    const int n0 = in_band / rows * BN;
+
+    i32x4 xq[kXLoads], wq[kWLoads];
+    const auto fetch = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i) {
+            const int e = i * kThreads + threadIdx.x;
+            const int64_t m = min(m0 + e / kPieces, a.M - 1);
+            const int k = k0 + e % kPieces * 16;
+            xq[i] = k < a.K ? code_piece(a, m, k) : i32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < kWLoads; ++i) {
+            const int e = i * kThreads + threadIdx.x;
+            const int n = min(n0 + e / kPieces, a.N - 1);
+            const int k = k0 + e % kPieces * 16;
+            wq[i] = k < a.K ? weight_piece(a, n, k) : i32x4{0, 0, 0, 0};
+        }
+    };
+    const auto place = [](int r, int p) { return r * kPieces + (p ^ ((r >> 1) & 7)); };
+    const auto put = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i) {
+            const int e = i * kThreads + threadIdx.x;
+            xs[b][place(e / kPieces, e % kPieces)] = xq[i];
+        }
+#pragma unroll
+        for (int i = 0; i < kWLoads; ++i) {
+            const int e = i * kThreads + threadIdx.x;
+            ws[b][place(e / kPieces, e % kPieces)] = wq[i];
+        }
+    };
+
+    i32x4 acc[WM / 16][WN / 16];
+#pragma unroll
+    for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < WN / 16; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    fetch(0);
+    put(0);
+    __syncthreads();
+    int b = 0;
+    for (int k0 = 0; k0 < a.K; k0 += kTileK, b ^= 1) {
+        const bool more = k0 + kTileK < a.K;
+        if (more) fetch(k0 + kTileK);
+#pragma unroll
+        for (int kc = 0; kc < kTileK / 64; ++kc) {
+            i32x4 xf[WM / 16], wf[WN / 16];
+#pragma unroll
+            for (int i = 0; i < WM / 16; ++i) xf[i] = xs[b][place(wm + i * 16 + col, kc * 4 + part)];
+#pragma unroll
+            for (int j = 0; j < WN / 16; ++j) wf[j] = ws[b][place(wn + j * 16 + col, kc * 4 + part)];
+#pragma unroll
+            for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < WN / 16; ++j) acc[i][j] = mfma(wf[j], xf[i], acc[i][j]);
+        }
+        if (more) put(b ^ 1);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < WN / 16; ++j) {
+        const int n = n0 + wn + j * 16 + part * 4;
+        if (n >= a.N) continue;
+        const ColumnScale c = column_scale(a, n);
+#pragma unroll
+        for (int i = 0; i < WM / 16; ++i) {
+            const int64_t m = m0 + wm + i * 16 + col;
+            if (m < a.M) finish(a, m, n, acc[i][j], a.a_scale[m], c);
+        }
+    }
+}
+
+// ---- launches ----------------------------------------------------------------------------
+
+constexpr int kRowsMostK = 1024;
+
+template <int XB, bool NORM, int KT, int MT>
+hipError_t launch_rows(I8Args a, const GnArgs& g, hipStream_t stream) {
+    constexpr int kBM = 16 * MT;
+    int64_t row_blocks;
+    if (NORM) {
+        a.m_blocks = (int32_t)((g.S + kBM - 1) / kBM);
+        row_blocks = (int64_t)g.N * a.m_blocks;
+    } else {
+        row_blocks = (a.M + kBM - 1) / kBM;
+    }
+    // output tiles are shared out where the row blocks alone leave compute units idle
+    const int tiles = (a.N + 15) / 16;
+    const int64_t want = std::max<int64_t>(1, 512 / row_blocks);
+    a.tiles_per_block = (int32_t)std::max<int64_t>(std::min(tiles, kRowsWaves),
+                                                   (tiles + want - 1) / want);
+    a.n_blocks = (tiles + a.tiles_per_block - 1) / a.tiles_per_block;
+    i8_rows_kernel<XB, NORM, KT, MT>
+        <<<(uint32_t)(row_blocks * a.n_blocks), kRowsThreads, 0, stream>>>(a, g);
+    return hipGetLastError();
+}
+
+template <int XB, bool NORM>
+hipError_t rows_by_depth(const I8Args& a, const GnArgs& g, hipStream_t stream) {
+    if (a.K <= 128) return launch_rows<XB, NORM, 2, 4>(a, g, stream);
+    if (a.K <= 256) return launch_rows<XB, NORM, 4, 4>(a, g, stream);
+    if (a.K <= 512) return launch_rows<XB, NORM, 8, 4>(a, g, stream);
+    return launch_rows<XB, NORM, 16, 4>(a, g, stream);
+}
+
+template <int XB>
+hipError_t launch_skinny(const I8Args& a, hipStream_t stream) {
+    const int runs = (a.K + 63) / 64, tiles = (a.N + 15) / 16;
+    int kw = kSkinnyWaves;
+    while (kw > 1 && runs < 2 * kw) kw /= 2;
+    const uint32_t blocks = (uint32_t)((tiles + kSkinnyWaves / kw - 1) / (kSkinnyWaves / kw));
+    const size_t lds = XB ? (size_t)a.M * (runs * 64 + 16) : 0;
+    if constexpr (XB != 0) {
+        i8_skinny_kernel<XB, 1><<<blocks, kSkinnyThreads, lds, stream>>>(a, kw);
+    } else {
+        if (a.M <= 16) i8_skinny_kernel<XB, 1><<<blocks, kSkinnyThreads, 0, stream>>>(a, kw);
+        else if (a.M <= 32) i8_skinny_kernel<XB, 2><<<blocks, kSkinnyThreads, 0, stream>>>(a, kw);
+        else i8_skinny_kernel<XB, 4><<<blocks, kSkinnyThreads, 0, stream>>>(a, kw);
+    }
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN>
+hipError_t launch_tile(const I8Args& a, hipStream_t stream) {
+    const int64_t blocks = (a.M + BM - 1) / BM * ((a.N + BN - 1) / BN);
+    i8_tile_kernel<BM, BN, WM, WN>
+        <<<(uint32_t)blocks, BM / WM * (BN / WN) * kWave, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_tiles(const I8Args& a, hipStream_t stream) {
+    const auto blocks = [&](int bm, int bn) {
+        return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn);
+    };
+    if (blocks(256, 256) >= 200) return launch_tile<256, 256, 128, 64>(a, stream);
+    if (blocks(128, 128) >= 256) return launch_tile<128, 128, 64, 64>(a, stream);
+    return launch_tile<64, 64, 32, 32>(a, stream);
 }
 
 }  // namespace
 
-hipError_t launch_i8_quantize(const I8Args& a, hipStream_t stream) {
-    const uint32_t blocks = (uint32_t)((a.M + 3) / 4);
-    i8_quantize_kernel<<<blocks, kQuantThreads, 0, stream>>>(a);
+I8Path i8_path(int64_t M, int64_t K, int64_t N, bool codes, bool norm) {
+    if (norm) return K <= kRowsMostK ? I8Path::kRows : I8Path::kTiles;
+    if (M <= 16 && !codes && (size_t)M * ((K + 63) / 64 * 64 + 16) <= kSkinnyLds)
+        return I8Path::kSkinny;
+    if (M <= 64) return I8Path::kSkinnyCodes;
+    if (K <= kRowsMostK) return I8Path::kRows;
+    return I8Path::kTiles;
+}
+
+hipError_t launch_i8_quantize(const I8Args& a, const GnArgs* norm, hipStream_t stream) {
+    const uint32_t blocks = (uint32_t)((a.M + kQuantThreads / kWave - 1) / (kQuantThreads / kWave));
+    if (norm) {
+        if (a.x_dtype == DA_F32)
+            i8_norm_quantize_kernel<4><<<blocks, kQuantThreads, 0, stream>>>(a, *norm);
+        else
+            i8_norm_quantize_kernel<2><<<blocks, kQuantThreads, 0, stream>>>(a, *norm);
+        return hipGetLastError();
+    }
+    if (a.x_dtype == DA_F32) i8_quantize_kernel<4><<<blocks, kQuantThreads, 0, stream>>>(a);
+    else i8_quantize_kernel<2><<<blocks, kQuantThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
-hipError_t launch_i8_matmul(const I8Args& a, hipStream_t stream) {
-    const uint32_t blocks = (uint32_t)((a.M + 63) / 64 * ((a.N + 63) / 64));
-    i8_matmul_kernel<<<blocks, 256, 0, stream>>>(a);
-    return hipGetLastError();
+hipError_t launch_i8_product(const I8Args& a, I8Path path, bool codes, const GnArgs* norm,
+                             hipStream_t stream) {
+    const bool wide = a.x_dtype == DA_F32;
+    switch (path) {
+        case I8Path::kRows:
+            if (norm)
+                return wide ? rows_by_depth<4, true>(a, *norm, stream)
+                            : rows_by_depth<2, true>(a, *norm, stream);
+            if (codes) return rows_by_depth<0, false>(a, GnArgs{}, stream);
+            return wide ? rows_by_depth<4, false>(a, GnArgs{}, stream)
+                        : rows_by_depth<2, false>(a, GnArgs{}, stream);
+        case I8Path::kSkinny:
+            return wide ? launch_skinny<4>(a, stream) : launch_skinny<2>(a, stream);
+        case I8Path::kSkinnyCodes:
+            return launch_skinny<0>(a, stream);
+        default:
+            return launch_tiles(a, stream);
+    }
 }
 
 }  // namespace da

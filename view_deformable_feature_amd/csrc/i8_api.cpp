@@ -59,6 +59,11 @@ da_status check_workspace(uint64_t need, const void* workspace, size_t workspace
     return DA_OK;
 }
 
+// Paths whose product reads codes that were written to memory first.
+bool through_memory(da::I8Path path) {
+    return path == da::I8Path::kTiles || path == da::I8Path::kSkinnyCodes;
+}
+
 // Codes and scales of a quantised [M, K].
 uint64_t codes_bytes(int64_t M, int64_t K) { return part_bytes((uint64_t)M * K); }
 uint64_t quantised_bytes(int64_t M, int64_t K) { return codes_bytes(M, K) + part_bytes(M * 4); }
@@ -94,7 +99,7 @@ da_status i8_quantize_rows(int64_t rows, int64_t channels, int32_t x_dtype, cons
     a.x = x;
     a.a = codes;
     a.a_scale = scale;
-    return da::report_hip(da::launch_i8_quantize(a, static_cast<hipStream_t>(stream)),
+    return da::report_hip(da::launch_i8_quantize(a, nullptr, static_cast<hipStream_t>(stream)),
                           "row quantisation launch");
 }
 
@@ -125,22 +130,26 @@ da_status i8_matmul(const i8_problem* p, const int8_t* a_codes, const float* a_s
     a.w_scale = w_scale;
     a.bias = bias;
     a.out = out;
-    return da::report_hip(da::launch_i8_matmul(a, static_cast<hipStream_t>(stream)),
-                          "8-bit product launch");
+    const da::I8Path path = da::i8_path(a.M, a.K, a.N, true, false);
+    return da::report_hip(
+        da::launch_i8_product(a, path, true, nullptr, static_cast<hipStream_t>(stream)),
+        "8-bit product launch");
 }
 
 da_status i8_linear_workspace_size(const i8_problem* p, size_t* bytes) {
     if (!bytes) return report_error(DA_ERR_INVALID_ARG, "bytes is NULL");
     const da_status st = check_problem(p, false);
     if (st != DA_OK) return st;
-    *bytes = (size_t)quantised_bytes(p->rows, p->in_channels);
+    const da::I8Path path = da::i8_path(p->rows, p->in_channels, p->out_channels, false, false);
+    *bytes = through_memory(path) ? (size_t)quantised_bytes(p->rows, p->in_channels) : 0;
     return DA_OK;
 }
 
 da_status i8_linear(const i8_problem* p, const void* x, const int8_t* w, const float* w_scale,
                     const float* bias, void* out, void* workspace, size_t workspace_bytes,
                     void* stream) {
-    da_status st = check_problem(p, false);
+    size_t need = 0;
+    da_status st = i8_linear_workspace_size(p, &need);
     if (st != DA_OK) return st;
     if (p->rows == 0) return DA_OK;
     if (!x || !w || !w_scale || !out)
@@ -148,31 +157,39 @@ da_status i8_linear(const i8_problem* p, const void* x, const int8_t* w, const f
     if (!aligned(x, elem_bytes(p->x_dtype)) || !aligned(w_scale, 4) || !aligned(bias, 4) ||
         !aligned(out, elem_bytes(p->out_dtype)))
         return report_error(DA_ERR_INVALID_ARG, "a tensor is not element aligned");
-    st = check_workspace(quantised_bytes(p->rows, p->in_channels), workspace, workspace_bytes);
+    st = check_workspace(need, workspace, workspace_bytes);
     if (st != DA_OK) return st;
     da::I8Args a = args_of(p->rows, p->in_channels, p->out_channels, p->activation, p->x_dtype,
                            p->out_dtype);
-    unsigned char* base = static_cast<unsigned char*>(workspace);
     a.x = x;
-    a.a = reinterpret_cast<int8_t*>(base);
-    a.a_scale = reinterpret_cast<float*>(base + codes_bytes(p->rows, p->in_channels));
     a.w = w;
     a.w_scale = w_scale;
     a.bias = bias;
     a.out = out;
-    hipError_t e = da::launch_i8_quantize(a, static_cast<hipStream_t>(stream));
-    if (e == hipSuccess) e = da::launch_i8_matmul(a, static_cast<hipStream_t>(stream));
+    const da::I8Path path = da::i8_path(a.M, a.K, a.N, false, false);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    if (through_memory(path)) {
+        unsigned char* base = static_cast<unsigned char*>(workspace);
+        a.a = reinterpret_cast<int8_t*>(base);
+        a.a_scale = reinterpret_cast<float*>(base + codes_bytes(a.M, a.K));
+        e = da::launch_i8_quantize(a, nullptr, s);
+    }
+    if (e == hipSuccess) e = da::launch_i8_product(a, path, false, nullptr, s);
     return da::report_hip(e, "8-bit linear launch");
 }
 
 da_status i8_norm_linear_workspace_size(const gn_problem* p, int64_t out_channels, size_t* bytes) {
     if (!bytes) return report_error(DA_ERR_INVALID_ARG, "bytes is NULL");
-    uint64_t stats = 0;
-    da_status st = da::gn_stats_bytes(p, stats);
+    uint64_t need = 0;
+    da_status st = da::gn_stats_bytes(p, need);
     if (st != DA_OK) return st;
-    st = check_sizes(p->batch * p->rows, p->channels, out_channels);
+    const int64_t M = p->batch * p->rows;
+    st = check_sizes(M, p->channels, out_channels);
     if (st != DA_OK) return st;
-    *bytes = (size_t)(p->batch ? stats + quantised_bytes(p->batch * p->rows, p->channels) : 0);
+    if (through_memory(da::i8_path(M, p->channels, out_channels, false, true)))
+        need += quantised_bytes(M, p->channels);
+    *bytes = p->batch ? (size_t)need : 0;
     return DA_OK;
 }
 
@@ -193,26 +210,27 @@ da_status i8_norm_linear(const gn_problem* p, int64_t out_channels, const void* 
     if (st != DA_OK) return st;
     const int64_t M = p->batch * p->rows;
     da::I8Args a = args_of(M, p->channels, out_channels, DA_ACT_NONE, p->x_dtype, p->out_dtype);
-    unsigned char* base = static_cast<unsigned char*>(workspace);
     a.x = x;
-    a.a = reinterpret_cast<int8_t*>(base);
-    base += codes_bytes(M, p->channels);
-    a.a_scale = reinterpret_cast<float*>(base);
-    base += part_bytes(M * 4);
     a.w = w;
     a.w_scale = w_scale;
     a.bias = bias;
     a.out = out;
     a.norm_weight = norm_weight;
     a.norm_bias = norm_bias;
-    a.S = p->rows;
-    a.G = (int32_t)p->groups;
-    a.cpg = (int32_t)(p->channels / p->groups);
-    a.norm_act = p->activation;
-    hipError_t e = da::enqueue_gn_stats(p, x, base, &a.mean, &a.rstd,
-                                        static_cast<hipStream_t>(stream));
-    if (e == hipSuccess) e = da::launch_i8_quantize(a, static_cast<hipStream_t>(stream));
-    if (e == hipSuccess) e = da::launch_i8_matmul(a, static_cast<hipStream_t>(stream));
+    const da::I8Path path = da::i8_path(a.M, a.K, a.N, false, true);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    unsigned char* base = static_cast<unsigned char*>(workspace);
+    if (through_memory(path)) {
+        a.a = reinterpret_cast<int8_t*>(base);
+        base += codes_bytes(a.M, a.K);
+        a.a_scale = reinterpret_cast<float*>(base);
+        base += part_bytes(a.M * 4);
+    }
+    da::GnArgs g;
+    hipError_t e = da::enqueue_gn_stats(p, x, base, through_memory(path), g, s);
+    if (e == hipSuccess && through_memory(path)) e = da::launch_i8_quantize(a, &g, s);
+    if (e == hipSuccess)
+        e = da::launch_i8_product(a, path, false, through_memory(path) ? nullptr : &g, s);
     return da::report_hip(e, "normalised 8-bit linear launch");
 }
 

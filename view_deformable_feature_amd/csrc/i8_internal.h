@@ -7,11 +7,13 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include "gn_internal.h"
+
 namespace da {
 
 struct I8Args {
     const void* x;            // [M, K] of x_dtype (quantising kernels)
-    int8_t* a;                // [M, K] codes
+    int8_t* a;                // [M, K] codes (workspace where x is quantised first)
     float* a_scale;           // [M]
     const int8_t* w;          // [N, K]
     const float* w_scale;     // [N]
@@ -20,16 +22,26 @@ struct I8Args {
     int64_t M;
     int32_t K, N;
     int32_t act, x_dtype, out_dtype;
+    int32_t n_blocks;         // rows kernel: workgroups that share a block of rows
+    int32_t tiles_per_block;  // rows kernel: 16-column tiles of one of them
     // a row passes through group norm and an activation before it is quantised
-    const float* mean;        // [images, G], or NULL
-    const float* rstd;        // [images, G]
     const float* norm_weight; // [K] or NULL
     const float* norm_bias;   // [K] or NULL
-    int64_t S;                // rows of an image
-    int32_t G, cpg, norm_act;
+    int32_t m_blocks;         // rows kernel: row blocks of an image
 };
 
-hipError_t launch_i8_quantize(const I8Args& a, hipStream_t stream);
-hipError_t launch_i8_matmul(const I8Args& a, hipStream_t stream);
+// Which kernels a problem takes; the workspace goes by it.
+enum class I8Path {
+    kRows,      // one kernel that quantises its rows itself
+    kSkinny,    // one kernel, few rows: the weights are streamed once
+    kTiles,     // quantised rows in memory, then a tiled product
+    kSkinnyCodes,  // quantised rows in memory, then the streaming kernel
+};
+I8Path i8_path(int64_t M, int64_t K, int64_t N, bool codes, bool norm);
+
+hipError_t launch_i8_quantize(const I8Args& a, const GnArgs* norm, hipStream_t stream);
+// The product on `path`; quantising paths read x, the others a and a_scale.
+hipError_t launch_i8_product(const I8Args& a, I8Path path, bool codes, const GnArgs* norm,
+                             hipStream_t stream);
 
 }  // namespace da

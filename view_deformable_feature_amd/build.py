@@ -23,7 +23,7 @@ SOURCES = [os.path.join(CSRC, f)
                      "i8_api.cpp")]
 HEADERS = [os.path.join(INCLUDE, f) for f in ("deformagg.h", "dcn.h", "group_norm.h", "int8.h")] + [
     os.path.join(CSRC, f) for f in ("da_internal.h", "da_device.h", "da_pack.h", "dcn_internal.h",
-                                    "host_errors.h", "act_device.h", "gn_internal.h", "gn_device.h",
+                                    "host_errors.h", "act_device.h", "gn_internal.h",
                                     "i8_internal.h")]
 EXPORTS = os.path.join(CSRC, "exports.map")   # the C ABI is the only export
 ARCH = "gfx950"

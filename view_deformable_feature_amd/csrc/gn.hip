@@ -8,7 +8,7 @@
 #include <stdint.h>
 
 #include "act_device.h"
-#include "gn_device.h"
+#include "gn_internal.h"
 
 namespace da {
 namespace {
@@ -45,11 +45,11 @@ __device__ __forceinline__ Slab slab_of(const GnArgs& a, int s, int threads) {
     return b;
 }
 
-// out[u] = sum of red[r * cols + j] over r < R and the `per` columns of unit u, by one
-// wave per unit.  Every thread of the workgroup calls it; red is complete on entry, out
+// out[u] = factor * the sum of red[r * cols + j] over r < R and the `per` columns of unit u,
+// by one wave per unit.  Every thread of the workgroup calls it; red is complete on entry, out
 // on return.
 __device__ __forceinline__ void unit_sums(const float* red, int R, int cols, int per, int nunits,
-                                          float* out) {
+                                          float factor, float* out) {
     const int lane = threadIdx.x & (kWave - 1), nw = blockDim.x / kWave;
     for (int u = threadIdx.x / kWave; u < nunits; u += nw) {
         float t = 0.0f;
@@ -58,9 +58,84 @@ __device__ __forceinline__ void unit_sums(const float* red, int R, int cols, int
             t += red[r * cols + u * per + j];
         }
         for (int m = kWave / 2; m; m >>= 1) t += __shfl_xor(t, m);
-        if (lane == 0) out[u] = t;
+        if (lane == 0) out[u] = t * factor;
     }
     __syncthreads();
+}
+
+__device__ __forceinline__ double wave_sum(double t) {
+    for (int m = kWave / 2; m; m >>= 1) t += __shfl_xor(t, m);
+    return t;
+}
+
+// The group's first value in image n: all of the group's means are formed and kept as
+// differences from it, so that a large common offset cancels before anything is rounded.
+__device__ __forceinline__ float origin_of(const GnArgs& a, int n, int g) {
+    return load_elem(a.x, (int64_t)n * a.S * a.C + (int64_t)g * a.cpg, a.x_dtype);
+}
+
+// 1 / sqrt(var + eps), rounded once; squares past binary32 leave no number.
+__device__ __forceinline__ float rstd_of(double var, float eps) {
+    return var < 0x1p127 ? (float)(1.0 / sqrt(var + (double)eps)) : __uint_as_float(0x7fc00000u);
+}
+
+// A workgroup's statistics from its threads': each of cnt rows of V channels, with the sums
+// of their differences from `first` and of those differences' squares, taken about that
+// value so that a large common offset cancels before anything is rounded.  Leaves in um
+// the units' means less the group's origin, in uq their sums of squared deviations from that
+// mean.  red holds one value per thread where a vector lies in one unit, else V.
+template <int V>
+__device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int n, float rows,
+                                             int cnt, const float (&first)[V],
+                                             const float (&sum)[V], const float (&sq)[V],
+                                             float* red, float* um, float* uq) {
+    const int per_ch = a.upg == 1 ? a.cpg : b.width;
+    const bool whole = per_ch % V == 0;
+    const int cols = whole ? b.cols : b.width, per = whole ? per_ch / V : per_ch;
+    const float rc = cnt ? 1.0f / cnt : 0.0f, inv = 1.0f / (rows * per_ch);
+    float m[V];   // this thread's channel means, less the origin
+    const int u0 = b.v * V / per_ch;
+    float origin = origin_of(a, n, b.g0 + u0);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (!whole) origin = origin_of(a, n, b.g0 + (b.v * V + e) / per_ch);
+        m[e] = (first[e] - origin) + sum[e] * rc;
+    }
+    if (b.r < b.R) {
+        if (whole) {
+            float t = 0.0f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) t += m[e];
+            red[b.r * cols + b.v] = t * cnt;
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) red[b.r * cols + b.v * V + e] = m[e] * cnt;
+        }
+    }
+    __syncthreads();
+    unit_sums(red, b.R, cols, per, b.nunits, inv, um);
+    float dev[V], mean = um[u0];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (!whole) mean = um[(b.v * V + e) / per_ch];
+        const float d = m[e] - mean;
+        // sum of squares about m is sq - sum^2 / cnt, below zero by rounding alone; a NaN stays
+        const float t = sq[e] - sum[e] * sum[e] * rc;
+        dev[e] = cnt ? (t < 0.0f ? 0.0f : t) + cnt * d * d : 0.0f;
+    }
+    if (b.r < b.R) {
+        if (whole) {
+            float t = 0.0f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) t += dev[e];
+            red[b.r * cols + b.v] = t;
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) red[b.r * cols + b.v * V + e] = dev[e];
+        }
+    }
+    __syncthreads();
+    unit_sums(red, b.R, cols, per, b.nunits, 1.0f, uq);
 }
 
 // One chunk: (mean less the group's origin, M2) of each unit, where M2 is the sum of
@@ -105,53 +180,46 @@ __global__ __launch_bounds__(kGnThreads) void gn_stats_kernel(GnArgs a) {
                 }
         }
     }
-    // one value per thread where a vector lies in one unit, else one per channel
-    const int per_ch = a.upg == 1 ? a.cpg : b.width;
-    const bool whole = per_ch % V == 0;
-    const int cols = whole ? b.cols : b.width, per = whole ? per_ch / V : per_ch;
-    const float rc = cnt ? 1.0f / cnt : 0.0f;
-    float m[V];   // this thread's channel means, less the origin
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-        m[e] = (first[e] - origin_of(a, n, b.g0 + (b.v * V + e) / per_ch)) + sum[e] * rc;
-    if (b.r < b.R) {
-        if (whole) {
-            float t = 0.0f;
-#pragma unroll
-            for (int e = 0; e < V; ++e) t += m[e];
-            red[b.r * cols + b.v] = t * cnt;
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) red[b.r * cols + b.v * V + e] = m[e] * cnt;
-        }
-    }
-    __syncthreads();
-    unit_sums(red, b.R, cols, per, b.nunits, um);
-    const float total = (float)(r1 - r0) * per_ch;
-    float dev[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const float d = m[e] - um[(b.v * V + e) / per_ch] / total;
-        // sum of squares about m is sq - sum^2 / cnt, below zero by rounding alone; a NaN stays
-        const float t = sq[e] - sum[e] * sum[e] * rc;
-        dev[e] = cnt ? (t < 0.0f ? 0.0f : t) + cnt * d * d : 0.0f;
-    }
-    if (b.r < b.R) {
-        if (whole) {
-            float t = 0.0f;
-#pragma unroll
-            for (int e = 0; e < V; ++e) t += dev[e];
-            red[b.r * cols + b.v] = t;
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) red[b.r * cols + b.v * V + e] = dev[e];
-        }
-    }
-    __syncthreads();
-    unit_sums(red, b.R, cols, per, b.nunits, uq);
+    join_threads(a, b, n, (float)(r1 - r0), cnt, first, sum, sq, red, um, uq);
     float2* part = a.unit_part + ((int64_t)n * a.chunks + chunk) * a.units + b.unit0;
     for (int u = threadIdx.x; u < b.nunits; u += kGnThreads)
-        part[u] = make_float2(um[u] / total, uq[u]);
+        part[u] = make_float2(um[u], uq[u]);
+}
+
+// The chunks' statistics of groups g0 .. g0 + ngroups - 1 joined in binary64, one wave
+// per group: mean and rstd into LDS.  Every thread of the workgroup calls it.
+__device__ __forceinline__ void join_stats(const GnArgs& a, int n, int g0, int ngroups, float* gm,
+                                           float* gr) {
+    const int lane = threadIdx.x & (kWave - 1), nw = blockDim.x / kWave;
+    const double total = (double)a.S * a.cpg;
+    for (int j = threadIdx.x / kWave; j < ngroups; j += nw) {
+        const int g = g0 + j;
+        const float2* part = a.unit_part + (int64_t)n * a.chunks * a.units + (int64_t)g * a.upg;
+        const int entries = a.chunks * a.upg;
+        double sum = 0.0, m2 = 0.0;
+        for (int e = lane; e < entries; e += kWave) {
+            const int c = e / a.upg, u = e - c * a.upg;
+            const int64_t r0 = c * a.rows_per_chunk;
+            const double cnt = (double)(min(r0 + a.rows_per_chunk, a.S) - r0) *
+                               min(a.cpu, a.cpg - u * a.cpu);
+            sum += cnt * part[(int64_t)c * a.units + u].x;
+        }
+        const double mean = wave_sum(sum) / total;
+        for (int e = lane; e < entries; e += kWave) {
+            const int c = e / a.upg, u = e - c * a.upg;
+            const int64_t r0 = c * a.rows_per_chunk;
+            const double cnt = (double)(min(r0 + a.rows_per_chunk, a.S) - r0) *
+                               min(a.cpu, a.cpg - u * a.cpu);
+            const float2 q = part[(int64_t)c * a.units + u];
+            m2 += q.y + cnt * (q.x - mean) * (q.x - mean);
+        }
+        const double var = wave_sum(m2) / total;
+        if (lane == 0) {
+            gm[j] = (float)(mean + (double)origin_of(a, n, g));
+            gr[j] = rstd_of(var, a.eps);
+        }
+    }
+    __syncthreads();
 }
 
 // mean and rstd alone: 4 groups to a workgroup.
@@ -170,26 +238,17 @@ __global__ __launch_bounds__(kGnThreads) void gn_join_kernel(GnArgs a) {
 
 template <typename T, int V>
 __global__ __launch_bounds__(kGnThreads) void gn_apply_kernel(GnArgs a) {
-    __shared__ float gm[kGnThreads * V], gr[kGnThreads * V];
     const int s = blockIdx.x % a.slabs;
     const int chunk = (blockIdx.x / a.slabs) % a.chunks;
     const int n = blockIdx.x / a.slabs / a.chunks;
     const Slab b = slab_of<V>(a, s, kGnThreads);
-    const int ngroups = a.upg == 1 ? b.nunits : 1;
-    join_stats(a, n, b.g0, ngroups, gm, gr);
-    if (chunk == 0 && (a.upg == 1 || s % a.upg == 0)) {
-        for (int j = threadIdx.x; j < ngroups; j += kGnThreads) {
-            if (a.mean) a.mean[(int64_t)n * a.G + b.g0 + j] = gm[j];
-            if (a.rstd) a.rstd[(int64_t)n * a.G + b.g0 + j] = gr[j];
-        }
-    }
     if (b.r >= b.R) return;
     float mu[V], sc[V], bi[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         const int c = b.v * V + e, j = a.upg == 1 ? c / a.cpg : 0;
-        mu[e] = gm[j];
-        sc[e] = gr[j] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
+        mu[e] = a.mean[(int64_t)n * a.G + b.g0 + j];
+        sc[e] = a.rstd[(int64_t)n * a.G + b.g0 + j] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
         bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
     }
     const int64_t r0 = chunk * a.rows_per_chunk, r1 = min(r0 + a.rows_per_chunk, a.S);
@@ -211,6 +270,30 @@ __global__ __launch_bounds__(kGnThreads) void gn_apply_kernel(GnArgs a) {
                 activate(z, a.act);
                 store_vec(a.out, base + (row + i * b.R) * a.C, z, a.out_dtype);
             }
+    }
+}
+
+// The threads' sums A and B of each channel added up over their rows: ra[c], rb[c] for c <
+// width.  Rows fold in halves: R -> ceil(R / 2) -> ... -> 1.
+template <int V>
+__device__ __forceinline__ void fold_rows(const Slab& b, const float (&A)[V], const float (&B)[V],
+                                          float* ra, float* rb) {
+    if (b.r < b.R) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            ra[b.r * b.width + b.v * V + e] = A[e];
+            rb[b.r * b.width + b.v * V + e] = B[e];
+        }
+    }
+    __syncthreads();
+    for (int R = b.R; R > 1;) {
+        const int half = (R + 1) / 2, n2 = (R - half) * b.width;
+        for (int e = threadIdx.x; e < n2; e += blockDim.x) {
+            ra[e] += ra[e + half * b.width];
+            rb[e] += rb[e + half * b.width];
+        }
+        R = half;
+        __syncthreads();
     }
 }
 
@@ -269,23 +352,8 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_stats_kernel(GnArgs a) {
                     }
                 }
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            ra[b.r * b.width + b.v * V + e] = A[e];
-            rb[b.r * b.width + b.v * V + e] = B[e];
-        }
     }
-    __syncthreads();
-    // rows folded in halves: R -> ceil(R / 2) -> ... -> 1
-    for (int R = b.R; R > 1;) {
-        const int half = (R + 1) / 2, n2 = (R - half) * b.width;
-        for (int e = threadIdx.x; e < n2; e += kGnThreads) {
-            ra[e] += ra[e + half * b.width];
-            rb[e] += rb[e + half * b.width];
-        }
-        R = half;
-        __syncthreads();
-    }
+    fold_rows(b, A, B, ra, rb);
     float2* cp = a.chan_part + ((int64_t)n * a.chunks + chunk) * a.C + b.ch0;
     for (int c = threadIdx.x; c < b.width; c += kGnThreads) {
         cp[c] = make_float2(ra[c], rb[c]);
@@ -295,8 +363,8 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_stats_kernel(GnArgs a) {
     }
     __syncthreads();
     const int per = a.upg == 1 ? a.cpg : b.width;
-    unit_sums(ra, 1, b.width, per, b.nunits, ua);
-    unit_sums(rb, 1, b.width, per, b.nunits, ub);
+    unit_sums(ra, 1, b.width, per, b.nunits, 1.0f, ua);
+    unit_sums(rb, 1, b.width, per, b.nunits, 1.0f, ub);
     float2* up = a.unit_part + ((int64_t)n * a.chunks + chunk) * a.units + b.unit0;
     for (int u = threadIdx.x; u < b.nunits; u += kGnThreads) up[u] = make_float2(ua[u], ub[u]);
 }
@@ -326,6 +394,29 @@ __device__ __forceinline__ void channel_sums(const GnArgs& a, int block) {
     }
 }
 
+// The averages over each (image, group) of weight * dz and weight * dz * xhat from the chunks'
+// sums: 4 groups to a workgroup.
+__global__ __launch_bounds__(kGnThreads) void gn_bwd_join_kernel(GnArgs a) {
+    const int blocks = (a.G + kGnJoin - 1) / kGnJoin;
+    const int n = blockIdx.x / blocks;
+    const int g = (blockIdx.x - n * blocks) * kGnJoin + threadIdx.x / kWave;
+    if (g >= a.G) return;
+    const int lane = threadIdx.x & (kWave - 1);
+    const double inv = 1.0 / ((double)a.S * a.cpg);
+    const float2* part = a.unit_part + (int64_t)n * a.chunks * a.units + (int64_t)g * a.upg;
+    double t1 = 0.0, t2 = 0.0;
+    for (int e = lane; e < a.chunks * a.upg; e += kWave) {
+        const int c = e / a.upg, u = e - c * a.upg;
+        const float2 q = part[(int64_t)c * a.units + u];
+        t1 += q.x;
+        t2 += q.y;
+    }
+    t1 = wave_sum(t1);
+    t2 = wave_sum(t2);
+    if (lane == 0)
+        a.group_sums[(int64_t)n * a.G + g] = make_float2((float)(t1 * inv), (float)(t2 * inv));
+}
+
 // grad_x of one chunk; the workgroups after the last chunk's form grad_weight and
 // grad_bias.
 template <typename T, int V>
@@ -334,34 +425,10 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int6
         channel_sums(a, blockIdx.x - chunk_blocks);
         return;
     }
-    __shared__ float m1[kGnThreads * V], m2[kGnThreads * V];
     const int s = blockIdx.x % a.slabs;
     const int chunk = (blockIdx.x / a.slabs) % a.chunks;
     const int n = blockIdx.x / a.slabs / a.chunks;
     const Slab b = slab_of<V>(a, s, kGnThreads);
-    const int ngroups = a.upg == 1 ? b.nunits : 1;
-    {
-        const int lane = threadIdx.x & (kWave - 1), nw = kGnThreads / kWave;
-        const double inv = 1.0 / ((double)a.S * a.cpg);
-        for (int j = threadIdx.x / kWave; j < ngroups; j += nw) {
-            const float2* part = a.unit_part + (int64_t)n * a.chunks * a.units +
-                                 (int64_t)(b.g0 + j) * a.upg;
-            double t1 = 0.0, t2 = 0.0;
-            for (int e = lane; e < a.chunks * a.upg; e += kWave) {
-                const int c = e / a.upg, u = e - c * a.upg;
-                const float2 q = part[(int64_t)c * a.units + u];
-                t1 += q.x;
-                t2 += q.y;
-            }
-            t1 = wave_sum(t1);
-            t2 = wave_sum(t2);
-            if (lane == 0) {
-                m1[j] = (float)(t1 * inv);
-                m2[j] = (float)(t2 * inv);
-            }
-        }
-        __syncthreads();
-    }
     if (b.r >= b.R) return;
     float mu[V], rs[V], w[V], bi[V], c1[V], c2[V];
 #pragma unroll
@@ -371,8 +438,9 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int6
         rs[e] = a.rstd[(int64_t)n * a.G + b.g0 + j];
         w[e] = a.weight ? a.weight[b.ch0 + c] : 1.0f;
         bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
-        c1[e] = m1[j];
-        c2[e] = m2[j];
+        const float2 q = a.group_sums[(int64_t)n * a.G + b.g0 + j];
+        c1[e] = q.x;
+        c2[e] = q.y;
     }
     const int64_t r0 = chunk * a.rows_per_chunk, r1 = min(r0 + a.rows_per_chunk, a.S);
     const int64_t base = ((int64_t)n * a.S) * a.C + b.ch0 + b.v * V;
@@ -406,10 +474,217 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int6
     }
 }
 
+// ---- an image's slab in one workgroup ----------------------------------------------------
+//
+// Where a slab of one image fits the registers of a workgroup, it is read once, its
+// statistics are formed there and it is normalised and written from there: the floor of
+// traffic, one launch.  Consecutive slabs go to one XCD, whose L2 then holds the 128-byte
+// lines that two slabs share.
+__device__ __forceinline__ int xcd_run(int id, int total) {
+    const int x = id % 8, i = id / 8;
+    return x * (total / 8) + min(x, total % 8) + i;
+}
+
+template <typename T, int V, int NV, bool STORE>
+__global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
+    __shared__ float red[kGnWholeThreads * V];
+    __shared__ float um[kGnWholeThreads], uq[kGnWholeThreads];
+    const int id = xcd_run(blockIdx.x, a.N * a.slabs);
+    const int n = id / a.slabs, s = id - n * a.slabs;
+    const Slab b = slab_of<V>(a, s, blockDim.x);
+    const int64_t base = (int64_t)n * a.S * a.C + b.ch0 + b.v * V;
+    const T* p = static_cast<const T*>(a.x) + base;
+    const int S = b.r < b.R ? (int)a.S : 0;
+    Raw<T, V> q[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int row = b.r + i * b.R;
+        if (row < S) q[i] = Raw<T, V>::load(p + (int64_t)row * a.C);
+        else q[i] = Raw<T, V>::zero();
+    }
+    float first[V], sum[V], sq[V];
+    q[0].unpack(first);
+    int cnt = b.r < S;
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = sq[e] = 0.0f;
+#pragma unroll
+    for (int i = 1; i < NV; ++i) {
+        if (b.r + i * b.R < S) {
+            float x[V];
+            q[i].unpack(x);
+            ++cnt;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float d = x[e] - first[e];
+                sum[e] += d;
+                sq[e] = fmaf(d, d, sq[e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) q[i].forget();
+    join_threads(a, b, n, (float)a.S, cnt, first, sum, sq, red, um, uq);
+    for (int u = threadIdx.x; u < b.nunits; u += blockDim.x) {
+        const float var = uq[u] / ((float)a.S * a.cpg);
+        um[u] = um[u] + origin_of(a, n, b.g0 + u);
+        uq[u] = rstd_of(var, a.eps);
+        if (a.mean) a.mean[(int64_t)n * a.G + b.g0 + u] = um[u];
+        if (a.rstd) a.rstd[(int64_t)n * a.G + b.g0 + u] = uq[u];
+    }
+    if constexpr (STORE) {
+        __syncthreads();
+        float mu[V], sc[V], bi[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const int c = b.v * V + e, j = c / a.cpg;
+            mu[e] = um[j];
+            sc[e] = uq[j] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
+            bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int row = b.r + i * b.R;
+            if (row < S) {
+                float z[V];
+                q[i].unpack(z);
+#pragma unroll
+                for (int e = 0; e < V; ++e) z[e] = fmaf(z[e] - mu[e], sc[e], bi[e]);
+                activate(z, a.act);
+                store_vec(a.out, base + (int64_t)row * a.C, z, a.out_dtype);
+            }
+        }
+    }
+}
+
+// The same for the gradients (grad_out of x's type): dz stays in registers in binary32, so the
+// derivative of the activation is formed once.
+template <typename T, int V, int NV>
+__global__ __launch_bounds__(kGnWholeBwdThreads) void gn_bwd_whole_kernel(GnArgs a) {
+    __shared__ float ra[kGnWholeBwdThreads * V], rb[kGnWholeBwdThreads * V];
+    __shared__ float ua[kGnWholeBwdThreads], ub[kGnWholeBwdThreads];
+    const int id = xcd_run(blockIdx.x, a.N * a.slabs);
+    const int n = id / a.slabs, s = id - n * a.slabs;
+    const Slab b = slab_of<V>(a, s, blockDim.x);
+    const int64_t base = (int64_t)n * a.S * a.C + b.ch0 + b.v * V;
+    const T* p = static_cast<const T*>(a.x) + base;
+    const T* gp = static_cast<const T*>(a.grad_out) + base;
+    const int S = b.r < b.R ? (int)a.S : 0;
+    Raw<T, V> q[NV], dq[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int row = b.r + i * b.R;
+        if (row < S) {
+            q[i] = Raw<T, V>::load(p + (int64_t)row * a.C);
+            dq[i] = Raw<T, V>::load(gp + (int64_t)row * a.C);
+        } else {
+            q[i] = dq[i] = Raw<T, V>::zero();
+        }
+    }
+    const float* mean = a.mean + (int64_t)n * a.G + b.g0;
+    const float* rstd = a.rstd + (int64_t)n * a.G + b.g0;
+    float dz[NV][V], A[V], B[V];
+    {
+        float mu[V], sc[V], bi[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const int c = b.v * V + e, j = c / a.cpg;
+            mu[e] = mean[j];
+            sc[e] = rstd[j] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
+            bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
+            A[e] = B[e] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float x[V], z[V];
+            q[i].unpack(x);
+            dq[i].unpack(dz[i]);   // zeros past the last row
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                x[e] -= mu[e];
+                z[e] = fmaf(x[e], sc[e], bi[e]);
+            }
+            activate_grad(dz[i], z, a.act);
+            if (b.r + i * b.R < S) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    A[e] += dz[i][e];
+                    B[e] = fmaf(dz[i][e], x[e], B[e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) B[e] *= rstd[(b.v * V + e) / a.cpg];
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) q[i].forget();
+    fold_rows(b, A, B, ra, rb);
+    float2* cp = a.chan_part + (int64_t)n * a.C + b.ch0;
+    for (int c = threadIdx.x; c < b.width; c += blockDim.x) {
+        cp[c] = make_float2(ra[c], rb[c]);
+        const float w = a.weight ? a.weight[b.ch0 + c] : 1.0f;
+        ra[c] *= w;
+        rb[c] *= w;
+    }
+    if (!a.grad_x) return;
+    __syncthreads();
+    const float inv = 1.0f / ((float)a.S * a.cpg);
+    unit_sums(ra, 1, b.width, a.cpg, b.nunits, inv, ua);
+    unit_sums(rb, 1, b.width, a.cpg, b.nunits, inv, ub);
+    // rstd * (w dz - m1 - xhat m2) as two multiply-adds
+    float mu[V], k1[V], k2[V], k3[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const int c = b.v * V + e, j = c / a.cpg;
+        mu[e] = mean[j];
+        const float rs = rstd[j];
+        k1[e] = rs * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
+        k2[e] = -rs * rs * ub[j];
+        k3[e] = -rs * ua[j];
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int row = b.r + i * b.R;
+        if (row < S) {
+            float x[V];
+            q[i].unpack(x);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                x[e] = fmaf(dz[i][e], k1[e], fmaf(x[e] - mu[e], k2[e], k3[e]));
+            store_as(static_cast<T*>(a.grad_x) + base + (int64_t)row * a.C, x);
+        }
+    }
+}
+
+// ---- launches ----------------------------------------------------------------------------
+
+template <typename T, int V, bool STORE>
+hipError_t forward_whole(const GnArgs& a, hipStream_t stream) {
+    const uint32_t blocks = (uint32_t)(a.N * a.slabs);
+    if (a.vecs <= 4) gn_whole_kernel<T, V, 4, STORE><<<blocks, a.threads, 0, stream>>>(a);
+    else if (a.vecs <= 8) gn_whole_kernel<T, V, 8, STORE><<<blocks, a.threads, 0, stream>>>(a);
+    else gn_whole_kernel<T, V, 16, STORE><<<blocks, a.threads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+uint32_t join_blocks(const GnArgs& a) {
+    return (uint32_t)(a.N * ((a.G + kGnJoin - 1) / kGnJoin));
+}
+
 template <typename T, int V>
-hipError_t forward(const GnArgs& a, hipStream_t stream) {
+hipError_t forward_stats(const GnArgs& a, hipStream_t stream) {
+    if (a.threads) return forward_whole<T, V, false>(a, stream);
     const uint32_t blocks = (uint32_t)((int64_t)a.N * a.chunks * a.slabs);
     gn_stats_kernel<T, V><<<blocks, kGnThreads, 0, stream>>>(a);
+    gn_join_kernel<<<join_blocks(a), kGnThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t forward(const GnArgs& a, hipStream_t stream) {
+    if (a.threads) return forward_whole<T, V, true>(a, stream);
+    const hipError_t e = forward_stats<T, V>(a, stream);
+    if (e != hipSuccess) return e;
+    const uint32_t blocks = (uint32_t)((int64_t)a.N * a.chunks * a.slabs);
     gn_apply_kernel<T, V><<<blocks, kGnThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
@@ -417,9 +692,22 @@ hipError_t forward(const GnArgs& a, hipStream_t stream) {
 template <typename T, int V>
 hipError_t backward(const GnArgs& a, hipStream_t stream) {
     const int64_t blocks = (int64_t)a.N * a.chunks * a.slabs;
-    if (blocks) gn_bwd_stats_kernel<T, V><<<(uint32_t)blocks, kGnThreads, 0, stream>>>(a);
-    const int64_t dx = a.grad_x ? blocks : 0;
     const int64_t ch = a.grad_weight || a.grad_bias ? (a.C + kGnChanBlock - 1) / kGnChanBlock : 0;
+    int64_t dx = 0;
+    if (blocks && a.threads) {
+        if (a.vecs <= 2)
+            gn_bwd_whole_kernel<T, V, 2><<<(uint32_t)blocks, a.threads, 0, stream>>>(a);
+        else if (a.vecs <= 4)
+            gn_bwd_whole_kernel<T, V, 4><<<(uint32_t)blocks, a.threads, 0, stream>>>(a);
+        else
+            gn_bwd_whole_kernel<T, V, 8><<<(uint32_t)blocks, a.threads, 0, stream>>>(a);
+    } else if (blocks) {
+        gn_bwd_stats_kernel<T, V><<<(uint32_t)blocks, kGnThreads, 0, stream>>>(a);
+        if (a.grad_x) {
+            gn_bwd_join_kernel<<<join_blocks(a), kGnThreads, 0, stream>>>(a);
+            dx = blocks;
+        }
+    }
     if (dx + ch)
         gn_bwd_apply_kernel<T, V><<<(uint32_t)(dx + ch), kGnThreads, 0, stream>>>(a, dx);
     return hipGetLastError();
@@ -439,13 +727,9 @@ hipError_t by_type(int dtype, bool vec, F&& f) {
 
 }  // namespace
 
-hipError_t launch_gn_stats(const GnArgs& a, bool vec, bool joined, hipStream_t stream) {
+hipError_t launch_gn_stats(const GnArgs& a, bool vec, hipStream_t stream) {
     return by_type(a.x_dtype, vec, [&](auto t, auto v) {
-        const uint32_t blocks = (uint32_t)((int64_t)a.N * a.chunks * a.slabs);
-        gn_stats_kernel<decltype(t), decltype(v)::value><<<blocks, kGnThreads, 0, stream>>>(a);
-        if (joined)
-            gn_join_kernel<<<a.N * ((a.G + kGnJoin - 1) / kGnJoin), kGnThreads, 0, stream>>>(a);
-        return hipGetLastError();
+        return forward_stats<decltype(t), decltype(v)::value>(a, stream);
     });
 }
 

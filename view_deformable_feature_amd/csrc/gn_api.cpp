@@ -54,8 +54,50 @@ da_status check_problem(const gn_problem* p) {
 // Workspace parts in bytes, 256-byte aligned.
 uint64_t part_bytes(uint64_t n) { return (n + 255) & ~uint64_t(255); }
 
+// The layout of an image's slab in one workgroup of up to `threads` threads, `most` vectors
+// to a thread; false where none fits.  Of the widths that fit, the widest that leaves a
+// workgroup for every compute unit, else the narrowest of at least 64 bytes of a row.
+bool lay_out_whole(const gn_problem* p, int vec, int threads, int most, da::GnArgs& a) {
+    const int64_t C = p->channels, elem = elem_bytes(p->x_dtype);
+    const int64_t base = std::lcm(C / p->groups, (int64_t)vec);
+    const bool small = p->batch * p->rows * C * elem <= (4 << 20);
+    const auto vectors = [&](int64_t width, int t) {
+        const int64_t R = t / (width / vec);
+        return R ? (p->rows + R - 1) / R : INT64_MAX;
+    };
+    int64_t width = 0;
+    for (int64_t w = base; w <= C && (w == base || w * elem <= 256); w *= 2) {
+        if (vectors(w, threads) > most) break;
+        if (w < C && w * elem < 64 && !small) continue;
+        if (width && p->batch * ((C + w - 1) / w) < 256) break;
+        width = w;
+    }
+    if (!width) return false;
+    a.threads = 256;
+    while (a.threads < threads && vectors(width, a.threads) > most / 4) a.threads *= 2;
+    a.vecs = (int32_t)vectors(width, a.threads);
+    a.slab_ch = (int32_t)width;
+    a.upg = 1;
+    a.cpu = a.cpg;
+    a.slabs = (int32_t)((C + width - 1) / width);
+    a.units = a.G;
+    a.rows_per_chunk = a.S;
+    a.chunks = 1;
+    return true;
+}
+
+// What a pass can keep of a whole image's slab (threads 0: it goes by chunks).
+struct Keeps {
+    int threads, vecs;
+};
+constexpr Keeps kForward = {da::kGnWholeThreads, da::kGnWholeVecs};
+Keeps backward_keeps(const gn_problem* p) {
+    return p->x_dtype == p->out_dtype ? Keeps{da::kGnWholeBwdThreads, da::kGnWholeBwdVecs}
+                                      : Keeps{0, 0};
+}
+
 // The layout for vectors of `vec` channels (1, or 16 bytes' worth).
-void lay_out(const gn_problem* p, int vec, da::GnArgs& a) {
+void lay_out(const gn_problem* p, int vec, Keeps keeps, da::GnArgs& a) {
     memset(&a, 0, sizeof a);
     const int64_t C = p->channels, cpg = C / p->groups, most = (int64_t)da::kGnThreads * vec;
     a.S = p->rows;
@@ -67,6 +109,7 @@ void lay_out(const gn_problem* p, int vec, da::GnArgs& a) {
     a.x_dtype = p->x_dtype;
     a.out_dtype = p->out_dtype;
     a.eps = p->eps;
+    if (keeps.threads && lay_out_whole(p, vec, keeps.threads, keeps.vecs, a)) return;
     const int64_t base = std::lcm(cpg, (int64_t)vec);
     if (base <= most) {
         // whole groups and whole vectors; 256 bytes of a row where that many fit
@@ -109,14 +152,30 @@ uint64_t chan_part_bytes(const da::GnArgs& a) {
     return part_bytes((uint64_t)a.N * a.chunks * a.C * sizeof(float2));
 }
 
-// Both layouts' needs, since the size is asked for before the pointers are known.
-uint64_t need_bytes(const gn_problem* p, bool backward) {
+uint64_t group_bytes(const gn_problem* p) { return part_bytes((uint64_t)p->batch * p->groups * 4); }
+
+// Workspace: forward, the chunks' statistics and (where the caller keeps none) mean and rstd;
+// backward, the chunks' sums and the groups' averages.  The larger of both layouts' needs,
+// since the size is asked for before the pointers are known.
+uint64_t need_forward(const gn_problem* p, bool stats_kept) {
     uint64_t need = 0;
     for (int vec : {1, 16 / elem_bytes(p->x_dtype)}) {
         if (vec > 1 && !vectors_fit(p)) continue;
         da::GnArgs a;
-        lay_out(p, vec, a);
-        need = std::max(need, unit_part_bytes(a) + (backward ? chan_part_bytes(a) : 0));
+        lay_out(p, vec, kForward, a);
+        const uint64_t stats = stats_kept || !a.threads ? 2 * group_bytes(p) : 0;
+        need = std::max(need, stats + (a.threads ? 0 : unit_part_bytes(a)));
+    }
+    return need;
+}
+uint64_t need_backward(const gn_problem* p) {
+    uint64_t need = 0;
+    for (int vec : {1, 16 / elem_bytes(p->x_dtype)}) {
+        if (vec > 1 && !vectors_fit(p)) continue;
+        da::GnArgs a;
+        lay_out(p, vec, backward_keeps(p), a);
+        need = std::max(need, chan_part_bytes(a) +
+                                  (a.threads ? 0 : unit_part_bytes(a) + 2 * group_bytes(p)));
     }
     return need;
 }
@@ -148,26 +207,24 @@ da_status gn_stats_bytes(const gn_problem* p, uint64_t& bytes) {
     for (int vec : {1, 16 / elem_bytes(p->x_dtype)}) {
         if (vec > 1 && !vectors_fit(p)) continue;
         GnArgs a;
-        lay_out(p, vec, a);
+        lay_out(p, vec, kForward, a);
         const da_status grid = check_grid(a);
         if (grid != DA_OK) return grid;
     }
-    bytes = need_bytes(p, false) + 2 * part_bytes((uint64_t)p->batch * p->groups * 4);
+    bytes = need_forward(p, true);
     return DA_OK;
 }
 
-hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace, bool joined,
-                            GnArgs& a, hipStream_t stream) {
+hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace, GnArgs& a,
+                            hipStream_t stream) {
     const bool vec = vectors_fit(p) && aligned(x, 16);
-    lay_out(p, vec ? 16 / elem_bytes(p->x_dtype) : 1, a);
+    lay_out(p, vec ? 16 / elem_bytes(p->x_dtype) : 1, kForward, a);
     unsigned char* base = static_cast<unsigned char*>(workspace);
     a.x = x;
     a.mean = reinterpret_cast<float*>(base);
-    base += part_bytes((uint64_t)p->batch * p->groups * 4);
-    a.rstd = reinterpret_cast<float*>(base);
-    base += part_bytes((uint64_t)p->batch * p->groups * 4);
-    a.unit_part = reinterpret_cast<float2*>(base);
-    return launch_gn_stats(a, vec, joined, stream);
+    a.rstd = reinterpret_cast<float*>(base + group_bytes(p));
+    a.unit_part = reinterpret_cast<float2*>(base + 2 * group_bytes(p));
+    return launch_gn_stats(a, vec, stream);
 }
 
 }  // namespace da
@@ -178,7 +235,7 @@ da_status gn_forward_workspace_size(const gn_problem* p, size_t* bytes) {
     if (!bytes) return report_error(DA_ERR_INVALID_ARG, "bytes is NULL");
     const da_status st = check_problem(p);
     if (st != DA_OK) return st;
-    *bytes = (size_t)need_bytes(p, false);
+    *bytes = (size_t)need_forward(p, false);
     return DA_OK;
 }
 
@@ -199,10 +256,10 @@ da_status gn_forward(const gn_problem* p, const void* x, const float* weight, co
     const int wide = 16 / xb;
     const bool vec = vectors_fit(p) && aligned(x, 16) && aligned(out, std::min(16, wide * ob));
     da::GnArgs a;
-    lay_out(p, vec ? wide : 1, a);
+    lay_out(p, vec ? wide : 1, kForward, a);
     st = check_grid(a);
     if (st != DA_OK) return st;
-    st = check_workspace(need_bytes(p, false), workspace, workspace_bytes);
+    st = check_workspace(need_forward(p, false), workspace, workspace_bytes);
     if (st != DA_OK) return st;
     a.x = x;
     a.weight = weight;
@@ -210,7 +267,12 @@ da_status gn_forward(const gn_problem* p, const void* x, const float* weight, co
     a.out = out;
     a.mean = mean;
     a.rstd = rstd;
-    a.unit_part = static_cast<float2*>(workspace);
+    if (!a.threads) {
+        unsigned char* base = static_cast<unsigned char*>(workspace);
+        if (!mean) a.mean = reinterpret_cast<float*>(base);
+        if (!rstd) a.rstd = reinterpret_cast<float*>(base + group_bytes(p));
+        a.unit_part = reinterpret_cast<float2*>(base + 2 * group_bytes(p));
+    }
     return da::report_hip(da::launch_gn_forward(a, vec, static_cast<hipStream_t>(stream)),
                           "group norm forward launch");
 }
@@ -219,7 +281,7 @@ da_status gn_backward_workspace_size(const gn_problem* p, size_t* bytes) {
     if (!bytes) return report_error(DA_ERR_INVALID_ARG, "bytes is NULL");
     const da_status st = check_problem(p);
     if (st != DA_OK) return st;
-    *bytes = (size_t)need_bytes(p, true);
+    *bytes = (size_t)need_backward(p);
     return DA_OK;
 }
 
@@ -245,10 +307,10 @@ da_status gn_backward(const gn_problem* p, const void* x, const void* grad_out, 
     const bool vec = vectors_fit(p) && aligned(x, 16) && aligned(grad_x, 16) &&
                      aligned(grad_out, std::min(16, wide * ob));
     da::GnArgs a;
-    lay_out(p, vec ? wide : 1, a);
+    lay_out(p, vec ? wide : 1, backward_keeps(p), a);
     st = check_grid(a);
     if (st != DA_OK) return st;
-    st = check_workspace(need_bytes(p, true), workspace, workspace_bytes);
+    st = check_workspace(need_backward(p), workspace, workspace_bytes);
     if (st != DA_OK) return st;
     a.x = x;
     a.grad_out = grad_out;
@@ -259,9 +321,12 @@ da_status gn_backward(const gn_problem* p, const void* x, const void* grad_out, 
     a.grad_x = grad_x;
     a.grad_weight = grad_weight;
     a.grad_bias = grad_bias;
-    a.unit_part = static_cast<float2*>(workspace);
-    a.chan_part = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) +
-                                            unit_part_bytes(a));
+    unsigned char* base = static_cast<unsigned char*>(workspace);
+    a.chan_part = reinterpret_cast<float2*>(base);
+    if (!a.threads) {
+        a.group_sums = reinterpret_cast<float2*>(base + chan_part_bytes(a));
+        a.unit_part = reinterpret_cast<float2*>(base + chan_part_bytes(a) + 2 * group_bytes(p));
+    }
     return da::report_hip(da::launch_gn_backward(a, vec, static_cast<hipStream_t>(stream)),
                           "group norm backward launch");
 }

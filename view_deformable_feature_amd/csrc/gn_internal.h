@@ -18,6 +18,11 @@
 namespace da {
 
 constexpr int kGnThreads = 256;
+// A slab of a whole image in one workgroup: at most so many threads, and vectors to a thread.
+// The forward keeps 64 registers of x of the 128 that 1024 threads may have, the backward 32
+// of x and 64 of dz (with 1024 threads it spilled 45 of them at half as many vectors).
+constexpr int kGnWholeThreads = 1024, kGnWholeVecs = 16;
+constexpr int kGnWholeBwdThreads = 512, kGnWholeBwdVecs = 8;
 
 struct GnArgs {
     const void* x;            // [N, S, C] of x_dtype
@@ -33,24 +38,27 @@ struct GnArgs {
     float2* unit_part;        // [N, chunks, units]: (mean, sum of squared deviations), or the
                               // backward's sums of weight * dz and weight * dz * xhat
     float2* chan_part;        // backward: [N, chunks, C] sums of dz and dz * xhat
+    float2* group_sums;       // backward: [N, G] averages of weight * dz and weight * dz * xhat
     int64_t S;
     int64_t rows_per_chunk;
     int32_t N, C, G, cpg;
     int32_t slab_ch, slabs;
     int32_t upg, cpu, units;
     int32_t chunks;           // row chunks of an image (statistics and apply alike)
+    int32_t threads, vecs;    // an image's slab in one workgroup (chunks 1): threads, vectors
+                              // per thread; 0: by chunks
     int32_t act, x_dtype, out_dtype;
     float eps;
 };
 
 // Statistics alone, for a kernel that normalises as it reads: workspace bytes (and the
-// problem's checks); then a filled in and the chunks' statistics enqueued, and where
-// `joined`, mean and rstd [N, G] in that workspace (256-byte aligned) as well.
+// problem's checks); then a filled in and mean and rstd [N, G] enqueued into that workspace
+// (256-byte aligned).
 da_status gn_stats_bytes(const gn_problem* p, uint64_t& bytes);
-hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace, bool joined,
-                            GnArgs& a, hipStream_t stream);
+hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace, GnArgs& a,
+                            hipStream_t stream);
 
-hipError_t launch_gn_stats(const GnArgs& a, bool vec, bool joined, hipStream_t stream);
+hipError_t launch_gn_stats(const GnArgs& a, bool vec, hipStream_t stream);
 hipError_t launch_gn_forward(const GnArgs& a, bool vec, hipStream_t stream);
 hipError_t launch_gn_backward(const GnArgs& a, bool vec, hipStream_t stream);
 

@@ -15,7 +15,6 @@
 #include <algorithm>
 
 #include "act_device.h"
-#include "gn_device.h"
 #include "i8_internal.h"
 
 namespace da {
@@ -122,16 +121,15 @@ struct NormCoef {
         for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e] - mu[e], sc[e], bi[e]);
         activate(v, act);
     }
-    // of channels c .. c + 7: mean_of and rstd_of give a group's
-    template <typename F, typename G>
-    __device__ __forceinline__ void load(const I8Args& a, int cpg, int c, F&& mean_of, G&& rstd_of) {
+    // of channels c .. c + 7 of image n
+    __device__ __forceinline__ void load(const I8Args& a, const GnArgs& g, int64_t n, int c) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             mu[e] = sc[e] = bi[e] = 0.0f;   // a column past K holds 0
             if (c + e < a.K) {
-                const int j = (c + e) / cpg;
-                mu[e] = mean_of(j);
-                sc[e] = rstd_of(j) * (a.norm_weight ? a.norm_weight[c + e] : 1.0f);
+                const int64_t j = n * g.G + (c + e) / g.cpg;
+                mu[e] = g.mean[j];
+                sc[e] = g.rstd[j] * (a.norm_weight ? a.norm_weight[c + e] : 1.0f);
                 if (a.norm_bias) bi[e] = a.norm_bias[c + e];
             }
         }
@@ -201,14 +199,13 @@ __global__ __launch_bounds__(kQuantThreads) void i8_norm_quantize_kernel(I8Args 
     const int lane = threadIdx.x & (kWave - 1);
     if (m >= a.M) return;
     const bool bf16 = a.x_dtype == DA_BF16;
-    const float* mean = g.mean + m / g.S * g.G;
-    const float* rstd = g.rstd + m / g.S * g.G;
+    const int64_t image = m / g.S;
     const auto value = [&](int c, float (&v)[8]) {
         Eight<XB> q;
         q.load(a.x, m, c, a.K);
         q.unpack(v, bf16);
         NormCoef f;
-        f.load(a, g.cpg, c, [&](int j) { return mean[j]; }, [&](int j) { return rstd[j]; });
+        f.load(a, g, image, c);
         f.apply(v, g.act);
     };
     float v[8];
@@ -329,15 +326,14 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_kernel(I8Args a, GnArgs 
     constexpr int kBM = 16 * MT, kKp = 64 * KT, kStride = kKp + 16;   // odd 16-byte units
     __shared__ __align__(16) unsigned char codes[kBM * kStride];
     __shared__ float scales[kBM];
-    __shared__ float gm[NORM ? kKp : 1], gr[NORM ? kKp : 1];   // at most K groups
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int nb = blockIdx.x % a.n_blocks;
     int64_t m0 = blockIdx.x / a.n_blocks, mend = a.M;
+    int64_t image = 0;
     if constexpr (NORM) {   // a block stays in one image
-        const int n = (int)(m0 / a.m_blocks);
-        m0 = n * g.S + (m0 - (int64_t)n * a.m_blocks) * kBM;
-        mend = (n + 1) * g.S;
-        join_stats(g, n, 0, g.G, gm, gr);
+        image = m0 / a.m_blocks;
+        m0 = image * g.S + (m0 - image * a.m_blocks) * kBM;
+        mend = (image + 1) * g.S;
     } else {
         m0 *= kBM;
     }
@@ -362,8 +358,7 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_kernel(I8Args a, GnArgs 
         if constexpr (NORM) {
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                f[j].load(a, g.cpg, c0 + j * L * 8, [&](int k) { return gm[k]; },
-                          [&](int k) { return gr[k]; });
+                f[j].load(a, g, image, c0 + j * L * 8);
         }
 #pragma unroll 1
         for (int b = 0; b < kIters; b += kBatch) {

@@ -227,7 +227,7 @@ da_status i8_norm_linear(const gn_problem* p, int64_t out_channels, const void* 
         base += part_bytes(a.M * 4);
     }
     da::GnArgs g;
-    hipError_t e = da::enqueue_gn_stats(p, x, base, through_memory(path), g, s);
+    hipError_t e = da::enqueue_gn_stats(p, x, base, g, s);
     if (e == hipSuccess && through_memory(path)) e = da::launch_i8_quantize(a, &g, s);
     if (e == hipSuccess)
         e = da::launch_i8_product(a, path, false, through_memory(path) ? nullptr : &g, s);

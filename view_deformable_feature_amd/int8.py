@@ -14,69 +14,89 @@ kernels of libdeformagg.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
 import torch
 
-from . import _lib
-from .api import _DTYPES, _FLOATS, _need, _ptr, _stream
-from .norm import _activation, _gn_problem, _params, _size, _workspace, _ws_args
+from . import _lib, norm
+from ._call import call, maybe, need, scratch, size
+from .api import _DTYPES, _FLOATS
+from .norm import _activation
 
 __all__ = ["i8_quantize_rows", "i8_matmul", "i8_linear", "i8_norm_linear",
            "i8_matmul_workspace_size", "i8_linear_workspace_size",
            "i8_norm_linear_workspace_size"]
 
 
-def _layer(w, w_scale, bias, dev, K) -> int:
+def _layer(w, w_scale, bias, dev, K):
+    """(out channels, addresses of codes, scales and bias) of a layer."""
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a [out_channels, in_channels] tensor of codes")
-    N = w.shape[0]
-    _need(w, "w", torch.int8, dev, (N, K))
-    _need(w_scale, "w_scale", torch.float32, dev, (N,))
-    if bias is not None:
-        _need(bias, "bias", torch.float32, dev, (N,))
-    return N
+    N = w.shape[:1]
+    pw = need(w, "w", torch.int8, dev, N + (K,))
+    return (N[0], pw, need(w_scale, "w_scale", torch.float32, dev, N),
+            maybe(bias, "bias", torch.float32, dev, N))
 
 
-def _rows(x: torch.Tensor, name: str) -> Tuple[int, int]:
+def _rows(x, name: str, dtypes):
+    """(M, K, type) of rows x [..., K]."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError(f"{name} must be a [..., K] tensor")
-    return math.prod(x.shape[:-1]), x.shape[-1]
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {x.dtype}, expected one of {tuple(dtypes)}")
+    shape = x.shape
+    return math.prod(shape[:-1]), shape[-1]
 
 
-def _out(out, out_dtype, shape, dev):
-    if out is None:
-        return torch.empty(shape, device=dev, dtype=out_dtype)
-    _need(out, "out", _FLOATS, dev, shape)
-    return out
-
-
-def _problem(M, K, N, activation, x_dtype, out_dtype) -> _lib.I8Problem:
+@functools.lru_cache(maxsize=256)
+def _plan(func, M, K, N, activation, x_dtype, out_dtype):
+    """(problem, workspace bytes) of a problem's sizes and types; the library only reads the
+    problem."""
     if out_dtype not in _DTYPES:
         raise TypeError(f"output dtype must be among {_FLOATS}")
-    return _lib.I8Problem(M, K, N, _activation(activation), x_dtype, _DTYPES[out_dtype], 0)
+    prob = ctypes.byref(_lib.I8Problem(M, K, N, _activation(activation), x_dtype,
+                                       _DTYPES[out_dtype], 0))
+    return prob, size(func + "_workspace_size", prob)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_plan(shape, dtype, groups, eps, activation, N, out_dtype):
+    if out_dtype not in _DTYPES:
+        raise TypeError(f"output dtype must be among {_FLOATS}")
+    prob = ctypes.byref(norm._problem(shape, dtype, groups, eps, activation, out_dtype))
+    return prob, size("i8_norm_linear_workspace_size", prob, N)
 
 
 def i8_quantize_rows(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """(codes [..., K] int8, scale [...] float32) of x [..., K], row by row."""
-    lib = _lib.load()
-    M, K = _rows(x, "x")
-    dev = x.device
-    _need(x, "x", _FLOATS, dev)
-    codes = torch.empty(x.shape, device=dev, dtype=torch.int8)
-    scale = torch.empty(x.shape[:-1], device=dev, dtype=torch.float32)
-    with torch.cuda.device(dev):
-        st = lib.i8_quantize_rows(M, K, _DTYPES[x.dtype], _ptr(x), _ptr(codes), _ptr(scale),
-                                  _stream(dev))
-    _lib.check(st, "i8_quantize_rows")
+    M, K = _rows(x, "x", _FLOATS)
+    dev, shape = x.device, x.shape
+    px = need(x, "x", x.dtype, dev, shape)
+    codes = torch.empty(shape, device=dev, dtype=torch.int8)
+    scale = torch.empty(shape[:-1], device=dev, dtype=torch.float32)
+    call("i8_quantize_rows", dev, M, K, _DTYPES[x.dtype], px, codes.data_ptr(), scale.data_ptr())
     return codes, scale
+
+
+def _product(func, dev, lead, plan, rows, layer, out, odt, workspace):
+    """out of a planned product; ``rows``: the addresses that stand for the rows."""
+    prob, bytes_needed = plan
+    N, pw, ps, pb = layer
+    shape = lead + (N,)
+    if out is None:
+        out = torch.empty(shape, device=dev, dtype=odt)
+    po = need(out, "out", odt, dev, shape)
+    workspace = scratch(workspace, bytes_needed, dev)
+    pws, nws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    call(func, dev, prob, *rows, pw, ps, pb, po, pws, nws)
+    return out
 
 
 def i8_matmul_workspace_size(rows: int, in_channels: int, out_channels: int) -> int:
     """Bytes of ``workspace`` that ``i8_matmul`` uses."""
-    prob = _problem(rows, in_channels, out_channels, "none", 0, torch.float32)
-    return _size("i8_matmul_workspace_size", ctypes.byref(prob))
+    return _plan("i8_matmul", rows, in_channels, out_channels, "none", 0, torch.float32)[1]
 
 
 def i8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -85,22 +105,14 @@ def i8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """act((a @ w.T) * a_scale * w_scale + bias) [..., N] of codes a [..., K] with a scale per
     row, float32 unless ``out`` / ``out_dtype`` says otherwise."""
-    lib = _lib.load()
-    M, K = _rows(a, "a")
-    dev = a.device
-    _need(a, "a", torch.int8, dev)
-    _need(a_scale, "a_scale", torch.float32, dev, a.shape[:-1])
-    N = _layer(w, w_scale, bias, dev, K)
+    M, K = _rows(a, "a", (torch.int8,))
+    dev, lead = a.device, a.shape[:-1]
+    rows = (need(a, "a", torch.int8, dev, a.shape),
+            need(a_scale, "a_scale", torch.float32, dev, lead))
+    layer = _layer(w, w_scale, bias, dev, K)
     odt = out.dtype if out is not None else (out_dtype or torch.float32)
-    prob = _problem(M, K, N, activation, 0, odt)
-    out = _out(out, odt, a.shape[:-1] + (N,), dev)
-    need = _size("i8_matmul_workspace_size", ctypes.byref(prob))
-    workspace = _workspace(workspace, need, dev)
-    with torch.cuda.device(dev):
-        st = lib.i8_matmul(ctypes.byref(prob), _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale),
-                           _ptr(bias), _ptr(out), *_ws_args(workspace), _stream(dev))
-    _lib.check(st, "i8_matmul")
-    return out
+    plan = _plan("i8_matmul", M, K, layer[0], activation, 0, odt)
+    return _product("i8_matmul", dev, lead, plan, rows, layer, out, odt, workspace)
 
 
 def i8_linear_workspace_size(rows: int, in_channels: int, out_channels: int,
@@ -108,8 +120,8 @@ def i8_linear_workspace_size(rows: int, in_channels: int, out_channels: int,
     """Bytes of ``workspace`` that ``i8_linear`` uses for rows of ``dtype``."""
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be among {_FLOATS}")
-    prob = _problem(rows, in_channels, out_channels, "none", _DTYPES[dtype], torch.float32)
-    return _size("i8_linear_workspace_size", ctypes.byref(prob))
+    return _plan("i8_linear", rows, in_channels, out_channels, "none", _DTYPES[dtype],
+                 torch.float32)[1]
 
 
 def i8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -118,27 +130,20 @@ def i8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """act(x @ (w * w_scale).T + bias) [..., N] with each row of x [..., K] quantised to 8 bits
     on the way, float32 unless ``out`` / ``out_dtype`` says otherwise."""
-    lib = _lib.load()
-    M, K = _rows(x, "x")
+    M, K = _rows(x, "x", _FLOATS)
     dev = x.device
-    _need(x, "x", _FLOATS, dev)
-    N = _layer(w, w_scale, bias, dev, K)
+    rows = (need(x, "x", x.dtype, dev, x.shape),)
+    layer = _layer(w, w_scale, bias, dev, K)
     odt = out.dtype if out is not None else (out_dtype or torch.float32)
-    prob = _problem(M, K, N, activation, _DTYPES[x.dtype], odt)
-    out = _out(out, odt, x.shape[:-1] + (N,), dev)
-    need = _size("i8_linear_workspace_size", ctypes.byref(prob))
-    workspace = _workspace(workspace, need, dev)
-    with torch.cuda.device(dev):
-        st = lib.i8_linear(ctypes.byref(prob), _ptr(x), _ptr(w), _ptr(w_scale), _ptr(bias),
-                           _ptr(out), *_ws_args(workspace), _stream(dev))
-    _lib.check(st, "i8_linear")
-    return out
+    plan = _plan("i8_linear", M, K, layer[0], activation, _DTYPES[x.dtype], odt)
+    return _product("i8_linear", dev, x.shape[:-1], plan, rows, layer, out, odt, workspace)
 
 
 def i8_norm_linear_workspace_size(x: torch.Tensor, groups: int, out_channels: int) -> int:
     """Bytes of ``workspace`` that ``i8_norm_linear`` uses for x."""
-    prob = _gn_problem(x, groups, 0.0, "none", torch.float32)
-    return _size("i8_norm_linear_workspace_size", ctypes.byref(prob), int(out_channels))
+    _rows(x, "x", _FLOATS)
+    return _norm_plan(x.shape, x.dtype, int(groups), 0.0, "none", int(out_channels),
+                      torch.float32)[1]
 
 
 def i8_norm_linear(x: torch.Tensor, groups: int, norm_weight: Optional[torch.Tensor],
@@ -150,19 +155,15 @@ def i8_norm_linear(x: torch.Tensor, groups: int, norm_weight: Optional[torch.Ten
     """The projection [N, ..., out_channels] of act(group norm of x [N, ..., C]), each
     normalised row quantised to 8 bits on the way; ``activation`` stands between norm and
     projection.  float32 unless ``out`` / ``out_dtype`` says otherwise."""
-    lib = _lib.load()
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x must be a [N, ..., C] tensor")
+    _, C = _rows(x, "x", _FLOATS)
+    dev = x.device
+    rows = (need(x, "x", x.dtype, dev, x.shape),
+            maybe(norm_weight, "norm_weight", torch.float32, dev, (C,)),
+            maybe(norm_bias, "norm_bias", torch.float32, dev, (C,)))
+    layer = _layer(w, w_scale, bias, dev, C)
     odt = out.dtype if out is not None else (out_dtype or torch.float32)
-    prob = _gn_problem(x, groups, eps, activation, odt)
-    dev, C = x.device, x.shape[-1]
-    _need(x, "x", _FLOATS, dev)
-    _params(norm_weight, norm_bias, dev, C)
-    N = _layer(w, w_scale, bias, dev, C)
-    out = _out(out, odt, x.shape[:-1] + (N,), dev)
-    need = _size("i8_norm_linear_workspace_size", ctypes.byref(prob), N)
-    workspace = _workspace(workspace, need, dev)
-    with torch.cuda.device(dev):
-        st = lib.i8_norm_linear(ctypes.byref(prob), N, _ptr(x), _ptr(norm_weight), _ptr(norm_bias),
-                                _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(out),
-                                *_ws_args(workspace), _stream(dev))
-    _lib.check(st, "i8_norm_linear")
-    return out
+    plan = _norm_plan(x.shape, x.dtype, int(groups), float(eps), activation, layer[0], odt)
+    return _product("i8_norm_linear", dev, x.shape[:-1], plan, (layer[0],) + rows, layer, out,
+                    odt, workspace)

@@ -12,13 +12,15 @@ kernels of libdeformagg.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
 import torch
 
 from . import _lib
-from .api import _DTYPES, _FLOATS, _need, _ptr, _stream
+from ._call import call, maybe, need, scratch, size
+from .api import _DTYPES, _FLOATS
 
 __all__ = ["gn_forward", "gn_backward", "gn_workspace_size", "gn_backward_workspace_size",
            "GroupNormActFunction", "group_norm_act"]
@@ -34,53 +36,37 @@ def _activation(name: str) -> int:
     return code
 
 
-def _gn_problem(x: torch.Tensor, groups: int, eps: float, activation: str,
-                out_dtype: torch.dtype) -> _lib.GNProblem:
+def _problem(shape, dtype, groups, eps, activation, out_dtype) -> _lib.GNProblem:
+    return _lib.GNProblem(shape[0], math.prod(shape[1:-1]), shape[-1], groups, eps,
+                          _activation(activation), _DTYPES[dtype], _DTYPES[out_dtype], 0, 0)
+
+
+@functools.lru_cache(maxsize=256)
+def _plan(func, shape, dtype, groups, eps, activation, out_dtype):
+    """(problem, workspace bytes) of a problem's sizes and types; the library only reads the
+    problem."""
+    prob = ctypes.byref(_problem(shape, dtype, groups, eps, activation, out_dtype))
+    return prob, size(func + "_workspace_size", prob)
+
+
+def _planned(func, x, groups, eps, activation, out_dtype):
     if not isinstance(x, torch.Tensor) or x.dim() < 2:
         raise ValueError("x must be a [N, ..., C] tensor")
     if x.dtype not in _DTYPES or out_dtype not in _DTYPES:
         raise TypeError(f"input / output dtypes must be among {_FLOATS}")
-    shape = x.shape
-    return _lib.GNProblem(shape[0], math.prod(shape[1:-1]), shape[-1], int(groups), float(eps),
-                          _activation(activation), _DTYPES[x.dtype], _DTYPES[out_dtype], 0, 0)
-
-
-def _params(weight, bias, dev, C):
-    if weight is not None:
-        _need(weight, "weight", torch.float32, dev, (C,))
-    if bias is not None:
-        _need(bias, "bias", torch.float32, dev, (C,))
-
-
-def _size(func: str, *args) -> int:
-    n = ctypes.c_size_t(0)
-    _lib.check(getattr(_lib.load(), func)(*args, ctypes.byref(n)), func)
-    return n.value
-
-
-def _workspace(workspace: Optional[torch.Tensor], need: int, dev) -> Optional[torch.Tensor]:
-    if workspace is None:
-        return torch.empty(need, device=dev, dtype=torch.uint8) if need else None
-    _need(workspace, "workspace", torch.uint8, dev)
-    if workspace.numel() < need:
-        raise ValueError(f"workspace has {workspace.numel()} bytes, {need} needed")
-    return workspace
-
-
-def _ws_args(workspace: Optional[torch.Tensor]):
-    return (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
+    return _plan(func, x.shape, x.dtype, int(groups), float(eps), activation, out_dtype)
 
 
 def gn_workspace_size(x: torch.Tensor, groups: int) -> int:
     """Bytes of ``workspace`` that ``gn_forward`` uses for x."""
-    prob = _gn_problem(x, groups, 0.0, "none", x.dtype)
-    return _size("gn_forward_workspace_size", ctypes.byref(prob))
+    return _planned("gn_forward", x, groups, 0.0, "none", x.dtype)[1]
 
 
-def gn_backward_workspace_size(x: torch.Tensor, groups: int) -> int:
-    """Bytes of ``workspace`` that ``gn_backward`` uses for x."""
-    prob = _gn_problem(x, groups, 0.0, "none", x.dtype)
-    return _size("gn_backward_workspace_size", ctypes.byref(prob))
+def gn_backward_workspace_size(x: torch.Tensor, groups: int,
+                               grad_dtype: Optional[torch.dtype] = None) -> int:
+    """Bytes of ``workspace`` that ``gn_backward`` uses for x and a grad_out of ``grad_dtype``
+    (x's type unless given)."""
+    return _planned("gn_backward", x, groups, 0.0, "none", grad_dtype or x.dtype)[1]
 
 
 def gn_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
@@ -91,24 +77,21 @@ def gn_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
     """(out [N, ..., C], mean [N, G] float32, rstd [N, G] float32): act of the normalised,
     scaled and shifted x.  out has x's type unless ``out`` / ``out_dtype`` says otherwise;
     ``out`` may be x itself."""
-    lib = _lib.load()
     odt = out.dtype if out is not None else (out_dtype or x.dtype)
-    prob = _gn_problem(x, groups, eps, activation, odt)
-    dev = x.device
-    _need(x, "x", _FLOATS, dev)
-    _params(weight, bias, dev, x.shape[-1])
+    prob, bytes_needed = _planned("gn_forward", x, groups, eps, activation, odt)
+    dev, shape = x.device, x.shape
+    C = shape[-1:]
+    px = need(x, "x", x.dtype, dev, shape)
+    pw = maybe(weight, "weight", torch.float32, dev, C)
+    pb = maybe(bias, "bias", torch.float32, dev, C)
     if out is None:
-        out = torch.empty(x.shape, device=dev, dtype=odt)
-    else:
-        _need(out, "out", _FLOATS, dev, x.shape)
-    need = _size("gn_forward_workspace_size", ctypes.byref(prob))
-    mean = torch.empty((x.shape[0], int(groups)), device=dev, dtype=torch.float32)
-    rstd = torch.empty((x.shape[0], int(groups)), device=dev, dtype=torch.float32)
-    workspace = _workspace(workspace, need, dev)
-    with torch.cuda.device(dev):
-        st = lib.gn_forward(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out),
-                            _ptr(mean), _ptr(rstd), *_ws_args(workspace), _stream(dev))
-    _lib.check(st, "gn_forward")
+        out = torch.empty(shape, device=dev, dtype=odt)
+    po = need(out, "out", odt, dev, shape)
+    mean = torch.empty((shape[0], int(groups)), device=dev, dtype=torch.float32)
+    rstd = torch.empty((shape[0], int(groups)), device=dev, dtype=torch.float32)
+    workspace = scratch(workspace, bytes_needed, dev)
+    pws, nws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    call("gn_forward", dev, prob, px, pw, pb, po, mean.data_ptr(), rstd.data_ptr(), pws, nws)
     return out, mean, rstd
 
 
@@ -121,30 +104,26 @@ def gn_backward(x: torch.Tensor, grad_out: torch.Tensor, mean: torch.Tensor, rst
     """(grad_x of x's type, grad_weight [C] float32, grad_bias [C] float32), from what
     ``gn_forward`` was given and returned.  ``grad_x`` may be grad_out itself; ``need_x`` and
     ``need_params`` false leave out that part (None in its place)."""
-    lib = _lib.load()
     if not isinstance(grad_out, torch.Tensor) or grad_out.dtype not in _DTYPES:
         raise TypeError(f"grad_out must be a tensor of one of {_FLOATS}")
-    prob = _gn_problem(x, groups, 0.0, activation, grad_out.dtype)
-    dev, C = x.device, x.shape[-1]
-    _need(x, "x", _FLOATS, dev)
-    _need(grad_out, "grad_out", _FLOATS, dev, x.shape)
-    stats = (x.shape[0], int(groups))
-    _need(mean, "mean", torch.float32, dev, stats)
-    _need(rstd, "rstd", torch.float32, dev, stats)
-    _params(weight, bias, dev, C)
-    if grad_x is not None:
-        _need(grad_x, "grad_x", x.dtype, dev, x.shape)
-    elif need_x:
-        grad_x = torch.empty(x.shape, device=dev, dtype=x.dtype)
-    need = _size("gn_backward_workspace_size", ctypes.byref(prob))
-    gw = torch.empty((C,), device=dev, dtype=torch.float32) if need_params else None
-    gb = torch.empty((C,), device=dev, dtype=torch.float32) if need_params else None
-    workspace = _workspace(workspace, need, dev)
-    with torch.cuda.device(dev):
-        st = lib.gn_backward(ctypes.byref(prob), _ptr(x), _ptr(grad_out), _ptr(mean), _ptr(rstd),
-                             _ptr(weight), _ptr(bias), _ptr(grad_x), _ptr(gw), _ptr(gb),
-                             *_ws_args(workspace), _stream(dev))
-    _lib.check(st, "gn_backward")
+    prob, bytes_needed = _planned("gn_backward", x, groups, 0.0, activation, grad_out.dtype)
+    dev, shape = x.device, x.shape
+    C, stats = shape[-1:], (shape[0], int(groups))
+    px = need(x, "x", x.dtype, dev, shape)
+    pg = need(grad_out, "grad_out", grad_out.dtype, dev, shape)
+    pm = need(mean, "mean", torch.float32, dev, stats)
+    pr = need(rstd, "rstd", torch.float32, dev, stats)
+    pw = maybe(weight, "weight", torch.float32, dev, C)
+    pb = maybe(bias, "bias", torch.float32, dev, C)
+    if grad_x is None and need_x:
+        grad_x = torch.empty(shape, device=dev, dtype=x.dtype)
+    pgx = maybe(grad_x, "grad_x", x.dtype, dev, shape)
+    gw = torch.empty(C, device=dev, dtype=torch.float32) if need_params else None
+    gb = torch.empty(C, device=dev, dtype=torch.float32) if need_params else None
+    pgw, pgb = (gw.data_ptr(), gb.data_ptr()) if need_params else (None, None)
+    workspace = scratch(workspace, bytes_needed, dev)
+    pws, nws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    call("gn_backward", dev, prob, px, pg, pm, pr, pw, pb, pgx, pgw, pgb, pws, nws)
     return grad_x, gw, gb
 
 

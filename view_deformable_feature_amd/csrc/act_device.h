@@ -5,7 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "da_internal.h"
+#include "da_device.h"
 #include "group_norm.h"
 
 namespace da {
@@ -153,12 +153,6 @@ __device__ __forceinline__ void load_vec(const void* base, int64_t i, float (&v)
         load_as(static_cast<const _Float16*>(base) + i, v);
     else
         load_as(static_cast<const float*>(base) + i, v);
-}
-
-__device__ __forceinline__ float load_elem(const void* base, int64_t i, int dtype) {
-    float v[1];
-    load_vec(base, i, v, dtype);
-    return v[0];
 }
 
 }  // namespace da

@@ -22,12 +22,12 @@ struct I8Args {
     int64_t M;
     int32_t K, N;
     int32_t act, x_dtype, out_dtype;
-    int32_t n_blocks;         // rows kernel: workgroups that share a block of rows
-    int32_t tiles_per_block;  // rows kernel: 16-column tiles of one of them
+    int32_t slices;           // rows kernel: slices of the output channels
+    int32_t tiles_per_slice;  // rows kernel: 16-channel tiles of a slice
+    int32_t blocks_per_image; // rows kernel: workgroups that share an image's rows
     // a row passes through group norm and an activation before it is quantised
     const float* norm_weight; // [K] or NULL
     const float* norm_bias;   // [K] or NULL
-    int32_t m_blocks;         // rows kernel: row blocks of an image
 };
 
 // Which kernels a problem takes; the workspace goes by it.

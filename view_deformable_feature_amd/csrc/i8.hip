@@ -168,110 +168,114 @@ struct NormCoef {
     }
 };
 
-// One wave per row; a row's first 2048 numbers stay in registers, what is past them is read
-// again.
-constexpr int kQuantThreads = 256;
-template <int XB>
-__global__ __launch_bounds__(kQuantThreads) void i8_quantize_kernel(I8Args a) {
-    constexpr int kHold = 4;
-    const int64_t m = (int64_t)blockIdx.x * (kQuantThreads / kWave) + threadIdx.x / kWave;
+// L lanes to a row, 64 / L rows to a wave; a row's first HOLD pieces per lane stay in
+// registers, what is past them is read again.  Behind a norm L is 64, and a wave has up to 8
+// consecutive rows of one image, for which it keeps the coefficients of the pieces held.
+constexpr int kQuantThreads = 256, kQuantWaves = kQuantThreads / kWave;
+template <int XB, bool NORM, int L, int HOLD>
+__global__ __launch_bounds__(kQuantThreads) void i8_quantize_kernel(I8Args a, GnArgs g,
+                                                                     int rows_per_wave) {
     const int lane = threadIdx.x & (kWave - 1);
-    if (m >= a.M) return;
+    const int64_t wave = (int64_t)blockIdx.x * kQuantWaves + threadIdx.x / kWave;
     const bool bf16 = a.x_dtype == DA_BF16;
-    Eight<XB> hold[kHold];
-    float v[8];
-    uint32_t big = 0;
+    int64_t m = wave * (kWave / L) + lane / L, end = min(m + 1, a.M), image = 0;
+    NormCoef f[NORM ? HOLD : 1];
+    if constexpr (NORM) {
+        const int64_t per = (g.S + rows_per_wave - 1) / rows_per_wave;   // waves of an image
+        image = wave / per;
+        if (image >= g.N) return;
+        m = image * g.S + (wave - image * per) * rows_per_wave;
+        end = min(m + rows_per_wave, (image + 1) * g.S);
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-        const int c = (i * kWave + lane) * 8;
-        if (c < a.K) hold[i].load(a.x, m, c, a.K);
-        else hold[i].zero();
+        for (int i = 0; i < HOLD; ++i) f[i].load(a, g, image, (i * L + lane) * 8);
     }
+    for (; m < end; ++m) {
+        Eight<XB> hold[HOLD];
+        float v[8];
+        uint32_t big = 0;
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-        hold[i].unpack(v, bf16);
-        big = max(big, magnitude(v));
-    }
-    for (int c = (kHold * kWave + lane) * 8; c < a.K; c += kWave * 8) {
-        Eight<XB> t;
-        t.load(a.x, m, c, a.K);
-        t.unpack(v, bf16);
-        big = max(big, magnitude(v));
-    }
-    for (int s = kWave / 2; s; s >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, s));
-    const RowScale s = row_scale(big);
-    const auto put = [&](const Eight<XB>& t, int c) {
-        t.unpack(v, bf16);
-        const u32x2 q = {pack_codes(v, s), pack_codes(v + 4, s)};
-        int8_t* p = a.a + m * a.K + c;
-        if (c + 8 <= a.K) {
-            __builtin_memcpy(p, &q, 8);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 7; ++e)
-                if (c + e < a.K) p[e] = (int8_t)(q[e / 4] >> (8 * (e & 3)));
+        for (int i = 0; i < HOLD; ++i) {
+            const int c = (i * L + lane % L) * 8;
+            if (c < a.K) hold[i].load(a.x, m, c, a.K);
+            else hold[i].zero();
         }
-    };
+        // numbers from column c on, normalised where a norm stands in front
+        const auto of = [&](const Eight<XB>& q, const NormCoef& coef) {
+            q.unpack(v, bf16);
+            if constexpr (NORM) coef.apply(v, g.act);
+        };
+        const auto again = [&](int c) {
+            Eight<XB> q;
+            q.load(a.x, m, c, a.K);
+            NormCoef coef;
+            if constexpr (NORM) coef.load(a, g, image, c);
+            of(q, coef);
+        };
 #pragma unroll
-    for (int i = 0; i < kHold; ++i)
-        if ((i * kWave + lane) * 8 < a.K) put(hold[i], (i * kWave + lane) * 8);
-    for (int c = (kHold * kWave + lane) * 8; c < a.K; c += kWave * 8) {
-        Eight<XB> t;
-        t.load(a.x, m, c, a.K);
-        put(t, c);
-    }
-    if (lane == 0) a.a_scale[m] = s.scale;
-}
-
-// The same behind a group norm whose means and rstds are in memory: rows past the rows
-// kernel's depth, read twice.
-template <int XB>
-__global__ __launch_bounds__(kQuantThreads) void i8_norm_quantize_kernel(I8Args a, GnArgs g) {
-    const int64_t m = (int64_t)blockIdx.x * (kQuantThreads / kWave) + threadIdx.x / kWave;
-    const int lane = threadIdx.x & (kWave - 1);
-    if (m >= a.M) return;
-    const bool bf16 = a.x_dtype == DA_BF16;
-    const int64_t image = m / g.S;
-    const auto value = [&](int c, float (&v)[8]) {
-        Eight<XB> q;
-        q.load(a.x, m, c, a.K);
-        q.unpack(v, bf16);
-        NormCoef f;
-        f.load(a, g, image, c);
-        f.apply(v, g.act);
-    };
-    float v[8];
-    uint32_t big = 0;
-    for (int c = lane * 8; c < a.K; c += kWave * 8) {
-        value(c, v);
-        big = max(big, magnitude(v));
-    }
-    for (int s = kWave / 2; s; s >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, s));
-    const RowScale s = row_scale(big);
-    for (int c = lane * 8; c < a.K; c += kWave * 8) {
-        value(c, v);
-        const u32x2 q = {pack_codes(v, s), pack_codes(v + 4, s)};
+        for (int i = 0; i < HOLD; ++i) {
+            of(hold[i], f[NORM ? i : 0]);
+            big = max(big, magnitude(v));
+        }
+        for (int c = (HOLD * L + lane % L) * 8; c < a.K; c += L * 8) {
+            again(c);
+            big = max(big, magnitude(v));
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c + e < a.K) a.a[m * a.K + c + e] = (int8_t)(q[e / 4] >> (8 * (e & 3)));
+        for (int s = L / 2; s; s >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, s));
+        const RowScale s = row_scale(big);
+        const auto put = [&](int c) {
+            const u32x2 q = {pack_codes(v, s), pack_codes(v + 4, s)};
+            int8_t* p = a.a + m * a.K + c;
+            if (c + 8 <= a.K) {
+                __builtin_memcpy(p, &q, 8);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (c + e < a.K) p[e] = (int8_t)(q[e / 4] >> (8 * (e & 3)));
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < HOLD; ++i) {
+            const int c = (i * L + lane % L) * 8;
+            if (c < a.K) {
+                of(hold[i], f[NORM ? i : 0]);
+                put(c);
+            }
+        }
+        for (int c = (HOLD * L + lane % L) * 8; c < a.K; c += L * 8) {
+            again(c);
+            put(c);
+        }
+        if (lane % L == 0) a.a_scale[m] = s.scale;
     }
-    if (lane == 0) a.a_scale[m] = s.scale;
 }
 
 // ---- pieces of the operands --------------------------------------------------------------
 
-// 16 codes of row `row` of [.., K] from column k on (k < K), zeros past K.  Any alignment.
+// The 16 codes of row `row` of [.., K] from column k on (k < K), zeros past K.  Any alignment.
+// A row's broken last piece is the end of its last 16 codes, shifted down.
 __device__ __forceinline__ i32x4 bytes_of(const int8_t* base, int64_t row, int k, int K) {
-    const int8_t* p = base + row * K + k;
-    i32x4 q = {0, 0, 0, 0};
-    if (k + 16 <= K) {
-        __builtin_memcpy(&q, p, 16);
+    const int8_t* p = base + row * K;
+    uint64_t lo = 0, hi = 0;
+    if (K >= 16) {
+        const int at = min(k, K - 16), s = (k - at) * 8;   // 0 .. 120 bits
+        __builtin_memcpy(&lo, p + at, 8);
+        __builtin_memcpy(&hi, p + at + 8, 8);
+        if (s >= 64) {
+            lo = hi >> (s - 64);
+            hi = 0;
+        } else if (s) {
+            lo = lo >> s | hi << (64 - s);
+            hi >>= s;
+        }
     } else {
-#pragma unroll
-        for (int i = 0; i < 15; ++i)
-            if (k + i < K) q[i / 4] |= (int)((uint32_t)(uint8_t)p[i] << (8 * (i & 3)));
+        for (int i = 0; k + i < K; ++i) {
+            const uint64_t b = (uint64_t)(uint8_t)p[k + i] << (8 * (i & 7));
+            lo |= i < 8 ? b : 0;
+            hi |= i < 8 ? 0 : b;
+        }
     }
-    return q;
+    return i32x4{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
 }
 
 // A piece of a row as it lies in memory: eight numbers, or sixteen codes.
@@ -479,11 +483,13 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && (NORM || XB == 4) ? 2 : 4)
     };
     if (u < units) fetch(u);
 
+    const auto wr = make_rsrc(a.w + (int64_t)t0 * 16 * a.K, (uint32_t)min(wrows, a.N - t0 * 16) * a.K);
     for (int e = threadIdx.x; e < wrows * KT * 4; e += kRowsThreads) {
         const int r = e / (KT * 4), c = e % (KT * 4) * 16, n = t0 * 16 + r;
-        i32x4 w = {0, 0, 0, 0};
-        if (n < a.N && c < a.K) w = bytes_of(a.w, n, c, a.K);
-        *reinterpret_cast<i32x4*>(ws + r * kStride + c) = w;
+        Sixteen w;
+        w.load(wr, c + 16 <= a.K ? r * a.K + c : kOutside);
+        if (a.K % 16 && n < a.N && c < a.K && c + 16 > a.K) w.load(a.w, n, c, a.K);
+        *reinterpret_cast<i32x4*>(ws + r * kStride + c) = w.q;
     }
     for (int e = threadIdx.x; e < wrows; e += kRowsThreads) {
         const int n = t0 * 16 + e;
@@ -573,211 +579,15 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && (NORM || XB == 4) ? 2 : 4)
     }
 }
 
-// ---- panel kernel ------------------------------------------------------------------------
-//
-// 257 to 1024 columns, where a wave's rows no longer fit its registers twice over: a
-// workgroup brings 16 * MT rows into LDS as codes, and its waves deal the 16-channel tiles
-// of the output among them, the weights coming from L2 into registers a tile ahead.
-
-constexpr int kPanelThreads = 256;
-constexpr int kPanelWaves = kPanelThreads / kWave;
-
-template <int XB, bool NORM, int KT, int MT>
-__global__ __launch_bounds__(kPanelThreads, 3) void i8_panel_kernel(I8Args a, GnArgs g) {
-    constexpr int kBM = 16 * MT, kStride = rows_stride(KT);
-    __shared__ __align__(16) unsigned char codes[kBM * kStride];
-    __shared__ uint32_t row_info[kBM];   // scale (codes), or the largest magnitude's bits
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int slice = blockIdx.x % a.slices;
-    int64_t m0 = blockIdx.x / a.slices, mend = a.M, image = 0;
-    if constexpr (NORM) {   // a workgroup stays in one image
-        image = m0 / a.blocks_per_image;
-        m0 = image * g.S + (m0 - image * a.blocks_per_image) * kBM;
-        mend = (image + 1) * g.S;
-    } else {
-        m0 *= kBM;
-    }
-    const int rows = (int)min<int64_t>(mend - m0, kBM);
-
-    if constexpr (XB == 0) {
-        const auto xr = make_rsrc(a.a + m0 * a.K, rows * a.K);
-        constexpr int kPer = KT * 4;   // pieces of 16 to a row
-#pragma unroll
-        for (int i = 0; i < kBM * kPer / kPanelThreads; ++i) {
-            const int e = i * kPanelThreads + threadIdx.x, r = e / kPer, c = e % kPer * 16;
-            Sixteen q;
-            if (a.K % 16 == 0) q.load(xr, c < a.K ? r * a.K + c : kOutside);
-            else if (r < rows && c < a.K) q.load(a.a, m0 + r, c, a.K);
-            else q.zero();
-            *reinterpret_cast<i32x4*>(codes + r * kStride + c) = q.q;
-        }
-        if (threadIdx.x < kBM)
-            row_info[threadIdx.x] =
-                (int)threadIdx.x < rows ? __float_as_uint(a.a_scale[m0 + threadIdx.x]) : 0u;
-    } else {
-        // a wave's 4 * MT rows one after the other, NV vectors of eight to a lane
-        constexpr int NV = KT / 8, kIters = 4 * MT, kBatch = 8 / NV;
-        const auto xr = make_rsrc(static_cast<const char*>(a.x) + m0 * a.K * XB, rows * a.K * XB);
-        const bool bf16 = a.x_dtype == DA_BF16, pieces = a.K % 8 == 0;
-        const int c0 = lane * 8, r0 = wave * kIters;
-        NormCoef f[NORM ? NV : 1];
-        if constexpr (NORM) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) f[j].load(a, g, image, c0 + j * kWave * 8);
-        }
-#pragma unroll 1
-        for (int b = 0; b < kIters; b += kBatch) {
-            Eight<XB> q[kBatch][NV];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const int r = r0 + b + i, c = c0 + j * kWave * 8;
-                    if (pieces) q[i][j].load(xr, c < a.K ? (r * a.K + c) * XB : kOutside);
-                    else if (r < rows && c < a.K) q[i][j].load(a.x, m0 + r, c, a.K);
-                    else q[i][j].zero();
-                }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int r = r0 + b + i;
-                float v[NV][8];
-                uint32_t big = 0;
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    q[i][j].unpack(v[j], bf16);
-                    if constexpr (NORM) {
-                        f[j].apply(v[j], g.act);
-                        big = max(big, magnitude(v[j]));
-                    } else {
-                        big = max(big, q[i][j].magnitude());
-                    }
-                }
-                if constexpr (!NORM) big = Eight<XB>::widen(big, bf16);
-#pragma unroll
-                for (int s = kWave / 2; s; s >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, s));
-                const RowScale s = row_scale(big);
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-                    *reinterpret_cast<u32x2*>(codes + r * kStride + c0 + j * kWave * 8) =
-                        u32x2{pack_codes(v[j], s), pack_codes(v[j] + 4, s)};
-                if (lane == 0) row_info[r] = big;
-            }
-        }
-    }
-    __syncthreads();
-
-    const int col = lane % 16, part = lane / 16;
-    int at_row = col * kStride + part * 16;
-    float rs[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-        rs[mt] = XB == 0 ? __uint_as_float(row_info[mt * 16 + col])
-                         : row_scale(row_info[mt * 16 + col]).scale;
-
-    // a wave's weights come in halves of 512 columns, the next half and the next tile's scales
-    // on their way while one is multiplied; what is fetched past a row of the weights meets
-    // codes that are zero
-    const int tiles = (a.N + 15) / 16;
-    const int t1 = min(tiles, (slice + 1) * a.tiles_per_slice);
-    const auto wr = make_rsrc(a.w, (uint32_t)((int64_t)a.N * a.K) & ~3u);
-    const auto sr = make_rsrc(a.w_scale, a.N * 4u), br = make_rsrc(a.bias, a.bias ? a.N * 4u : 0u);
-    const uint32_t w_at = col * a.K + part * 16;
-    const auto weights = [&](int t, int kc0, i32x4 (&wf)[8]) {
-        if (a.K % 16 && t == tiles - 1) {   // the matrix may end inside a piece
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int k = (kc0 + i) * 64 + part * 16;
-                wf[i] = k < a.K ? bytes_of(a.w, min(t * 16 + col, a.N - 1), k, a.K)
-                                : i32x4{0, 0, 0, 0};
-            }
-        } else {
-            Sixteen q;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                q.load(wr, w_at + (uint32_t)(t * 16 * a.K) + (kc0 + i) * 64);
-                wf[i] = q.q;
-            }
-        }
-    };
-    const auto scales = [&](int t) {
-        ColumnScale c;
-        Sixteen s, b;
-        s.load(sr, part * 16 + t * 64);
-        b.load(br, part * 16 + t * 64);
-        __builtin_memcpy(c.s, &s.q, 16);
-        __builtin_memcpy(c.b, &b.q, 16);
-        return c;
-    };
-    const int ob = a.out_dtype == DA_F32 ? 4 : 2;
-    const auto outr = make_rsrc(static_cast<char*>(a.out) + m0 * a.N * ob, rows * a.N * ob);
-    uint32_t out_at[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) out_at[mt] = (uint32_t)(((mt * 16 + col) * a.N + part * 4) * ob);
-
-    int t = slice * a.tiles_per_slice + wave;
-    if (t >= t1) return;
-    i32x4 wf[8];
-    weights(t, 0, wf);
-    ColumnScale cs = scales(t);
-    for (; t < t1; t += kPanelWaves) {
-        const int tn = t + kPanelWaves;
-        // the rows' operands are read anew for each tile: kept, they would fill the registers
-        asm volatile("" : "+v"(at_row));
-        ColumnScale csn = cs;
-        i32x4 acc[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) acc[mt] = i32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int kc0 = 0; kc0 < KT; kc0 += 8) {
-            i32x4 next[8] = {};
-            if (kc0 + 8 < KT) {
-                weights(t, kc0 + 8, next);
-            } else if (tn < t1) {
-                weights(tn, 0, next);
-                csn = scales(tn);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    acc[mt] = mfma(wf[i], *reinterpret_cast<const i32x4*>(
-                                              codes + at_row + mt * 16 * kStride + (kc0 + i) * 64),
-                                   acc[mt]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) wf[i] = next[i];
-        }
-        if (t * 16 + 16 <= a.N) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                float y[4];
-                scaled(acc[mt], rs[mt], cs, y);
-                activate(y, a.act);
-                store_four(outr, out_at[mt], (uint32_t)(t * 16 * ob), y, a.out_dtype);
-            }
-        } else {   // the last tile, not all of it in the row
-            const int n = t * 16 + part * 4;
-            if (n < a.N) {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    if (mt * 16 + col < rows)
-                        finish(a, m0 + mt * 16 + col, n, acc[mt], rs[mt], cs);
-            }
-        }
-        cs = csn;
-    }
-}
-
 // ---- streaming kernel --------------------------------------------------------------------
 //
-// At most 16 * MT rows: a wave takes 16 output channels and every KW-th run of 64 columns,
+// Few rows, 16 * MT at a time: a wave takes 16 output channels and every KW-th run of 64 columns,
 // the weights going from memory into operand registers, several runs in flight; the KW
 // waves' sums meet in LDS.  The rows' codes come from memory (XB 0), or the workgroup
 // quantises up to 16 rows of x into LDS first.
 
 constexpr int kSkinnyThreads = 512;
 constexpr int kSkinnyWaves = kSkinnyThreads / kWave;
-constexpr int kSkinnyRuns = 8;                 // weight runs of a wave in flight
 constexpr size_t kSkinnyLds = 48 * 1024;       // of codes
 
 template <int XB, int MT>
@@ -786,58 +596,108 @@ __global__ __launch_bounds__(kSkinnyThreads) void i8_skinny_kernel(I8Args a, int
     __shared__ __align__(16) i32x4 meet[kSkinnyWaves][MT][kWave];
     __shared__ uint32_t bigs[16][kSkinnyWaves];
     __shared__ float scales[16];
+    constexpr int kRuns = MT == 1 ? 8 : 4;   // of a wave in flight, in pairs of 128 columns
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int col = lane % 16, part = lane / 16;
     const int kw = wave % kw_count;
-    const int tile = blockIdx.x * (kSkinnyWaves / kw_count) + wave / kw_count;
     const int tiles = (a.N + 15) / 16, runs = (a.K + 63) / 64;
-    const int stride = runs * 64 + 16;
-    const int n = min(tile * 16 + col, a.N - 1);
+    const int blocks = (tiles + kSkinnyWaves / kw_count - 1) / (kSkinnyWaves / kw_count);
+    const int64_t m0 = (int64_t)(blockIdx.x / blocks) * (16 * MT);
+    const int rows = (int)min<int64_t>(a.M - m0, 16 * MT);
+    const int tile = blockIdx.x % blocks * (kSkinnyWaves / kw_count) + wave / kw_count;
+    const int stride = runs * 64 + 16, step = kRuns * kw_count;
     const bool live = tile < tiles;
+    const int n = tile * 16 + col, wrows = live ? min(16, a.N - tile * 16) : 0;
 
-    i32x4 wf[kSkinnyRuns];
+    struct Runs {
+        Sixteen w[kRuns], x[XB == 0 ? MT : 1][XB == 0 ? kRuns : 1];
+    } next;
+    const auto column = [&](int c, int i) {
+        return (c + i / 2 * 2 * kw_count + 2 * kw + i % 2) * 64 + part * 16;
+    };
+    const auto wr = make_rsrc(a.w + (live ? (int64_t)tile * 16 * a.K : 0), (uint32_t)wrows * a.K);
+    const auto xr = make_rsrc(a.a + (XB == 0 ? m0 * a.K : 0), XB == 0 ? (uint32_t)rows * a.K : 0u);
     const auto fetch = [&](int c) {
 #pragma unroll
-        for (int i = 0; i < kSkinnyRuns; ++i) {
-            const int k = (c + i * kw_count) * 64 + part * 16;
-            wf[i] = live && k < a.K ? bytes_of(a.w, n, k, a.K) : i32x4{0, 0, 0, 0};
+        for (int i = 0; i < kRuns; ++i) {
+            const int k = column(c, i);
+            next.w[i].load(wr, k + 16 <= a.K ? col * a.K + k : kOutside);
+            if constexpr (XB == 0) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    next.x[mt][i].load(xr, k + 16 <= a.K ? (mt * 16 + col) * a.K + k : kOutside);
+            }
+        }
+        if (a.K % 16 && (c + step) * 64 > a.K) {   // the rows' broken last pieces are among these
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) {
+                const int k = column(c, i);
+                if (k < a.K && k + 16 > a.K) {
+                    if (col < wrows) next.w[i].load(a.w, n, k, a.K);
+                    if constexpr (XB == 0) {
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            if (mt * 16 + col < rows)
+                                next.x[mt][i].load(a.a, m0 + mt * 16 + col, k, a.K);
+                    }
+                }
+            }
         }
     };
-    fetch(kw);   // on its way while the rows are quantised
+    fetch(0);   // on its way while the rows are quantised
 
     if constexpr (XB != 0) {
-        // 8 / 2^j waves to a row
+        // 8 / 2^j waves to a row; a lane keeps the first two pieces of it
         const bool bf16 = a.x_dtype == DA_BF16;
         int share = 1;
-        while (share < kSkinnyWaves && kSkinnyWaves / (2 * share) >= (int)a.M) share *= 2;
-        const int part_of = wave % share;
-        for (int m = wave / share; m < (int)a.M; m += kSkinnyWaves / share) {
+        while (share < kSkinnyWaves && kSkinnyWaves / (2 * share) >= rows) share *= 2;
+        const int part_of = wave % share, skip = share * kWave * 8;
+        constexpr int kHold = 2;
+        for (int first = 0; first < rows; first += kSkinnyWaves / share) {
+            const int m = first + wave / share, c0 = (part_of * kWave + lane) * 8;
+            Eight<XB> hold[kHold];
+            float v[8];
             uint32_t big = 0;
-            for (int c = (part_of * kWave + lane) * 8; c < a.K; c += share * kWave * 8) {
-                Eight<XB> q;
-                float v[8];
-                q.load(a.x, m, c, a.K);
-                q.unpack(v, bf16);
-                big = max(big, magnitude(v));
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) {
+                if (m < rows && c0 + i * skip < a.K) hold[i].load(a.x, m, c0 + i * skip, a.K);
+                else hold[i].zero();
             }
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) big = max(big, hold[i].magnitude());
+            if (m < rows)
+                for (int c = c0 + kHold * skip; c < a.K; c += skip) {
+                    Eight<XB> q;
+                    q.load(a.x, m, c, a.K);
+                    big = max(big, q.magnitude());
+                }
+            big = Eight<XB>::widen(big, bf16);
+#pragma unroll
             for (int s = kWave / 2; s; s >>= 1) big = max(big, (uint32_t)__shfl_xor((int)big, s));
-            if (lane == 0) bigs[m][part_of] = big;
-        }
-        __syncthreads();
-        for (int m = wave / share; m < (int)a.M; m += kSkinnyWaves / share) {
-            uint32_t big = 0;
-            for (int i = 0; i < share; ++i) big = max(big, bigs[m][i]);
-            const RowScale s = row_scale(big);
-            for (int c = (part_of * kWave + lane) * 8; c < runs * 64; c += share * kWave * 8) {
-                Eight<XB> q;
-                float v[8];
-                if (c < a.K) q.load(a.x, m, c, a.K);
-                else q.zero();
-                q.unpack(v, bf16);
-                *reinterpret_cast<u32x2*>(codes + m * stride + c) =
-                    u32x2{pack_codes(v, s), pack_codes(v + 4, s)};
+            if (share > 1) {
+                if (lane == 0) bigs[wave / share][part_of] = big;
+                __syncthreads();
+                for (int i = 0; i < share; ++i) big = max(big, bigs[wave / share][i]);
             }
-            if (part_of == 0 && lane == 0) scales[m] = s.scale;
+            if (m < rows) {
+                const RowScale s = row_scale(big);
+                const auto put = [&](const Eight<XB>& q, int c) {
+                    q.unpack(v, bf16);
+                    *reinterpret_cast<u32x2*>(codes + m * stride + c) =
+                        u32x2{pack_codes(v, s), pack_codes(v + 4, s)};
+                };
+#pragma unroll
+                for (int i = 0; i < kHold; ++i)
+                    if (c0 + i * skip < runs * 64) put(hold[i], c0 + i * skip);
+                for (int c = c0 + kHold * skip; c < runs * 64; c += skip) {
+                    Eight<XB> q;
+                    if (c < a.K) q.load(a.x, m, c, a.K);
+                    else q.zero();
+                    put(q, c);
+                }
+                if (part_of == 0 && lane == 0) scales[m] = s.scale;
+            }
+            if (share > 1) __syncthreads();   // bigs is written again for the next rows
         }
         __syncthreads();
     }
@@ -845,29 +705,23 @@ __global__ __launch_bounds__(kSkinnyThreads) void i8_skinny_kernel(I8Args a, int
     i32x4 acc[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[mt] = i32x4{0, 0, 0, 0};
-    for (int c = kw; c < runs;) {
-        i32x4 now[kSkinnyRuns];
+    for (int c = 0; c < runs; c += step) {
+        const Runs now = next;
+        if (c + step < runs) fetch(c + step);
 #pragma unroll
-        for (int i = 0; i < kSkinnyRuns; ++i) now[i] = wf[i];
-        const int at = c;
-        c += kSkinnyRuns * kw_count;
-        if (c < runs) fetch(c);
-#pragma unroll
-        for (int i = 0; i < kSkinnyRuns; ++i) {
-            const int k = (at + i * kw_count) * 64 + part * 16;
+        for (int i = 0; i < kRuns; ++i)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 i32x4 x = {0, 0, 0, 0};
-                const int m = mt * 16 + col;
                 if constexpr (XB != 0) {
-                    if (m < (int)a.M && k < runs * 64)
-                        x = *reinterpret_cast<const i32x4*>(codes + m * stride + k);
+                    const int k = column(c, i);
+                    if (col < rows && k < runs * 64)
+                        x = *reinterpret_cast<const i32x4*>(codes + col * stride + k);
                 } else {
-                    if (m < (int)a.M && k < a.K) x = bytes_of(a.a, m, k, a.K);
+                    x = now.x[mt][i].q;
                 }
-                acc[mt] = mfma(now[i], x, acc[mt]);
+                acc[mt] = mfma(now.w[i].q, x, acc[mt]);
             }
-        }
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) meet[wave][mt][lane] = acc[mt];
@@ -880,118 +734,261 @@ __global__ __launch_bounds__(kSkinnyThreads) void i8_skinny_kernel(I8Args a, int
         i32x4 t = meet[wave - kw][mt][lane];
         for (int i = 1; i < kw_count; ++i) t += meet[wave - kw + i][mt][lane];
         const int m = mt * 16 + col;
-        if (m < (int)a.M) finish(a, m, nn, t, XB != 0 ? scales[m] : a.a_scale[m], cs);
+        if (m < rows) finish(a, m0 + m, nn, t, XB != 0 ? scales[m] : a.a_scale[m0 + m], cs);
     }
 }
 
 // ---- tiled product -----------------------------------------------------------------------
 //
-// BM rows by BN output channels to a workgroup, 128 columns at a time through LDS, each
-// wave WM x WN of it; the next 128 columns are on their way to registers while the matrix
-// cores work.  A 16-byte piece p of an LDS row r sits at place p ^ f(r), so that the 16 rows
-// an operand is read from fall into different banks.
+// 64 rows by 64 output channels to a workgroup of four waves, 128 columns at a time through
+// LDS, the next 128 on their way to registers meanwhile.  A 16-byte piece p of an LDS row r sits at place
+// p ^ (r / 2 % 8): the 16 rows an operand is read from then fall into different banks.
 
-constexpr int kTileK = 128;
+constexpr int kTileK = 128, kTile = 64, kTileThreads = 256;
 
-template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(BM / WM * (BN / WN) * kWave) void i8_tile_kernel(I8Args a) {
-    constexpr int kThreads = BM / WM * (BN / WN) * kWave;
-    constexpr int kPieces = kTileK / 16;                       // of a row
-    constexpr int kXLoads = BM * kPieces / kThreads, kWLoads = BN * kPieces / kThreads;
-    static_assert(BM * kPieces % kThreads == 0 && BN * kPieces % kThreads == 0, "whole loads");
-    __shared__ __align__(16) i32x4 xs[2][BM * kPieces], ws[2][BN * kPieces];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int col = lane % 16, part = lane / 16;
-    const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
-
-    // Workgroups go round the 8 XCDs: each gets a run of consecutive tiles, and runs go down
-    // 8 row tiles before the next column tile, so that an XCD's L2 sees few operands.
-    const int mt = (int)((a.M + BM - 1) / BM), nt = (a.N + BN - 1) / BN;
-    int id = blockIdx.x;
-    {
-        const int total = mt * nt, per = total / 8, extra = total % 8;
-        const int x = id % 8, i = id / 8;
-        id = x * per + min(x, extra) + i;
-    }
+// Workgroups go round the 8 XCDs: each gets a run of consecutive tiles, and runs go down 8 row
+// tiles before the next column tile, so that an XCD's L2 sees few operands.
+__device__ __forceinline__ void tile_of(int id, int mt, int nt, int& m, int& n) {
+    const int total = mt * nt, x = id % 8, i = id / 8;
+    id = x * (total / 8) + min(x, total % 8) + i;
     const int band = id / (8 * nt), in_band = id - band * 8 * nt;
     const int rows = min(8, mt - band * 8);
-    const int64_t m0 = (int64_t)(band * 8 + in_band % rows) * BM;
-    const int n0 = in_band / rows * BN;
+    m = band * 8 + in_band % rows;
+    n = in_band / rows;
+}
 
-    i32x4 xq[kXLoads], wq[kWLoads];
-    const auto fetch = [&](int k0) {
+__global__ __launch_bounds__(kTileThreads) void i8_tile_kernel(I8Args a) {
+    constexpr int kPieces = kTileK / 16, kLoads = kTile * kPieces / kTileThreads, W = 32;
+    __shared__ __align__(16) i32x4 xs[2][kTile * kPieces], ws[2][kTile * kPieces];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int col = lane % 16, part = lane / 16;
+    const int wm = wave % 2 * W, wn = wave / 2 * W;
+    const int mt = (int)((a.M + kTile - 1) / kTile), nt = (a.N + kTile - 1) / kTile;
+    int tile_m, tile_n;
+    tile_of(blockIdx.x, mt, nt, tile_m, tile_n);
+    const int64_t m0 = (int64_t)tile_m * kTile;
+    const int n0 = tile_n * kTile;
+    const int rows = (int)min<int64_t>(a.M - m0, kTile), cols = min(a.N - n0, kTile);
+
+    // A thread's pieces: rows `row` and row + 32 of either operand, at one place of theirs.
+    // Whole pieces come through buffer resources whose ranges end with the block's last row,
+    // so that no row is looked at; a row's broken last piece is put together from bytes.
+    struct Stage {
+        i32x4 x[kLoads], w[kLoads];
+    } next;
+    const int piece = threadIdx.x % kPieces * 16, row = threadIdx.x / kPieces;
+    constexpr int kRowStep = kTileThreads / kPieces;
+    const auto xr = make_rsrc(a.a + m0 * a.K, (uint32_t)rows * a.K);
+    const auto wr = make_rsrc(a.w + (int64_t)n0 * a.K, (uint32_t)cols * a.K);
+    const auto load = [](__amdgpu_buffer_rsrc_t r, uint32_t voff, int k0) {
+        return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, k0, 0));
+    };
+    const auto fetch = [&](int k0, Stage& s) {
+        if (k0 >= a.K) return;
+        const int k = k0 + piece;
 #pragma unroll
-        for (int i = 0; i < kXLoads; ++i) {
-            const int e = i * kThreads + threadIdx.x;
-            const int64_t m = min(m0 + e / kPieces, a.M - 1);
-            const int k = k0 + e % kPieces * 16;
-            xq[i] = k < a.K ? bytes_of(a.a, m, k, a.K) : i32x4{0, 0, 0, 0};
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t at = k + 16 <= a.K ? (row + i * kRowStep) * a.K + piece : kOutside;
+            s.x[i] = load(xr, at, k0);
+            s.w[i] = load(wr, at, k0);
         }
+        if (a.K % 16 && k0 + kTileK > a.K && k < a.K && k + 16 > a.K) {
 #pragma unroll
-        for (int i = 0; i < kWLoads; ++i) {
-            const int e = i * kThreads + threadIdx.x;
-            const int n = min(n0 + e / kPieces, a.N - 1);
-            const int k = k0 + e % kPieces * 16;
-            wq[i] = k < a.K ? bytes_of(a.w, n, k, a.K) : i32x4{0, 0, 0, 0};
+            for (int i = 0; i < kLoads; ++i) {
+                const int r = row + i * kRowStep;
+                if (r < rows) s.x[i] = bytes_of(a.a, m0 + r, k, a.K);
+                if (r < cols) s.w[i] = bytes_of(a.w, n0 + r, k, a.K);
+            }
         }
     };
     const auto place = [](int r, int p) { return r * kPieces + (p ^ ((r >> 1) & 7)); };
-    const auto put = [&](int b) {
+    const auto put = [&](int b, const Stage& s) {
 #pragma unroll
-        for (int i = 0; i < kXLoads; ++i) {
-            const int e = i * kThreads + threadIdx.x;
-            xs[b][place(e / kPieces, e % kPieces)] = xq[i];
-        }
-#pragma unroll
-        for (int i = 0; i < kWLoads; ++i) {
-            const int e = i * kThreads + threadIdx.x;
-            ws[b][place(e / kPieces, e % kPieces)] = wq[i];
+        for (int i = 0; i < kLoads; ++i) {
+            xs[b][place(row + i * kRowStep, piece / 16)] = s.x[i];
+            ws[b][place(row + i * kRowStep, piece / 16)] = s.w[i];
         }
     };
+
+    i32x4 acc[W / 16][W / 16];
+#pragma unroll
+    for (int i = 0; i < W / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < W / 16; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    const auto multiply = [&](int b) {
+#pragma unroll
+        for (int kc = 0; kc < kTileK / 64; ++kc) {
+            i32x4 xf[W / 16], wf[W / 16];
+#pragma unroll
+            for (int j = 0; j < W / 16; ++j) {
+                wf[j] = ws[b][place(wn + j * 16 + col, kc * 4 + part)];
+                xf[j] = xs[b][place(wm + j * 16 + col, kc * 4 + part)];
+            }
+#pragma unroll
+            for (int i = 0; i < W / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < W / 16; ++j) acc[i][j] = mfma(wf[j], xf[i], acc[i][j]);
+        }
+    };
+    fetch(0, next);
+    float rs[W / 16];
+    ColumnScale cs[W / 16];
+#pragma unroll
+    for (int i = 0; i < W / 16; ++i) {
+        const int m = wm + i * 16 + col;
+        rs[i] = m < rows ? a.a_scale[m0 + m] : 0.0f;
+        cs[i] = column_scale(a, min(n0 + wn + i * 16 + part * 4, a.N));
+    }
+    put(0, next);
+    __syncthreads();
+    int b = 0;
+    for (int k0 = 0; k0 < a.K; k0 += kTileK, b ^= 1) {
+        fetch(k0 + kTileK, next);
+        multiply(b);
+        if (k0 + kTileK < a.K) put(b ^ 1, next);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < W / 16; ++j) {
+        const int n = n0 + wn + j * 16 + part * 4;
+        if (n >= a.N) continue;
+#pragma unroll
+        for (int i = 0; i < W / 16; ++i) {
+            const int m = wm + i * 16 + col;
+            if (m < rows) finish(a, m0 + m, n, acc[i][j], rs[i], cs[j]);
+        }
+    }
+}
+
+// ---- large products ----------------------------------------------------------------------
+//
+// 256 rows by 256 output channels to a workgroup of eight waves, 128 x 64 to a wave, columns
+// in whole runs of 128.  The next 128 columns go from memory straight into the other half of
+// LDS while these are multiplied, and a run's operands are read while the run before it is
+// in the matrix cores.  An instruction that fills LDS puts lane l's 16 bytes at place l of a
+// run of 1 KB, so the swizzle of the tiled kernel is in the addresses the lanes fetch from.
+
+constexpr int kBigTile = 256, kBigThreads = 512;
+constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;   // instruction classes of a schedule
+
+__global__ __launch_bounds__(kBigThreads, 2) void i8_big_kernel(I8Args a) {
+    constexpr int kPieces = kTileK / 16, WM = 128, WN = 64;
+    // four arrays, not one: the compiler then sees that what is filled is not what is read
+    __shared__ __align__(16) i32x4 x0[kBigTile * kPieces], x1[kBigTile * kPieces];
+    __shared__ __align__(16) i32x4 w0[kBigTile * kPieces], w1[kBigTile * kPieces];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int col = lane % 16, part = lane / 16;
+    const int wm = wave % 2 * WM, wn = wave / 2 * WN;
+    const int mt = (int)((a.M + kBigTile - 1) / kBigTile), nt = (a.N + kBigTile - 1) / kBigTile;
+    int tile_m, tile_n;
+    tile_of(blockIdx.x, mt, nt, tile_m, tile_n);
+    const int64_t m0 = (int64_t)tile_m * kBigTile;
+    const int n0 = tile_n * kBigTile;
+    const int rows = (int)min<int64_t>(a.M - m0, kBigTile);
+
+    const auto xr = make_rsrc(a.a + m0 * a.K, (uint32_t)rows * a.K);
+    const auto wr = make_rsrc(a.w + (int64_t)n0 * a.K, (uint32_t)min(a.N - n0, kBigTile) * a.K);
+    // rows i * 64 + wave * 8 + lane / 8
+    const int row = wave * 8 + lane / kPieces;
+    const uint32_t at = row * a.K + ((lane % kPieces) ^ ((row >> 1) & 7)) * 16;
+    const auto fetch = [&](int k0, i32x4* xs, i32x4* ws) {
+#pragma unroll
+        for (int i = 0; i < kBigTile / 64; ++i) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                xr, (__attribute__((address_space(3))) void*)(xs + (i * 64 + wave * 8) * kPieces), 16,
+                at + i * 64 * a.K, k0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                wr, (__attribute__((address_space(3))) void*)(ws + (i * 64 + wave * 8) * kPieces), 16,
+                at + i * 64 * a.K, k0, 0, 0);
+        }
+    };
+    const auto place = [](int r, int p) { return r * kPieces + (p ^ ((r >> 1) & 7)); };
 
     i32x4 acc[WM / 16][WN / 16];
 #pragma unroll
     for (int i = 0; i < WM / 16; ++i)
 #pragma unroll
         for (int j = 0; j < WN / 16; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    fetch(0);
-    put(0);
-    __syncthreads();
-    int b = 0;
-    for (int k0 = 0; k0 < a.K; k0 += kTileK, b ^= 1) {
-        const bool more = k0 + kTileK < a.K;
-        if (more) fetch(k0 + kTileK);
+    const auto step = [&](const i32x4* xs, const i32x4* ws) {
 #pragma unroll
         for (int kc = 0; kc < kTileK / 64; ++kc) {
             i32x4 xf[WM / 16], wf[WN / 16];
 #pragma unroll
-            for (int i = 0; i < WM / 16; ++i) xf[i] = xs[b][place(wm + i * 16 + col, kc * 4 + part)];
+            for (int j = 0; j < WN / 16; ++j) wf[j] = ws[place(wn + j * 16 + col, kc * 4 + part)];
 #pragma unroll
-            for (int j = 0; j < WN / 16; ++j) wf[j] = ws[b][place(wn + j * 16 + col, kc * 4 + part)];
+            for (int i = 0; i < WM / 16; ++i) xf[i] = xs[place(wm + i * 16 + col, kc * 4 + part)];
 #pragma unroll
             for (int i = 0; i < WM / 16; ++i)
 #pragma unroll
                 for (int j = 0; j < WN / 16; ++j) acc[i][j] = mfma(wf[j], xf[i], acc[i][j]);
         }
-        if (more) put(b ^ 1);
+        // the order of the step: the first run's operands, then a read to every two products
+        // while there are any, so that the second run's are there when the first is done
+        __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 12, 0);
+#pragma unroll
+        for (int i = 0; i < 12; ++i) {
+            __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(kSchedMatrix, 40, 0);
+    };
+    fetch(0, x0, w0);
+    __syncthreads();
+    for (int k0 = 0;;) {
+        if (k0 + kTileK < a.K) fetch(k0 + kTileK, x1, w1);
+        step(x0, w0);
         __syncthreads();
+        k0 += kTileK;
+        if (k0 >= a.K) break;
+        if (k0 + kTileK < a.K) fetch(k0 + kTileK, x0, w0);
+        step(x1, w1);
+        __syncthreads();
+        k0 += kTileK;
+        if (k0 >= a.K) break;
     }
+
+    // all scales at once, then stores only
+    const int ob = a.out_dtype == DA_F32 ? 4 : 2;
+    const auto outr = make_rsrc(static_cast<char*>(a.out) + m0 * a.N * ob, (uint32_t)rows * a.N * ob);
+    const auto rr = make_rsrc(a.a_scale + m0, rows * 4u);
+    const auto sr = make_rsrc(a.w_scale, a.N * 4u), br = make_rsrc(a.bias, a.bias ? a.N * 4u : 0u);
+    float rs[WM / 16];
+    ColumnScale cs[WN / 16];
+#pragma unroll
+    for (int i = 0; i < WM / 16; ++i)
+        rs[i] = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(rr, (wm + i * 16 + col) * 4, 0, 0));
 #pragma unroll
     for (int j = 0; j < WN / 16; ++j) {
-        const int n = n0 + wn + j * 16 + part * 4;
-        if (n >= a.N) continue;
-        const ColumnScale c = column_scale(a, n);
+        Sixteen s, b;
+        s.load(sr, (n0 + wn + j * 16 + part * 4) * 4u);
+        b.load(br, (n0 + wn + j * 16 + part * 4) * 4u);
+        __builtin_memcpy(cs[j].s, &s.q, 16);
+        __builtin_memcpy(cs[j].b, &b.q, 16);
+    }
 #pragma unroll
-        for (int i = 0; i < WM / 16; ++i) {
-            const int64_t m = m0 + wm + i * 16 + col;
-            if (m < a.M) finish(a, m, n, acc[i][j], a.a_scale[m], c);
+    for (int i = 0; i < WM / 16; ++i) {
+        const int m = wm + i * 16 + col;
+        const uint32_t out_at = (uint32_t)((m * a.N + part * 4) * ob);
+#pragma unroll
+        for (int j = 0; j < WN / 16; ++j) {
+            const int nt0 = n0 + wn + j * 16;
+            if (nt0 + 16 <= a.N) {
+                float y[4];
+                scaled(acc[i][j], rs[i], cs[j], y);
+                activate(y, a.act);
+                store_four(outr, out_at, (uint32_t)(nt0 * ob), y, a.out_dtype);
+            } else if (nt0 + part * 4 < a.N && m < rows) {
+                finish(a, m0 + m, nt0 + part * 4, acc[i][j], rs[i], cs[j]);
+            }
         }
     }
 }
 
 // ---- launches ----------------------------------------------------------------------------
 
-constexpr int kRowsMostK = 256, kPanelMostK = 1024;
+constexpr int kRowsMostK = 256;
 
 template <int XB, bool NORM, int KT>
 hipError_t launch_rows(I8Args a, const GnArgs& g, hipStream_t stream) {
@@ -1014,97 +1011,99 @@ hipError_t launch_rows(I8Args a, const GnArgs& g, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int XB, bool NORM, int KT, int MT>
-hipError_t launch_panel(I8Args a, const GnArgs& g, hipStream_t stream) {
-    constexpr int kBM = 16 * MT;
-    int64_t blocks = (a.M + kBM - 1) / kBM;
-    if (NORM) {
-        a.blocks_per_image = (int32_t)((g.S + kBM - 1) / kBM);
-        blocks = (int64_t)g.N * a.blocks_per_image;
-    }
-    // output tiles are shared out where the row blocks alone leave compute units idle
-    const int tiles = (a.N + 15) / 16;
-    const int64_t want = std::max<int64_t>(1, 512 / blocks);
-    a.tiles_per_slice = (int32_t)std::max<int64_t>(std::min(tiles, kPanelWaves),
-                                                   (tiles + want - 1) / want);
-    a.slices = (tiles + a.tiles_per_slice - 1) / a.tiles_per_slice;
-    i8_panel_kernel<XB, NORM, KT, MT>
-        <<<(uint32_t)(blocks * a.slices), kPanelThreads, 0, stream>>>(a, g);
-    return hipGetLastError();
-}
-
 template <int XB, bool NORM>
 hipError_t rows_by_depth(const I8Args& a, const GnArgs& g, hipStream_t stream) {
     if (a.K <= 128) return launch_rows<XB, NORM, 2>(a, g, stream);
-    if (a.K <= kRowsMostK) return launch_rows<XB, NORM, 4>(a, g, stream);
-    const int64_t blocks = NORM ? (int64_t)g.N * ((g.S + 63) / 64) : (a.M + 63) / 64;
-    // 64 rows share what is fetched of the weights; 32 where that many row blocks are few
-    if (a.K <= 512)
-        return blocks < 128 ? launch_panel<XB, NORM, 8, 2>(a, g, stream)
-                            : launch_panel<XB, NORM, 8, 4>(a, g, stream);
-    return blocks < 128 ? launch_panel<XB, NORM, 16, 2>(a, g, stream)
-                        : launch_panel<XB, NORM, 16, 4>(a, g, stream);
+    return launch_rows<XB, NORM, 4>(a, g, stream);
 }
 
 template <int XB>
 hipError_t launch_skinny(const I8Args& a, hipStream_t stream) {
     const int runs = (a.K + 63) / 64, tiles = (a.N + 15) / 16;
     int kw = kSkinnyWaves;
-    while (kw > 1 && runs < 2 * kw) kw /= 2;
-    const uint32_t blocks = (uint32_t)((tiles + kSkinnyWaves / kw - 1) / (kSkinnyWaves / kw));
+    while (kw > 1 && runs < 4 * kw) kw /= 2;   // at least two pairs of runs to a wave
+    const int mt = XB != 0 || a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
+    const uint32_t blocks = (uint32_t)((tiles + kSkinnyWaves / kw - 1) / (kSkinnyWaves / kw) *
+                                       ((a.M + 16 * mt - 1) / (16 * mt)));
     const size_t lds = XB ? (size_t)a.M * (runs * 64 + 16) : 0;
     if constexpr (XB != 0) {
         i8_skinny_kernel<XB, 1><<<blocks, kSkinnyThreads, lds, stream>>>(a, kw);
     } else {
-        if (a.M <= 16) i8_skinny_kernel<XB, 1><<<blocks, kSkinnyThreads, 0, stream>>>(a, kw);
-        else if (a.M <= 32) i8_skinny_kernel<XB, 2><<<blocks, kSkinnyThreads, 0, stream>>>(a, kw);
+        if (mt == 1) i8_skinny_kernel<XB, 1><<<blocks, kSkinnyThreads, 0, stream>>>(a, kw);
+        else if (mt == 2) i8_skinny_kernel<XB, 2><<<blocks, kSkinnyThreads, 0, stream>>>(a, kw);
         else i8_skinny_kernel<XB, 4><<<blocks, kSkinnyThreads, 0, stream>>>(a, kw);
     }
     return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN>
-hipError_t launch_tile(const I8Args& a, hipStream_t stream) {
-    const int64_t blocks = (a.M + BM - 1) / BM * ((a.N + BN - 1) / BN);
-    i8_tile_kernel<BM, BN, WM, WN>
-        <<<(uint32_t)blocks, BM / WM * (BN / WN) * kWave, 0, stream>>>(a);
-    return hipGetLastError();
+// A product that fills the compute units with 256 x 256 tiles
+bool big(int64_t M, int64_t K, int64_t N) {
+    return (M + 255) / 256 * ((N + 255) / 256) >= 200 && K % kTileK == 0 && N < (1 << 20);
 }
 
 hipError_t launch_tiles(const I8Args& a, hipStream_t stream) {
-    const auto blocks = [&](int bm, int bn) {
-        return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn);
+    const auto blocks = [&](int t) {
+        return (uint32_t)((a.M + t - 1) / t * ((a.N + t - 1) / t));
     };
-    if (blocks(256, 256) >= 200) return launch_tile<256, 256, 128, 64>(a, stream);
-    if (blocks(128, 128) >= 256) return launch_tile<128, 128, 64, 64>(a, stream);
-    return launch_tile<64, 64, 32, 32>(a, stream);
+    if (big(a.M, a.K, a.N)) i8_big_kernel<<<blocks(kBigTile), kBigThreads, 0, stream>>>(a);
+    else i8_tile_kernel<<<blocks(kTile), kTileThreads, 0, stream>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
+// Which kernel, by times measured on an MI355X (us a call of i8_linear in a captured graph):
+//  - up to 256 columns the rows kernel: 50176 x 256 x 216 takes 20 (quantised in memory, then
+//    tiled 30), 100 x 256 x 2496 takes 5.8 (streamed 12);
+//  - up to 16 rows the streaming kernel: one row of 4096 x 4096 takes 6.8, and quantising on
+//    the way saves a launch where the rows fit LDS; up to 64, and beyond them with 1024 columns
+//    or more up to 128 rows or 64 tiles (one 64 x 64 tile walks its columns at 0.65 us per
+//    128): 128 x 4096 x 256 takes 18 (tiled 33), 100 x 4096 x 4096 29 (33), 200 x 2048 x 1024 12
+//    (20), but 256 x 1024 x 4096 19 (13) and 256 x 512 x 512 11 (9);
+//  - else tiles.
 I8Path i8_path(int64_t M, int64_t K, int64_t N, bool codes, bool norm) {
-    // ranges of buffer resources: the weights, and 64 rows of a binary32 result
-    const bool rows = K <= kPanelMostK && N * K < (int64_t(1) << 31) && N < (1 << 22);
+    // 16 rows of a binary32 result are the range of a buffer resource
+    const bool rows = K <= kRowsMostK && N < (1 << 22);
     if (norm) return rows ? I8Path::kRows : I8Path::kTiles;
     if (M <= 16 && !codes && (size_t)M * ((K + 63) / 64 * 64 + 16) <= kSkinnyLds)
         return I8Path::kSkinny;
-    if (M <= 64) return I8Path::kSkinnyCodes;
+    if (M <= 16) return I8Path::kSkinnyCodes;
     if (rows) return I8Path::kRows;
+    const int64_t tiles = (M + kTile - 1) / kTile * ((N + kTile - 1) / kTile);
+    if (M <= 64 || (K >= 1024 && M <= 256 && (M <= 128 || tiles <= 64))) return I8Path::kSkinnyCodes;
     return I8Path::kTiles;
 }
 
-hipError_t launch_i8_quantize(const I8Args& a, const GnArgs* norm, hipStream_t stream) {
-    const uint32_t blocks = (uint32_t)((a.M + kQuantThreads / kWave - 1) / (kQuantThreads / kWave));
-    if (norm) {
-        if (a.x_dtype == DA_F32)
-            i8_norm_quantize_kernel<4><<<blocks, kQuantThreads, 0, stream>>>(a, *norm);
-        else
-            i8_norm_quantize_kernel<2><<<blocks, kQuantThreads, 0, stream>>>(a, *norm);
-        return hipGetLastError();
-    }
-    if (a.x_dtype == DA_F32) i8_quantize_kernel<4><<<blocks, kQuantThreads, 0, stream>>>(a);
-    else i8_quantize_kernel<2><<<blocks, kQuantThreads, 0, stream>>>(a);
+namespace {
+
+template <int XB, bool NORM, int L, int HOLD>
+hipError_t quantize(const I8Args& a, const GnArgs& g, hipStream_t stream) {
+    // rows one after the other only where there are waves enough without
+    const int rows = (int)std::min<int64_t>(8, std::max<int64_t>(1, a.M / 2048));
+    const int64_t waves = NORM ? g.N * ((g.S + rows - 1) / rows)
+                               : (a.M + kWave / L - 1) / (kWave / L);
+    i8_quantize_kernel<XB, NORM, L, HOLD>
+        <<<(uint32_t)((waves + kQuantWaves - 1) / kQuantWaves), kQuantThreads, 0, stream>>>(a, g, rows);
     return hipGetLastError();
+}
+
+template <int XB>
+hipError_t quantize(const I8Args& a, const GnArgs* norm, hipStream_t stream) {
+    if (norm)
+        return a.K <= 1024 ? quantize<XB, true, 64, 2>(a, *norm, stream)
+                           : quantize<XB, true, 64, 4>(a, *norm, stream);
+    const GnArgs none{};
+    if (a.K <= 64) return quantize<XB, false, 8, 1>(a, none, stream);
+    if (a.K <= 128) return quantize<XB, false, 16, 1>(a, none, stream);
+    if (a.K <= 256) return quantize<XB, false, 32, 1>(a, none, stream);
+    if (a.K <= 512) return quantize<XB, false, 64, 1>(a, none, stream);
+    return quantize<XB, false, 64, 4>(a, none, stream);
+}
+
+}  // namespace
+
+hipError_t launch_i8_quantize(const I8Args& a, const GnArgs* norm, hipStream_t stream) {
+    return a.x_dtype == DA_F32 ? quantize<4>(a, norm, stream) : quantize<2>(a, norm, stream);
 }
 
 hipError_t launch_i8_product(const I8Args& a, I8Path path, bool codes, const GnArgs* norm,

@@ -133,7 +133,7 @@ def codes(x):
 
 def product(a, a_scale, w, w_scale, bias, name):
     """(out, bound before rounding to 16 bits) of codes."""
-    s = (a.cpu().long().double() @ w.cpu().long().double().t())
+    s = a.cpu().double() @ w.cpu().double().t()
     y = s * a_scale.cpu().double()[:, None] * w_scale.cpu().double()[None, :]
     mag = y.abs()
     if bias is not None:

@@ -176,7 +176,8 @@ def test_views_off_alignment(dtype):
         check("grad_x", gx, dx, rounded(tx, dx, dtype))
 
 
-@pytest.mark.parametrize("shape", [(2, 33, 64, 4), (2, 5000, 64, 4), (1, 9, 21, 3)])
+@pytest.mark.parametrize("shape", [(2, 33, 64, 4), (2, 5000, 64, 4), (1, 9, 21, 3),
+                                   (4, 40000, 64, 8), (1, 30011, 4096, 1)])
 def test_in_place(shape):
     x, w, b, dy = _inputs(shape, BF16, 57)
     out, mean, rstd = vdf.gn_forward(x, shape[3], w, b, EPS, "silu")

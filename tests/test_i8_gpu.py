@@ -72,6 +72,21 @@ def test_linear_sizes(M, K, N):
     assert torch.equal(out, both)
 
 
+@pytest.mark.parametrize("M, K, N", [(3950, 384, 3990), (3950, 128, 3985), (3841, 256 + 128, 4100),
+                                     (25700, 640, 510), (3950, 300, 3990), (3950, 272, 4001)])
+@pytest.mark.parametrize("out_dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_large_products(M, K, N, out_dtype):
+    """Enough 256 x 256 tiles to fill the card, with ragged edges, and the columns that keep
+    such a product on smaller tiles."""
+    say(f"[i8] large {M} {K} {N} {out_dtype}")
+    a, s = _codes(M, K, 201)
+    w, ws, b = _layer(N, K, 202)
+    out = vdf.i8_matmul(a, s, w, ws, b, activation="relu", out_dtype=out_dtype)
+    torch.cuda.synchronize()
+    ref, tol = product(a, s, w, ws, b, "relu")
+    check("out", out, ref, rounded(tol, ref, out_dtype))
+
+
 @pytest.mark.parametrize("act_name", ["none", "relu", "silu", "gelu"])
 @pytest.mark.parametrize("out_dtype", [F32, BF16, F16], ids=["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M", [2, 150, 700])

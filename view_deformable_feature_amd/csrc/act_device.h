@@ -75,6 +75,17 @@ __device__ __forceinline__ void activate_grad(float (&d)[V], const float (&z)[V]
     }
 }
 
+// f with the activation as a constant: loops inside f then have no branch on it.
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+    switch (act) {
+        case DA_ACT_RELU: f(std::integral_constant<int, DA_ACT_RELU>{}); break;
+        case DA_ACT_SILU: f(std::integral_constant<int, DA_ACT_SILU>{}); break;
+        case DA_ACT_GELU: f(std::integral_constant<int, DA_ACT_GELU>{}); break;
+        default: f(std::integral_constant<int, DA_ACT_NONE>{});
+    }
+}
+
 // Raw storage of V elements of T, moved in one access: V = 16 bytes' worth, or 1.
 template <typename T, int V>
 struct Raw {

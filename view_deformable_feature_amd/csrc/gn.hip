@@ -63,9 +63,18 @@ __device__ __forceinline__ void unit_sums(const float* red, int R, int cols, int
     __syncthreads();
 }
 
-__device__ __forceinline__ double wave_sum(double t) {
-    for (int m = kWave / 2; m; m >>= 1) t += __shfl_xor(t, m);
-    return t;
+// Units of a thread's channels: channel e of vector v lies in unit u[e] of the slab.
+template <int V>
+__device__ __forceinline__ void units_of(const Slab& b, int per_ch, int (&u)[V]) {
+    int unit = b.v * V / per_ch, left = per_ch - (b.v * V - unit * per_ch);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        u[e] = unit;
+        if (--left == 0) {
+            ++unit;
+            left = per_ch;
+        }
+    }
 }
 
 // The group's first value in image n: all of the group's means are formed and kept as
@@ -94,11 +103,12 @@ __device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int
     const int cols = whole ? b.cols : b.width, per = whole ? per_ch / V : per_ch;
     const float rc = cnt ? 1.0f / cnt : 0.0f, inv = 1.0f / (rows * per_ch);
     float m[V];   // this thread's channel means, less the origin
-    const int u0 = b.v * V / per_ch;
-    float origin = origin_of(a, n, b.g0 + u0);
+    int u[V];
+    units_of(b, per_ch, u);
+    float origin = origin_of(a, n, b.g0 + u[0]);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        if (!whole) origin = origin_of(a, n, b.g0 + (b.v * V + e) / per_ch);
+        if (!whole) origin = origin_of(a, n, b.g0 + u[e]);
         m[e] = (first[e] - origin) + sum[e] * rc;
     }
     if (b.r < b.R) {
@@ -114,10 +124,10 @@ __device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int
     }
     __syncthreads();
     unit_sums(red, b.R, cols, per, b.nunits, inv, um);
-    float dev[V], mean = um[u0];
+    float dev[V], mean = um[u[0]];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        if (!whole) mean = um[(b.v * V + e) / per_ch];
+        if (!whole) mean = um[u[e]];
         const float d = m[e] - mean;
         // sum of squares about m is sq - sum^2 / cnt, below zero by rounding alone; a NaN stays
         const float t = sq[e] - sum[e] * sum[e] * rc;
@@ -159,7 +169,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_stats_kernel(GnArgs a) {
     if (b.r < b.R) {
         int64_t row = r0 + b.r;
         if (row < r1) Raw<T, V>::load(p + row * a.C).unpack(first);
-        constexpr int U = 4;
+        constexpr int U = 8;
         for (; row < r1; row += U * b.R) {
             Raw<T, V> q[U];
 #pragma unroll
@@ -182,41 +192,63 @@ __global__ __launch_bounds__(kGnThreads) void gn_stats_kernel(GnArgs a) {
     }
     join_threads(a, b, n, (float)(r1 - r0), cnt, first, sum, sq, red, um, uq);
     float2* part = a.unit_part + ((int64_t)n * a.chunks + chunk) * a.units + b.unit0;
-    for (int u = threadIdx.x; u < b.nunits; u += kGnThreads)
+    for (int u = threadIdx.x; u < b.nunits; u += kGnThreads) {
         part[u] = make_float2(um[u], uq[u]);
+        // kept: x may be overwritten in place by the time the chunks are joined
+        if (chunk == 0 && (a.upg == 1 || s % a.upg == 0))
+            a.origins[(int64_t)n * a.G + b.g0 + u] = origin_of(a, n, b.g0 + u);
+    }
 }
 
-// The chunks' statistics of groups g0 .. g0 + ngroups - 1 joined in binary64, one wave
-// per group: mean and rstd into LDS.  Every thread of the workgroup calls it.
+// The chunks' statistics of groups g0 .. g0 + ngroups - 1 joined in binary64, a run of 8 to
+// 64 lanes to a group: mean and rstd into LDS.  Every thread of the workgroup calls it.
 __device__ __forceinline__ void join_stats(const GnArgs& a, int n, int g0, int ngroups, float* gm,
                                            float* gr) {
-    const int lane = threadIdx.x & (kWave - 1), nw = blockDim.x / kWave;
+    const int run = ngroups <= 4 ? 64 : ngroups <= 8 ? 32 : ngroups <= 16 ? 16 : 8;
+    const int lane = threadIdx.x & (run - 1), entries = a.chunks * a.upg;
     const double total = (double)a.S * a.cpg;
-    for (int j = threadIdx.x / kWave; j < ngroups; j += nw) {
-        const int g = g0 + j;
+    constexpr int kHold = 4;
+    for (int j0 = 0; j0 < ngroups; j0 += kGnThreads / run) {
+        const int j = j0 + (int)threadIdx.x / run, g = g0 + min(j, ngroups - 1);
         const float2* part = a.unit_part + (int64_t)n * a.chunks * a.units + (int64_t)g * a.upg;
-        const int entries = a.chunks * a.upg;
-        double sum = 0.0, m2 = 0.0;
-        for (int e = lane; e < entries; e += kWave) {
-            const int c = e / a.upg, u = e - c * a.upg;
+        // entry e: unit e % upg of chunk e / upg, and how many values it stands for
+        const auto entry = [&](int e, float2& q, double& cnt) {
+            const int c = a.upg == 1 ? e : e / a.upg, u = e - c * a.upg;
             const int64_t r0 = c * a.rows_per_chunk;
-            const double cnt = (double)(min(r0 + a.rows_per_chunk, a.S) - r0) *
-                               min(a.cpu, a.cpg - u * a.cpu);
-            sum += cnt * part[(int64_t)c * a.units + u].x;
+            q = part[(int64_t)c * a.units + u];
+            cnt = (double)(min(r0 + a.rows_per_chunk, a.S) - r0) * min(a.cpu, a.cpg - u * a.cpu);
+        };
+        float2 q[kHold];
+        double cnt[kHold], sum = 0.0, m2 = 0.0;
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            q[i] = make_float2(0.0f, 0.0f);
+            cnt[i] = 0.0;
+            if (lane + i * run < entries) entry(lane + i * run, q[i], cnt[i]);
         }
-        const double mean = wave_sum(sum) / total;
-        for (int e = lane; e < entries; e += kWave) {
-            const int c = e / a.upg, u = e - c * a.upg;
-            const int64_t r0 = c * a.rows_per_chunk;
-            const double cnt = (double)(min(r0 + a.rows_per_chunk, a.S) - r0) *
-                               min(a.cpu, a.cpg - u * a.cpu);
-            const float2 q = part[(int64_t)c * a.units + u];
-            m2 += q.y + cnt * (q.x - mean) * (q.x - mean);
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) sum += cnt[i] * q[i].x;
+        for (int e = lane + kHold * run; e < entries; e += run) {
+            entry(e, q[0], cnt[0]);
+            sum += cnt[0] * q[0].x;
         }
-        const double var = wave_sum(m2) / total;
-        if (lane == 0) {
-            gm[j] = (float)(mean + (double)origin_of(a, n, g));
-            gr[j] = rstd_of(var, a.eps);
+        for (int m = run / 2; m; m >>= 1) sum += __shfl_xor(sum, m);
+        const double mean = sum / total;
+        if (entries > kHold * run) {   // the first entry was read over
+            q[0] = make_float2(0.0f, 0.0f);
+            cnt[0] = 0.0;
+            entry(lane, q[0], cnt[0]);
+        }
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) m2 += q[i].y + cnt[i] * (q[i].x - mean) * (q[i].x - mean);
+        for (int e = lane + kHold * run; e < entries; e += run) {
+            entry(e, q[0], cnt[0]);
+            m2 += q[0].y + cnt[0] * (q[0].x - mean) * (q[0].x - mean);
+        }
+        for (int m = run / 2; m; m >>= 1) m2 += __shfl_xor(m2, m);
+        if (lane == 0 && j < ngroups) {
+            gm[j] = (float)(mean + (double)a.origins[(int64_t)n * a.G + g]);
+            gr[j] = rstd_of(m2 / total, a.eps);
         }
     }
     __syncthreads();
@@ -238,17 +270,30 @@ __global__ __launch_bounds__(kGnThreads) void gn_join_kernel(GnArgs a) {
 
 template <typename T, int V>
 __global__ __launch_bounds__(kGnThreads) void gn_apply_kernel(GnArgs a) {
+    __shared__ float gm[kGnThreads * V], gr[kGnThreads * V];
     const int s = blockIdx.x % a.slabs;
     const int chunk = (blockIdx.x / a.slabs) % a.chunks;
     const int n = blockIdx.x / a.slabs / a.chunks;
     const Slab b = slab_of<V>(a, s, kGnThreads);
+    // every workgroup joins the chunks of its groups itself: a launch less, and with others to
+    // run meanwhile the wait for them is hidden
+    const int ngroups = a.upg == 1 ? b.nunits : 1;
+    join_stats(a, n, b.g0, ngroups, gm, gr);
+    if (chunk == 0 && (a.upg == 1 || s % a.upg == 0)) {
+        for (int j = threadIdx.x; j < ngroups; j += kGnThreads) {
+            if (a.mean) a.mean[(int64_t)n * a.G + b.g0 + j] = gm[j];
+            if (a.rstd) a.rstd[(int64_t)n * a.G + b.g0 + j] = gr[j];
+        }
+    }
     if (b.r >= b.R) return;
     float mu[V], sc[V], bi[V];
+    int u[V];
+    units_of(b, a.upg == 1 ? a.cpg : b.width, u);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const int c = b.v * V + e, j = a.upg == 1 ? c / a.cpg : 0;
-        mu[e] = a.mean[(int64_t)n * a.G + b.g0 + j];
-        sc[e] = a.rstd[(int64_t)n * a.G + b.g0 + j] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
+        const int c = b.v * V + e, j = u[e];
+        mu[e] = gm[j];
+        sc[e] = gr[j] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
         bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
     }
     const int64_t r0 = chunk * a.rows_per_chunk, r1 = min(r0 + a.rows_per_chunk, a.S);
@@ -316,9 +361,11 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_stats_kernel(GnArgs a) {
     for (int e = 0; e < V; ++e) A[e] = B[e] = 0.0f;
     if (b.r < b.R) {
         float mu[V], rs[V], w[V], bi[V];
+        int u[V];
+        units_of(b, a.upg == 1 ? a.cpg : b.width, u);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const int c = b.v * V + e, j = a.upg == 1 ? c / a.cpg : 0;
+            const int c = b.v * V + e, j = u[e];
             mu[e] = a.mean[(int64_t)n * a.G + b.g0 + j];
             rs[e] = a.rstd[(int64_t)n * a.G + b.g0 + j];
             w[e] = a.weight ? a.weight[b.ch0 + c] : 1.0f;
@@ -394,27 +441,33 @@ __device__ __forceinline__ void channel_sums(const GnArgs& a, int block) {
     }
 }
 
-// The averages over each (image, group) of weight * dz and weight * dz * xhat from the chunks'
-// sums: 4 groups to a workgroup.
-__global__ __launch_bounds__(kGnThreads) void gn_bwd_join_kernel(GnArgs a) {
-    const int blocks = (a.G + kGnJoin - 1) / kGnJoin;
-    const int n = blockIdx.x / blocks;
-    const int g = (blockIdx.x - n * blocks) * kGnJoin + threadIdx.x / kWave;
-    if (g >= a.G) return;
-    const int lane = threadIdx.x & (kWave - 1);
+// The averages over (image n, groups g0 .. g0 + ngroups - 1) of weight * dz and weight * dz *
+// xhat from the chunks' sums, as join_stats.
+__device__ __forceinline__ void join_sums(const GnArgs& a, int n, int g0, int ngroups, float* m1,
+                                          float* m2) {
+    const int run = ngroups <= 4 ? 64 : ngroups <= 8 ? 32 : ngroups <= 16 ? 16 : 8;
+    const int lane = threadIdx.x & (run - 1), entries = a.chunks * a.upg;
     const double inv = 1.0 / ((double)a.S * a.cpg);
-    const float2* part = a.unit_part + (int64_t)n * a.chunks * a.units + (int64_t)g * a.upg;
-    double t1 = 0.0, t2 = 0.0;
-    for (int e = lane; e < a.chunks * a.upg; e += kWave) {
-        const int c = e / a.upg, u = e - c * a.upg;
-        const float2 q = part[(int64_t)c * a.units + u];
-        t1 += q.x;
-        t2 += q.y;
+    for (int j0 = 0; j0 < ngroups; j0 += kGnThreads / run) {
+        const int j = j0 + (int)threadIdx.x / run, g = g0 + min(j, ngroups - 1);
+        const float2* part = a.unit_part + (int64_t)n * a.chunks * a.units + (int64_t)g * a.upg;
+        double t1 = 0.0, t2 = 0.0;
+        for (int e = lane; e < entries; e += run) {
+            const int c = a.upg == 1 ? e : e / a.upg;
+            const float2 q = part[(int64_t)c * a.units + e - c * a.upg];
+            t1 += q.x;
+            t2 += q.y;
+        }
+        for (int m = run / 2; m; m >>= 1) {
+            t1 += __shfl_xor(t1, m);
+            t2 += __shfl_xor(t2, m);
+        }
+        if (lane == 0 && j < ngroups) {
+            m1[j] = (float)(t1 * inv);
+            m2[j] = (float)(t2 * inv);
+        }
     }
-    t1 = wave_sum(t1);
-    t2 = wave_sum(t2);
-    if (lane == 0)
-        a.group_sums[(int64_t)n * a.G + g] = make_float2((float)(t1 * inv), (float)(t2 * inv));
+    __syncthreads();
 }
 
 // grad_x of one chunk; the workgroups after the last chunk's form grad_weight and
@@ -425,22 +478,25 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int6
         channel_sums(a, blockIdx.x - chunk_blocks);
         return;
     }
+    __shared__ float m1[kGnThreads * V], m2[kGnThreads * V];
     const int s = blockIdx.x % a.slabs;
     const int chunk = (blockIdx.x / a.slabs) % a.chunks;
     const int n = blockIdx.x / a.slabs / a.chunks;
     const Slab b = slab_of<V>(a, s, kGnThreads);
+    join_sums(a, n, b.g0, a.upg == 1 ? b.nunits : 1, m1, m2);
     if (b.r >= b.R) return;
     float mu[V], rs[V], w[V], bi[V], c1[V], c2[V];
+    int u[V];
+    units_of(b, a.upg == 1 ? a.cpg : b.width, u);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const int c = b.v * V + e, j = a.upg == 1 ? c / a.cpg : 0;
+        const int c = b.v * V + e, j = u[e];
         mu[e] = a.mean[(int64_t)n * a.G + b.g0 + j];
         rs[e] = a.rstd[(int64_t)n * a.G + b.g0 + j];
         w[e] = a.weight ? a.weight[b.ch0 + c] : 1.0f;
         bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
-        const float2 q = a.group_sums[(int64_t)n * a.G + b.g0 + j];
-        c1[e] = q.x;
-        c2[e] = q.y;
+        c1[e] = m1[j];
+        c2[e] = m2[j];
     }
     const int64_t r0 = chunk * a.rows_per_chunk, r1 = min(r0 + a.rows_per_chunk, a.S);
     const int64_t base = ((int64_t)n * a.S) * a.C + b.ch0 + b.v * V;
@@ -507,20 +563,20 @@ __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
     int cnt = b.r < S;
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] = sq[e] = 0.0f;
+    const auto count = [&](const Raw<T, V>& r) {
+        float x[V];
+        r.unpack(x);
+        ++cnt;
 #pragma unroll
-    for (int i = 1; i < NV; ++i) {
-        if (b.r + i * b.R < S) {
-            float x[V];
-            q[i].unpack(x);
-            ++cnt;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = x[e] - first[e];
-                sum[e] += d;
-                sq[e] = fmaf(d, d, sq[e]);
-            }
+        for (int e = 0; e < V; ++e) {
+            const float d = x[e] - first[e];
+            sum[e] += d;
+            sq[e] = fmaf(d, d, sq[e]);
         }
-    }
+    };
+#pragma unroll
+    for (int i = 1; i < NV; ++i)
+        if (b.r + i * b.R < S) count(q[i]);
 #pragma unroll
     for (int i = 0; i < NV; ++i) q[i].forget();
     join_threads(a, b, n, (float)a.S, cnt, first, sum, sq, red, um, uq);
@@ -534,25 +590,34 @@ __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
     if constexpr (STORE) {
         __syncthreads();
         float mu[V], sc[V], bi[V];
+        int u[V];
+        units_of(b, a.cpg, u);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const int c = b.v * V + e, j = c / a.cpg;
-            mu[e] = um[j];
-            sc[e] = uq[j] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
+            const int c = b.v * V + e;
+            mu[e] = um[u[e]];
+            sc[e] = uq[u[e]] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
             bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int row = b.r + i * b.R;
-            if (row < S) {
+        const auto write = [&](auto act, auto same) {
+            const auto put = [&](const Raw<T, V>& r, int row) {
                 float z[V];
-                q[i].unpack(z);
+                r.unpack(z);
 #pragma unroll
                 for (int e = 0; e < V; ++e) z[e] = fmaf(z[e] - mu[e], sc[e], bi[e]);
-                activate(z, a.act);
-                store_vec(a.out, base + (int64_t)row * a.C, z, a.out_dtype);
-            }
-        }
+                activate(z, act);
+                const int64_t at = base + (int64_t)row * a.C;
+                if constexpr (same) store_as(static_cast<T*>(a.out) + at, z);
+                else store_vec(a.out, at, z, a.out_dtype);
+            };
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (b.r + i * b.R < S) put(q[i], b.r + i * b.R);
+        };
+        with_activation(a.act, [&](auto act) {
+            if (a.out_dtype == a.x_dtype) write(act, std::true_type{});
+            else write(act, std::false_type{});
+        });
     }
 }
 
@@ -583,37 +648,41 @@ __global__ __launch_bounds__(kGnWholeBwdThreads) void gn_bwd_whole_kernel(GnArgs
     const float* mean = a.mean + (int64_t)n * a.G + b.g0;
     const float* rstd = a.rstd + (int64_t)n * a.G + b.g0;
     float dz[NV][V], A[V], B[V];
+    int u[V];
+    units_of(b, a.cpg, u);
     {
         float mu[V], sc[V], bi[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const int c = b.v * V + e, j = c / a.cpg;
+            const int c = b.v * V + e, j = u[e];
             mu[e] = mean[j];
             sc[e] = rstd[j] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
             bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
             A[e] = B[e] = 0.0f;
         }
+        with_activation(a.act, [&](auto act) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float x[V], z[V];
-            q[i].unpack(x);
-            dq[i].unpack(dz[i]);   // zeros past the last row
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                x[e] -= mu[e];
-                z[e] = fmaf(x[e], sc[e], bi[e]);
-            }
-            activate_grad(dz[i], z, a.act);
-            if (b.r + i * b.R < S) {
+            for (int i = 0; i < NV; ++i) {
+                float x[V], z[V];
+                q[i].unpack(x);
+                dq[i].unpack(dz[i]);   // zeros past the last row
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    A[e] += dz[i][e];
-                    B[e] = fmaf(dz[i][e], x[e], B[e]);
+                    x[e] -= mu[e];
+                    z[e] = fmaf(x[e], sc[e], bi[e]);
+                }
+                activate_grad(dz[i], z, act);
+                if (b.r + i * b.R < S) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        A[e] += dz[i][e];
+                        B[e] = fmaf(dz[i][e], x[e], B[e]);
+                    }
                 }
             }
-        }
+        });
 #pragma unroll
-        for (int e = 0; e < V; ++e) B[e] *= rstd[(b.v * V + e) / a.cpg];
+        for (int e = 0; e < V; ++e) B[e] *= rstd[u[e]];
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) q[i].forget();
@@ -634,7 +703,7 @@ __global__ __launch_bounds__(kGnWholeBwdThreads) void gn_bwd_whole_kernel(GnArgs
     float mu[V], k1[V], k2[V], k3[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const int c = b.v * V + e, j = c / a.cpg;
+        const int c = b.v * V + e, j = u[e];
         mu[e] = mean[j];
         const float rs = rstd[j];
         k1[e] = rs * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
@@ -662,7 +731,7 @@ hipError_t forward_whole(const GnArgs& a, hipStream_t stream) {
     const uint32_t blocks = (uint32_t)(a.N * a.slabs);
     if (a.vecs <= 4) gn_whole_kernel<T, V, 4, STORE><<<blocks, a.threads, 0, stream>>>(a);
     else if (a.vecs <= 8) gn_whole_kernel<T, V, 8, STORE><<<blocks, a.threads, 0, stream>>>(a);
-    else gn_whole_kernel<T, V, 16, STORE><<<blocks, a.threads, 0, stream>>>(a);
+    else gn_whole_kernel<T, V, kGnWholeVecs, STORE><<<blocks, a.threads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -682,9 +751,8 @@ hipError_t forward_stats(const GnArgs& a, hipStream_t stream) {
 template <typename T, int V>
 hipError_t forward(const GnArgs& a, hipStream_t stream) {
     if (a.threads) return forward_whole<T, V, true>(a, stream);
-    const hipError_t e = forward_stats<T, V>(a, stream);
-    if (e != hipSuccess) return e;
     const uint32_t blocks = (uint32_t)((int64_t)a.N * a.chunks * a.slabs);
+    gn_stats_kernel<T, V><<<blocks, kGnThreads, 0, stream>>>(a);
     gn_apply_kernel<T, V><<<blocks, kGnThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
@@ -703,10 +771,7 @@ hipError_t backward(const GnArgs& a, hipStream_t stream) {
             gn_bwd_whole_kernel<T, V, 8><<<(uint32_t)blocks, a.threads, 0, stream>>>(a);
     } else if (blocks) {
         gn_bwd_stats_kernel<T, V><<<(uint32_t)blocks, kGnThreads, 0, stream>>>(a);
-        if (a.grad_x) {
-            gn_bwd_join_kernel<<<join_blocks(a), kGnThreads, 0, stream>>>(a);
-            dx = blocks;
-        }
+        if (a.grad_x) dx = blocks;
     }
     if (dx + ch)
         gn_bwd_apply_kernel<T, V><<<(uint32_t)(dx + ch), kGnThreads, 0, stream>>>(a, dx);

@@ -74,7 +74,7 @@ bool lay_out_whole(const gn_problem* p, int vec, int threads, int most, da::GnAr
     }
     if (!width) return false;
     a.threads = 256;
-    while (a.threads < threads && vectors(width, a.threads) > most / 4) a.threads *= 2;
+    while (a.threads < threads && vectors(width, a.threads) > 4) a.threads *= 2;
     a.vecs = (int32_t)vectors(width, a.threads);
     a.slab_ch = (int32_t)width;
     a.upg = 1;
@@ -154,17 +154,17 @@ uint64_t chan_part_bytes(const da::GnArgs& a) {
 
 uint64_t group_bytes(const gn_problem* p) { return part_bytes((uint64_t)p->batch * p->groups * 4); }
 
-// Workspace: forward, the chunks' statistics and (where the caller keeps none) mean and rstd;
-// backward, the chunks' sums and the groups' averages.  The larger of both layouts' needs,
-// since the size is asked for before the pointers are known.
+// Workspace: forward, the chunks' statistics (and mean and rstd, for a caller that reads them
+// from there); backward, the chunks' sums.  The larger of both layouts' needs, since the size
+// is asked for before the pointers are known.
 uint64_t need_forward(const gn_problem* p, bool stats_kept) {
     uint64_t need = 0;
     for (int vec : {1, 16 / elem_bytes(p->x_dtype)}) {
         if (vec > 1 && !vectors_fit(p)) continue;
         da::GnArgs a;
         lay_out(p, vec, kForward, a);
-        const uint64_t stats = stats_kept || !a.threads ? 2 * group_bytes(p) : 0;
-        need = std::max(need, stats + (a.threads ? 0 : unit_part_bytes(a)));
+        need = std::max(need, (stats_kept ? 2 * group_bytes(p) : 0) +
+                                  (a.threads ? 0 : group_bytes(p) + unit_part_bytes(a)));
     }
     return need;
 }
@@ -174,8 +174,7 @@ uint64_t need_backward(const gn_problem* p) {
         if (vec > 1 && !vectors_fit(p)) continue;
         da::GnArgs a;
         lay_out(p, vec, backward_keeps(p), a);
-        need = std::max(need, chan_part_bytes(a) +
-                                  (a.threads ? 0 : unit_part_bytes(a) + 2 * group_bytes(p)));
+        need = std::max(need, chan_part_bytes(a) + (a.threads ? 0 : unit_part_bytes(a)));
     }
     return need;
 }
@@ -223,7 +222,8 @@ hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace,
     a.x = x;
     a.mean = reinterpret_cast<float*>(base);
     a.rstd = reinterpret_cast<float*>(base + group_bytes(p));
-    a.unit_part = reinterpret_cast<float2*>(base + 2 * group_bytes(p));
+    a.origins = reinterpret_cast<float*>(base + 2 * group_bytes(p));
+    a.unit_part = reinterpret_cast<float2*>(base + 3 * group_bytes(p));
     return launch_gn_stats(a, vec, stream);
 }
 
@@ -267,12 +267,9 @@ da_status gn_forward(const gn_problem* p, const void* x, const float* weight, co
     a.out = out;
     a.mean = mean;
     a.rstd = rstd;
-    if (!a.threads) {
-        unsigned char* base = static_cast<unsigned char*>(workspace);
-        if (!mean) a.mean = reinterpret_cast<float*>(base);
-        if (!rstd) a.rstd = reinterpret_cast<float*>(base + group_bytes(p));
-        a.unit_part = reinterpret_cast<float2*>(base + 2 * group_bytes(p));
-    }
+    a.origins = static_cast<float*>(workspace);
+    if (!a.threads)
+        a.unit_part = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + group_bytes(p));
     return da::report_hip(da::launch_gn_forward(a, vec, static_cast<hipStream_t>(stream)),
                           "group norm forward launch");
 }
@@ -323,10 +320,7 @@ da_status gn_backward(const gn_problem* p, const void* x, const void* grad_out, 
     a.grad_bias = grad_bias;
     unsigned char* base = static_cast<unsigned char*>(workspace);
     a.chan_part = reinterpret_cast<float2*>(base);
-    if (!a.threads) {
-        a.group_sums = reinterpret_cast<float2*>(base + chan_part_bytes(a));
-        a.unit_part = reinterpret_cast<float2*>(base + chan_part_bytes(a) + 2 * group_bytes(p));
-    }
+    if (!a.threads) a.unit_part = reinterpret_cast<float2*>(base + chan_part_bytes(a));
     return da::report_hip(da::launch_gn_backward(a, vec, static_cast<hipStream_t>(stream)),
                           "group norm backward launch");
 }

@@ -35,10 +35,10 @@ struct GnArgs {
     void* grad_x;             // [N, S, C] of x_dtype, or NULL
     float* grad_weight;       // [C] or NULL
     float* grad_bias;         // [C] or NULL
-    float2* unit_part;        // [N, chunks, units]: (mean, sum of squared deviations), or the
+    float* origins;           // [N, G]: the groups' first values, which means are taken from
+    float2* unit_part;        // [N, chunks, units]: (mean less that, sum of squared deviations), or the
                               // backward's sums of weight * dz and weight * dz * xhat
     float2* chan_part;        // backward: [N, chunks, C] sums of dz and dz * xhat
-    float2* group_sums;       // backward: [N, G] averages of weight * dz and weight * dz * xhat
     int64_t S;
     int64_t rows_per_chunk;
     int32_t N, C, G, cpg;

@@ -409,7 +409,7 @@ constexpr uint32_t kOutside = 0x80000000u;   // past every range (each is below 
 __host__ __device__ constexpr int rows_stride(int kt) { return kt * 64 + 16; }
 
 template <int XB, bool NORM, int KT>
-__global__ __launch_bounds__(kRowsThreads, KT == 4 && (NORM || XB == 4) ? 2 : 4) void i8_rows_kernel(I8Args a,
+__global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_rows_kernel(I8Args a,
                                                                                        GnArgs g) {
     constexpr int kStride = rows_stride(KT);
     constexpr int kPieces = XB == 0 ? 1 : 2;   // per 16 numbers of a lane

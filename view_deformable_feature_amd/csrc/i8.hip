@@ -398,7 +398,8 @@ __device__ __forceinline__ void finish(const I8Args& a, int64_t m, int n, const 
 
 constexpr int kRowsThreads = 512;
 constexpr int kRowsWaves = kRowsThreads / kWave;
-constexpr size_t kRowsLds = 64 * 1024;   // of weights: two workgroups to a compute unit
+constexpr size_t kRowsLdsAll = 80 * 1024;   // two workgroups to a compute unit
+constexpr size_t kRowsLds = 60 * 1024;      // of weights
 
 // Whole pieces of x go through a buffer resource: what lies past the wave's rows reads as
 // zero, without a comparison.
@@ -428,6 +429,8 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
     float* mu = bias + a.tiles_per_slice * 16;   // [64 * KT] each
     float* sc = mu + 64 * KT;
     float* bi = sc + 64 * KT;
+    unsigned char* stage = reinterpret_cast<unsigned char*>(NORM ? bi + 64 * KT : mu) +
+                           wave * 16 * a.N * (a.out_dtype == DA_F32 ? 4 : 2);
 
     // rows: units of 16, within one image behind a norm
     int64_t base = 0, rows_end = a.M, u = (int64_t)block * kRowsWaves + wave;
@@ -566,7 +569,16 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
             ColumnScale cs;
             __builtin_memcpy(cs.s, sp, 16);
             __builtin_memcpy(cs.b, sp + a.tiles_per_slice * 16, 16);
-            if (t * 16 + 16 <= a.N) {
+            if (a.staged) {
+                float y[4];
+                scaled(acc, rs, cs, y);
+                activate(y, a.act);
+                if (t * 16 + part * 4 < a.N) {
+                    const int at = col * a.N + t * 16 + part * 4;
+                    if (ob == 4) *reinterpret_cast<f32x4*>(stage + at * 4) = f32x4{y[0], y[1], y[2], y[3]};
+                    else store_vec(static_cast<void*>(stage), at, y, a.out_dtype);
+                }
+            } else if (t * 16 + 16 <= a.N) {
                 float y[4];
                 scaled(acc, rs, cs, y);
                 activate(y, a.act);
@@ -575,6 +587,14 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
                 const int n = t * 16 + part * 4;
                 if (n < a.N && col < rows) finish(a, m0 + col, n, acc, rs, cs);
             }
+        }
+        if (a.staged) {
+            // the unit's rows are one run of memory: lines are written whole
+            __builtin_amdgcn_wave_barrier();
+            for (int p = lane * 16; p < rows * a.N * ob; p += kWave * 16)
+                __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(stage + p),
+                                                       outr, (uint32_t)p, 0, 0);
+            __builtin_amdgcn_wave_barrier();
         }
     }
 }
@@ -1004,8 +1024,15 @@ hipError_t launch_rows(I8Args a, const GnArgs& g, hipStream_t stream) {
     // workgroups beyond what is resident at once would bring the weights in again
     const int64_t cap = std::max<int64_t>(1, 512 / (images * a.slices));
     a.blocks_per_image = (int32_t)std::min(blocks, cap);
-    const size_t lds = (size_t)a.tiles_per_slice * 16 * (rows_stride(KT) + 8) +
-                       (NORM ? 3 * 64 * KT * 4 : 0);
+    size_t lds = (size_t)a.tiles_per_slice * 16 * (rows_stride(KT) + 8) +
+                 (NORM ? 3 * 64 * KT * 4 : 0);
+    // Results by way of LDS where whole rows of whole 16-byte pieces fit, two workgroups to a
+    // compute unit: 200704 x 128 x 108 into binary32 takes 32 us so, 40 us from the registers,
+    // whose 64-byte pieces of 432-byte rows no line of memory begins or ends with.  Parts of
+    // rows gain nothing: 50176 x 256 x 216 took 23 us by pieces of 128 bytes, 20 us directly.
+    const size_t row = (size_t)a.N * (a.out_dtype == DA_F32 ? 4 : 2);
+    a.staged = a.slices == 1 && row % 16 == 0 && lds + kRowsWaves * 16 * row <= kRowsLdsAll;
+    if (a.staged) lds += kRowsWaves * 16 * row;
     i8_rows_kernel<XB, NORM, KT>
         <<<(uint32_t)(images * a.blocks_per_image * a.slices), kRowsThreads, lds, stream>>>(a, g);
     return hipGetLastError();

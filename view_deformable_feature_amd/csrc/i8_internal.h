@@ -25,6 +25,7 @@ struct I8Args {
     int32_t slices;           // rows kernel: slices of the output channels
     int32_t tiles_per_slice;  // rows kernel: 16-channel tiles of a slice
     int32_t blocks_per_image; // rows kernel: workgroups that share an image's rows
+    int32_t staged;           // rows kernel: results leave by way of LDS
     // a row passes through group norm and an activation before it is quantised
     const float* norm_weight; // [K] or NULL
     const float* norm_bias;   // [K] or NULL

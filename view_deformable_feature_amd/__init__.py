@@ -12,8 +12,8 @@ from .api import (DeformableAggregationFunction, da_backward, da_backward_accumu
 from .pack import (PackLevelsFunction, da_pack_levels, da_unpack_levels,  # noqa: F401
                    feature_maps_format, pack_layout, pack_levels)
 
-from .dcn import (DCNFunction, dcn_backward, dcn_forward, dcn_out_size,  # noqa: F401
-                  dcn_workspace_size, deformable_conv)
+from .dcn import (DCNFunction, dcn_backward, dcn_forward, dcn_forward_projected,  # noqa: F401
+                  dcn_out_size, dcn_workspace_size, deformable_conv)
 
 from .norm import (GroupNormActFunction, gn_backward, gn_backward_workspace_size,  # noqa: F401
                    gn_forward, gn_workspace_size, group_norm_act)

@@ -19,9 +19,10 @@ import torch
 
 from . import _lib
 from .api import _DTYPES, _FLOATS, _need, _ptr, _stream
+from .int8 import i8_linear
 
-__all__ = ["dcn_out_size", "dcn_forward", "dcn_backward", "dcn_workspace_size",
-           "DCNFunction", "deformable_conv"]
+__all__ = ["dcn_out_size", "dcn_forward", "dcn_forward_projected", "dcn_backward",
+           "dcn_workspace_size", "DCNFunction", "deformable_conv"]
 
 Pair = Union[int, Tuple[int, int]]
 
@@ -81,6 +82,28 @@ def dcn_forward(input: torch.Tensor, offset_mask: torch.Tensor, groups: int, ker
                              _stream(dev))
     _lib.check(st, "dcn_forward")
     return out
+
+
+def dcn_forward_projected(input: torch.Tensor, proj: torch.Tensor, proj_scale: torch.Tensor,
+                          proj_bias: Optional[torch.Tensor], groups: int, kernel: Pair = 3,
+                          pad: Pair = 1, dilation: Pair = 1, out: Optional[torch.Tensor] = None,
+                          out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """``dcn_forward`` at stride 1 with its offset_mask made from input as DCNv4 makes it, by
+    one linear layer per pixel, here in 8 bits as a model is served: proj int8 [G * 3K, C] with
+    a scale per row (``i8_quantize_rows`` of the layer's weights) and its bias.  The output is
+    as large as the input; kernel, pad and dilation have to say so."""
+    if not isinstance(input, torch.Tensor) or input.dim() != 4:
+        raise ValueError("input must be a [N, H, W, C] tensor")
+    N, H, W, _ = input.shape
+    if dcn_out_size(H, W, kernel, 1, pad, dilation) != (H, W):
+        raise ValueError("kernel, pad and dilation must keep the size of the input")
+    kh, kw = _pair(kernel)
+    if not isinstance(proj, torch.Tensor) or proj.dim() != 2 or \
+            proj.shape[0] != int(groups) * 3 * kh * kw:
+        raise ValueError(f"proj must be a [{int(groups) * 3 * kh * kw}, C] tensor of codes")
+    offset_mask = i8_linear(input, proj, proj_scale, proj_bias)
+    return dcn_forward(input, offset_mask.view(N, H, W, int(groups), 3 * kh * kw), groups, kernel,
+                       1, pad, dilation, out=out, out_dtype=out_dtype)
 
 
 def dcn_workspace_size(input: torch.Tensor, groups: int, kernel: Pair = 3, stride: Pair = 1,

@@ -69,8 +69,8 @@ DA_API da_status gn_forward_workspace_size(const gn_problem* problem, size_t* by
  *              NULL.
  *   workspace  device scratch of gn_forward_workspace_size() bytes, 256-byte aligned (may
  *              be NULL when that is 0); contents on entry do not matter.
- * Errors: DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (more than 2^16 channels, 2^31
- * workgroups or more), DA_ERR_HIP.
+ * Errors: DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (more than 2^16 channels, a launch of 2^32
+ * threads or more: about 2^24 images), DA_ERR_HIP.
  */
 DA_API da_status gn_forward(const gn_problem* problem, const void* x, const float* weight,
                             const float* bias, void* out, float* mean, float* rstd,

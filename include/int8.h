@@ -38,7 +38,9 @@ extern "C" {
 #endif
 
 /* Problem description.  rows may be 0 (nothing to do); in_channels in [1, 131071],
- * out_channels >= 1; rows and out_channels below 2^31. */
+ * out_channels in [1, 2^24).  A launch has fewer than 2^32 threads, which bounds rows to
+ * 2^26 with more than 256 input channels (2^27 to 2^29 with fewer) and rows times
+ * out_channels to 2^36.  out must not overlap an input. */
 typedef struct {
     int64_t rows;         /* M                                             */
     int64_t in_channels;  /* K                                             */
@@ -72,8 +74,8 @@ DA_API da_status i8_matmul_workspace_size(const i8_problem* problem, size_t* byt
  *   out        device [M, N] of out_dtype, element aligned, fully overwritten.
  *   workspace  device scratch of i8_matmul_workspace_size() bytes, 256-byte aligned (may
  *              be NULL when that is 0); contents on entry do not matter.
- * Errors: DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (more than 131071 input channels, 2^31
- * rows or output channels, 2^31 workgroups), DA_ERR_HIP.
+ * Errors: DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (more than 131071 input channels, rows or
+ * output channels past the limits above), DA_ERR_HIP.
  */
 DA_API da_status i8_matmul(const i8_problem* problem, const int8_t* a, const float* a_scale,
                            const int8_t* w, const float* w_scale, const float* bias, void* out,
@@ -98,7 +100,7 @@ DA_API da_status i8_norm_linear_workspace_size(const gn_problem* problem, int64_
  * i8_norm_linear -- group norm with its activation (group_norm.h), each normalised row
  * quantised from its binary32 values, then the product: out[n, s, :] of [N, S,
  * out_channels].  problem describes x, the groups, eps and the activation between norm and
- * product; problem->out_dtype is the type of out.
+ * product; problem->out_dtype is the type of out.  At most 2^22 images.
  *   x                         device [N, S, C] of x_dtype, element aligned.
  *   norm_weight, norm_bias    device float [C], or NULL, as in gn_forward.
  *   w, w_scale, bias          the projection's codes [out_channels, C], scales and bias

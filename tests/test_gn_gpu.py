@@ -340,3 +340,30 @@ def test_every_half_precision_rounding_is_once():
         got, _, _ = vdf.gn_forward(x, 4, w, b, EPS, "silu", out_dtype=dt)
         torch.cuda.synchronize()
         assert torch.equal(got, full.to(dt)) and HALF[dt]
+
+
+def test_more_values_than_32_bits_count():
+    """2 x 1100003 x 2048 bfloat16 values: places past 2^32 in the second image's rows."""
+    N, S, C, G = 2, 1100003, 2048, 32
+    x = torch.empty((N, S, C), device="cuda", dtype=BF16)
+    gen = torch.Generator(device="cuda").manual_seed(70)
+    for n in range(N):
+        for r in range(0, S, 100000):
+            part = x[n, r:r + 100000]
+            part.copy_(torch.randn(part.shape, generator=gen, device="cuda", dtype=BF16))
+    w = torch.rand((C,), device="cuda") + 0.5
+    out, mean, rstd = vdf.gn_forward(x, G, w, None, EPS, "relu")
+    torch.cuda.synchronize()
+    for n, r in ((0, 0), (1, 0), (1, S - 300)):
+        rows = x[n, r:r + 300].double()
+        z = ((rows.view(-1, G, C // G) - mean[n].double()[None, :, None])
+             * rstd[n].double()[None, :, None]).view(-1, C) * w.double()
+        want = z.clamp_min(0)
+        got = out[n, r:r + 300].double()
+        assert ((got - want).abs() <= 2.0 ** -8 * want + 1e-5).all()
+    # the averages of 70 million normal numbers
+    assert mean.abs().max() < 1e-3 and (rstd - 1).abs().max() < 1e-3
+    gx, _, _ = vdf.gn_backward(x, out, mean, rstd, G, w, None, "none", need_params=False,
+                               grad_x=out)
+    torch.cuda.synchronize()
+    assert gx[1, -1].isfinite().all() and gx[1, -1].abs().max() > 0

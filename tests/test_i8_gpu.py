@@ -354,3 +354,21 @@ def test_reference_by_hand():
     want = [[(127 + 2 * k) * 0.01 * 0.5, -508 * 0.01 * 2.0], [446 * 2.0 * 0.5, 320 * 2.0 * 2.0]]
     assert np.allclose(out.cpu().numpy(), np.array(want), rtol=1e-6)
     assert act(torch.tensor(-1.0), "relu") == 0
+
+
+def test_more_values_than_32_bits_count():
+    """17 million rows of 256 numbers: places past 2^32 of x, and of the result."""
+    M, K, N = 17_000_003, 256, 260
+    x = torch.empty((M, K), device="cuda", dtype=BF16)
+    gen = torch.Generator(device="cuda").manual_seed(120)
+    for r in range(0, M, 1 << 20):
+        part = x[r:r + (1 << 20)]
+        part.copy_(torch.randn(part.shape, generator=gen, device="cuda", dtype=BF16))
+    w, ws, b = _layer(N, K, 121)
+    out = vdf.i8_linear(x, w, ws, b, out_dtype=BF16)
+    last = vdf.i8_linear(x[-1000:].contiguous(), w, ws, b, out_dtype=BF16)
+    q, s = vdf.i8_quantize_rows(x)
+    ql, sl = vdf.i8_quantize_rows(x[-1000:].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(out[-1000:], last)
+    assert torch.equal(q[-1000:], ql) and torch.equal(s[-1000:], sl)

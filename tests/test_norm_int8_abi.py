@@ -83,6 +83,7 @@ GN_BAD = [
     (dict(rows=1 << 31), 2, "2^31"),
     (dict(batch=1 << 30, rows=1 << 30), 2, "2^45"),
     (dict(batch=1 << 30, rows=1 << 12, channels=1 << 16, groups=1 << 16), 2, "workgroups"),
+    (dict(batch=1 << 25, rows=1), 2, "workgroups"),
 ]
 
 
@@ -145,6 +146,8 @@ I8_BAD = [
     (dict(rows=1 << 31), 2, "2^31"),
     (dict(out_channels=1 << 31), 2, "2^31"),
     (dict(rows=(1 << 31) - 1, out_channels=1 << 20), 2, "workgroups"),
+    (dict(rows=1, out_channels=1 << 24), 2, "2^24"),
+    (dict(rows=1 << 26, in_channels=257, out_channels=1), 2, "workgroups"),
     (dict(activation=5), 1, "activation"),
     (dict(out_dtype=3), 1, "da_dtype"),
     (dict(x_dtype=7), 1, "da_dtype"),
@@ -175,6 +178,8 @@ def test_i8_rejects_pointers(lib):
         assert _lin(lib, p, **kw) == 1 and "aligned" in _msg(lib)
         assert _nl(lib, _gn(), **kw) == 1 and "aligned" in _msg(lib)
     assert _nl(lib, _gn(), nw=FAKE + 2) == 1 and "aligned" in _msg(lib)
+    assert _nl(lib, _gn(batch=1 << 22, rows=1)) == 2 and "2^22" in _msg(lib)
+    assert lib.i8_quantize_rows(1 << 26, 300, 0, vp(FAKE), vp(FAKE), vp(FAKE), None) == 2
     assert _nl(lib, _gn(), D=0) == 1 and "out_channels" in _msg(lib)
     assert _mm(lib, _i8(x_dtype=1)) == 1 and "x_dtype" in _msg(lib)
     assert lib.i8_quantize_rows(4, 8, 0, None, vp(FAKE), vp(FAKE), None) == 1

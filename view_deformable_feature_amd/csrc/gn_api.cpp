@@ -190,9 +190,12 @@ da_status check_workspace(uint64_t need, const void* workspace, size_t workspace
     return DA_OK;
 }
 
+// A launch has fewer than 2^32 threads (256 groups' joins take 64 workgroups).
 da_status check_grid(const da::GnArgs& a) {
-    if ((int64_t)a.N * a.chunks * a.slabs + a.C >= (int64_t(1) << 31))
-        return report_error(DA_ERR_UNSUPPORTED, "2^31 workgroups or more");
+    const int64_t threads = a.threads ? a.threads : da::kGnThreads;
+    if (((int64_t)a.N * a.chunks * a.slabs + a.C) * threads >= (int64_t(1) << 32) ||
+        (int64_t)a.N * ((a.G + 3) / 4) * da::kGnThreads >= (int64_t(1) << 32))
+        return report_error(DA_ERR_UNSUPPORTED, "2^32 threads of workgroups or more");
     return DA_OK;
 }
 

@@ -27,8 +27,13 @@ da_status check_sizes(int64_t M, int64_t K, int64_t N) {
         return report_error(DA_ERR_UNSUPPORTED, "in_channels > %lld", (long long)kMostK);
     if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31))
         return report_error(DA_ERR_UNSUPPORTED, "2^31 rows or output channels or more");
-    if ((M + 63) / 64 * ((N + 63) / 64) >= (int64_t(1) << 31))
-        return report_error(DA_ERR_UNSUPPORTED, "2^31 workgroups or more");
+    // a launch has fewer than 2^32 threads: 256 to 64 x 64 results, 512 to 16 output channels of
+    // up to 256 rows in groups of 64, 64 or fewer to a row that is quantised
+    const int64_t lanes = K <= 64 ? 8 : K <= 128 ? 16 : K <= 256 ? 32 : 64;
+    if ((M + 63) / 64 * ((N + 63) / 64) >= (int64_t(1) << 24) || N >= (int64_t(1) << 24) ||
+        M * lanes >= (int64_t(1) << 32) - 256)
+        return report_error(DA_ERR_UNSUPPORTED,
+                            "2^32 threads of workgroups or more (or 2^24 output channels)");
     return DA_OK;
 }
 
@@ -187,6 +192,8 @@ da_status i8_norm_linear_workspace_size(const gn_problem* p, int64_t out_channel
     const int64_t M = p->batch * p->rows;
     st = check_sizes(M, p->channels, out_channels);
     if (st != DA_OK) return st;
+    if (p->batch >= (int64_t(1) << 22))   // a workgroup of 512 threads and more to an image
+        return report_error(DA_ERR_UNSUPPORTED, "2^22 images or more (2^32 threads of workgroups)");
     if (through_memory(da::i8_path(M, p->channels, out_channels, false, true)))
         need += quantised_bytes(M, p->channels);
     *bytes = p->batch ? (size_t)need : 0;

@@ -40,7 +40,7 @@ extern "C" {
 /* Problem description.  rows may be 0 (nothing to do); in_channels in [1, 131071],
  * out_channels in [1, 2^24).  A launch has fewer than 2^32 threads, which bounds rows to
  * 2^26 with more than 256 input channels (2^27 to 2^29 with fewer) and rows times
- * out_channels to 2^36.  out must not overlap an input. */
+ * out_channels to 2^36.  out must not overlap an input; x (the codes) and w are checked. */
 typedef struct {
     int64_t rows;         /* M                                             */
     int64_t in_channels;  /* K                                             */
@@ -54,14 +54,14 @@ typedef struct {
 /*
  * i8_quantize_rows -- codes and scales of each row of x [rows, channels].
  *   x      device [rows, channels] of x_dtype, element aligned.
- *   codes  device int8 [rows, channels], fully overwritten.
+ *   codes  device int8 [rows, channels], fully overwritten; must not overlap x.
  *   scale  device float [rows], fully overwritten.
  */
 DA_API da_status i8_quantize_rows(int64_t rows, int64_t channels, int32_t x_dtype, const void* x,
                                   int8_t* codes, float* scale, void* stream);
 
-/* i8_matmul_workspace_size -- bytes of device workspace i8_matmul needs (0 for most
- * problems). */
+/* i8_matmul_workspace_size -- bytes of device workspace i8_matmul needs (0 for every
+ * problem at present). */
 DA_API da_status i8_matmul_workspace_size(const i8_problem* problem, size_t* bytes);
 
 /*
@@ -100,7 +100,8 @@ DA_API da_status i8_norm_linear_workspace_size(const gn_problem* problem, int64_
  * i8_norm_linear -- group norm with its activation (group_norm.h), each normalised row
  * quantised from its binary32 values, then the product: out[n, s, :] of [N, S,
  * out_channels].  problem describes x, the groups, eps and the activation between norm and
- * product; problem->out_dtype is the type of out.  At most 2^22 images.
+ * product; problem->out_dtype is the type of out.  Fewer than 2^22 images
+ * times runs of 224 output channels.
  *   x                         device [N, S, C] of x_dtype, element aligned.
  *   norm_weight, norm_bias    device float [C], or NULL, as in gn_forward.
  *   w, w_scale, bias          the projection's codes [out_channels, C], scales and bias

@@ -179,6 +179,7 @@ def test_i8_rejects_pointers(lib):
         assert _nl(lib, _gn(), **kw) == 1 and "aligned" in _msg(lib)
     assert _nl(lib, _gn(), nw=FAKE + 2) == 1 and "aligned" in _msg(lib)
     assert _nl(lib, _gn(batch=1 << 22, rows=1)) == 2 and "2^22" in _msg(lib)
+    assert _nl(lib, _gn(batch=511, rows=1), D=1 << 22) == 2 and "224" in _msg(lib)
     assert lib.i8_quantize_rows(1 << 26, 300, 0, vp(FAKE), vp(FAKE), vp(FAKE), None) == 2
     assert _nl(lib, _gn(), D=0) == 1 and "out_channels" in _msg(lib)
     assert _mm(lib, _i8(x_dtype=1)) == 1 and "x_dtype" in _msg(lib)
@@ -240,3 +241,19 @@ def test_binding_refuses():
     with pytest.raises(_lib.DAError, match="131071"):
         vdf.i8_matmul_workspace_size(4, 1 << 20, 8)
     assert vdf.gn_workspace_size(torch.zeros((0, 5, 8)), 2) == 0
+
+
+def test_result_over_an_operand_is_refused(lib):
+    """out over x, the codes or w, from either side."""
+    x, w, far = 0x10000000, 0x40000000, 0x70000000
+    p = _i8(rows=64)      # 64 x K and N x K codes are more than 16 bytes
+    for over in (x, x + 16, x - 16):
+        assert _lin(lib, p, x=x, w=w, out=over) == 1 and "overlaps x" in _msg(lib)
+        assert _mm(lib, _i8(rows=64, x_dtype=0), a=x, w=w, out=over) == 1
+        assert "overlaps x" in _msg(lib)
+        assert _nl(lib, _gn(), x=x, w=w, out=over) == 1 and "overlaps x" in _msg(lib)
+        assert lib.i8_quantize_rows(64, 64, 0, vp(x), vp(over), vp(far), None) == 1
+        assert "overlaps x" in _msg(lib)
+    for over in (w, w + 16, w - 16):
+        assert _lin(lib, p, x=x, w=w, out=over) == 1 and "overlaps w" in _msg(lib)
+        assert _nl(lib, _gn(), x=x, w=w, out=over) == 1 and "overlaps w" in _msg(lib)

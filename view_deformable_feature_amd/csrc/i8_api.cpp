@@ -85,6 +85,21 @@ da::I8Args args_of(int64_t M, int64_t K, int64_t N, int32_t act, int32_t x_dtype
     return a;
 }
 
+// out [M, N] shares a byte with an operand of so many bytes
+da_status check_apart(const void* out, uint64_t out_bytes, const void* in, uint64_t in_bytes,
+                      const char* name) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(out), y = reinterpret_cast<uintptr_t>(in);
+    if (x < y + in_bytes && y < x + out_bytes)
+        return report_error(DA_ERR_INVALID_ARG, "the result overlaps %s", name);
+    return DA_OK;
+}
+da_status check_apart(int64_t M, int64_t K, int64_t N, const void* out, int32_t out_dtype,
+                      const void* x, int x_bytes, const void* w) {
+    const uint64_t bytes = (uint64_t)M * N * elem_bytes(out_dtype);
+    const da_status st = check_apart(out, bytes, x, (uint64_t)M * K * x_bytes, "x");
+    return st != DA_OK ? st : check_apart(out, bytes, w, (uint64_t)N * K, "w");
+}
+
 }  // namespace
 
 extern "C" {
@@ -100,6 +115,9 @@ da_status i8_quantize_rows(int64_t rows, int64_t channels, int32_t x_dtype, cons
         return report_error(DA_ERR_INVALID_ARG, "x / codes / scale is NULL");
     if (!aligned(x, elem_bytes(x_dtype)) || !aligned(scale, 4))
         return report_error(DA_ERR_INVALID_ARG, "x / scale is not element aligned");
+    st = check_apart(codes, (uint64_t)rows * channels, x, (uint64_t)rows * channels * elem_bytes(x_dtype),
+                     "x");
+    if (st != DA_OK) return st;
     da::I8Args a = args_of(rows, channels, 1, DA_ACT_NONE, x_dtype, DA_F32);
     a.x = x;
     a.a = codes;
@@ -127,6 +145,8 @@ da_status i8_matmul(const i8_problem* p, const int8_t* a_codes, const float* a_s
     if (!aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4) ||
         !aligned(out, elem_bytes(p->out_dtype)))
         return report_error(DA_ERR_INVALID_ARG, "a tensor is not element aligned");
+    st = check_apart(p->rows, p->in_channels, p->out_channels, out, p->out_dtype, a_codes, 1, w);
+    if (st != DA_OK) return st;
     da::I8Args a = args_of(p->rows, p->in_channels, p->out_channels, p->activation, p->x_dtype,
                            p->out_dtype);
     a.a = const_cast<int8_t*>(a_codes);
@@ -164,6 +184,9 @@ da_status i8_linear(const i8_problem* p, const void* x, const int8_t* w, const f
         return report_error(DA_ERR_INVALID_ARG, "a tensor is not element aligned");
     st = check_workspace(need, workspace, workspace_bytes);
     if (st != DA_OK) return st;
+    st = check_apart(p->rows, p->in_channels, p->out_channels, out, p->out_dtype, x,
+                     elem_bytes(p->x_dtype), w);
+    if (st != DA_OK) return st;
     da::I8Args a = args_of(p->rows, p->in_channels, p->out_channels, p->activation, p->x_dtype,
                            p->out_dtype);
     a.x = x;
@@ -192,8 +215,10 @@ da_status i8_norm_linear_workspace_size(const gn_problem* p, int64_t out_channel
     const int64_t M = p->batch * p->rows;
     st = check_sizes(M, p->channels, out_channels);
     if (st != DA_OK) return st;
-    if (p->batch >= (int64_t(1) << 22))   // a workgroup of 512 threads and more to an image
-        return report_error(DA_ERR_UNSUPPORTED, "2^22 images or more (2^32 threads of workgroups)");
+    // 512 threads or more to an image and a slice of the weights (224 output channels or more)
+    if (p->batch * ((out_channels + 223) / 224) >= (int64_t(1) << 22))
+        return report_error(DA_ERR_UNSUPPORTED,
+                            "2^22 images times runs of 224 output channels, or more");
     if (through_memory(da::i8_path(M, p->channels, out_channels, false, true)))
         need += quantised_bytes(M, p->channels);
     *bytes = p->batch ? (size_t)need : 0;
@@ -216,6 +241,8 @@ da_status i8_norm_linear(const gn_problem* p, int64_t out_channels, const void* 
     st = check_workspace(need, workspace, workspace_bytes);
     if (st != DA_OK) return st;
     const int64_t M = p->batch * p->rows;
+    st = check_apart(M, p->channels, out_channels, out, p->out_dtype, x, elem_bytes(p->x_dtype), w);
+    if (st != DA_OK) return st;
     da::I8Args a = args_of(M, p->channels, out_channels, DA_ACT_NONE, p->x_dtype, p->out_dtype);
     a.x = x;
     a.w = w;

@@ -4,6 +4,10 @@
 // Lanes lie along the channels of a row, so every access is a run of whole 16-byte
 // vectors, and a thread stays with one vector of channels: its weights, its groups'
 // statistics and the backward's per-channel sums sit in registers.
+//
+// The operator has a handful of operations to a value, so memory bounds it: at the 5.2 TB/s
+// of a copy too large for the caches, forward floors are one read and one write.  Times here
+// are of one MI355X, inputs and outputs in rotation so that no call finds its own in cache.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -151,6 +155,11 @@ __device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int
 // One chunk: (mean less the group's origin, M2) of each unit, where M2 is the sum of
 // squared deviations from that mean.  Each thread takes its squares about its first row,
 // then moves them to the unit's mean.
+//
+// By chunks x is read twice: 6 x 11264 x 256 binary32 (69 MB) takes 22 us here and 26 us in
+// gn_apply_kernel, 47 us a call (floor 27 us), the second read coming in part from cache.
+// Rows of 256 bytes to a slab and 16 rows to a thread; with a slab per group (32 bytes of a
+// row) held in LDS and read once it took 62 us, since an image has too few workgroups.
 template <typename T, int V>
 __global__ __launch_bounds__(kGnThreads) void gn_stats_kernel(GnArgs a) {
     __shared__ float red[kGnThreads * V];
@@ -276,7 +285,8 @@ __global__ __launch_bounds__(kGnThreads) void gn_apply_kernel(GnArgs a) {
     const int n = blockIdx.x / a.slabs / a.chunks;
     const Slab b = slab_of<V>(a, s, kGnThreads);
     // every workgroup joins the chunks of its groups itself: a launch less, and with others to
-    // run meanwhile the wait for them is hidden
+    // run meanwhile the wait for them is hidden (by one wave to a group, one after the other,
+    // it took longer than the normalisation; by runs of lanes it is not seen)
     const int ngroups = a.upg == 1 ? b.nunits : 1;
     join_stats(a, n, b.g0, ngroups, gm, gr);
     if (chunk == 0 && (a.upg == 1 || s % a.upg == 0)) {
@@ -535,7 +545,10 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int6
 // Where a slab of one image fits the registers of a workgroup, it is read once, its
 // statistics are formed there and it is normalised and written from there: the floor of
 // traffic, one launch.  Consecutive slabs go to one XCD, whose L2 then holds the 128-byte
-// lines that two slabs share.
+// lines that two slabs share.  64 x 3136 x 128 bfloat16 (103 MB in and out) takes 32 us, 3.2
+// TB/s: each compute unit has one workgroup, which reads, then computes, then writes, and no
+// other fills the gaps (a copy of as much takes 20 us, the two passes by chunks 45 us).  Small
+// maps are bound by the launch: 6 x 176 x 256 binary32 takes 6.6 us.
 __device__ __forceinline__ int xcd_run(int id, int total) {
     const int x = id % 8, i = id / 8;
     return x * (total / 8) + min(x, total % 8) + i;
@@ -622,7 +635,11 @@ __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
 }
 
 // The same for the gradients (grad_out of x's type): dz stays in registers in binary32, so the
-// derivative of the activation is formed once.
+// derivative of the activation is formed once.  64 x 784 x 256 bfloat16 with SiLU (77 MB in and
+// out) takes 31 us and 3.5 us for the channels' sums behind it (floor 15 us); as in the
+// forward a compute unit reads, computes and writes by turns, by chunks it took 70 us.  Where
+// no slab fits, 3 x 1665 x 96 binary16 (2.9 MB) takes 16 us by chunks: 9.4 and 7.5 us of two
+// launches of 60 workgroups, whose loads, joins and exchanges follow one another.
 template <typename T, int V, int NV>
 __global__ __launch_bounds__(kGnWholeBwdThreads) void gn_bwd_whole_kernel(GnArgs a) {
     __shared__ float ra[kGnWholeBwdThreads * V], rb[kGnWholeBwdThreads * V];

@@ -168,6 +168,8 @@ struct NormCoef {
     }
 };
 
+// Rows to codes and scales in memory: for a caller, and before the kernels that read codes.
+// Bound by memory, and by its own latency for few rows (1237 x 1000 bfloat16, 3.7 MB: 4.3 us).
 // L lanes to a row, 64 / L rows to a wave; a row's first HOLD pieces per lane stay in
 // registers, what is past them is read again.  Behind a norm L is 64, and a wave has up to 8
 // consecutive rows of one image, for which it keeps the coefficients of the pieces held.
@@ -395,6 +397,14 @@ __device__ __forceinline__ void finish(const I8Args& a, int64_t m, int n, const 
 // wave waits for another, and the next rows are on their way while these are multiplied.
 // x is read once per slice (the second time from cache), out is written once, and no codes
 // go through memory.
+//
+// Memory bounds it where rows are many: 200704 x 128 x 108 from bfloat16 into binary32 (138
+// MB) takes 32 us, 4.3 TB/s (a copy of as much 27 us).  900 x 256 x 2496 codes take 8.8 us:
+// a launch, the fill of LDS and the first rows are waited for before the first product.  Behind
+// a norm 50176 x 256 x 216 takes 26 us and the statistics 9 us; by their instructions 12.8
+// million activations and codes are some 11 us, and with one unit of rows to a wave nothing
+// overlaps its loads and stores but the other workgroup of the compute unit.  That takes 128
+// registers: with 256, and half the waves, the call was 39.5 us in place of 35.4.
 
 constexpr int kRowsThreads = 512;
 constexpr int kRowsWaves = kRowsThreads / kWave;
@@ -515,7 +525,8 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
             for (int kc = 0; kc < KT; ++kc) x[kc] = q[kc][0].q;
         } else {
             // normalised numbers are kept between the two steps; the barriers to the scheduler
-            // keep the runs of 64 columns from being unpacked all at once
+            // keep the numbers from being worked on all at once (four at a time behind a norm:
+            // 11 registers spilled where 16 at a time spilled 41)
             float z[KT][16];
             uint32_t big = 0;
 #pragma unroll
@@ -528,15 +539,18 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
                         const f32x4 m4 = *reinterpret_cast<const f32x4*>(mu + c + e);
                         const f32x4 s4 = *reinterpret_cast<const f32x4*>(sc + c + e);
                         const f32x4 b4 = *reinterpret_cast<const f32x4*>(bi + c + e);
+                        float y[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            z[kc][e + i] = fmaf(z[kc][e + i] - m4[i], s4[i], b4[i]);
-                    }
-                    activate(z[kc], g.act);
+                            y[i] = fmaf(z[kc][e + i] - m4[i], s4[i], b4[i]);
+                        activate(y, g.act);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        big = max(big, __float_as_uint(z[kc][e]) & 0x7fffffffu);
-                    __builtin_amdgcn_sched_barrier(0);
+                        for (int i = 0; i < 4; ++i) {
+                            z[kc][e + i] = y[i];
+                            big = max(big, __float_as_uint(y[i]) & 0x7fffffffu);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 } else {
                     big = max(big, max(q[kc][0].magnitude(), q[kc][1].magnitude()));
                 }
@@ -589,11 +603,14 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
             }
         }
         if (a.staged) {
-            // the unit's rows are one run of memory: lines are written whole
+            // the unit's rows are one run of memory: lines are written whole.  The wave's own LDS
+            // accesses complete in order; the fences keep the compiler to it.
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
             for (int p = lane * 16; p < rows * a.N * ob; p += kWave * 16)
                 __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(stage + p),
                                                        outr, (uint32_t)p, 0, 0);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }
     }
@@ -604,7 +621,9 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
 // Few rows, 16 * MT at a time: a wave takes 16 output channels and every KW-th run of 64 columns,
 // the weights going from memory into operand registers, several runs in flight; the KW
 // waves' sums meet in LDS.  The rows' codes come from memory (XB 0), or the workgroup
-// quantises up to 16 rows of x into LDS first.
+// quantises up to 16 rows of x into LDS first.  One row of 4096 by 4096 x 4096 codes takes 7.4
+// us, 2.3 TB/s of weights (floor 3.2 us): the launch, the row's scale and the sums' meeting are
+// waited for one after the other; the first weights are on their way before the row is read.
 
 constexpr int kSkinnyThreads = 512;
 constexpr int kSkinnyWaves = kSkinnyThreads / kWave;
@@ -761,7 +780,9 @@ __global__ __launch_bounds__(kSkinnyThreads) void i8_skinny_kernel(I8Args a, int
 // ---- tiled product -----------------------------------------------------------------------
 //
 // 64 rows by 64 output channels to a workgroup of four waves, 128 columns at a time through
-// LDS, the next 128 on their way to registers meanwhile.  A 16-byte piece p of an LDS row r sits at place
+// LDS, the next 128 on their way to registers meanwhile.  For products too small to fill the
+// chip with larger tiles, so bound by a tile's walk along its columns (0.65 us per 128): 1237 x
+// 1000 x 777 takes 11.5 us, 12544 x 512 x 432 with its quantisation 24 us.  A 16-byte piece p of an LDS row r sits at place
 // p ^ (r / 2 % 8): the 16 rows an operand is read from then fall into different banks.
 
 constexpr int kTileK = 128, kTile = 64, kTileThreads = 256;
@@ -883,7 +904,10 @@ __global__ __launch_bounds__(kTileThreads) void i8_tile_kernel(I8Args a) {
 // ---- large products ----------------------------------------------------------------------
 //
 // 256 rows by 256 output channels to a workgroup of eight waves, 128 x 64 to a wave, columns
-// in whole runs of 128.  The next 128 columns go from memory straight into the other half of
+// in whole runs of 128.  8192 x 4096 x 4096 takes 128 us into the same result each time, 140 to
+// 150 us with operands and results in rotation: 1.8 to 2.1 POP/s, bound by the matrix cores (the
+// library's 8-bit product without scales reaches 2.1).  Tiles of 64 took 200 us; a grid of as many workgroups as are
+// resident, each with several tiles, spilled and was slower.  The next 128 columns go from memory straight into the other half of
 // LDS while these are multiplied, and a run's operands are read while the run before it is
 // in the matrix cores.  An instruction that fills LDS puts lane l's 16 bytes at place l of a
 // run of 1 KB, so the swizzle of the tiled kernel is in the addresses the lanes fetch from.

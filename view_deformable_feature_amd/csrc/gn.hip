@@ -547,7 +547,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int6
 // traffic, one launch.  Consecutive slabs go to one XCD, whose L2 then holds the 128-byte
 // lines that two slabs share.  64 x 3136 x 128 bfloat16 (103 MB in and out) takes 32 us, 3.2
 // TB/s: each compute unit has one workgroup, which reads, then computes, then writes, and no
-// other fills the gaps (a copy of as much takes 20 us, the two passes by chunks 45 us).  Small
+// other fills the gaps (a copy of as much takes 20 us).  Small
 // maps are bound by the launch: 6 x 176 x 256 binary32 takes 6.6 us.
 __device__ __forceinline__ int xcd_run(int id, int total) {
     const int x = id % 8, i = id / 8;
@@ -637,7 +637,7 @@ __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
 // The same for the gradients (grad_out of x's type): dz stays in registers in binary32, so the
 // derivative of the activation is formed once.  64 x 784 x 256 bfloat16 with SiLU (77 MB in and
 // out) takes 31 us and 3.5 us for the channels' sums behind it (floor 15 us); as in the
-// forward a compute unit reads, computes and writes by turns, by chunks it took 70 us.  Where
+// forward a compute unit reads, computes and writes by turns.  Where
 // no slab fits, 3 x 1665 x 96 binary16 (2.9 MB) takes 16 us by chunks: 9.4 and 7.5 us of two
 // launches of 60 workgroups, whose loads, joins and exchanges follow one another.
 template <typename T, int V, int NV>

@@ -56,11 +56,18 @@ uint64_t part_bytes(uint64_t n) { return (n + 255) & ~uint64_t(255); }
 
 // The layout of an image's slab in one workgroup of up to `threads` threads, `most` vectors
 // to a thread; false where none fits.  Of the widths that fit, the widest that leaves a
-// workgroup for every compute unit, else the narrowest of at least 64 bytes of a row.
+// workgroup for every compute unit, else the narrowest of at least 64 bytes of a row.  Measured
+// (us in a captured graph, whole slabs and by chunks): 64 x 784 x 256 bfloat16 forward 18 and
+// 40, backward 33 and 70; 6 x 176 x 256 binary32 6.7 and 10.5, 8.6 and 10.6; 1 x 196 x 512
+// binary16 6.2 and 13, 9.0 and 15.7.  Small maps of few rows may go by 16 and 32 bytes, for
+// more workgroups: 2 x 784 x 256 bfloat16 takes 7.0 so and 9.5 by 64 bytes; but each row is a
+// line fetched for a piece of it, and 2 x 4096 x 64 bfloat16 takes 12.1 (chunks 12.4), 2 x 8192
+// x 64 17.5 (12.8); backward, with half the threads, 2 x 2048 x 64 12.7 (14.7) and 2 x 4096 x 64
+// 16.7 (14.7).
 bool lay_out_whole(const gn_problem* p, int vec, int threads, int most, da::GnArgs& a) {
     const int64_t C = p->channels, elem = elem_bytes(p->x_dtype);
     const int64_t base = std::lcm(C / p->groups, (int64_t)vec);
-    const bool small = p->batch * p->rows * C * elem <= (4 << 20);
+    const bool small = p->batch * p->rows * C * elem <= (4 << 20) && p->rows <= 4 * threads;
     const auto vectors = [&](int64_t width, int t) {
         const int64_t R = t / (width / vec);
         return R ? (p->rows + R - 1) / R : INT64_MAX;
@@ -125,11 +132,14 @@ void lay_out(const gn_problem* p, int vec, Keeps keeps, da::GnArgs& a) {
         a.upg = (int32_t)((cpg + a.cpu - 1) / a.cpu);
         a.slabs = a.units = a.G * a.upg;
     }
-    // row chunks: 16 rows to a thread, fewer where that leaves too few workgroups
+    // row chunks: 16 rows to a thread, fewer where that leaves less than two workgroups to a
+    // compute unit.  More chunks than that cost more in every workgroup's join than they bring:
+    // with eight to a compute unit 64 x 3136 x 128 bfloat16 took 172 us backward (79), 1 x
+    // 40000 x 256 71 forward (37).
     const int64_t R = std::max<int64_t>(1, da::kGnThreads / (a.slab_ch / vec));
     int64_t per_thread = 16;
     while (per_thread > 4 &&
-           (int64_t)a.N * a.slabs * ((a.S + R * per_thread - 1) / (R * per_thread)) < 2048)
+           (int64_t)a.N * a.slabs * ((a.S + R * per_thread - 1) / (R * per_thread)) < 512)
         per_thread /= 2;
     int64_t rows = R * per_thread;
     constexpr int64_t kMaxChunks = 1024;   // read again by every workgroup of the image

@@ -1087,9 +1087,12 @@ hipError_t launch_skinny(const I8Args& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// A product that fills the compute units with 256 x 256 tiles
+// A product with a 256 x 256 tile for every other compute unit or more (us, against 64 x 64 tiles):
+// 4096 x 1024 x 4096, 256 tiles, takes 30.5 (47.6); 1024 x 4096 x 8192, 128 tiles, 56 (71); 1792 x
+// 4096 x 4096, 112 tiles, 55 (66), but 1792 x 1024 x 4096 24.5 (24.2) and 1536 x 512 x 4096, 96
+// tiles, 18.6 (15.1).
 bool big(int64_t M, int64_t K, int64_t N) {
-    return (M + 255) / 256 * ((N + 255) / 256) >= 200 && K % kTileK == 0 && N < (1 << 20);
+    return (M + 255) / 256 * ((N + 255) / 256) >= 128 && K % kTileK == 0 && N < (1 << 20);
 }
 
 hipError_t launch_tiles(const I8Args& a, hipStream_t stream) {

@@ -169,7 +169,7 @@ struct NormCoef {
 };
 
 // Rows to codes and scales in memory: for a caller, and before the kernels that read codes.
-// Bound by memory, and by its own latency for few rows (1237 x 1000 bfloat16, 3.7 MB: 4.3 us).
+// Bound by memory, and by its own latency for few rows (1237 x 1000 of 16 bits, 3.7 MB: 4.3 us).
 // L lanes to a row, 64 / L rows to a wave; a row's first HOLD pieces per lane stay in
 // registers, what is past them is read again.  Behind a norm L is 64, and a wave has up to 8
 // consecutive rows of one image, for which it keeps the coefficients of the pieces held.

@@ -38,6 +38,12 @@ SHAPES = {
     "level_8x22": (6, 176, 256, 8),
     "stage_28x28": (3, 784, 256, 32),
     "level_64x176": (1, 11264, 256, 32),
+    "stage_56x56": (4, 3136, 128, 32),
+    # slabs of less than 64 bytes of a row: the most rows (forward 4096, backward 2048), one more
+    "narrow_2048": (1, 2048, 64, 8),
+    "narrow_2049": (1, 2049, 64, 8),
+    "narrow_4096": (2, 4096, 64, 8),
+    "narrow_4097": (2, 4097, 64, 8),
 }
 
 

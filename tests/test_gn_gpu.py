@@ -10,7 +10,7 @@ import torch
 
 import view_deformable_feature_amd as vdf
 from gpu_helpers import say
-from norm_int8_reference import HALF, Norm, check, rounded
+from norm_int8_reference import HALF, U, Norm, check, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -373,3 +373,24 @@ def test_more_values_than_32_bits_count():
                                grad_x=out)
     torch.cuda.synchronize()
     assert gx[1, -1].isfinite().all() and gx[1, -1].abs().max() > 0
+
+
+@pytest.mark.parametrize("shape, dtype", [((6, 176, 256, 8), F32), ((2, 784, 256, 32), BF16),
+                                          ((1, 196, 512, 32), F16), ((2, 4095, 64, 8), F32)])
+def test_mean_far_from_the_first_value(shape, dtype):
+    """Each group's first value is 1000, all others are whole numbers below 8, constant along
+    the rows.  Differences from the first value are whole numbers and a thread's sums of them are
+    exact, but for the thread (at most 16 rows, 8 channels) that holds it: its mean of that
+    channel is off by 2 u 1000, its sum over channels and that times its rows by u 8000 each.
+    Joined in 64 bits and rounded once, the mean is off by u |mean| and that thread's share of the
+    group; a join in 32 bits would round a number of the size of 1000."""
+    N, S, C, G = shape
+    x = (torch.arange(C) * 7 % 8).float().expand(N, S, C).clone()
+    x[:, 0, ::C // G] = 1000.0
+    x = x.to(dtype).cuda()
+    _, mean, rstd = vdf.gn_forward(x, G, None, None, EPS)
+    torch.cuda.synchronize()
+    ref = Norm(x, G, None, None, EPS, "none")
+    share = 18000.0 * 16 / (S * C // G)
+    check("mean", mean, ref.mean, U * (ref.mean.abs() + share))
+    check("rstd", rstd, ref.rstd, ref.stat_tols()[1])

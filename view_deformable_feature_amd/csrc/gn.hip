@@ -50,19 +50,21 @@ __device__ __forceinline__ Slab slab_of(const GnArgs& a, int s, int threads) {
 }
 
 // out[u] = factor * the sum of red[r * cols + j] over r < R and the `per` columns of unit u,
-// by one wave per unit.  Every thread of the workgroup calls it; red is complete on entry, out
-// on return.
+// by one wave per unit.  The threads' binary32 sums meet in binary64: a few additions a lane.
+// Every thread of the workgroup calls it; red is complete on entry, out on return.
+template <typename M>
 __device__ __forceinline__ void unit_sums(const float* red, int R, int cols, int per, int nunits,
-                                          float factor, float* out) {
+                                          double factor, M* out) {
     const int lane = threadIdx.x & (kWave - 1), nw = blockDim.x / kWave;
     for (int u = threadIdx.x / kWave; u < nunits; u += nw) {
-        float t = 0.0f;
+        double t = 0.0;
         for (int e = lane; e < R * per; e += kWave) {
             const int r = e / per, j = e - r * per;
             t += red[r * cols + u * per + j];
         }
+#pragma unroll 1   // unrolled it takes registers that the callers keep their rows in
         for (int m = kWave / 2; m; m >>= 1) t += __shfl_xor(t, m);
-        if (lane == 0) out[u] = t * factor;
+        if (lane == 0) out[u] = (M)(t * factor);
     }
     __syncthreads();
 }
@@ -92,21 +94,25 @@ __device__ __forceinline__ float rstd_of(double var, float eps) {
     return var < 0x1p127 ? (float)(1.0 / sqrt(var + (double)eps)) : __uint_as_float(0x7fc00000u);
 }
 
-// A workgroup's statistics from its threads': each of cnt rows of V channels, with the sums
+// A workgroup's statistics from its threads' (share: 1 over the number of a unit's values):
+// each of cnt rows of V channels, with the sums
 // of their differences from `first` and of those differences' squares, taken about that
 // value so that a large common offset cancels before anything is rounded.  Leaves in um
 // the units' means less the group's origin, in uq their sums of squared deviations from that
-// mean.  red holds one value per thread where a vector lies in one unit, else V.
-template <int V>
-__device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int n, float rows,
+// mean: in binary64 where the group's statistics are made from them at once (a difference
+// from an origin that is far from the mean, rounded to binary32, would be the mean's error), in
+// binary32 where they are one chunk's of many.  red holds one value per thread where a vector
+// lies in one unit, else V.
+template <int V, typename M>
+__device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int n, double share,
                                              int cnt, const float (&first)[V],
                                              const float (&sum)[V], const float (&sq)[V],
-                                             float* red, float* um, float* uq) {
+                                             float* red, M* um, M* uq) {
     const int per_ch = a.upg == 1 ? a.cpg : b.width;
     const bool whole = per_ch % V == 0;
     const int cols = whole ? b.cols : b.width, per = whole ? per_ch / V : per_ch;
-    const float rc = cnt ? 1.0f / cnt : 0.0f, inv = 1.0f / (rows * per_ch);
-    float m[V];   // this thread's channel means, less the origin
+    const float rc = cnt ? 1.0f / cnt : 0.0f;
+    float m[V], dev[V];   // this thread's channel means, less the origin; squares about them
     int u[V];
     units_of(b, per_ch, u);
     float origin = origin_of(a, n, b.g0 + u[0]);
@@ -114,6 +120,8 @@ __device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int
     for (int e = 0; e < V; ++e) {
         if (!whole) origin = origin_of(a, n, b.g0 + u[e]);
         m[e] = (first[e] - origin) + sum[e] * rc;
+        // sum of squares about m is sq - sum^2 / cnt, below zero by rounding alone; a NaN stays
+        dev[e] = sq[e] - sum[e] * sum[e] * rc;
     }
     if (b.r < b.R) {
         if (whole) {
@@ -127,15 +135,13 @@ __device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int
         }
     }
     __syncthreads();
-    unit_sums(red, b.R, cols, per, b.nunits, inv, um);
-    float dev[V], mean = um[u[0]];
+    unit_sums(red, b.R, cols, per, b.nunits, share, um);
+    float mean = (float)um[u[0]];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        if (!whole) mean = um[u[e]];
+        if (!whole) mean = (float)um[u[e]];
         const float d = m[e] - mean;
-        // sum of squares about m is sq - sum^2 / cnt, below zero by rounding alone; a NaN stays
-        const float t = sq[e] - sum[e] * sum[e] * rc;
-        dev[e] = cnt ? (t < 0.0f ? 0.0f : t) + cnt * d * d : 0.0f;
+        dev[e] = cnt ? (dev[e] < 0.0f ? 0.0f : dev[e]) + cnt * d * d : 0.0f;
     }
     if (b.r < b.R) {
         if (whole) {
@@ -149,7 +155,7 @@ __device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int
         }
     }
     __syncthreads();
-    unit_sums(red, b.R, cols, per, b.nunits, 1.0f, uq);
+    unit_sums(red, b.R, cols, per, b.nunits, 1.0, uq);
 }
 
 // One chunk: (mean less the group's origin, M2) of each unit, where M2 is the sum of
@@ -199,7 +205,8 @@ __global__ __launch_bounds__(kGnThreads) void gn_stats_kernel(GnArgs a) {
                 }
         }
     }
-    join_threads(a, b, n, (float)(r1 - r0), cnt, first, sum, sq, red, um, uq);
+    const double share = 1.0 / ((double)(r1 - r0) * (a.upg == 1 ? a.cpg : b.width));
+    join_threads(a, b, n, share, cnt, first, sum, sq, red, um, uq);
     float2* part = a.unit_part + ((int64_t)n * a.chunks + chunk) * a.units + b.unit0;
     for (int u = threadIdx.x; u < b.nunits; u += kGnThreads) {
         part[u] = make_float2(um[u], uq[u]);
@@ -420,8 +427,8 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_stats_kernel(GnArgs a) {
     }
     __syncthreads();
     const int per = a.upg == 1 ? a.cpg : b.width;
-    unit_sums(ra, 1, b.width, per, b.nunits, 1.0f, ua);
-    unit_sums(rb, 1, b.width, per, b.nunits, 1.0f, ub);
+    unit_sums(ra, 1, b.width, per, b.nunits, 1.0, ua);
+    unit_sums(rb, 1, b.width, per, b.nunits, 1.0, ub);
     float2* up = a.unit_part + ((int64_t)n * a.chunks + chunk) * a.units + b.unit0;
     for (int u = threadIdx.x; u < b.nunits; u += kGnThreads) up[u] = make_float2(ua[u], ub[u]);
 }
@@ -545,7 +552,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int6
 // Where a slab of one image fits the registers of a workgroup, it is read once, its
 // statistics are formed there and it is normalised and written from there: the floor of
 // traffic, one launch.  Consecutive slabs go to one XCD, whose L2 then holds the 128-byte
-// lines that two slabs share.  64 x 3136 x 128 bfloat16 (103 MB in and out) takes 32 us, 3.2
+// lines that two slabs share.  64 x 3136 x 128 bfloat16 (103 MB in and out) takes 30 us, 3.4
 // TB/s: each compute unit has one workgroup, which reads, then computes, then writes, and no
 // other fills the gaps (a copy of as much takes 20 us).  Small
 // maps are bound by the launch: 6 x 176 x 256 binary32 takes 6.6 us.
@@ -557,7 +564,8 @@ __device__ __forceinline__ int xcd_run(int id, int total) {
 template <typename T, int V, int NV, bool STORE>
 __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
     __shared__ float red[kGnWholeThreads * V];
-    __shared__ float um[kGnWholeThreads], uq[kGnWholeThreads];
+    __shared__ double um[kGnWholeUnits], uq[kGnWholeUnits];
+    __shared__ float gm[kGnWholeUnits], gr[kGnWholeUnits];
     const int id = xcd_run(blockIdx.x, a.N * a.slabs);
     const int n = id / a.slabs, s = id - n * a.slabs;
     const Slab b = slab_of<V>(a, s, blockDim.x);
@@ -592,13 +600,12 @@ __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
         if (b.r + i * b.R < S) count(q[i]);
 #pragma unroll
     for (int i = 0; i < NV; ++i) q[i].forget();
-    join_threads(a, b, n, (float)a.S, cnt, first, sum, sq, red, um, uq);
+    join_threads(a, b, n, a.share, cnt, first, sum, sq, red, um, uq);
     for (int u = threadIdx.x; u < b.nunits; u += blockDim.x) {
-        const float var = uq[u] / ((float)a.S * a.cpg);
-        um[u] = um[u] + origin_of(a, n, b.g0 + u);
-        uq[u] = rstd_of(var, a.eps);
-        if (a.mean) a.mean[(int64_t)n * a.G + b.g0 + u] = um[u];
-        if (a.rstd) a.rstd[(int64_t)n * a.G + b.g0 + u] = uq[u];
+        gm[u] = (float)(um[u] + (double)origin_of(a, n, b.g0 + u));
+        gr[u] = rstd_of(uq[u] * a.share, a.eps);
+        if (a.mean) a.mean[(int64_t)n * a.G + b.g0 + u] = gm[u];
+        if (a.rstd) a.rstd[(int64_t)n * a.G + b.g0 + u] = gr[u];
     }
     if constexpr (STORE) {
         __syncthreads();
@@ -608,8 +615,8 @@ __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const int c = b.v * V + e;
-            mu[e] = um[u[e]];
-            sc[e] = uq[u[e]] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
+            mu[e] = gm[u[e]];
+            sc[e] = gr[u[e]] * (a.weight ? a.weight[b.ch0 + c] : 1.0f);
             bi[e] = a.bias ? a.bias[b.ch0 + c] : 0.0f;
         }
         const auto write = [&](auto act, auto same) {
@@ -643,7 +650,7 @@ __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
 template <typename T, int V, int NV>
 __global__ __launch_bounds__(kGnWholeBwdThreads) void gn_bwd_whole_kernel(GnArgs a) {
     __shared__ float ra[kGnWholeBwdThreads * V], rb[kGnWholeBwdThreads * V];
-    __shared__ float ua[kGnWholeBwdThreads], ub[kGnWholeBwdThreads];
+    __shared__ float ua[kGnWholeUnits], ub[kGnWholeUnits];
     const int id = xcd_run(blockIdx.x, a.N * a.slabs);
     const int n = id / a.slabs, s = id - n * a.slabs;
     const Slab b = slab_of<V>(a, s, blockDim.x);
@@ -713,9 +720,8 @@ __global__ __launch_bounds__(kGnWholeBwdThreads) void gn_bwd_whole_kernel(GnArgs
     }
     if (!a.grad_x) return;
     __syncthreads();
-    const float inv = 1.0f / ((float)a.S * a.cpg);
-    unit_sums(ra, 1, b.width, a.cpg, b.nunits, inv, ua);
-    unit_sums(rb, 1, b.width, a.cpg, b.nunits, inv, ub);
+    unit_sums(ra, 1, b.width, a.cpg, b.nunits, a.share, ua);
+    unit_sums(rb, 1, b.width, a.cpg, b.nunits, a.share, ub);
     // rstd * (w dz - m1 - xhat m2) as two multiply-adds
     float mu[V], k1[V], k2[V], k3[V];
 #pragma unroll

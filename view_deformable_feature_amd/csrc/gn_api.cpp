@@ -74,7 +74,7 @@ bool lay_out_whole(const gn_problem* p, int vec, int threads, int most, da::GnAr
     };
     int64_t width = 0;
     for (int64_t w = base; w <= C && (w == base || w * elem <= 256); w *= 2) {
-        if (vectors(w, threads) > most) break;
+        if (vectors(w, threads) > most || w / (C / p->groups) > da::kGnWholeUnits) break;
         if (w < C && w * elem < 64 && !small) continue;
         if (width && p->batch * ((C + w - 1) / w) < 256) break;
         width = w;
@@ -112,6 +112,7 @@ void lay_out(const gn_problem* p, int vec, Keeps keeps, da::GnArgs& a) {
     a.C = (int32_t)C;
     a.G = (int32_t)p->groups;
     a.cpg = (int32_t)cpg;
+    a.share = 1.0 / ((double)a.S * (double)cpg);
     a.act = p->activation;
     a.x_dtype = p->x_dtype;
     a.out_dtype = p->out_dtype;

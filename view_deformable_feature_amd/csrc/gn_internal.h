@@ -23,6 +23,8 @@ constexpr int kGnThreads = 256;
 // of x and 64 of dz (with 1024 threads it spilled 45 of them at half as many vectors).
 constexpr int kGnWholeThreads = 1024, kGnWholeVecs = 16;
 constexpr int kGnWholeBwdThreads = 512, kGnWholeBwdVecs = 8;
+// Groups of such a slab: of one channel each, 256 bytes of a row hold the most.
+constexpr int kGnWholeUnits = 128;
 
 struct GnArgs {
     const void* x;            // [N, S, C] of x_dtype
@@ -41,6 +43,7 @@ struct GnArgs {
     float2* chan_part;        // backward: [N, chunks, C] sums of dz and dz * xhat
     int64_t S;
     int64_t rows_per_chunk;
+    double share;             // 1 / (S * cpg), the weight of a value in its group's averages
     int32_t N, C, G, cpg;
     int32_t slab_ch, slabs;
     int32_t upg, cpu, units;

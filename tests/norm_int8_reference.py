@@ -151,3 +151,18 @@ def check(what, got, ref, tol):
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} beyond their bound, the worst "
                              f"{float(worst):.3g} times it; first at {i}: {float(got[i])} for "
                              f"{float(ref[i])} +- {float(tol.expand_as(ref)[i]):.3g}")
+
+
+def gelu_tols(z):
+    """Bounds of GELU and of its derivative in binary32 at exactly known z [64 bits].  Phi's own is
+    (24 + 2 z^2) u of itself (act_device.h): 1 of the polynomial, 3 of its argument (a multiply-
+    add and the hardware's reciprocal) times 2.8, by which f changes with t at the most, 2 for
+    each rounding of the sum, which its last terms carry, 2 of the exponential and 3 of the
+    products; z^2 for z * z / 2, z^2 for its factor log2(e), twice rounded.  GELU adds the product
+    with z, the density half of the exponential's and two products."""
+    phi = 0.5 * torch.special.erfc(-z * math.sqrt(0.5))
+    density = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    rel = (24 + 2 * z * z) * U
+    return ((rel + U) * (z * phi).abs() + 2.0 ** -149,
+            rel * phi + (rel + 4 * U) * (z * density).abs() + 2 * U * act_grad(z, "gelu").abs()
+            + 2.0 ** -149)

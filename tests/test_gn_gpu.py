@@ -10,7 +10,7 @@ import torch
 
 import view_deformable_feature_amd as vdf
 from gpu_helpers import say
-from norm_int8_reference import HALF, U, Norm, check, rounded
+from norm_int8_reference import HALF, U, Norm, act_grad, check, gelu_tols, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -394,3 +394,15 @@ def test_mean_far_from_the_first_value(shape, dtype):
     share = 18000.0 * 16 / (S * C // G)
     check("mean", mean, ref.mean, U * (ref.mean.abs() + share))
     check("rstd", rstd, ref.rstd, ref.stat_tols()[1])
+
+
+def test_gelu_derivative_in_the_lower_tail():
+    """z = x exactly (mean 0, rstd 1 given, one row): grad_bias is the derivative, by whole slabs
+    and, with another type of grad_out, by chunks."""
+    z = (torch.arange(256) - 128).float() / 16
+    x, one = z.view(1, 1, 256).cuda(), torch.ones((1, 1), device="cuda")
+    for dtype in (F32, BF16):
+        dy = torch.ones((1, 1, 256), device="cuda", dtype=dtype)
+        _, _, db = vdf.gn_backward(x, dy, 0 * one, one, 1, None, None, "gelu")
+        torch.cuda.synchronize()
+        check("grad_bias", db, act_grad(z.double(), "gelu"), gelu_tols(z.double())[1])

@@ -8,7 +8,7 @@ import torch
 
 import view_deformable_feature_amd as vdf
 from gpu_helpers import say
-from norm_int8_reference import U, Norm, act, check, codes, product, rounded
+from norm_int8_reference import U, Norm, act, check, codes, gelu_tols, product, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -372,3 +372,19 @@ def test_more_values_than_32_bits_count():
     torch.cuda.synchronize()
     assert torch.equal(out[-1000:], last)
     assert torch.equal(q[-1000:], ql) and torch.equal(s[-1000:], sl)
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_gelu_keeps_its_digits_in_the_lower_tail(M):
+    """z = k / 16 exactly, from -7.94 to 7.94, of one code times one weight: K = 1 and, of rows
+    that are zero but for one column, 300."""
+    for K in (1, 300):
+        a = torch.zeros((M, K), dtype=torch.int8, device="cuda")
+        a[:, 0] = 1
+        w = torch.zeros((255, K), dtype=torch.int8, device="cuda")
+        w[:, 0] = torch.arange(-127, 128, device="cuda")
+        out = vdf.i8_matmul(a, torch.full((M,), 0.25, device="cuda"), w,
+                            torch.full((255,), 0.25, device="cuda"), activation="gelu")
+        torch.cuda.synchronize()
+        z = (torch.arange(-127, 128).double() / 16).expand(M, 255)
+        check("out", out, act(z, "gelu"), gelu_tols(z)[0])

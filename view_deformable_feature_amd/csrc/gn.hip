@@ -552,7 +552,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int6
 // Where a slab of one image fits the registers of a workgroup, it is read once, its
 // statistics are formed there and it is normalised and written from there: the floor of
 // traffic, one launch.  Consecutive slabs go to one XCD, whose L2 then holds the 128-byte
-// lines that two slabs share.  64 x 3136 x 128 bfloat16 (103 MB in and out) takes 30 us, 3.4
+// lines that two slabs share.  64 x 3136 x 128 bfloat16 (103 MB in and out) takes 31 us, 3.3
 // TB/s: each compute unit has one workgroup, which reads, then computes, then writes, and no
 // other fills the gaps (a copy of as much takes 20 us).  Small
 // maps are bound by the launch: 6 x 176 x 256 binary32 takes 6.6 us.

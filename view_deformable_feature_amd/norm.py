@@ -4,7 +4,7 @@
 Maps are channels last, [N, ..., C] with any number of dimensions between (they are the
 rows of an image): the layout ``dcn_forward`` and the aggregation work in, so a
 normalisation between two of them copies nothing.  Activations go by name: "none", "relu",
-"silu", "gelu" (by the error function).
+"silu", "gelu" (z times the normal distribution function of z).
 
 Only metadata checks and pointer passing happen here; every step runs in the HIP
 kernels of libdeformagg.

@@ -388,3 +388,45 @@ def test_gelu_keeps_its_digits_in_the_lower_tail(M):
         torch.cuda.synchronize()
         z = (torch.arange(-127, 128).double() / 16).expand(M, 255)
         check("out", out, act(z, "gelu"), gelu_tols(z)[0])
+
+
+@pytest.mark.parametrize("M, K, N", [(3950, 384, 3990), (300, 520, 100), (300, 384, 129),
+                                     (100, 2048, 300), (20, 1000, 70), (40, 520, 33), (9, 300, 50)])
+def test_codes_off_alignment(M, K, N):
+    """Codes one byte into larger buffers, scales, bias and result one element: 256 x 256 tiles
+    (which take only aligned codes), 64 x 64 tiles and the streaming kernel at 16, 32 and 64 rows
+    a workgroup give what they give for aligned ones, bit for bit."""
+    say(f"[i8] off alignment {M} {K} {N}")
+
+    def shifted(t):
+        v = torch.empty(t.numel() + 1, device="cuda", dtype=t.dtype)[1:].view(t.shape)
+        return v.copy_(t)
+
+    a, s = _codes(M, K, 130)
+    w, ws, b = _layer(N, K, 131)
+    want = vdf.i8_matmul(a, s, w, ws, b, activation="silu")
+    x = _rows(M, K, BF16, 132)
+    linear = vdf.i8_linear(x, w, ws, b)
+    torch.cuda.synchronize()
+    ref, tol = product(a, s, w, ws, b, "silu")
+    check("aligned", want, ref, tol)
+    for ai, wi in ((shifted(a), w), (a, shifted(w)), (shifted(a), shifted(w))):
+        got = vdf.i8_matmul(ai, shifted(s), wi, shifted(ws), shifted(b), activation="silu",
+                            out=shifted(want).fill_(float("nan")))
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    got = vdf.i8_linear(shifted(x), shifted(w), shifted(ws), shifted(b))
+    half = vdf.i8_matmul(shifted(a), s, w, ws, b, activation="silu", out=shifted(want.half()))
+    torch.cuda.synchronize()
+    assert torch.equal(got, linear) and torch.equal(half, want.half())
+
+
+def test_norm_linear_with_weights_off_alignment():
+    """Behind a norm: 256 x 256 tiles' worth of rows with weights at an odd address."""
+    x = torch.randn((2, 16500, 384), device="cuda")
+    w, ws, b = _layer(256, 384, 133)
+    wv = torch.empty(256 * 384 + 1, device="cuda", dtype=torch.int8)[1:].view(256, 384).copy_(w)
+    want = vdf.i8_norm_linear(x, 8, None, None, w, ws, b, activation="silu")
+    got = vdf.i8_norm_linear(x, 8, None, None, wv, ws, b, activation="silu")
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

@@ -1090,16 +1090,19 @@ hipError_t launch_skinny(const I8Args& a, hipStream_t stream) {
 // A product with a 256 x 256 tile for every other compute unit or more (us, against 64 x 64 tiles):
 // 4096 x 1024 x 4096, 256 tiles, takes 30.5 (47.6); 1024 x 4096 x 8192, 128 tiles, 56 (71); 1792 x
 // 4096 x 4096, 112 tiles, 55 (66), but 1792 x 1024 x 4096 24.5 (24.2) and 1536 x 512 x 4096, 96
-// tiles, 18.6 (15.1).
-bool big(int64_t M, int64_t K, int64_t N) {
-    return (M + 255) / 256 * ((N + 255) / 256) >= 128 && K % kTileK == 0 && N < (1 << 20);
+// tiles, 18.6 (15.1).  Its 16-byte fills of LDS are for aligned addresses: codes that begin
+// elsewhere go by the smaller tiles, whose loads into registers may lie anywhere.
+bool big(const I8Args& a) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.w);
+    return (a.M + 255) / 256 * ((a.N + 255) / 256) >= 128 && a.K % kTileK == 0 && at % 16 == 0 &&
+           a.N < (1 << 20);
 }
 
 hipError_t launch_tiles(const I8Args& a, hipStream_t stream) {
     const auto blocks = [&](int t) {
         return (uint32_t)((a.M + t - 1) / t * ((a.N + t - 1) / t));
     };
-    if (big(a.M, a.K, a.N)) i8_big_kernel<<<blocks(kBigTile), kBigThreads, 0, stream>>>(a);
+    if (big(a)) i8_big_kernel<<<blocks(kBigTile), kBigThreads, 0, stream>>>(a);
     else i8_tile_kernel<<<blocks(kTile), kTileThreads, 0, stream>>>(a);
     return hipGetLastError();
 }

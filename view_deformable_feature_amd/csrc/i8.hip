@@ -252,6 +252,14 @@ __global__ __launch_bounds__(kQuantThreads) void i8_quantize_kernel(I8Args a, Gn
     }
 }
 
+// How many of a tile's `most` rows are left.  In whole numbers, so that the ranges of the buffer
+// resources that are made of it are scalars: HIP's min of 64-bit numbers goes by binary64, in
+// vector registers, and every access through such a resource then runs in a loop over the lanes'
+// values of it.
+__device__ __forceinline__ int rows_left(int64_t left, int most) {
+    return left < most ? (int)left : most;
+}
+
 // ---- pieces of the operands --------------------------------------------------------------
 
 // The 16 codes of row `row` of [.., K] from column k on (k < K), zeros past K.  Any alignment.
@@ -472,7 +480,7 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
     const int odd_part = odd_c % 64 / 16, odd_piece = odd_c % 16 / per;
     const auto fetch = [&](int64_t unit) {
         const int64_t m0 = base + unit * 16;
-        const int rows = (int)min<int64_t>(rows_end - m0, 16);
+        const int rows = rows_left(rows_end - m0, 16);
         const void* x = XB ? a.x : a.a;
         const auto r = make_rsrc(static_cast<const char*>(x) + m0 * a.K * xbytes,
                                  (uint32_t)(rows * a.K * xbytes));
@@ -518,7 +526,7 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
         i32x4 x[KT];
         float rs;
         const int64_t m0 = base + u * 16;
-        const int rows = (int)min<int64_t>(rows_end - m0, 16);
+        const int rows = rows_left(rows_end - m0, 16);
         if constexpr (XB == 0) {
             rs = col < rows ? a.a_scale[m0 + col] : 0.0f;
 #pragma unroll
@@ -636,13 +644,14 @@ __global__ __launch_bounds__(kSkinnyThreads) void i8_skinny_kernel(I8Args a, int
     __shared__ uint32_t bigs[16][kSkinnyWaves];
     __shared__ float scales[16];
     constexpr int kRuns = MT == 1 ? 8 : 4;   // of a wave in flight, in pairs of 128 columns
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int col = lane % 16, part = lane / 16;
     const int kw = wave % kw_count;
     const int tiles = (a.N + 15) / 16, runs = (a.K + 63) / 64;
     const int blocks = (tiles + kSkinnyWaves / kw_count - 1) / (kSkinnyWaves / kw_count);
     const int64_t m0 = (int64_t)(blockIdx.x / blocks) * (16 * MT);
-    const int rows = (int)min<int64_t>(a.M - m0, 16 * MT);
+    const int rows = rows_left(a.M - m0, 16 * MT);
     const int tile = blockIdx.x % blocks * (kSkinnyWaves / kw_count) + wave / kw_count;
     const int stride = runs * 64 + 16, step = kRuns * kw_count;
     const bool live = tile < tiles;
@@ -809,7 +818,7 @@ __global__ __launch_bounds__(kTileThreads) void i8_tile_kernel(I8Args a) {
     tile_of(blockIdx.x, mt, nt, tile_m, tile_n);
     const int64_t m0 = (int64_t)tile_m * kTile;
     const int n0 = tile_n * kTile;
-    const int rows = (int)min<int64_t>(a.M - m0, kTile), cols = min(a.N - n0, kTile);
+    const int rows = rows_left(a.M - m0, kTile), cols = min(a.N - n0, kTile);
 
     // A thread's pieces: rows `row` and row + 32 of either operand, at one place of theirs.
     // Whole pieces come through buffer resources whose ranges end with the block's last row,
@@ -929,7 +938,7 @@ __global__ __launch_bounds__(kBigThreads, 2) void i8_big_kernel(I8Args a) {
     tile_of(blockIdx.x, mt, nt, tile_m, tile_n);
     const int64_t m0 = (int64_t)tile_m * kBigTile;
     const int n0 = tile_n * kBigTile;
-    const int rows = (int)min<int64_t>(a.M - m0, kBigTile);
+    const int rows = rows_left(a.M - m0, kBigTile);
 
     const auto xr = make_rsrc(a.a + m0 * a.K, (uint32_t)rows * a.K);
     const auto wr = make_rsrc(a.w + (int64_t)n0 * a.K, (uint32_t)min(a.N - n0, kBigTile) * a.K);

@@ -383,10 +383,10 @@ __device__ __forceinline__ void scaled(const i32x4& acc, float row, const Column
 
 // out[m, n .. n + 3] from the sums, as far as n stays below N.
 __device__ __forceinline__ void finish(const I8Args& a, int64_t m, int n, const i32x4& acc,
-                                       float row, const ColumnScale& c) {
+                                       float row, const ColumnScale& c, int act) {
     float y[4];
     scaled(acc, row, c, y);
-    activate(y, a.act);
+    activate(y, act);
     const int64_t at = m * a.N + n;
     if (a.out_dtype == DA_BF16)
         store_four(static_cast<__bf16*>(a.out) + at, y, a.N - n);
@@ -607,7 +607,7 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
                 store_four(outr, out_at, (uint32_t)(t * 16 * ob), y, a.out_dtype);
             } else {   // the last tile, not all of it in the row
                 const int n = t * 16 + part * 4;
-                if (n < a.N && col < rows) finish(a, m0 + col, n, acc, rs, cs);
+                if (n < a.N && col < rows) finish(a, m0 + col, n, acc, rs, cs, a.act);
             }
         }
         if (a.staged) {
@@ -782,7 +782,8 @@ __global__ __launch_bounds__(kSkinnyThreads) void i8_skinny_kernel(I8Args a, int
         i32x4 t = meet[wave - kw][mt][lane];
         for (int i = 1; i < kw_count; ++i) t += meet[wave - kw + i][mt][lane];
         const int m = mt * 16 + col;
-        if (m < rows) finish(a, m0 + m, nn, t, XB != 0 ? scales[m] : a.a_scale[m0 + m], cs);
+        if (m < rows)
+            finish(a, m0 + m, nn, t, XB != 0 ? scales[m] : a.a_scale[m0 + m], cs, a.act);
     }
 }
 
@@ -905,7 +906,7 @@ __global__ __launch_bounds__(kTileThreads) void i8_tile_kernel(I8Args a) {
 #pragma unroll
         for (int i = 0; i < W / 16; ++i) {
             const int m = wm + i * 16 + col;
-            if (m < rows) finish(a, m0 + m, n, acc[i][j], rs[i], cs[j]);
+            if (m < rows) finish(a, m0 + m, n, acc[i][j], rs[i], cs[j], a.act);
         }
     }
 }
@@ -1020,23 +1021,27 @@ __global__ __launch_bounds__(kBigThreads, 2) void i8_big_kernel(I8Args a) {
         __builtin_memcpy(cs[j].s, &s.q, 16);
         __builtin_memcpy(cs[j].b, &b.q, 16);
     }
+    // the activation is chosen outside the loops: 32 places with every activation in them do not
+    // fit the instruction cache
+    with_activation(a.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < WM / 16; ++i) {
-        const int m = wm + i * 16 + col;
-        const uint32_t out_at = (uint32_t)((m * a.N + part * 4) * ob);
+        for (int i = 0; i < WM / 16; ++i) {
+            const int m = wm + i * 16 + col;
+            const uint32_t out_at = (uint32_t)((m * a.N + part * 4) * ob);
 #pragma unroll
-        for (int j = 0; j < WN / 16; ++j) {
-            const int nt0 = n0 + wn + j * 16;
-            if (nt0 + 16 <= a.N) {
-                float y[4];
-                scaled(acc[i][j], rs[i], cs[j], y);
-                activate(y, a.act);
-                store_four(outr, out_at, (uint32_t)(nt0 * ob), y, a.out_dtype);
-            } else if (nt0 + part * 4 < a.N && m < rows) {
-                finish(a, m0 + m, nt0 + part * 4, acc[i][j], rs[i], cs[j]);
+            for (int j = 0; j < WN / 16; ++j) {
+                const int nt0 = n0 + wn + j * 16;
+                if (nt0 + 16 <= a.N) {
+                    float y[4];
+                    scaled(acc[i][j], rs[i], cs[j], y);
+                    activate(y, act);
+                    store_four(outr, out_at, (uint32_t)(nt0 * ob), y, a.out_dtype);
+                } else if (nt0 + part * 4 < a.N && m < rows) {
+                    finish(a, m0 + m, nt0 + part * 4, acc[i][j], rs[i], cs[j], act);
+                }
             }
         }
-    }
+    });
 }
 
 // ---- launches ----------------------------------------------------------------------------

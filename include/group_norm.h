@@ -13,10 +13,11 @@
  * with Phi the standard normal distribution function.  It is the norm that follows a
  * (deformable) convolution whose output is channels last, as dcn_forward's is: its
  * [N, H, W, C] is [N, H*W, C] here.  Means and variances are formed by averaging
- * deviations (never as a difference of large sums) and combined in binary64; all other
- * arithmetic is binary32, and a 16-bit result is rounded once to nearest even.  A NaN,
- * an infinity or a deviation whose square overflows binary32 makes its whole (image,
- * group) NaN, rstd among it; other groups are untouched by it.
+ * deviations (never as a difference of large sums); threads' and chunks' sums are combined
+ * in binary64, the gradients' too.  All other arithmetic is binary32, and a 16-bit result
+ * is rounded once to nearest even.  A NaN, an infinity or a deviation whose square
+ * overflows binary32 makes its whole (image, group) NaN, rstd among it; other groups are
+ * untouched by it.
  *
  * Conventions of the library (see deformagg.h): the caller owns every buffer, calls
  * are asynchronous on `stream` and may be captured into a HIP graph, every check runs

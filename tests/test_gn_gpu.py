@@ -406,3 +406,46 @@ def test_gelu_derivative_in_the_lower_tail():
         _, _, db = vdf.gn_backward(x, dy, 0 * one, one, 1, None, None, "gelu")
         torch.cuda.synchronize()
         check("grad_bias", db, act_grad(z.double(), "gelu"), gelu_tols(z.double())[1])
+
+
+@pytest.mark.parametrize("dy_dtype", [F32, BF16], ids=["whole", "chunks"])
+def test_parameter_gradients_of_many_images(dy_dtype):
+    """5000 images, one of them with a gradient of 1 and the others with 0.9 u each, which vanish
+    beside it where they are added one after the other in 32 bits.  Each image's own sum has one
+    term that is not 0, so grad_bias is exact before its one rounding; grad_weight's terms are
+    products of three rounded numbers, x - mean, rstd and the gradient."""
+    N, S, C, G = 5000, 2, 16, 2
+    x, _, _, _ = _inputs((N, S, C, G), F32, 66)
+    dy = torch.zeros((N, S, C))
+    dy[:, 0] = 0.8984375 * U
+    dy[0, 0] = 1
+    dy = dy.to(dy_dtype).cuda()
+    _, mean, rstd = vdf.gn_forward(x, G, None, None, EPS)
+    gx, dw, db = vdf.gn_backward(x, dy, mean, rstd, G)
+    torch.cuda.synchronize()
+    d = dy.cpu().double()
+    check("grad_bias", db, d.sum((0, 1)), 1.001 * U * d.sum((0, 1)))
+    per = C // G
+    xhat = ((x.cpu().double().view(N, S, G, per) - mean.cpu().double()[:, None, :, None])
+            * rstd.cpu().double()[:, None, :, None]).view(N, S, C)
+    terms = d * xhat
+    check("grad_weight", dw, terms.sum((0, 1)), 5 * U * terms.abs().sum((0, 1)))
+    check("grad_x", gx, *_grad_x_of(x, dy, mean, rstd, G))
+
+
+def _grad_x_of(x, dy, mean, rstd, G, w=None):
+    """grad_x without an activation from the given statistics, in 64 bits, and its bound: the
+    averages' terms and their sum over a thread's rows and channels round at most 32 times, the
+    result a few times more."""
+    N, S, C = x.shape
+
+    def split(t):
+        return t.double().reshape(N, S, G, C // G)
+
+    r = rstd.double()[:, None, :, None]
+    xhat = (split(x) - mean.double()[:, None, :, None]) * r
+    wdz = split(dy.double() * (1 if w is None else w.double()))
+    m1, m2 = wdz.mean((1, 3), keepdim=True), (wdz * xhat).mean((1, 3), keepdim=True)
+    tol = 40 * U * r * (wdz.abs() + wdz.abs().mean((1, 3), keepdim=True)
+                        + xhat.abs() * (wdz * xhat).abs().mean((1, 3), keepdim=True)) + 2.0 ** -149
+    return ((r * (wdz - m1 - xhat * m2)).reshape(N, S, C).cpu(), tol.reshape(N, S, C).cpu())

@@ -433,12 +433,13 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_stats_kernel(GnArgs a) {
     for (int u = threadIdx.x; u < b.nunits; u += kGnThreads) up[u] = make_float2(ua[u], ub[u]);
 }
 
-// grad_weight and grad_bias of 16 channels from the chunks' sums.
+// grad_weight and grad_bias of 16 channels from the chunks' sums: as many as there are images
+// and chunks, so joined in binary64.
 constexpr int kGnChanBlock = 16;
 __device__ __forceinline__ void channel_sums(const GnArgs& a, int block) {
-    __shared__ float2 red[kGnThreads];
+    __shared__ double2 red[kGnThreads];
     const int c = block * kGnChanBlock + threadIdx.x % kGnChanBlock;
-    float2 t = make_float2(0.0f, 0.0f);
+    double2 t = make_double2(0.0, 0.0);
     const int64_t parts = (int64_t)a.N * a.chunks;
     if (c < a.C)
         for (int64_t e = threadIdx.x / kGnChanBlock; e < parts; e += kGnThreads / kGnChanBlock) {
@@ -453,8 +454,8 @@ __device__ __forceinline__ void channel_sums(const GnArgs& a, int block) {
             t.x += red[e].x;
             t.y += red[e].y;
         }
-        if (a.grad_bias) a.grad_bias[c] = t.x;
-        if (a.grad_weight) a.grad_weight[c] = t.y;
+        if (a.grad_bias) a.grad_bias[c] = (float)t.x;
+        if (a.grad_weight) a.grad_weight[c] = (float)t.y;
     }
 }
 

@@ -16,8 +16,8 @@
  * deviations (never as a difference of large sums); threads' and chunks' sums are combined
  * in binary64, the gradients' too.  All other arithmetic is binary32, and a 16-bit result
  * is rounded once to nearest even.  A NaN, an infinity or a deviation whose square
- * overflows binary32 makes its whole (image, group) NaN, rstd among it; other groups are
- * untouched by it.
+ * overflows binary32 makes its whole (image, group) NaN, rstd among it, and deviations past
+ * 2^46 may, by the sum of their squares; other groups are untouched by it.
  *
  * Conventions of the library (see deformagg.h): the caller owns every buffer, calls
  * are asynchronous on `stream` and may be captured into a HIP graph, every check runs

@@ -449,3 +449,78 @@ def _grad_x_of(x, dy, mean, rstd, G, w=None):
     tol = 40 * U * r * (wdz.abs() + wdz.abs().mean((1, 3), keepdim=True)
                         + xhat.abs() * (wdz * xhat).abs().mean((1, 3), keepdim=True)) + 2.0 ** -149
     return ((r * (wdz - m1 - xhat * m2)).reshape(N, S, C).cpu(), tol.reshape(N, S, C).cpu())
+
+
+# Slabs of several groups in one workgroup, which maps of more than 4 MB and many images get.
+WIDE = {
+    "stage_28x28_batch": (12, 784, 256, 32),        # 64 bytes of a row: 2 to 4 groups
+    "stage_56x56_batch": (6, 3136, 128, 32),        # 16-bit forward: 8 groups, 13 vectors a thread
+    "four_vectors_wide": (64, 400, 256, 32),        # 16-bit backward: 128 bytes, 8 groups
+    "shorter_last_slab": (128, 200, 96, 3),         # 16-bit: slabs of 64 and 32 channels
+    "shorter_last_odd_slab": (90, 100, 105, 7),     # no vectors: slabs of 30 and 15 channels
+}
+
+
+@pytest.mark.parametrize("name", sorted(WIDE))
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=["f32", "bf16", "f16"])
+def test_wide_slabs(name, dtype):
+    say(f"[gn] wide {name} {WIDE[name]} {dtype}")
+    _check(WIDE[name], dtype, "gelu", seed=40 + sorted(WIDE).index(name))
+
+
+@pytest.mark.parametrize("shape", [(2, 300, 64, 4), (1, 40000, 64, 4), (1, 7, 4096, 1)],
+                         ids=["whole", "chunks", "units"])
+def test_large_deviations(shape):
+    """Deviations of up to 2^46, whose squares and their sums stay in binary32."""
+    x, _, _, _ = _inputs(shape, F32, 67)
+    x = x / x.abs().max() * 2.0 ** 46
+    _check(shape, F32, "none", seed=67, x=x)
+
+
+def test_gradients_of_more_values_than_32_bits_count():
+    """2 x 1100003 x 2048 bfloat16 values: grad_x at rows of both images, around and past place
+    2^32, and the parameters' gradients, against averages and sums formed in 64 bits by slices.
+    Each image's gradient has a mean and a share of x of its own, so that the averages of the
+    other image, or of other rows, would show.  A thread adds up 68 rows of 8 channels and a
+    workgroup 16 of its rows before the sums meet in 64 bits: 100 u of the magnitudes."""
+    N, S, C, G = 2, 1100003, 2048, 32
+    per, step = C // G, 25000
+    x = torch.empty((N, S, C), device="cuda", dtype=BF16)
+    dy = torch.empty_like(x)
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    for n in range(N):
+        for r in range(0, S, 100000):
+            xp, dp = x[n, r:r + 100000], dy[n, r:r + 100000]
+            xp.copy_(torch.randn(xp.shape, generator=gen, device="cuda", dtype=BF16))
+            dp.copy_(torch.randn(dp.shape, generator=gen, device="cuda", dtype=BF16))
+            dp.add_(xp, alpha=0.5 + n).add_(1.0 + n)
+    w = torch.rand((C,), generator=gen, device="cuda") + 0.5
+    _, mean, rstd = vdf.gn_forward(x, G, w, None, EPS, out=torch.empty_like(x))
+    gx, dw, db = vdf.gn_backward(x, dy, mean, rstd, G, w)
+    torch.cuda.synchronize()
+    say("[gn] 2^32 gradients done")
+
+    def parts(n, r, count):
+        """xhat and dy of some rows, in 64 bits, [rows, C]."""
+        m, s = (t[n].double().repeat_interleave(per)[None] for t in (mean, rstd))
+        return (x[n, r:r + count].double() - m) * s, dy[n, r:r + count].double()
+
+    sums = torch.zeros((4, N, C), device="cuda", dtype=torch.float64)   # dz, dz xhat; magnitudes
+    for n in range(N):
+        for r in range(0, S, step):
+            h, d = parts(n, r, step)
+            for k, t in enumerate((d, d * h)):
+                sums[k, n] += t.sum(0)
+                sums[k + 2, n] += t.abs().sum(0)
+    check("grad_bias", db, sums[0].sum(0).cpu(), 100 * U * sums[2].sum(0).cpu())
+    check("grad_weight", dw, sums[1].sum(0).cpu(), 100 * U * sums[3].sum(0).cpu())
+    means = (sums * w.double()).view(4, N, G, per).sum(3) / (S * per)
+    edge = 2 ** 32 // C - S
+    for n, r in ((0, 0), (0, S - 60), (1, 0), (1, edge - 30), (1, S - 60)):
+        h, d = parts(n, r, 60)
+        m1, m2, a1, a2 = (t.repeat_interleave(per)[None] for t in means[:, n])
+        s = rstd[n].double().repeat_interleave(per)[None]
+        want = s * (w.double() * d - m1 - h * m2)
+        tol = s * U * (8 * (w.double() * d).abs() + 100 * (a1 + h.abs() * a2))
+        check(f"grad_x of image {n} from row {r}", gx[n, r:r + 60], want.cpu(),
+              rounded(tol, want, BF16).cpu())

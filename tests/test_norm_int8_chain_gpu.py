@@ -137,3 +137,35 @@ def test_norm_between_two_streams_shares_nothing():
         torch.cuda.synchronize()
         for o, t in zip(outs, want):
             assert all(torch.equal(p, q) for p, q in zip(o, t))
+
+
+@pytest.mark.parametrize("C", [64, 320])
+def test_projected_convolution_into_buffers(C):
+    """offset_mask, workspace and out given: nothing is allocated, the results are the same."""
+    gen = torch.Generator().manual_seed(4103)
+    x = torch.randn((2, 9, 12, C), generator=gen).to(torch.bfloat16).cuda()
+    p, s = vdf.i8_quantize_rows((torch.randn((108, C), generator=gen) * (0.6 / C ** 0.5)).cuda())
+    b = (torch.randn(108, generator=gen) * 0.3).cuda()
+    want = vdf.dcn_forward_projected(x, p, s, b, 4)
+    offsets = vdf.i8_linear(x, p, s, b)
+    n = vdf.i8_linear_workspace_size(2 * 9 * 12, C, 108, x.dtype)
+    assert (n > 0) == (C == 320)
+    om = torch.full((2, 9, 12, 4, 27), float("nan"), device="cuda")
+    ws = torch.empty(max(1, n), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(want, float("nan"))
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    got = vdf.dcn_forward_projected(x, p, s, b, 4, out=out, offset_mask=om, workspace=ws)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+    torch.cuda.synchronize()
+    assert got is out and torch.equal(got, want)
+    assert torch.equal(om.view(2, 9, 12, 108), offsets)
+    none = vdf.dcn_forward_projected(x[:0], p, s, b, 4, offset_mask=om[:0])
+    assert none.shape == (0, 9, 12, C)
+    with pytest.raises(ValueError, match="offset_mask has shape"):
+        vdf.dcn_forward_projected(x, p, s, b, 4, offset_mask=om[..., :9].contiguous())
+    with pytest.raises(TypeError, match="offset_mask has dtype"):
+        vdf.dcn_forward_projected(x, p, s, b, 4, offset_mask=om.half())
+    if n:
+        with pytest.raises(ValueError, match="workspace"):
+            vdf.dcn_forward_projected(x, p, s, b, 4, workspace=ws[:n - 1])

@@ -87,11 +87,15 @@ def dcn_forward(input: torch.Tensor, offset_mask: torch.Tensor, groups: int, ker
 def dcn_forward_projected(input: torch.Tensor, proj: torch.Tensor, proj_scale: torch.Tensor,
                           proj_bias: Optional[torch.Tensor], groups: int, kernel: Pair = 3,
                           pad: Pair = 1, dilation: Pair = 1, out: Optional[torch.Tensor] = None,
-                          out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+                          out_dtype: Optional[torch.dtype] = None,
+                          offset_mask: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``dcn_forward`` at stride 1 with its offset_mask made from input as DCNv4 makes it, by
     one linear layer per pixel, here in 8 bits as a model is served: proj int8 [G * 3K, C] with
     a scale per row (``i8_quantize_rows`` of the layer's weights) and its bias.  The output is
-    as large as the input; kernel, pad and dilation have to say so."""
+    as large as the input; kernel, pad and dilation have to say so.  ``offset_mask`` [N, H, W, G,
+    3K] float32 receives the projection; ``workspace`` is ``i8_linear``'s, of
+    ``i8_linear_workspace_size(N * H * W, C, G * 3K, input.dtype)`` bytes."""
     if not isinstance(input, torch.Tensor) or input.dim() != 4:
         raise ValueError("input must be a [N, H, W, C] tensor")
     N, H, W, _ = input.shape
@@ -101,9 +105,14 @@ def dcn_forward_projected(input: torch.Tensor, proj: torch.Tensor, proj_scale: t
     if not isinstance(proj, torch.Tensor) or proj.dim() != 2 or \
             proj.shape[0] != int(groups) * 3 * kh * kw:
         raise ValueError(f"proj must be a [{int(groups) * 3 * kh * kw}, C] tensor of codes")
-    offset_mask = i8_linear(input, proj, proj_scale, proj_bias)
-    return dcn_forward(input, offset_mask.view(N, H, W, int(groups), 3 * kh * kw), groups, kernel,
-                       1, pad, dilation, out=out, out_dtype=out_dtype)
+    shape = (N, H, W, int(groups), 3 * kh * kw)
+    if offset_mask is not None:
+        _need(offset_mask, "offset_mask", torch.float32, input.device, shape)
+        offset_mask = offset_mask.view(N, H, W, shape[3] * shape[4])
+    offset_mask = i8_linear(input, proj, proj_scale, proj_bias, out=offset_mask,
+                            workspace=workspace)
+    return dcn_forward(input, offset_mask.view(shape), groups, kernel, 1, pad, dilation, out=out,
+                       out_dtype=out_dtype)
 
 
 def dcn_workspace_size(input: torch.Tensor, groups: int, kernel: Pair = 3, stride: Pair = 1,

@@ -13,9 +13,9 @@
  * with Phi the standard normal distribution function.  It is the norm that follows a
  * (deformable) convolution whose output is channels last, as dcn_forward's is: its
  * [N, H, W, C] is [N, H*W, C] here.  Means and variances are formed by averaging
- * deviations (never as a difference of large sums); threads' and chunks' sums are combined
- * in binary64, the gradients' too.  All other arithmetic is binary32, and a 16-bit result
- * is rounded once to nearest even.  A NaN, an infinity or a deviation whose square
+ * deviations (never as a difference of large sums) and combined in binary64, as are the
+ * gradients' sums over images and chunks; all other arithmetic is binary32, and a 16-bit
+ * result is rounded once to nearest even.  A NaN, an infinity or a deviation whose square
  * overflows binary32 makes its whole (image, group) NaN, rstd among it, and deviations past
  * 2^46 may, by the sum of their squares; other groups are untouched by it.
  *

@@ -524,3 +524,20 @@ def test_gradients_of_more_values_than_32_bits_count():
         tol = s * U * (8 * (w.double() * d).abs() + 100 * (a1 + h.abs() * a2))
         check(f"grad_x of image {n} from row {r}", gx[n, r:r + 60], want.cpu(),
               rounded(tol, want, BF16).cpu())
+
+
+@pytest.mark.parametrize("shape, dtype", [((2, 40003, 96, 8), F32), ((1, 30003, 192, 16), BF16),
+                                          ((1, 9001, 48, 3), F16), ((1, 605, 5200, 2), F32)])
+def test_mean_far_from_the_first_value_by_chunks(shape, dtype):
+    """The same by chunks and by units of a wide group, where every chunk's mean is the same
+    number far from the first value, so that roundings of it would not average out."""
+    N, S, C, G = shape
+    x = (torch.arange(C) * 7 % 8).float().expand(N, S, C).clone()
+    x[:, 0, ::C // G] = 1000.0
+    x = x.to(dtype).cuda()
+    _, mean, rstd = vdf.gn_forward(x, G, None, None, EPS)
+    torch.cuda.synchronize()
+    ref = Norm(x, G, None, None, EPS, "none")
+    share = 18000.0 * 16 / (S * C // G)
+    check("mean", mean, ref.mean, U * (ref.mean.abs() + share))
+    check("rstd", rstd, ref.rstd, ref.stat_tols()[1])

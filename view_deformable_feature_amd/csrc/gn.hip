@@ -50,21 +50,30 @@ __device__ __forceinline__ Slab slab_of(const GnArgs& a, int s, int threads) {
 }
 
 // out[u] = factor * the sum of red[r * cols + j] over r < R and the `per` columns of unit u,
-// by one wave per unit.  The threads' binary32 sums meet in binary64: a few additions a lane.
-// Every thread of the workgroup calls it; red is complete on entry, out on return.
+// added up in M, by a run of 8 to 64 lanes per unit: as many as have something to add and leave
+// all units to one pass, since a pass waits for its exchanges one after the other.  Every thread of the workgroup calls it;
+// red is complete on entry, out on return.
 template <typename M>
 __device__ __forceinline__ void unit_sums(const float* red, int R, int cols, int per, int nunits,
                                           double factor, M* out) {
-    const int lane = threadIdx.x & (kWave - 1), nw = blockDim.x / kWave;
-    for (int u = threadIdx.x / kWave; u < nunits; u += nw) {
-        double t = 0.0;
-        for (int e = lane; e < R * per; e += kWave) {
-            const int r = e / per, j = e - r * per;
-            t += red[r * cols + u * per + j];
-        }
+    int run = kWave;
+    while (run > 8 && (nunits * run > (int)blockDim.x || run / 2 >= R * per)) run /= 2;
+    const int lane = threadIdx.x & (run - 1), skip_r = run / per, skip_j = run - skip_r * per;
+    const int r0 = lane / per, j0 = lane - r0 * per;
+    for (int u = threadIdx.x / run; u - (int)threadIdx.x / run < nunits; u += blockDim.x / run) {
+        M t = 0;
+        if (u < nunits)
+            for (int r = r0, j = j0; r < R; r += skip_r) {
+                t += red[r * cols + u * per + j];
+                j += skip_j;
+                if (j >= per) {
+                    j -= per;
+                    ++r;
+                }
+            }
 #pragma unroll 1   // unrolled it takes registers that the callers keep their rows in
-        for (int m = kWave / 2; m; m >>= 1) t += __shfl_xor(t, m);
-        if (lane == 0) out[u] = (M)(t * factor);
+        for (int m = run / 2; m; m >>= 1) t += __shfl_xor(t, m);
+        if (lane == 0 && u < nunits) out[u] = (M)(t * factor);
     }
     __syncthreads();
 }
@@ -99,15 +108,14 @@ __device__ __forceinline__ float rstd_of(double var, float eps) {
 // of their differences from `first` and of those differences' squares, taken about that
 // value so that a large common offset cancels before anything is rounded.  Leaves in um
 // the units' means less the group's origin, in uq their sums of squared deviations from that
-// mean: in binary64 where the group's statistics are made from them at once (a difference
-// from an origin that is far from the mean, rounded to binary32, would be the mean's error), in
-// binary32 where they are one chunk's of many.  red holds one value per thread where a vector
-// lies in one unit, else V.
-template <int V, typename M>
+// mean, both in binary64: a difference from an origin far from the mean, rounded to binary32,
+// would be the mean's error.  red holds one value per thread where a vector lies in one unit,
+// else V.
+template <int V>
 __device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int n, double share,
                                              int cnt, const float (&first)[V],
                                              const float (&sum)[V], const float (&sq)[V],
-                                             float* red, M* um, M* uq) {
+                                             float* red, double* um, double* uq) {
     const int per_ch = a.upg == 1 ? a.cpg : b.width;
     const bool whole = per_ch % V == 0;
     const int cols = whole ? b.cols : b.width, per = whole ? per_ch / V : per_ch;
@@ -169,7 +177,7 @@ __device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int
 template <typename T, int V>
 __global__ __launch_bounds__(kGnThreads) void gn_stats_kernel(GnArgs a) {
     __shared__ float red[kGnThreads * V];
-    __shared__ float um[kGnThreads * V], uq[kGnThreads * V];
+    __shared__ double um[kGnUnits], uq[kGnUnits];
     const int s = blockIdx.x % a.slabs;
     const int chunk = (blockIdx.x / a.slabs) % a.chunks;
     const int n = blockIdx.x / a.slabs / a.chunks;
@@ -207,9 +215,9 @@ __global__ __launch_bounds__(kGnThreads) void gn_stats_kernel(GnArgs a) {
     }
     const double share = 1.0 / ((double)(r1 - r0) * (a.upg == 1 ? a.cpg : b.width));
     join_threads(a, b, n, share, cnt, first, sum, sq, red, um, uq);
-    float2* part = a.unit_part + ((int64_t)n * a.chunks + chunk) * a.units + b.unit0;
+    double2* part = a.stat_part + ((int64_t)n * a.chunks + chunk) * a.units + b.unit0;
     for (int u = threadIdx.x; u < b.nunits; u += kGnThreads) {
-        part[u] = make_float2(um[u], uq[u]);
+        part[u] = make_double2(um[u], uq[u]);
         // kept: x may be overwritten in place by the time the chunks are joined
         if (chunk == 0 && (a.upg == 1 || s % a.upg == 0))
             a.origins[(int64_t)n * a.G + b.g0 + u] = origin_of(a, n, b.g0 + u);
@@ -226,19 +234,19 @@ __device__ __forceinline__ void join_stats(const GnArgs& a, int n, int g0, int n
     constexpr int kHold = 4;
     for (int j0 = 0; j0 < ngroups; j0 += kGnThreads / run) {
         const int j = j0 + (int)threadIdx.x / run, g = g0 + min(j, ngroups - 1);
-        const float2* part = a.unit_part + (int64_t)n * a.chunks * a.units + (int64_t)g * a.upg;
+        const double2* part = a.stat_part + (int64_t)n * a.chunks * a.units + (int64_t)g * a.upg;
         // entry e: unit e % upg of chunk e / upg, and how many values it stands for
-        const auto entry = [&](int e, float2& q, double& cnt) {
+        const auto entry = [&](int e, double2& q, double& cnt) {
             const int c = a.upg == 1 ? e : e / a.upg, u = e - c * a.upg;
             const int64_t r0 = c * a.rows_per_chunk;
             q = part[(int64_t)c * a.units + u];
             cnt = (double)(min(r0 + a.rows_per_chunk, a.S) - r0) * min(a.cpu, a.cpg - u * a.cpu);
         };
-        float2 q[kHold];
+        double2 q[kHold];
         double cnt[kHold], sum = 0.0, m2 = 0.0;
 #pragma unroll
         for (int i = 0; i < kHold; ++i) {
-            q[i] = make_float2(0.0f, 0.0f);
+            q[i] = make_double2(0.0, 0.0);
             cnt[i] = 0.0;
             if (lane + i * run < entries) entry(lane + i * run, q[i], cnt[i]);
         }
@@ -251,7 +259,7 @@ __device__ __forceinline__ void join_stats(const GnArgs& a, int n, int g0, int n
         for (int m = run / 2; m; m >>= 1) sum += __shfl_xor(sum, m);
         const double mean = sum / total;
         if (entries > kHold * run) {   // the first entry was read over
-            q[0] = make_float2(0.0f, 0.0f);
+            q[0] = make_double2(0.0, 0.0);
             cnt[0] = 0.0;
             entry(lane, q[0], cnt[0]);
         }
@@ -286,7 +294,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_join_kernel(GnArgs a) {
 
 template <typename T, int V>
 __global__ __launch_bounds__(kGnThreads) void gn_apply_kernel(GnArgs a) {
-    __shared__ float gm[kGnThreads * V], gr[kGnThreads * V];
+    __shared__ float gm[kGnUnits], gr[kGnUnits];
     const int s = blockIdx.x % a.slabs;
     const int chunk = (blockIdx.x / a.slabs) % a.chunks;
     const int n = blockIdx.x / a.slabs / a.chunks;
@@ -364,7 +372,7 @@ __device__ __forceinline__ void fold_rows(const Slab& b, const float (&A)[V], co
 template <typename T, int V>
 __global__ __launch_bounds__(kGnThreads) void gn_bwd_stats_kernel(GnArgs a) {
     __shared__ float ra[kGnThreads * V], rb[kGnThreads * V];
-    __shared__ float ua[kGnThreads * V], ub[kGnThreads * V];
+    __shared__ float ua[kGnUnits], ub[kGnUnits];
     const int s = blockIdx.x % a.slabs;
     const int chunk = (blockIdx.x / a.slabs) % a.chunks;
     const int n = blockIdx.x / a.slabs / a.chunks;
@@ -496,7 +504,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int6
         channel_sums(a, blockIdx.x - chunk_blocks);
         return;
     }
-    __shared__ float m1[kGnThreads * V], m2[kGnThreads * V];
+    __shared__ float m1[kGnUnits], m2[kGnUnits];
     const int s = blockIdx.x % a.slabs;
     const int chunk = (blockIdx.x / a.slabs) % a.chunks;
     const int n = blockIdx.x / a.slabs / a.chunks;
@@ -565,8 +573,8 @@ __device__ __forceinline__ int xcd_run(int id, int total) {
 template <typename T, int V, int NV, bool STORE>
 __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
     __shared__ float red[kGnWholeThreads * V];
-    __shared__ double um[kGnWholeUnits], uq[kGnWholeUnits];
-    __shared__ float gm[kGnWholeUnits], gr[kGnWholeUnits];
+    __shared__ double um[kGnUnits], uq[kGnUnits];
+    __shared__ float gm[kGnUnits], gr[kGnUnits];
     const int id = xcd_run(blockIdx.x, a.N * a.slabs);
     const int n = id / a.slabs, s = id - n * a.slabs;
     const Slab b = slab_of<V>(a, s, blockDim.x);
@@ -651,7 +659,7 @@ __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
 template <typename T, int V, int NV>
 __global__ __launch_bounds__(kGnWholeBwdThreads) void gn_bwd_whole_kernel(GnArgs a) {
     __shared__ float ra[kGnWholeBwdThreads * V], rb[kGnWholeBwdThreads * V];
-    __shared__ float ua[kGnWholeUnits], ub[kGnWholeUnits];
+    __shared__ float ua[kGnUnits], ub[kGnUnits];
     const int id = xcd_run(blockIdx.x, a.N * a.slabs);
     const int n = id / a.slabs, s = id - n * a.slabs;
     const Slab b = slab_of<V>(a, s, blockDim.x);

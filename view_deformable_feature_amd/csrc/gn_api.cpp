@@ -74,7 +74,7 @@ bool lay_out_whole(const gn_problem* p, int vec, int threads, int most, da::GnAr
     };
     int64_t width = 0;
     for (int64_t w = base; w <= C && (w == base || w * elem <= 256); w *= 2) {
-        if (vectors(w, threads) > most || w / (C / p->groups) > da::kGnWholeUnits) break;
+        if (vectors(w, threads) > most || w / (C / p->groups) > da::kGnUnits) break;
         if (w < C && w * elem < 64 && !small) continue;
         if (width && p->batch * ((C + w - 1) / w) < 256) break;
         width = w;
@@ -156,6 +156,9 @@ bool vectors_fit(const gn_problem* p) {
     return std::lcm(cpg, vec) <= da::kGnThreads * vec || cpg % vec == 0;
 }
 
+uint64_t stat_part_bytes(const da::GnArgs& a) {
+    return part_bytes((uint64_t)a.N * a.chunks * a.units * sizeof(double2));
+}
 uint64_t unit_part_bytes(const da::GnArgs& a) {
     return part_bytes((uint64_t)a.N * a.chunks * a.units * sizeof(float2));
 }
@@ -175,7 +178,7 @@ uint64_t need_forward(const gn_problem* p, bool stats_kept) {
         da::GnArgs a;
         lay_out(p, vec, kForward, a);
         need = std::max(need, (stats_kept ? 2 * group_bytes(p) : 0) +
-                                  (a.threads ? 0 : group_bytes(p) + unit_part_bytes(a)));
+                                  (a.threads ? 0 : group_bytes(p) + stat_part_bytes(a)));
     }
     return need;
 }
@@ -237,7 +240,7 @@ hipError_t enqueue_gn_stats(const gn_problem* p, const void* x, void* workspace,
     a.mean = reinterpret_cast<float*>(base);
     a.rstd = reinterpret_cast<float*>(base + group_bytes(p));
     a.origins = reinterpret_cast<float*>(base + 2 * group_bytes(p));
-    a.unit_part = reinterpret_cast<float2*>(base + 3 * group_bytes(p));
+    a.stat_part = reinterpret_cast<double2*>(base + 3 * group_bytes(p));
     return launch_gn_stats(a, vec, stream);
 }
 
@@ -283,7 +286,7 @@ da_status gn_forward(const gn_problem* p, const void* x, const float* weight, co
     a.rstd = rstd;
     a.origins = static_cast<float*>(workspace);
     if (!a.threads)
-        a.unit_part = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + group_bytes(p));
+        a.stat_part = reinterpret_cast<double2*>(static_cast<unsigned char*>(workspace) + group_bytes(p));
     return da::report_hip(da::launch_gn_forward(a, vec, static_cast<hipStream_t>(stream)),
                           "group norm forward launch");
 }

@@ -23,8 +23,9 @@ constexpr int kGnThreads = 256;
 // of x and 64 of dz (with 1024 threads it spilled 45 of them at half as many vectors).
 constexpr int kGnWholeThreads = 1024, kGnWholeVecs = 16;
 constexpr int kGnWholeBwdThreads = 512, kGnWholeBwdVecs = 8;
-// Groups of such a slab: of one channel each, 256 bytes of a row hold the most.
-constexpr int kGnWholeUnits = 128;
+// Units of any slab: groups of one channel each, 256 bytes of a row hold the most (a slab is wider
+// only where a single group, or a few that share vectors, are).
+constexpr int kGnUnits = 128;
 
 struct GnArgs {
     const void* x;            // [N, S, C] of x_dtype
@@ -38,8 +39,8 @@ struct GnArgs {
     float* grad_weight;       // [C] or NULL
     float* grad_bias;         // [C] or NULL
     float* origins;           // [N, G]: the groups' first values, which means are taken from
-    float2* unit_part;        // [N, chunks, units]: (mean less that, sum of squared deviations), or the
-                              // backward's sums of weight * dz and weight * dz * xhat
+    double2* stat_part;       // [N, chunks, units]: mean less that, sum of squared deviations
+    float2* unit_part;        // backward: [N, chunks, units] sums of weight * dz and weight * dz * xhat
     float2* chan_part;        // backward: [N, chunks, C] sums of dz and dz * xhat
     int64_t S;
     int64_t rows_per_chunk;

@@ -325,6 +325,14 @@ __device__ __forceinline__ float dpp(float v) {
     return __int_as_float(
         __builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, row_mask, 0xF, false));
 }
+template <int ctrl, int row_mask>
+__device__ __forceinline__ double dpp(double v) {
+    typedef int pair __attribute__((ext_vector_type(2)));
+    const pair p = __builtin_bit_cast(pair, v);
+    const pair q = {__builtin_amdgcn_update_dpp(0, p[0], ctrl, row_mask, 0xF, false),
+                    __builtin_amdgcn_update_dpp(0, p[1], ctrl, row_mask, 0xF, false)};
+    return __builtin_bit_cast(double, q);
+}
 
 // Sum of v over each aligned group of n lanes (n a power of two, 1..64, the same
 // in every lane).  The group's total ends up in its LAST lane; the other lanes
@@ -336,7 +344,8 @@ __device__ __forceinline__ float dpp(float v) {
 //   every lane of a 16-lane row holds the row's total; row_bcast:15 then adds
 //   row r-1's total into odd rows, and row_bcast:31 the total of rows 0-1 into
 //   rows 2-3.
-__device__ __forceinline__ float group_sum(float v, int n) {
+template <typename T>
+__device__ __forceinline__ T group_sum(T v, int n) {
     if (n > 1) v += dpp<0xB1, 0xF>(v);     // quad_perm [1,0,3,2]
     if (n > 2) v += dpp<0x4E, 0xF>(v);     // quad_perm [2,3,0,1]
     if (n > 4) v += dpp<0x141, 0xF>(v);    // row_half_mirror

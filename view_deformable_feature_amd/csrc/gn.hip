@@ -71,9 +71,8 @@ __device__ __forceinline__ void unit_sums(const float* red, int R, int cols, int
                     ++r;
                 }
             }
-#pragma unroll 1   // unrolled it takes registers that the callers keep their rows in
-        for (int m = run / 2; m; m >>= 1) t += __shfl_xor(t, m);
-        if (lane == 0 && u < nunits) out[u] = (M)(t * factor);
+        t = group_sum(t, run);
+        if (lane == run - 1 && u < nunits) out[u] = (M)(t * factor);
     }
     __syncthreads();
 }

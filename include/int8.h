@@ -65,7 +65,8 @@ DA_API da_status i8_quantize_rows(int64_t rows, int64_t channels, int32_t x_dtyp
 DA_API da_status i8_matmul_workspace_size(const i8_problem* problem, size_t* bytes);
 
 /*
- * i8_matmul -- out from codes.
+ * i8_matmul -- out from codes, which may begin at any byte (large products are faster where a
+ * and w are 16-byte aligned).
  *   a          device int8 [M, K].
  *   a_scale    device float [M].
  *   w          device int8 [N, K].

@@ -5,8 +5,8 @@
 // vectors, and a thread stays with one vector of channels: its weights, its groups'
 // statistics and the backward's per-channel sums sit in registers.
 //
-// The operator has a handful of operations to a value, so memory bounds it: at the 5.2 TB/s
-// of a copy too large for the caches, forward floors are one read and one write.  Times here
+// The operator has a handful of operations to a value, so memory bounds it: its floor is a copy
+// of as many bytes, which reaches 4.9 to 5.3 TB/s from 100 MB on and 6.4 at 77 MB.  Times here
 // are of one MI355X, inputs and outputs in rotation so that no call finds its own in cache.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -51,8 +51,8 @@ __device__ __forceinline__ Slab slab_of(const GnArgs& a, int s, int threads) {
 
 // out[u] = factor * the sum of red[r * cols + j] over r < R and the `per` columns of unit u,
 // added up in M, by a run of 8 to 64 lanes per unit: as many as have something to add and leave
-// all units to one pass, since a pass waits for its exchanges one after the other.  Every thread of the workgroup calls it;
-// red is complete on entry, out on return.
+// all units to one pass, since a pass waits for its exchanges one after the other.  Every thread
+// of the workgroup calls it; red is complete on entry, out on return.
 template <typename M>
 __device__ __forceinline__ void unit_sums(const float* red, int R, int cols, int per, int nunits,
                                           double factor, M* out) {
@@ -103,13 +103,12 @@ __device__ __forceinline__ float rstd_of(double var, float eps) {
 }
 
 // A workgroup's statistics from its threads' (share: 1 over the number of a unit's values):
-// each of cnt rows of V channels, with the sums
-// of their differences from `first` and of those differences' squares, taken about that
-// value so that a large common offset cancels before anything is rounded.  Leaves in um
-// the units' means less the group's origin, in uq their sums of squared deviations from that
-// mean, both in binary64: a difference from an origin far from the mean, rounded to binary32,
-// would be the mean's error.  red holds one value per thread where a vector lies in one unit,
-// else V.
+// each of cnt rows of V channels, with the sums of their differences from `first` and of those
+// differences' squares, taken about that value so that a large common offset cancels before
+// anything is rounded.  Leaves in um the units' means less the group's origin, in uq their sums
+// of squared deviations from that mean, both in binary64: a difference from an origin far from
+// the mean, rounded to binary32, would be the mean's error.  red holds one value per thread
+// where a vector lies in one unit, else V.
 template <int V>
 __device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int n, double share,
                                              int cnt, const float (&first)[V],
@@ -169,8 +168,9 @@ __device__ __forceinline__ void join_threads(const GnArgs& a, const Slab& b, int
 // squared deviations from that mean.  Each thread takes its squares about its first row,
 // then moves them to the unit's mean.
 //
-// By chunks x is read twice: 6 x 11264 x 256 binary32 (69 MB) takes 22 us here and 26 us in
-// gn_apply_kernel, 47 us a call (floor 27 us), the second read coming in part from cache.
+// By chunks x is read twice: 6 x 11264 x 256 binary32 (69 MB) takes 23 us here and 26 us in
+// gn_apply_kernel, 48 us a call (floor 28 us).  The second read comes in part from cache; this one
+// runs at 3 TB/s, two batches of loads to a thread, the second asked for when the first is added up.
 // Rows of 256 bytes to a slab and 16 rows to a thread; with a slab per group (32 bytes of a
 // row) held in LDS and read once it took 62 us, since an image has too few workgroups.
 template <typename T, int V>
@@ -560,10 +560,10 @@ __global__ __launch_bounds__(kGnThreads) void gn_bwd_apply_kernel(GnArgs a, int6
 // Where a slab of one image fits the registers of a workgroup, it is read once, its
 // statistics are formed there and it is normalised and written from there: the floor of
 // traffic, one launch.  Consecutive slabs go to one XCD, whose L2 then holds the 128-byte
-// lines that two slabs share.  64 x 3136 x 128 bfloat16 (103 MB in and out) takes 31 us, 3.3
+// lines that two slabs share.  64 x 3136 x 128 bfloat16 (103 MB in and out) takes 29 us, 3.5
 // TB/s: each compute unit has one workgroup, which reads, then computes, then writes, and no
-// other fills the gaps (a copy of as much takes 20 us).  Small
-// maps are bound by the launch: 6 x 176 x 256 binary32 takes 6.6 us.
+// other fills the gaps (a copy of as much takes 21 us).  Small maps are bound by the launch:
+// 6 x 176 x 256 binary32 takes 6.0 us.
 __device__ __forceinline__ int xcd_run(int id, int total) {
     const int x = id % 8, i = id / 8;
     return x * (total / 8) + min(x, total % 8) + i;
@@ -651,10 +651,10 @@ __global__ __launch_bounds__(kGnWholeThreads) void gn_whole_kernel(GnArgs a) {
 
 // The same for the gradients (grad_out of x's type): dz stays in registers in binary32, so the
 // derivative of the activation is formed once.  64 x 784 x 256 bfloat16 with SiLU (77 MB in and
-// out) takes 31 us and 3.5 us for the channels' sums behind it (floor 15 us); as in the
-// forward a compute unit reads, computes and writes by turns.  Where
-// no slab fits, 3 x 1665 x 96 binary16 (2.9 MB) takes 16 us by chunks: 9.4 and 7.5 us of two
-// launches of 60 workgroups, whose loads, joins and exchanges follow one another.
+// out) takes 30.8 us and 4.0 us for the channels' sums behind it (floor 12 us); as in the
+// forward a compute unit reads, computes and writes by turns.  Where no slab fits, 3 x 1665 x 96
+// binary16 (2.9 MB) takes 16 us by chunks: 10 and 7 us of two launches of 60 workgroups, whose
+// loads, joins and exchanges follow one another.
 template <typename T, int V, int NV>
 __global__ __launch_bounds__(kGnWholeBwdThreads) void gn_bwd_whole_kernel(GnArgs a) {
     __shared__ float ra[kGnWholeBwdThreads * V], rb[kGnWholeBwdThreads * V];

@@ -57,13 +57,13 @@ uint64_t part_bytes(uint64_t n) { return (n + 255) & ~uint64_t(255); }
 // The layout of an image's slab in one workgroup of up to `threads` threads, `most` vectors
 // to a thread; false where none fits.  Of the widths that fit, the widest that leaves a
 // workgroup for every compute unit, else the narrowest of at least 64 bytes of a row.  Measured
-// (us in a captured graph, whole slabs and by chunks): 64 x 784 x 256 bfloat16 forward 18 and
-// 40, backward 33 and 70; 6 x 176 x 256 binary32 6.7 and 10.5, 8.6 and 10.6; 1 x 196 x 512
-// binary16 6.2 and 13, 9.0 and 15.7.  Small maps of few rows may go by 16 and 32 bytes, for
-// more workgroups: 2 x 784 x 256 bfloat16 takes 7.0 so and 9.5 by 64 bytes; but each row is a
-// line fetched for a piece of it, and 2 x 4096 x 64 bfloat16 takes 12.1 (chunks 12.4), 2 x 8192
-// x 64 17.5 (12.8); backward, with half the threads, 2 x 2048 x 64 12.7 (14.7) and 2 x 4096 x 64
-// 16.7 (14.7).
+// (us in a captured graph, whole slabs and by chunks): 64 x 784 x 256 bfloat16 forward 17 and
+// 27, backward 33 and 43; 6 x 176 x 256 binary32 6.3 and 10.6, 8.6 and 10.6; 1 x 196 x 512
+// binary16 6.0 and 12.4, 9.0 and 14.8.  Small maps of few rows may go by 16 and 32 bytes, for
+// more workgroups: 2 x 784 x 256 bfloat16 takes 6.8 so and 9.4 by 64 bytes; but each row is a
+// line fetched for a piece of it, and 2 x 4096 x 64 bfloat16 takes 11.8 (chunks 11.8), 2 x 8192
+// x 64 17.1 (12.0); backward, with half the threads, 2 x 2048 x 64 12.8 (13.6) and 2 x 4096 x 64
+// 16.8 (13.7).
 bool lay_out_whole(const gn_problem* p, int vec, int threads, int most, da::GnArgs& a) {
     const int64_t C = p->channels, elem = elem_bytes(p->x_dtype);
     const int64_t base = std::lcm(C / p->groups, (int64_t)vec);
@@ -98,6 +98,8 @@ struct Keeps {
     int threads, vecs;
 };
 constexpr Keeps kForward = {da::kGnWholeThreads, da::kGnWholeVecs};
+// A grad_out of another type than x goes by chunks: 64 x 784 x 256 bfloat16 with a binary32
+// gradient takes 44 us (115 MB), 33 with its own type (77 MB).
 Keeps backward_keeps(const gn_problem* p) {
     return p->x_dtype == p->out_dtype ? Keeps{da::kGnWholeBwdThreads, da::kGnWholeBwdVecs}
                                       : Keeps{0, 0};
@@ -135,8 +137,8 @@ void lay_out(const gn_problem* p, int vec, Keeps keeps, da::GnArgs& a) {
     }
     // row chunks: 16 rows to a thread, fewer where that leaves less than two workgroups to a
     // compute unit.  More chunks than that cost more in every workgroup's join than they bring:
-    // with eight to a compute unit 64 x 3136 x 128 bfloat16 took 172 us backward (79), 1 x
-    // 40000 x 256 71 forward (37).
+    // with eight to a compute unit 64 x 3136 x 128 bfloat16 takes 154 us backward (72), 1 x
+    // 40000 x 256 67 forward (35).
     const int64_t R = std::max<int64_t>(1, da::kGnThreads / (a.slab_ch / vec));
     int64_t per_thread = 16;
     while (per_thread > 4 &&

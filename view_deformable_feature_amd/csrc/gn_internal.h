@@ -19,8 +19,9 @@ namespace da {
 
 constexpr int kGnThreads = 256;
 // A slab of a whole image in one workgroup: at most so many threads, and vectors to a thread.
-// The forward keeps 64 registers of x of the 128 that 1024 threads may have, the backward 32
-// of x and 64 of dz (with 1024 threads it spilled 45 of them at half as many vectors).
+// The forward keeps 64 registers of x of the 128 that 1024 threads may have (with 16 vectors of 16
+// bits it spills 4 of the others), the backward 32 of x and 64 of dz (with 1024 threads it
+// spilled 45 of them at half as many vectors).
 constexpr int kGnWholeThreads = 1024, kGnWholeVecs = 16;
 constexpr int kGnWholeBwdThreads = 512, kGnWholeBwdVecs = 8;
 // Units of any slab: groups of one channel each, 256 bytes of a row hold the most (a slab is wider

@@ -169,7 +169,8 @@ struct NormCoef {
 };
 
 // Rows to codes and scales in memory: for a caller, and before the kernels that read codes.
-// Bound by memory, and by its own latency for few rows (1237 x 1000 of 16 bits, 3.7 MB: 4.3 us).
+// Bound by memory (65536 x 1024 bfloat16, 201 MB, 47 us, 4.3 TB/s), and by its own latency for few
+// rows (1237 x 1000 of 16 bits, 3.7 MB: 4.4 us).
 // L lanes to a row, 64 / L rows to a wave; a row's first HOLD pieces per lane stay in
 // registers, what is past them is read again.  Behind a norm L is 64, and a wave has up to 8
 // consecutive rows of one image, for which it keeps the coefficients of the pieces held.
@@ -407,12 +408,12 @@ __device__ __forceinline__ void finish(const I8Args& a, int64_t m, int n, const 
 // go through memory.
 //
 // Memory bounds it where rows are many: 200704 x 128 x 108 from bfloat16 into binary32 (138
-// MB) takes 32 us, 4.3 TB/s (a copy of as much 27 us).  900 x 256 x 2496 codes take 8.8 us:
+// MB) takes 30 us, 4.6 TB/s (a copy of as much 28 us).  900 x 256 x 2496 codes take 9 us:
 // a launch, the fill of LDS and the first rows are waited for before the first product.  Behind
-// a norm 50176 x 256 x 216 takes 26 us and the statistics 9 us; by their instructions 12.8
+// a norm 50176 x 256 x 216 takes 25 us and the statistics 9 us; by their instructions 12.8
 // million activations and codes are some 11 us, and with one unit of rows to a wave nothing
 // overlaps its loads and stores but the other workgroup of the compute unit.  That takes 128
-// registers: with 256, and half the waves, the call was 39.5 us in place of 35.4.
+// registers: with 256, and half the waves, the call is 37.1 us in place of 31.9.
 
 constexpr int kRowsThreads = 512;
 constexpr int kRowsWaves = kRowsThreads / kWave;
@@ -534,7 +535,7 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
         } else {
             // normalised numbers are kept between the two steps; the barriers to the scheduler
             // keep the numbers from being worked on all at once (four at a time behind a norm:
-            // 11 registers spilled where 16 at a time spilled 41)
+            // 8 registers spilled)
             float z[KT][16];
             uint32_t big = 0;
 #pragma unroll
@@ -629,8 +630,8 @@ __global__ __launch_bounds__(kRowsThreads, KT == 4 && XB == 4 ? 2 : 4) void i8_r
 // Few rows, 16 * MT at a time: a wave takes 16 output channels and every KW-th run of 64 columns,
 // the weights going from memory into operand registers, several runs in flight; the KW
 // waves' sums meet in LDS.  The rows' codes come from memory (XB 0), or the workgroup
-// quantises up to 16 rows of x into LDS first.  One row of 4096 by 4096 x 4096 codes takes 7.4
-// us, 2.3 TB/s of weights (floor 3.2 us): the launch, the row's scale and the sums' meeting are
+// quantises up to 16 rows of x into LDS first.  One row of 4096 by 4096 x 4096 codes takes 7.6
+// us, 2.2 TB/s of weights (floor 4 us): the launch, the row's scale and the sums' meeting are
 // waited for one after the other; the first weights are on their way before the row is read.
 
 constexpr int kSkinnyThreads = 512;
@@ -791,9 +792,10 @@ __global__ __launch_bounds__(kSkinnyThreads) void i8_skinny_kernel(I8Args a, int
 //
 // 64 rows by 64 output channels to a workgroup of four waves, 128 columns at a time through
 // LDS, the next 128 on their way to registers meanwhile.  For products too small to fill the
-// chip with larger tiles, so bound by a tile's walk along its columns (0.65 us per 128): 1237 x
-// 1000 x 777 takes 11.5 us, 12544 x 512 x 432 with its quantisation 24 us.  A 16-byte piece p of an LDS row r sits at place
-// p ^ (r / 2 % 8): the 16 rows an operand is read from then fall into different banks.
+// chip with larger tiles, so bound by a tile's walk along its columns (0.6 us per 128): 1237 x
+// 1000 x 777 takes 11.2 us, 12544 x 512 x 432 with its quantisation 23 us.  A 16-byte piece p of
+// an LDS row r sits at place p ^ (r / 2 % 8): the 16 rows an operand is read from then fall into
+// different banks.
 
 constexpr int kTileK = 128, kTile = 64, kTileThreads = 256;
 
@@ -914,13 +916,14 @@ __global__ __launch_bounds__(kTileThreads) void i8_tile_kernel(I8Args a) {
 // ---- large products ----------------------------------------------------------------------
 //
 // 256 rows by 256 output channels to a workgroup of eight waves, 128 x 64 to a wave, columns
-// in whole runs of 128.  8192 x 4096 x 4096 takes 128 us into the same result each time, 140 to
-// 150 us with operands and results in rotation: 1.8 to 2.1 POP/s, bound by the matrix cores (the
-// library's 8-bit product without scales reaches 2.1).  Tiles of 64 took 200 us; a grid of as many workgroups as are
-// resident, each with several tiles, spilled and was slower.  The next 128 columns go from memory straight into the other half of
-// LDS while these are multiplied, and a run's operands are read while the run before it is
-// in the matrix cores.  An instruction that fills LDS puts lane l's 16 bytes at place l of a
-// run of 1 KB, so the swizzle of the tiled kernel is in the addresses the lanes fetch from.
+// in whole runs of 128.  8192 x 4096 x 4096 takes 109 us into the same result each time, 129 us
+// with operands and results in rotation: 2.1 to 2.5 POP/s, bound by the matrix cores (the
+// library's 8-bit product without scales reaches 2.2 in rotation).  Tiles of 64 took 200 us; a
+// grid of as many workgroups as are resident, each with several tiles, spilled and was slower.
+// The next 128 columns go from memory straight into the other half of LDS while these are
+// multiplied, and a run's operands are read while the run before it is in the matrix cores.
+// An instruction that fills LDS puts lane l's 16 bytes at place l of a run of 1 KB, so the
+// swizzle of the tiled kernel is in the addresses the lanes fetch from.
 
 constexpr int kBigTile = 256, kBigThreads = 512;
 constexpr int kSchedMatrix = 0x8, kSchedLdsRead = 0x100;   // instruction classes of a schedule
@@ -1065,9 +1068,9 @@ hipError_t launch_rows(I8Args a, const GnArgs& g, hipStream_t stream) {
     size_t lds = (size_t)a.tiles_per_slice * 16 * (rows_stride(KT) + 8) +
                  (NORM ? 3 * 64 * KT * 4 : 0);
     // Results by way of LDS where whole rows of whole 16-byte pieces fit, two workgroups to a
-    // compute unit: 200704 x 128 x 108 into binary32 takes 32 us so, 40 us from the registers,
+    // compute unit: 200704 x 128 x 108 into binary32 takes 33 us so, 42 us from the registers,
     // whose 64-byte pieces of 432-byte rows no line of memory begins or ends with.  Parts of
-    // rows gain nothing: 50176 x 256 x 216 took 23 us by pieces of 128 bytes, 20 us directly.
+    // rows gained nothing: 50176 x 256 x 216 took 23 us by pieces of 128 bytes, 20 us directly.
     const size_t row = (size_t)a.N * (a.out_dtype == DA_F32 ? 4 : 2);
     a.staged = a.slices == 1 && row % 16 == 0 && lds + kRowsWaves * 16 * row <= kRowsLdsAll;
     if (a.staged) lds += kRowsWaves * 16 * row;
@@ -1102,9 +1105,9 @@ hipError_t launch_skinny(const I8Args& a, hipStream_t stream) {
 }
 
 // A product with a 256 x 256 tile for every other compute unit or more (us, against 64 x 64 tiles):
-// 4096 x 1024 x 4096, 256 tiles, takes 30.5 (47.6); 1024 x 4096 x 8192, 128 tiles, 56 (71); 1792 x
-// 4096 x 4096, 112 tiles, 55 (66), but 1792 x 1024 x 4096 24.5 (24.2) and 1536 x 512 x 4096, 96
-// tiles, 18.6 (15.1).  Its 16-byte fills of LDS are for aligned addresses: codes that begin
+// 4096 x 1024 x 4096, 256 tiles, takes 25 (49); 1024 x 4096 x 8192, 128 tiles, 53 (72); 1792 x
+// 4096 x 4096, 112 tiles, 52 (61), but 1792 x 512 x 4096 16.8 (14.7) and 1536 x 512 x 4096, 96
+// tiles, 16.3 (14.1).  Its 16-byte fills of LDS are for aligned addresses: codes that begin
 // elsewhere go by the smaller tiles, whose loads into registers may lie anywhere.
 bool big(const I8Args& a) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.w);
@@ -1124,13 +1127,15 @@ hipError_t launch_tiles(const I8Args& a, hipStream_t stream) {
 }  // namespace
 
 // Which kernel, by times measured on an MI355X (us a call of i8_linear in a captured graph):
-//  - up to 256 columns the rows kernel: 50176 x 256 x 216 takes 20 (quantised in memory, then
-//    tiled 30), 100 x 256 x 2496 takes 5.8 (streamed 12);
-//  - up to 16 rows the streaming kernel: one row of 4096 x 4096 takes 6.8, and quantising on
+//  - up to 256 columns the rows kernel: 50176 x 256 x 216 takes 19 (quantised in memory, then
+//    tiled 25), 200704 x 128 x 108 24 (52), 100 x 256 x 2496 5.9 (7.5), but 900 x 256 x 2496, whose
+//    78 slices read x as many times, 11.5 (9.2);
+//  - up to 16 rows the streaming kernel: one row of 4096 x 4096 takes 6.7, and quantising on
 //    the way saves a launch where the rows fit LDS; up to 64, and beyond them with 1024 columns
-//    or more up to 128 rows or 64 tiles (one 64 x 64 tile walks its columns at 0.65 us per
-//    128): 128 x 4096 x 256 takes 18 (tiled 33), 100 x 4096 x 4096 29 (33), 200 x 2048 x 1024 12
-//    (20), but 256 x 1024 x 4096 19 (13) and 256 x 512 x 512 11 (9);
+//    or more up to 128 rows or 64 tiles (one 64 x 64 tile walks its columns at 0.6 us per
+//    128): 64 x 4096 x 4096 takes 19 (tiled 31), 128 x 4096 x 256 18 (31), 100 x 4096 x 4096 28
+//    (31), 200 x 2048 x 1024 12 (18), but 48 x 512 x 432 10 (9), 256 x 1024 x 4096 18 (13) and
+//    256 x 512 x 512 11 (9);
 //  - else tiles.
 I8Path i8_path(int64_t M, int64_t K, int64_t N, bool codes, bool norm) {
     // 16 rows of a binary32 result are the range of a buffer resource

@@ -1,0 +1,380 @@
+"""Attention to states of another length, forward and backward, on the GPU against the definition
+in 64 bits (attention_reference.py has the bounds and how they come about): head sizes and
+types, shared key heads, one token and many, ragged lengths and masks, empty rows, NaN in invisible
+places, strides, splits of the keys, streams, graphs and autograd."""
+import itertools
+import math
+
+import pytest
+import torch
+
+import view_deformable_feature_amd as vdf
+from attention_reference import BF16, F16, F32, Attention, check
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+TYPES = pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=["f32", "bf16", "f16"])
+
+# B, Nq, Nk, H, Hk, D
+SHAPES = {
+    "one_of_each": (1, 1, 1, 1, 1, 8),
+    "one_key": (2, 5, 1, 2, 1, 16),
+    "one_query": (2, 1, 70, 4, 4, 32),
+    "shared_heads": (2, 3, 129, 8, 2, 64),
+    "three_to_a_head": (1, 43, 65, 9, 3, 40),
+    "rows_32": (1, 32, 300, 2, 2, 24),
+    "rows_33": (1, 33, 300, 2, 2, 24),
+    "tile_edges": (1, 128, 128, 1, 1, 128),
+    "past_tile_edges": (1, 129, 257, 1, 1, 128),
+    "odd": (3, 77, 205, 3, 1, 72),
+    "head_96": (1, 61, 99, 2, 1, 96),
+    "head_112": (2, 40, 131, 2, 2, 112),
+    "head_80": (1, 130, 64, 4, 2, 80),
+    "many_keys": (1, 7, 3001, 2, 1, 48),          # split over workgroups
+    "wide_32": (4, 130, 150, 64, 64, 32),         # the wide form in each head size
+    "wide_64": (3, 200, 67, 48, 48, 64),
+    "wide_96": (2, 129, 130, 64, 64, 88),
+    "wide_128": (2, 140, 190, 64, 64, 128),
+    "wide_shared": (2, 70, 100, 256, 64, 56),
+    "units_of_eight": (8, 100, 96, 8, 8, 32),
+    "units_of_seven": (7, 50, 96, 1, 1, 64),
+}
+
+
+def _inputs(shape, dtype, seed, lens=False, mask=False):
+    B, Nq, Nk, H, Hk, D = shape
+    gen = torch.Generator().manual_seed(seed)
+    q = (torch.randn((B, Nq, H, D), generator=gen) * 1.3).to(dtype).cuda()
+    k = (torch.randn((B, Nk, Hk, D), generator=gen) + 0.3).to(dtype).cuda()
+    v = (torch.randn((B, Nk, Hk, D), generator=gen) + torch.randn(D, generator=gen)).to(dtype).cuda()
+    go = torch.randn((B, Nq, H, D), generator=gen).to(dtype).cuda()
+    kv = torch.randint(0, Nk + 1, (B,), generator=gen, dtype=torch.int32).cuda() if lens else None
+    m = (torch.rand((B, Nk), generator=gen) < 0.7).cuda() if mask else None
+    return q, k, v, go, kv, m
+
+
+def _check(q, k, v, go, kv=None, m=None, scale=None):
+    out, lse = vdf.attn_forward(q, k, v, kv, m, scale)
+    torch.cuda.synchronize()
+    ref = Attention(q, k, v, kv, m, scale)
+    ref.check_forward(out, lse)
+    grads = vdf.attn_backward(q, k, v, out, lse, go, kv, m, scale)
+    torch.cuda.synchronize()
+    assert all(g.dtype == q.dtype for g in grads)
+    ref.check_backward(grads, go)
+    return out, lse, grads
+
+
+@pytest.mark.parametrize("name", sorted(SHAPES))
+@TYPES
+def test_shapes(name, dtype):
+    say(f"[attn] {name} {SHAPES[name]} {dtype}")
+    _check(*_inputs(SHAPES[name], dtype, 10 + sorted(SHAPES).index(name)))
+
+
+@pytest.mark.parametrize("name", ["one_query", "shared_heads", "odd", "past_tile_edges", "many_keys",
+                                  "wide_64", "wide_128", "units_of_seven"])
+@pytest.mark.parametrize("lens, mask", [(True, False), (False, True), (True, True)],
+                         ids=["lens", "mask", "both"])
+@TYPES
+def test_visible_keys(name, lens, mask, dtype):
+    """Ragged lengths, masks, and NaN and infinities in all that is invisible."""
+    say(f"[attn] visible {name} {lens} {mask} {dtype}")
+    q, k, v, go, kv, m = _inputs(SHAPES[name], dtype, 50 + sorted(SHAPES).index(name), lens, mask)
+    B, Nk = k.shape[:2]
+    see = torch.ones((B, Nk), dtype=torch.bool, device="cuda")
+    if lens:
+        see &= torch.arange(Nk, device="cuda") < kv[:, None]
+    if mask:
+        see &= m
+    k[~see] = math.nan
+    v[~see] = math.inf
+    _check(q, k, v, go, kv, m)
+
+
+@TYPES
+def test_rows_without_a_visible_key(dtype):
+    """An entry of length 0, one below 0, one whose mask is all false, beside whole ones; more
+    than Nk counts as Nk.  Their out, gradients and their keys' gradients are exactly 0."""
+    q, k, v, go, _, _ = _inputs((5, 40, 90, 4, 2, 32), dtype, 90)
+    kv = torch.tensor([90, 0, -3, 1000, 90], dtype=torch.int32, device="cuda")
+    m = torch.ones((5, 90), dtype=torch.bool, device="cuda")
+    m[4] = False
+    for t in (k, v):
+        t[1:3] = math.nan
+        t[4] = math.nan
+    out, lse, (dq, dk, dv) = _check(q, k, v, go, kv, m)
+    for b in (1, 2, 4):
+        assert all((t[b] == 0).all() for t in (out, dq, dk, dv)) and (lse[b] == -math.inf).all()
+
+
+def test_no_keys_and_no_queries():
+    q, k, v, go, _, _ = _inputs((2, 5, 1, 2, 1, 16), BF16, 91)
+    k, v = k[:, :0], v[:, :0]
+    out, lse = vdf.attn_forward(q, k, v)
+    dq, dk, dv = vdf.attn_backward(q, k, v, out, lse, go)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and (lse == -math.inf).all() and (dq == 0).all() and dk.shape == k.shape
+    q, k, v, go, _, _ = _inputs((2, 1, 9, 2, 1, 16), BF16, 92)
+    q, go = q[:, :0], go[:, :0]
+    out, lse = vdf.attn_forward(q, k, v)
+    dq, dk, dv = vdf.attn_backward(q, k, v, out.contiguous(), lse, go.contiguous())
+    torch.cuda.synchronize()
+    assert out.shape == q.shape and (dk == 0).all() and (dv == 0).all()
+    none = vdf.attn_forward(q[:0], k[:0], v[:0])[0]
+    assert none.shape == (0, 0, 2, 16)
+
+
+@TYPES
+def test_views_of_one_projection(dtype):
+    """q, k and v as views of one projection's output, sequence first, and heads apart; memory
+    behind the last token is never read."""
+    gen = torch.Generator().manual_seed(93)
+    B, N, H, D = 2, 75, 4, 32
+    packed = torch.randn((B, N, 3, H, D), generator=gen).to(dtype).cuda()
+    q, k, v = packed.unbind(2)
+    go = torch.randn((B, N, H, D), generator=gen).to(dtype).cuda()
+    _check(q, k, v, go)
+    packed = torch.randn((N, B, 3, H, D), generator=gen).to(dtype).cuda()
+    q, k, v = (t.transpose(0, 1) for t in packed.unbind(2))
+    _check(q, k, v, go)
+    packed = torch.randn((B, H, N, 2 * D), generator=gen).to(dtype).cuda()
+    packed[..., D:] = math.nan
+    _check(q, packed[..., :D].transpose(1, 2), v, go)
+    # one entry's states for all
+    k1, v1 = (t[:1].expand(B, -1, -1, -1) for t in (k, v))
+    _check(q, k1, v1, go)
+
+
+@TYPES
+def test_results_and_gradients_with_strides(dtype):
+    """out heads first, into a part of a wider buffer whose rest stays; grad_out heads first."""
+    q, k, v, go, _, _ = _inputs((2, 140, 90, 4, 2, 48), dtype, 109)
+    buf = torch.full((2, 4, 140, 64), 7.0, dtype=dtype, device="cuda")
+    out, lse = vdf.attn_forward(q, k, v, out=buf[..., :48].transpose(1, 2))
+    strided = go.transpose(1, 2).contiguous().transpose(1, 2)
+    grads = vdf.attn_backward(q, k, v, out, lse, strided)
+    torch.cuda.synchronize()
+    ref = Attention(q, k, v)
+    ref.check_forward(out, lse)
+    ref.check_backward(grads, go)
+    assert (buf[..., 48:] == 7).all()
+
+
+@TYPES
+def test_large_scores(dtype):
+    """Scores of hundreds: one key takes all the weight; growing along the keys, so that the
+    running maximum moves in every tile."""
+    q, k, v, go, _, _ = _inputs((1, 40, 700, 2, 2, 32), dtype, 94)
+    grow = torch.linspace(0, 12, 700, device="cuda")[None, :, None, None]
+    _check(q, (k + grow).to(dtype), v, go, scale=1.0)
+    _check(q, (k - grow).to(dtype), v, go, scale=1.0)
+
+
+def test_small_and_large_gradients_in_binary16():
+    """dP of 1e5 and gradients of 1e-4, whose p (dP - delta) leaves binary16's range at either
+    end: results come out as if it did not."""
+    q, k, v, go, _, _ = _inputs((1, 70, 500, 2, 1, 64), F16, 95)
+    _check(q, k, v, (go * 2.0 ** -13).to(F16))
+    q, k, v, go, _, _ = _inputs((1, 70, 900, 2, 1, 64), F16, 96)
+    _check(q, (k / 64).to(F16), (v * 100).to(F16), (go * 200).to(F16))
+
+
+@pytest.mark.parametrize("scale", [0.01, 0.5, 3.0])
+def test_scale(scale):
+    for dtype in (F32, BF16):
+        _check(*_inputs((2, 40, 90, 2, 2, 24), dtype, 97), scale=scale)
+
+
+def test_nothing_is_written_past_the_end():
+    """Results in buffers with a border, and the workspace's."""
+    q, k, v, go, _, _ = _inputs((1, 3, 2000, 2, 1, 40), BF16, 98)
+    n = vdf.attn_workspace_size(q, k, v)
+    assert n > 0
+    ws = torch.full((n + 512,), 0x5a, dtype=torch.uint8, device="cuda")
+    buf = torch.full((q.numel() + 64,), 7.0, dtype=BF16, device="cuda")
+    out, lse = vdf.attn_forward(q, k, v, out=buf[:q.numel()].view(q.shape), workspace=ws[:n])
+    torch.cuda.synchronize()
+    assert (buf[q.numel():] == 7).all() and (ws[n:] == 0x5a).all()
+    Attention(q, k, v).check_forward(out, lse)
+    n = vdf.attn_backward_workspace_size(q, k, v)
+    ws = torch.full((n + 512,), 0x5a, dtype=torch.uint8, device="cuda")
+    vdf.attn_backward(q, k, v, out, lse, go, workspace=ws[:n])
+    torch.cuda.synchronize()
+    assert (ws[n:] == 0x5a).all()
+
+
+def test_parts_of_the_gradients():
+    q, k, v, go, kv, m = _inputs((2, 30, 90, 4, 2, 32), BF16, 99, True, True)
+    out, lse = vdf.attn_forward(q, k, v, kv, m)
+    dq, dk, dv = vdf.attn_backward(q, k, v, out, lse, go, kv, m)
+    a = vdf.attn_backward(q, k, v, out, lse, go, kv, m, need_kv=False)
+    b = vdf.attn_backward(q, k, v, out, lse, go, kv, m, need_q=False)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], dq) and a[1] is None and a[2] is None
+    assert b[0] is None and torch.equal(b[1], dk) and torch.equal(b[2], dv)
+
+
+def test_runs_are_the_same_bit_for_bit():
+    for shape in ((2, 1, 9000, 8, 2, 128), (2, 300, 400, 16, 4, 64)):
+        q, k, v, go, _, _ = _inputs(shape, BF16, 100)
+        out, lse = vdf.attn_forward(q, k, v)
+        grads = vdf.attn_backward(q, k, v, out, lse, go)
+        for _ in range(3):
+            again = vdf.attn_forward(q, k, v)
+            assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+            for g, w in zip(vdf.attn_backward(q, k, v, out, lse, go), grads):
+                assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("shape", [(2, 1, 9000, 8, 2, 64), (2, 130, 200, 64, 64, 32)],
+                         ids=["token", "wide"])
+def test_graph_replays_match_eager(shape):
+    """Forward and backward captured and replayed, with lengths that change between the replays,
+    eager work on the same buffers in between."""
+    q, k, v, go, kv, m = _inputs(shape, F16, 101, True, True)
+    ws = torch.empty(max(1, vdf.attn_workspace_size(q, k, v)), dtype=torch.uint8, device="cuda")
+    bws = torch.empty(vdf.attn_backward_workspace_size(q, k, v), dtype=torch.uint8, device="cuda")
+
+    def step():
+        out, lse = vdf.attn_forward(q, k, v, kv, m, workspace=ws)
+        return (out, lse, *vdf.attn_backward(q, k, v, out, lse, go, kv, m, workspace=bws))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for n in range(4):
+        kv.copy_(torch.tensor([shape[2] // (n + 1), 17 * n], dtype=torch.int32))
+        q.mul_(1.1)
+        ws.fill_(0xff)
+        bws.fill_(0xff)
+        for t in got:
+            t.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), f"replay {n}"
+
+
+def test_two_streams_at_once():
+    a = _inputs((2, 200, 700, 8, 4, 64), BF16, 102)
+    b = _inputs((1, 1, 9000, 8, 2, 128), BF16, 103)
+    want = [vdf.attn_forward(*x[:3]) for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = []
+        for s, x in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                got.append(vdf.attn_forward(*x[:3]))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+@pytest.mark.parametrize("dtype, shape", list(itertools.product(
+    [F32, BF16], [(2, 21, 40, 4, 2, 16), (1, 130, 70, 2, 2, 64)])))
+def test_autograd(dtype, shape):
+    q, k, v, go, kv, m = _inputs(shape, dtype, 104, True, True)
+    kv = kv.clamp_min(5)
+    leaves = [t.detach().clone().requires_grad_(True) for t in (q, k, v)]
+    out = vdf.cross_attention(*leaves, kv, m)
+    (out.float() * go.float()).sum().backward()
+    torch.cuda.synchronize()
+    Attention(q, k, v, kv, m).check_backward([t.grad for t in leaves], go)
+    assert all(t.grad.dtype == dtype for t in leaves)
+
+
+def test_autograd_of_views_and_shared_states():
+    """Queries off alignment and heads first, states shared by the batch entries, whose gradients
+    add up; a gradient wanted of the keys alone; a second derivative is refused."""
+    gen = torch.Generator().manual_seed(105)
+    base = torch.randn((2, 3, 10, 17), generator=gen).cuda().requires_grad_(True)
+    k = torch.randn((1, 30, 3, 16), generator=gen).cuda().requires_grad_(True)
+    v = torch.randn((1, 30, 3, 16), generator=gen).cuda()
+    q = base[..., 1:].transpose(1, 2)
+    out = vdf.cross_attention(q, k.expand(2, -1, -1, -1), v.expand(2, -1, -1, -1))
+    out.sum().backward()
+    torch.cuda.synchronize()
+    ref = Attention(q.detach(), k.detach().expand(2, -1, -1, -1), v.expand(2, -1, -1, -1))
+    (dq, tq), (dk, tk), _ = ref.backward(torch.ones_like(q))
+    check("q.grad", base.grad[..., 1:].transpose(1, 2), dq, tq)
+    check("k.grad", k.grad, dk.sum(0, keepdim=True), tk.sum(0, keepdim=True) + 2.0 ** -23 * dk.abs().sum(0, keepdim=True))
+    assert (base.grad[..., 0] == 0).all()
+    k2 = k.detach().requires_grad_(True)
+    g, = torch.autograd.grad(vdf.cross_attention(q.detach(), k2.expand(2, -1, -1, -1),
+                                                 v.expand(2, -1, -1, -1)).sum(), k2, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
+def test_gradient_against_differences():
+    """Central differences of the library's own forward in binary32 along the gradient: with a step
+    of h = 2^-7 of unit length the third derivative adds h^2 / 6 times at most (|q| + |k|)^3 / 8
+    scale^3 and a few lower terms, below 30 times the loss's magnitude here, and rounding
+    2^-18 sum |go| / h."""
+    q, k, v, go, _, _ = _inputs((1, 12, 20, 2, 1, 8), F32, 106)
+    out, lse = vdf.attn_forward(q, k, v)
+    grads = vdf.attn_backward(q, k, v, out, lse, go)
+    h = 2.0 ** -7
+    for i in range(3):
+        t = grads[i] / grads[i].norm()
+
+        def loss(sign):
+            x = [q, k, v]
+            x[i] = x[i] + sign * h * t
+            return (vdf.attn_forward(*x)[0].double() * go.double()).sum()
+
+        want = (loss(1) - loss(-1)) / (2 * h)
+        got = (grads[i].double() * t.double()).sum()
+        total = float((go.abs().double().sum()))
+        assert abs(float(got - want)) <= 30 * h * h / 6 * float(go.abs().max()) * 8 + 2.0 ** -18 * total / h
+
+
+def test_long_cache():
+    """One key head's states past 2^32 bytes from the first batch entry's: 2 x 70000 x 128 heads x
+    128 numbers in bfloat16, compared at a few heads and with ragged lengths."""
+    B, Nk, H, D = 2, 70000, 128, 128
+    gen = torch.Generator(device="cuda").manual_seed(107)
+    k = torch.empty((B, Nk, H, D), dtype=BF16, device="cuda")
+    v = torch.empty_like(k)
+    for t in (k, v):
+        for b in range(B):
+            for r in range(0, Nk, 10000):
+                t[b, r:r + 10000] = torch.randn(t[b, r:r + 10000].shape, generator=gen, device="cuda", dtype=BF16)
+    q = torch.randn((B, 1, H, D), generator=gen, device="cuda", dtype=BF16)
+    kv = torch.tensor([Nk, Nk - 12345], dtype=torch.int32, device="cuda")
+    out, lse = vdf.attn_forward(q, k, v, kv)
+    torch.cuda.synchronize()
+    for h in (0, 77, 127):
+        ref = Attention(q[:, :, h:h + 1], k[:, :, h:h + 1], v[:, :, h:h + 1], kv)
+        ref.check_forward(out[:, :, h:h + 1], lse[:, h:h + 1])
+
+
+def test_one_device_at_a_time():
+    q, k, v, _, kv, m = _inputs((2, 3, 9, 2, 1, 16), F32, 108, True, True)
+    with pytest.raises(ValueError, match="GPU"):
+        vdf.attn_forward(q, k, v, kv.cpu())
+    with pytest.raises(TypeError, match="kv_lens"):
+        vdf.attn_forward(q, k, v, kv.long())
+    with pytest.raises(TypeError, match="key_mask"):
+        vdf.attn_forward(q, k, v, kv, m.to(torch.uint8))
+    with pytest.raises(ValueError, match="key_mask"):
+        vdf.attn_forward(q, k, v, kv, m[:, :5])
+    with pytest.raises(ValueError, match="consecutive"):
+        vdf.attn_forward(q, k.transpose(1, 3).contiguous().transpose(1, 3), v)
+    with pytest.raises(TypeError, match="k has"):
+        vdf.attn_forward(q, k.half(), v.half())
+    with pytest.raises(vdf._lib.DAError, match="overlaps"):
+        vdf.attn_forward(q, k, v, out=q)
+    with pytest.raises(ValueError, match="out"):
+        vdf.attn_forward(q, k, v, out=q[:1])
+    with pytest.raises(vdf._lib.DAError, match="places of out"):
+        vdf.attn_forward(q, k, v, out=torch.empty_like(q)[:1].expand(2, -1, -1, -1))

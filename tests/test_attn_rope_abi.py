@@ -1,0 +1,343 @@
+"""The attention's and the rotation's entry points reject malformed calls on the host before any
+HIP call, and the binding checks its tensors (no GPU needed).  Pointers are fake, suitably
+aligned addresses: every call here fails a host-side check or asks for a size."""
+import ctypes
+
+import pytest
+import torch
+
+import view_deformable_feature_amd as vdf
+from view_deformable_feature_amd import _lib
+from view_deformable_feature_amd.build import build, is_stale
+
+FAKE = 0x10000000
+FAR = 0x7000000000
+FARTHER, FARTHEST = 0x7100000000, 0x7200000000
+vp = ctypes.c_void_p
+ref = ctypes.byref
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if is_stale():
+        build()
+    return _lib.load()
+
+
+def _msg(lib):
+    return lib.da_last_error().decode()
+
+
+def _dense(N, H, D):
+    return (ctypes.c_int64 * 3)(N * H * D, H * D, D)
+
+
+def _attn(**kw):
+    d = dict(batch=2, queries=30, keys=50, heads=8, key_heads=4, head_dim=32, scale=0.1, dtype=0,
+             flags=0, reserved=0)
+    d.update(kw)
+    for n, N, H in (("q", "queries", "heads"), ("k", "keys", "key_heads"), ("v", "keys", "key_heads"),
+                    ("out", "queries", "heads"), ("grad", "queries", "heads")):
+        d.setdefault(n + "_stride", _dense(min(d[N], 1 << 20), min(d[H], 1 << 10), d["head_dim"]))
+    return _lib.AttnProblem(**d)
+
+
+def _fwd(lib, p, q=FAKE, k=FAKE, v=FAKE, lens=FAKE, mask=FAKE, out=FAR, lse=FARTHER, ws=FAKE, n=1 << 60):
+    return lib.attn_forward(ref(p), vp(q), vp(k), vp(v), vp(lens), vp(mask), vp(out), vp(lse), vp(ws), n,
+                            None)
+
+
+def _bwd(lib, p, q=FAKE, k=FAKE, v=FAKE, out=FAKE, lse=FAKE, go=FAKE, lens=FAKE, mask=FAKE, gq=FAR,
+         gk=FARTHER, gv=FARTHEST, ws=FAKE, n=1 << 60):
+    return lib.attn_backward(ref(p), vp(q), vp(k), vp(v), vp(out), vp(lse), vp(go), vp(lens), vp(mask),
+                             vp(gq), vp(gk), vp(gv), vp(ws), n, None)
+
+
+ATTN_BAD = [
+    (dict(batch=-1), 1, ">= 0"),
+    (dict(queries=-1), 1, ">= 0"),
+    (dict(keys=-2), 1, ">= 0"),
+    (dict(heads=0), 1, ">= 1"),
+    (dict(key_heads=0), 1, ">= 1"),
+    (dict(head_dim=0), 1, ">= 1"),
+    (dict(key_heads=3), 1, "multiple of key_heads"),
+    (dict(dtype=3), 1, "da_dtype"),
+    (dict(scale=0.0), 1, "scale"),
+    (dict(scale=-1.0), 1, "scale"),
+    (dict(scale=float("nan")), 1, "scale"),
+    (dict(scale=float("inf")), 1, "scale"),
+    (dict(flags=1), 1, "flags"),
+    (dict(reserved=1), 1, "reserved"),
+    (dict(head_dim=20), 2, "multiple of 8"),
+    (dict(head_dim=136), 2, "up to 128"),
+    (dict(keys=1 << 31), 2, "2^31"),
+    (dict(queries=1 << 30), 2, "2^31"),
+    (dict(batch=1 << 30), 2, "2^31"),
+    (dict(heads=1 << 20, key_heads=1 << 20), 2, "2^24"),
+    (dict(queries=1 << 26, batch=1 << 20), 2, "2^45"),
+    (dict(q_stride=(ctypes.c_int64 * 3)(7680, -256, 32)), 1, "negative"),
+    (dict(k_stride=(ctypes.c_int64 * 3)(6400, 130, 32)), 1, "16 bytes"),
+    (dict(v_stride=(ctypes.c_int64 * 3)(6400, 128, 2)), 1, "16 bytes"),
+    (dict(v_stride=(ctypes.c_int64 * 3)(1 << 60, 128, 32)), 1, "16 bytes"),
+    (dict(k_stride=(ctypes.c_int64 * 3)(1 << 30, 1 << 22, 32)), 2, "2^24"),
+    (dict(q_stride=(ctypes.c_int64 * 3)(1 << 56, 256, 32), batch=1 << 9), 2, "2^62"),
+    (dict(out_stride=(ctypes.c_int64 * 3)(7680, 256, 30)), 1, "16 bytes"),
+]
+
+
+@pytest.mark.parametrize("kw, code, needle", ATTN_BAD)
+def test_attention_rejects_malformed_problem(lib, kw, code, needle):
+    p, n = _attn(**kw), ctypes.c_size_t(0)
+    assert _fwd(lib, p) == code and needle in _msg(lib)
+    assert _bwd(lib, p) == code and needle in _msg(lib)
+    assert lib.attn_forward_workspace_size(ref(p), ref(n)) == code
+    assert lib.attn_backward_workspace_size(ref(p), ref(n)) == code
+
+
+def test_attention_rejects_launches_past_32_bits(lib):
+    p = _attn(batch=1 << 15, queries=1 << 22, heads=1, key_heads=1, keys=8, head_dim=8,
+              **{n + "_stride": _dense(8 if n in "kv" else 1 << 22, 1, 8)
+                 for n in ("q", "k", "v", "out", "grad")})
+    far = 1 << 55
+    assert _fwd(lib, p, out=far, lse=2 * far) == 2 and "workgroups" in _msg(lib)
+    assert _bwd(lib, p, gq=far, gk=2 * far, gv=3 * far) == 2 and "workgroups" in _msg(lib)
+
+
+def test_attention_rejects_pointers(lib):
+    p, h = _attn(), _attn(dtype=1)
+    for kw in (dict(q=0), dict(k=0), dict(v=0), dict(out=0)):
+        assert _fwd(lib, p, **kw) == 1 and "NULL" in _msg(lib)
+    for kw in (dict(q=0), dict(k=0), dict(v=0), dict(out=0), dict(lse=0), dict(go=0), dict(gk=0),
+               dict(gv=0)):
+        assert _bwd(lib, p, **kw) == 1 and "NULL" in _msg(lib)
+    for kw in (dict(q=FAKE + 8), dict(k=FAKE + 4), dict(v=FAKE + 8), dict(out=FAR + 8),
+               dict(lse=FARTHER + 2), dict(lens=FAKE + 2)):
+        for x in (p, h):
+            assert _fwd(lib, x, **kw) == 1 and "aligned" in _msg(lib)
+    for kw in (dict(q=FAKE + 8), dict(out=FAKE + 8), dict(go=FAKE + 2), dict(gq=FAR + 8),
+               dict(gk=FARTHER + 4), dict(gv=FARTHEST + 8), dict(lse=FAKE + 2), dict(lens=FAKE + 1)):
+        assert _bwd(lib, p, **kw) == 1 and "aligned" in _msg(lib)
+    # q's 61440 bytes and k's 51200 from FAKE on
+    for out in (FAKE, FAKE + 61424, FAKE - 61424):
+        assert _fwd(lib, p, out=out) == 1 and "overlaps" in _msg(lib)
+    assert _fwd(lib, p, lse=FAKE + 16) == 1 and _fwd(lib, p, lse=FAR + 16) == 1
+    assert "overlaps" in _msg(lib)
+    for kw in (dict(gq=FAKE), dict(gk=FAKE + 61424), dict(gv=FAKE - 16)):
+        assert _bwd(lib, p, **kw) == 1 and "overlaps" in _msg(lib)
+    for kw in (dict(gq=FARTHER), dict(gk=FARTHEST - 16), dict(gv=FAR + 16)):
+        assert _bwd(lib, p, **kw) == 1 and "overlap" in _msg(lib)
+    for st in ((7680, 0, 32), (7680, 256, 16), (0, 256, 32)):
+        assert _fwd(lib, _attn(out_stride=(ctypes.c_int64 * 3)(*st))) == 1
+        assert "places of out overlap" in _msg(lib)
+    bad = _attn(grad_stride=(ctypes.c_int64 * 3)(7680, 250, 32))
+    assert _bwd(lib, bad) == 1 and "grad_out" in _msg(lib)
+    assert lib.attn_forward(None, *[None] * 8, 0, None) == 1 and "NULL" in _msg(lib)
+    assert lib.attn_backward(None, *[None] * 12, 0, None) == 1 and "NULL" in _msg(lib)
+    assert lib.attn_forward_workspace_size(ref(p), None) == 1
+    assert lib.attn_backward_workspace_size(ref(p), None) == 1
+
+
+def test_attention_workspaces(lib):
+    n = ctypes.c_size_t(0)
+    p = _attn(queries=1, keys=40000)            # few rows: keys are split
+    assert lib.attn_forward_workspace_size(ref(p), ref(n)) == 0 and n.value > 0
+    assert _fwd(lib, p, ws=0) == 1 and "workspace is NULL" in _msg(lib)
+    assert _fwd(lib, p, ws=FAKE + 128) == 1 and "256-byte" in _msg(lib)
+    assert _fwd(lib, p, n=n.value - 1) == 1 and str(n.value) in _msg(lib)
+    q = _attn()
+    assert lib.attn_backward_workspace_size(ref(q), ref(n)) == 0 and n.value >= 2 * 4 * 2 * 8 * 30
+    assert _bwd(lib, q, ws=0) == 1 and _bwd(lib, q, ws=FAKE + 4) == 1
+    assert _bwd(lib, q, n=n.value - 1) == 1 and str(n.value) in _msg(lib)
+    for kw in (dict(batch=0), dict(queries=0)):
+        e = _attn(**kw)
+        assert lib.attn_forward_workspace_size(ref(e), ref(n)) == 0 and n.value == 0
+        assert lib.attn_forward(ref(e), *[None] * 8, 0, None) == 0
+    assert lib.attn_backward(ref(_attn(batch=0)), *[None] * 12, 0, None) == 0
+
+
+def _rope(**kw):
+    d = dict(head_dim=32, rotated=16, eps=1e-6, magnitude=1.0, layout=0, dtype=0, flags=0, reserved=0)
+    d.update(kw)
+    return _lib.RopeProblem(**d)
+
+
+def _heads(**kw):
+    d = dict(batch=2, tokens=30, heads=8, pos_stride=30, pos_type=2, reserved=0)
+    d.update(kw)
+    for n in ("x_stride", "y_stride"):
+        d.setdefault(n, _dense(min(d["tokens"], 1 << 20), min(d["heads"], 1 << 10), 32))
+    return _lib.RopeTensor(**d)
+
+
+def _rot(lib, p, t, x=FAKE, pos=FAKE, f=FAKE, y=FAR):
+    return lib.rope_forward(ref(p), ref(t), vp(x), vp(pos), vp(f), vp(y), None)
+
+
+def _norm(lib, p, t, x=FAKE, pos=FAKE, w=FAKE, y=FAR, k=None, kx=FARTHER, ky=FARTHEST, f=FAKE):
+    none = [vp(kx), vp(FAKE), vp(FAKE), vp(ky)]
+    return lib.rope_norm_forward(ref(p), ref(t), vp(x), vp(pos), vp(w), vp(y),
+                                 None if k is None else ref(k), *none, vp(f), None)
+
+
+def _ngrad(lib, p, t, x=FAKE, pos=FAKE, w=FAKE, g=FAKE, dx=FAR, dw=FAKE, f=FAKE, ws=FAKE, n=1 << 40):
+    return lib.rope_norm_backward(ref(p), ref(t), vp(x), vp(pos), vp(w), vp(g), vp(dx), vp(dw),
+                                  None, *[None] * 6, vp(f), vp(ws), n, None)
+
+
+ROPE_BAD = [
+    (dict(head_dim=0), 1, "head_dim"),
+    (dict(rotated=17), 1, "even"),
+    (dict(rotated=34), 1, "within"),
+    (dict(rotated=-2), 1, "within"),
+    (dict(dtype=5), 1, "da_dtype"),
+    (dict(layout=2), 1, "rope_layout"),
+    (dict(magnitude=float("inf")), 1, "magnitude"),
+    (dict(flags=2), 1, "flags"),
+    (dict(reserved=1), 1, "reserved"),
+    (dict(head_dim=514), 2, "512"),
+]
+
+
+@pytest.mark.parametrize("kw, code, needle", ROPE_BAD)
+def test_rotation_rejects_malformed_problem(lib, kw, code, needle):
+    p, t, n = _rope(**kw), _heads(), ctypes.c_size_t(0)
+    for f in (_rot, _norm, _ngrad):
+        assert f(lib, p, t) == code and needle in _msg(lib)
+    assert lib.rope_norm_backward_workspace_size(ref(p), ref(t), None, ref(n)) == code
+
+
+TENSOR_BAD = [
+    (dict(batch=-1), 1, ">= 0"),
+    (dict(tokens=-1), 1, ">= 0"),
+    (dict(heads=0), 1, ">= 1"),
+    (dict(pos_type=4), 1, "pos_type"),
+    (dict(pos_stride=-1), 1, "pos_stride"),
+    (dict(reserved=1), 1, "reserved"),
+    (dict(x_stride=(ctypes.c_int64 * 3)(1, -1, 1)), 1, "stride"),
+    (dict(y_stride=(ctypes.c_int64 * 3)(1 << 57, 1, 1)), 1, "stride"),
+    (dict(batch=1 << 31), 2, "2^31"),
+    (dict(tokens=1 << 31), 2, "2^31"),
+    (dict(heads=1 << 31), 2, "2^31"),
+    (dict(batch=1 << 30, tokens=1 << 30), 2, "2^56"),
+    (dict(x_stride=(ctypes.c_int64 * 3)(1 << 55, 256, 32), batch=1 << 9), 2, "2^62"),
+]
+
+
+@pytest.mark.parametrize("kw, code, needle", TENSOR_BAD)
+def test_rotation_rejects_malformed_tensor(lib, kw, code, needle):
+    p, t, n = _rope(), _heads(**kw), ctypes.c_size_t(0)
+    for f in (_rot, _norm, _ngrad):
+        assert f(lib, p, t) == code and needle in _msg(lib)
+    assert _norm(lib, p, _heads(), k=t) == code
+    assert lib.rope_norm_backward_workspace_size(ref(p), ref(t), None, ref(n)) == code
+
+
+def test_rotation_rejects_pointers(lib):
+    p, t = _rope(), _heads()
+    for kw in (dict(x=0), dict(y=0), dict(f=0), dict(pos=0)):
+        assert _rot(lib, p, t, **kw) == 1 and "NULL" in _msg(lib)
+        assert _norm(lib, p, t, **kw) == 1 and "NULL" in _msg(lib)
+    for kw in (dict(x=0), dict(g=0), dict(f=0), dict(pos=0)):
+        assert _ngrad(lib, p, t, **kw) == 1 and "NULL" in _msg(lib)
+    for kw in (dict(x=FAKE + 2), dict(y=FAR + 1), dict(f=FAKE + 4), dict(pos=FAKE + 4)):
+        assert _rot(lib, p, t, **kw) == 1 and "aligned" in _msg(lib)
+        assert _norm(lib, p, t, **kw) == 1 and "aligned" in _msg(lib)
+    assert _norm(lib, p, t, w=FAKE + 2) == 1 and "aligned" in _msg(lib)
+    for kw in (dict(dx=FAR + 2), dict(w=FAKE + 2), dict(dw=FAKE + 1), dict(g=FAKE + 2)):
+        assert _ngrad(lib, p, t, **kw) == 1 and "aligned" in _msg(lib)
+    # a result beside x but not x, x itself with other strides, and places written twice
+    assert _rot(lib, p, t, y=FAKE + 64) == 1 and "overlaps" in _msg(lib)
+    other = _heads(y_stride=(ctypes.c_int64 * 3)(7680, 32, 960))
+    assert _rot(lib, p, other, y=FAKE) == 1 and "overlaps" in _msg(lib)
+    for s in ((7680, 0, 32), (7680, 256, 16), (256, 256, 32), (100, 256, 32)):
+        twice = _heads(y_stride=(ctypes.c_int64 * 3)(*s))
+        assert _rot(lib, p, twice) == 1 and "overlap" in _msg(lib)
+        assert _norm(lib, p, twice) == 1
+    # q's result over k, k's result over q's
+    k = _heads(heads=4)
+    assert _norm(lib, p, t, k=k, y=FARTHER) == 1 and "overlaps" in _msg(lib)
+    assert _norm(lib, p, t, k=k, ky=FAKE) == 1 and "overlaps" in _msg(lib)
+    assert _norm(lib, p, t, k=k, ky=FAR + 4096) == 1 and "overlaps" in _msg(lib)
+    assert _norm(lib, _rope(eps=-1.0), t) == 1 and "eps" in _msg(lib)
+    assert _norm(lib, _rope(flags=1), t) == 1 and "flags" in _msg(lib)
+    assert _ngrad(lib, p, t, dx=FAKE, g=FARTHER) == 1 and "overlaps" in _msg(lib)
+    assert _ngrad(lib, p, t, g=FARTHER, dx=FARTHER + 64) == 1 and "overlaps" in _msg(lib)
+    assert lib.rope_forward(ref(p), None, *[None] * 5) == 1
+    assert lib.rope_forward(None, ref(t), *[None] * 5) == 1
+    assert lib.rope_forward(ref(p), ref(_heads(batch=0)), *[None] * 5) == 0
+    assert lib.rope_norm_forward(ref(p), None, *[None] * 4, None, *[None] * 4, None, None) == 0
+    big = _heads(batch=1 << 14, tokens=1 << 20, heads=8)
+    assert _rot(lib, p, big, y=1 << 55) == 2 and "workgroups" in _msg(lib)
+
+
+def test_rotation_workspaces(lib):
+    p, t, n = _rope(), _heads(), ctypes.c_size_t(0)
+    assert lib.rope_norm_backward_workspace_size(ref(p), ref(t), None, ref(n)) == 0 and n.value > 0
+    assert _ngrad(lib, p, t, ws=0) == 1 and "workspace is NULL" in _msg(lib)
+    assert _ngrad(lib, p, t, ws=FAKE + 16) == 1 and "256-byte" in _msg(lib)
+    assert _ngrad(lib, p, t, n=n.value - 1) == 1 and str(n.value) in _msg(lib)
+    assert lib.rope_norm_backward_workspace_size(ref(p), ref(t), None, None) == 1
+
+
+def test_binding_refuses():
+    """Types, shapes, devices and names, before the library is called."""
+    q, k = torch.zeros((2, 5, 4, 8)), torch.zeros((2, 7, 2, 8))
+    f = torch.zeros(4, dtype=torch.float64)
+    with pytest.raises(ValueError, match="GPU"):
+        vdf.attn_forward(q, k, k)
+    with pytest.raises(ValueError, match="head_dim"):
+        vdf.attn_forward(q[0], k, k)
+    with pytest.raises(ValueError, match="fit together"):
+        vdf.attn_forward(q, k, k[:, :6])
+    with pytest.raises(ValueError, match="fit together"):
+        vdf.attn_forward(q[:1], k, k)
+    with pytest.raises(TypeError):
+        vdf.attn_forward(q.double(), k.double(), k.double())
+    with pytest.raises(_lib.DAError, match="scale"):
+        vdf.attn_forward(q, k, k, scale=0.0)
+    with pytest.raises(_lib.DAError, match="multiple of key_heads"):
+        vdf.attn_workspace_size(q[:, :, :3], k, k)
+    with pytest.raises(_lib.DAError, match="16 bytes"):
+        vdf.attn_workspace_size(q[..., :8], torch.zeros((2, 7, 2, 9))[..., :8],
+                                torch.zeros((2, 7, 2, 9))[..., :8])
+    assert vdf.attn_workspace_size(q, k, k) == 0 and vdf.attn_backward_workspace_size(q, k, k) > 0
+    with pytest.raises(ValueError, match="GPU"):
+        vdf.attn_backward(q, k, k, q, q, q)
+    with pytest.raises(ValueError, match="GPU"):
+        vdf.rope_forward(q, f)
+    with pytest.raises(ValueError, match="head_dim"):
+        vdf.rope_forward(q[0], f)
+    with pytest.raises(TypeError):
+        vdf.rope_forward(q.double(), f)
+    with pytest.raises(ValueError, match="GPU"):
+        vdf.rope_norm_forward(q, k, None, None, f)
+    with pytest.raises(ValueError, match="one type"):
+        vdf.rope_norm_forward(q, k.half(), None, None, f)
+    with pytest.raises(ValueError, match="grad_q_out"):
+        vdf.rope_norm_backward(q, None, q[:1], None, None, None, f)
+    assert vdf.rope_norm_backward_workspace_size(q, k) > 0
+    for kw in (dict(rotated=7), dict(base=1.0), dict(factor=0.5), dict(scaling="cubic"),
+               dict(scaling="blend"), dict(scaling="blend", trained=100, fast=1, slow=2)):
+        with pytest.raises(ValueError):
+            vdf.rope_frequencies(**dict(dict(rotated=8, device="cpu"), **kw))
+
+
+def test_frequencies():
+    """Each kind of scaling by its definition."""
+    def make(**kw):
+        return vdf.rope_frequencies(64, device="cpu", **kw)
+
+    plain, one = make()
+    i = torch.arange(32, dtype=torch.float64)
+    assert one == 1 and torch.equal(plain, 10000.0 ** (-i / 32))
+    assert torch.equal(make(scaling="linear", factor=4.0)[0], plain / 4)
+    wide = make(scaling="base", factor=8.0)[0]
+    assert wide[0] == 1 and abs(float(wide[-1] * 8 / plain[-1]) - 1) < 1e-14
+    blend, m = make(scaling="blend", factor=16.0, trained=4096)
+    turns = 4096 * plain / (2 * torch.pi)
+    assert abs(m - 1.2772588722239782) < 1e-15
+    assert torch.equal(blend[turns >= 40], plain[turns >= 40])
+    assert torch.allclose(blend[turns <= 0.7], plain[turns <= 0.7] / 16, rtol=1e-15)
+    assert ((blend <= plain) & (blend >= plain / 16 * (1 - 1e-15))).all() and (blend.diff() < 0).all()
+    assert vdf.rope_frequencies(0, device="cpu")[0].shape == (0,)
+    assert vdf.rope_frequencies(2, scaling="base", factor=2.0, device="cpu")[0].tolist() == [1.0]

@@ -1,8 +1,8 @@
 """Sparse4D-style deformable aggregation for AMD Instinct MI355X (gfx950).
 
 The computation lives in ``libdeformagg.so`` (HIP kernels behind a C ABI,
-declared in ``include/*.h``); ``api``, ``pack``, ``dcn``, ``norm`` and ``int8``
-bind it to PyTorch tensors.
+declared in ``include/*.h``); ``api``, ``pack``, ``dcn``, ``norm``, ``int8``,
+``rotary`` and ``attention`` bind it to PyTorch tensors.
 ``workloads`` draws seeded synthetic inputs.
 """
 from .api import (DeformableAggregationFunction, da_backward, da_backward_accumulate,  # noqa: F401
@@ -21,5 +21,13 @@ from .norm import (GroupNormActFunction, gn_backward, gn_backward_workspace_size
 from .int8 import (i8_linear, i8_linear_workspace_size, i8_matmul,  # noqa: F401
                    i8_matmul_workspace_size, i8_norm_linear, i8_norm_linear_workspace_size,
                    i8_quantize_rows)
+
+from .rotary import (NormRotaryFunction, RotaryFunction, norm_rotary, rope_forward,  # noqa: F401
+                     rope_frequencies, rope_norm_backward, rope_norm_backward_workspace_size,
+                     rope_norm_forward, rotary)
+
+from .attention import (CrossAttentionFunction, attn_backward,  # noqa: F401
+                        attn_backward_workspace_size, attn_forward, attn_workspace_size,
+                        cross_attention)
 
 __version__ = "1.2.0"

@@ -14,11 +14,13 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libdeformagg.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "deformagg.h")
 HEADER_PATHS = [os.path.join(os.path.dirname(HEADER_PATH), f)
-                for f in ("deformagg.h", "dcn.h", "group_norm.h", "int8.h")]
+                for f in ("deformagg.h", "dcn.h", "group_norm.h", "int8.h", "attention.h", "rotary.h")]
 
 DA_OK, DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED, DA_ERR_HIP = 0, 1, 2, 3
 DA_F32, DA_BF16, DA_F16 = 0, 1, 2
 DA_ACT_NONE, DA_ACT_RELU, DA_ACT_SILU, DA_ACT_GELU = 0, 1, 2, 3
+ROPE_LAYOUT_HALF, ROPE_LAYOUT_INTERLEAVED, ROPE_FLAG_INVERSE = 0, 1, 1
+ROPE_POS_INDEX, ROPE_POS_I32, ROPE_POS_I64, ROPE_POS_F32 = 0, 1, 2, 3
 DA_FLAG_SLICES_ALWAYS, DA_FLAG_SLICES_NEVER, DA_FLAG_BWD_REGATHER, DA_FLAG_BWD_ROW_ORDER = \
     1, 2, 4, 8
 DA_FLAG_DETERMINISTIC = 16
@@ -84,6 +86,52 @@ class I8Problem(ctypes.Structure):
         ("x_dtype", ctypes.c_int32),
         ("out_dtype", ctypes.c_int32),
         ("flags", ctypes.c_int32),
+    ]
+
+
+class AttnProblem(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("queries", ctypes.c_int64),
+        ("keys", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("key_heads", ctypes.c_int64),
+        ("head_dim", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64 * 3),
+        ("k_stride", ctypes.c_int64 * 3),
+        ("v_stride", ctypes.c_int64 * 3),
+        ("out_stride", ctypes.c_int64 * 3),
+        ("grad_stride", ctypes.c_int64 * 3),
+        ("scale", ctypes.c_float),
+        ("dtype", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class RopeProblem(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int64),
+        ("rotated", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("magnitude", ctypes.c_float),
+        ("layout", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class RopeTensor(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("tokens", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64 * 3),
+        ("y_stride", ctypes.c_int64 * 3),
+        ("pos_stride", ctypes.c_int64),
+        ("pos_type", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -167,6 +215,19 @@ def load() -> ctypes.CDLL:
                  "i8_linear_workspace_size", "i8_linear", "i8_norm_linear_workspace_size",
                  "i8_norm_linear"):
         getattr(lib, name).restype = ctypes.c_int
+    aprob, rprob, rten = (ctypes.POINTER(t) for t in (AttnProblem, RopeProblem, RopeTensor))
+    lib.attn_forward_workspace_size.argtypes = [aprob, szp]
+    lib.attn_forward.argtypes = [aprob] + [vp] * 8 + [size_t, vp]
+    lib.attn_backward_workspace_size.argtypes = [aprob, szp]
+    lib.attn_backward.argtypes = [aprob] + [vp] * 12 + [size_t, vp]
+    lib.rope_forward.argtypes = [rprob, rten] + [vp] * 5
+    lib.rope_norm_forward.argtypes = [rprob] + ([rten] + [vp] * 4) * 2 + [vp, vp]
+    lib.rope_norm_backward_workspace_size.argtypes = [rprob, rten, rten, szp]
+    lib.rope_norm_backward.argtypes = [rprob] + ([rten] + [vp] * 6) * 2 + [vp, vp, size_t, vp]
+    for name in ("attn_forward_workspace_size", "attn_forward", "attn_backward_workspace_size",
+                 "attn_backward", "rope_forward", "rope_norm_forward",
+                 "rope_norm_backward_workspace_size", "rope_norm_backward"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.da_status_string.argtypes = [ctypes.c_int]
     lib.da_status_string.restype = ctypes.c_char_p
     lib.da_last_error.argtypes = []
@@ -190,5 +251,5 @@ def declared_functions() -> List[str]:
         with open(path) as f:
             text = f.read()
         text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-        names += re.findall(r"\b((?:da|dcn|gn|i8)_[a-z0-9_]+)\s*\(", text)
+        names += re.findall(r"\b((?:da|dcn|gn|i8|attn|rope)_[a-z0-9_]+)\s*\(", text)
     return names

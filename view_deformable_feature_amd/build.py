@@ -20,11 +20,14 @@ PROBE_SOURCE = os.path.join(PKG_DIR, "csrc", "bw_probe.hip")
 SOURCES = [os.path.join(CSRC, f)
            for f in ("da_forward.hip", "da_backward.hip", "da_pack.hip", "da_api.cpp", "dcn.hip",
                      "dcn_api.cpp", "da_noalloc.hip", "gn.hip", "gn_api.cpp", "i8.hip",
-                     "i8_api.cpp")]
-HEADERS = [os.path.join(INCLUDE, f) for f in ("deformagg.h", "dcn.h", "group_norm.h", "int8.h")] + [
+                     "i8_api.cpp", "attn_forward.hip", "attn_grad_q.hip", "attn_grad_kv.hip",
+                     "attn_api.cpp", "rope.hip", "rope_api.cpp")]
+HEADERS = [os.path.join(INCLUDE, f) for f in ("deformagg.h", "dcn.h", "group_norm.h", "int8.h",
+                                                "attention.h", "rotary.h")] + [
     os.path.join(CSRC, f) for f in ("da_internal.h", "da_device.h", "da_pack.h", "dcn_internal.h",
-                                    "host_errors.h", "act_device.h", "gn_internal.h",
-                                    "i8_internal.h")]
+                                    "host_errors.h", "host_strides.h", "act_device.h", "gn_internal.h",
+                                    "i8_internal.h", "attn_device.h", "attn_internal.h",
+                                    "rope_internal.h")]
 EXPORTS = os.path.join(CSRC, "exports.map")   # the C ABI is the only export
 ARCH = "gfx950"
 

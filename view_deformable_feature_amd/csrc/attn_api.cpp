@@ -1,0 +1,302 @@
+// Host side of the attention: argument checks, the form a problem takes, dispatch.  Every check
+// runs before anything is enqueued.  Contract: include/attention.h.
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "attention.h"
+#include "attn_internal.h"
+#include "host_errors.h"
+#include "host_strides.h"
+
+namespace {
+
+using da::extent_bytes;
+using da::ranges_clash;
+using da::report_error;
+
+typedef da::wide_t wide;
+constexpr int64_t k2to31 = int64_t(1) << 31;
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+int elem_bytes(int32_t t) { return t == DA_F32 ? 4 : 2; }
+uint64_t part_bytes(uint64_t n) { return (n + 255) & ~uint64_t(255); }
+
+da_status check_strides(const char* name, const int64_t (&stride)[3], int64_t batch, int64_t tokens,
+                        int64_t heads, int64_t D, int e) {
+    for (int64_t s : stride) {
+        if (s < 0) return report_error(DA_ERR_INVALID_ARG, "a stride of %s is negative", name);
+        if (s > (int64_t(1) << 56) || s * e % 16 != 0)
+            return report_error(DA_ERR_INVALID_ARG, "a stride of %s is not a multiple of 16 bytes", name);
+    }
+    if (stride[1] * e >= (1 << 24))
+        return report_error(DA_ERR_UNSUPPORTED, "a token of %s takes 2^24 bytes or more", name);
+    if (extent_bytes(stride, batch, tokens, heads, D, e) >= ((wide)1 << 62))
+        return report_error(DA_ERR_UNSUPPORTED, "%s spans 2^62 bytes or more", name);
+    return DA_OK;
+}
+
+da_status check_problem(const attn_problem* p) {
+    if (!p) return report_error(DA_ERR_INVALID_ARG, "problem is NULL");
+    if (p->flags != 0 || p->reserved != 0)
+        return report_error(DA_ERR_INVALID_ARG, "problem.flags and problem.reserved must be 0");
+    if (p->batch < 0 || p->queries < 0 || p->keys < 0)
+        return report_error(DA_ERR_INVALID_ARG, "batch, queries and keys must be >= 0");
+    if (p->heads < 1 || p->key_heads < 1 || p->head_dim < 1)
+        return report_error(DA_ERR_INVALID_ARG, "heads, key_heads and head_dim must be >= 1");
+    if (p->heads % p->key_heads != 0)
+        return report_error(DA_ERR_INVALID_ARG, "heads (%lld) is not a multiple of key_heads (%lld)",
+                            (long long)p->heads, (long long)p->key_heads);
+    if (p->dtype != DA_F32 && p->dtype != DA_BF16 && p->dtype != DA_F16)
+        return report_error(DA_ERR_INVALID_ARG, "dtype %d is not a da_dtype", (int)p->dtype);
+    if (!isfinite(p->scale) || !(p->scale > 0.0f))
+        return report_error(DA_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (p->head_dim % 8 != 0 || p->head_dim > 128)
+        return report_error(DA_ERR_UNSUPPORTED, "head_dim is not a multiple of 8 up to 128");
+    const int e = elem_bytes(p->dtype);
+    if (p->batch >= k2to31 || p->queries >= k2to31 || p->keys >= k2to31 - 256 || p->heads >= k2to31 ||
+        (wide)p->queries * (p->heads / p->key_heads) >= k2to31 - 256 ||
+        (wide)p->batch * p->key_heads >= k2to31 || (wide)p->heads * p->head_dim * e >= (1 << 24))
+        return report_error(DA_ERR_UNSUPPORTED,
+                            "2^31 rows, keys or key heads, or heads of 2^24 bytes a token");
+    if ((wide)p->batch * p->queries * p->heads >= (wide)1 << 45 ||
+        (wide)p->batch * p->keys * p->key_heads >= (wide)1 << 45)
+        return report_error(DA_ERR_UNSUPPORTED, "2^45 rows or keys");
+    da_status st = check_strides("q", p->q_stride, p->batch, p->queries, p->heads, p->head_dim, e);
+    if (st == DA_OK) st = check_strides("k", p->k_stride, p->batch, p->keys, p->key_heads, p->head_dim, e);
+    if (st == DA_OK) st = check_strides("v", p->v_stride, p->batch, p->keys, p->key_heads, p->head_dim, e);
+    if (st == DA_OK)
+        st = check_strides("out", p->out_stride, p->batch, p->queries, p->heads, p->head_dim, e);
+    return st;
+}
+
+void describe(const attn_problem* p, da::AttnArgs& a) {
+    memset(&a, 0, sizeof a);
+    const int64_t e = elem_bytes(p->dtype);
+    a.q_batch = p->q_stride[0] * e, a.q_token = p->q_stride[1] * e, a.q_head = p->q_stride[2] * e;
+    a.k_batch = p->k_stride[0] * e, a.k_token = p->k_stride[1] * e, a.k_head = p->k_stride[2] * e;
+    a.v_batch = p->v_stride[0] * e, a.v_token = p->v_stride[1] * e, a.v_head = p->v_stride[2] * e;
+    a.o_batch = p->out_stride[0] * e, a.o_token = p->out_stride[1] * e, a.o_head = p->out_stride[2] * e;
+    a.g_batch = p->grad_stride[0] * e, a.g_token = p->grad_stride[1] * e, a.g_head = p->grad_stride[2] * e;
+    a.B = (int32_t)p->batch;
+    a.Nq = (int32_t)p->queries;
+    a.Nk = (int32_t)p->keys;
+    a.H = (int32_t)p->heads;
+    a.Hk = (int32_t)p->key_heads;
+    a.D = (int32_t)p->head_dim;
+    a.group = a.H / a.Hk;
+    a.rows = a.Nq * a.group;
+    a.splits = 1;
+    a.split_keys = std::max(a.Nk, 1);
+    a.scale = p->scale;
+    a.scale2 = (float)((double)p->scale * 1.4426950408889634);
+    a.dtype = p->dtype;
+}
+
+// The form for so many columns to a key head: wide where that gives every compute unit a workgroup,
+// else deep, four times as many; always deep where one of its workgroups has all columns.
+void choose_form(da::AttnArgs& a, int64_t columns) {
+    const int64_t units = (int64_t)a.B * a.Hk;
+    a.deep = columns <= da::kAttnDeep ||
+             units * ((columns + da::kAttnWide - 1) / da::kAttnWide) < 256;
+    const int64_t width = a.deep ? da::kAttnDeep : da::kAttnWide;
+    a.col_tiles = (int32_t)((columns + width - 1) / width);
+}
+
+// The forward's form; where even the deep one leaves compute units without work, the keys are
+// split over workgroups.
+void choose_forward(da::AttnArgs& a) {
+    choose_form(a, a.rows);
+    const int64_t blocks = (int64_t)a.B * a.Hk * a.col_tiles;
+    const int64_t tiles = (a.Nk + da::kAttnDeepTile - 1) / da::kAttnDeepTile;
+    if (a.deep && blocks < 256 && tiles > 1) {
+        const int64_t splits = std::min(tiles, 512 / std::max<int64_t>(blocks, 1));
+        const int64_t per = (tiles + splits - 1) / splits;
+        a.split_keys = (int32_t)(per * da::kAttnDeepTile);
+        a.splits = (int32_t)((tiles + per - 1) / per);
+    }
+}
+
+// Counts the workgroups; a launch has fewer than 2^32 threads.
+da_status count_blocks(da::AttnArgs& a) {
+    const wide blocks = (wide)a.B * a.Hk * a.col_tiles * a.splits;
+    if (blocks + 8 >= (wide(1) << 32) / da::kAttnThreads)
+        return report_error(DA_ERR_UNSUPPORTED, "2^32 threads of workgroups or more");
+    a.blocks = (int32_t)blocks;
+    return DA_OK;
+}
+
+uint64_t stat_bytes(const da::AttnArgs& a) {
+    return part_bytes((uint64_t)a.splits * a.B * a.Hk * a.rows * sizeof(float2));
+}
+uint64_t need_forward(const da::AttnArgs& a) {
+    if (a.splits == 1) return 0;
+    return stat_bytes(a) + part_bytes((uint64_t)a.splits * a.B * a.Hk * a.rows * a.D * sizeof(float));
+}
+uint64_t row_bytes(const da::AttnArgs& a) { return part_bytes((uint64_t)a.B * a.H * a.Nq * sizeof(float)); }
+
+da_status check_workspace(uint64_t need, const void* workspace, size_t workspace_bytes) {
+    if (!need) return DA_OK;
+    if (!workspace) return report_error(DA_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned(workspace, 256))
+        return report_error(DA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+    if (workspace_bytes < need)
+        return report_error(DA_ERR_INVALID_ARG, "workspace has %zu bytes, %llu needed",
+                            workspace_bytes, (unsigned long long)need);
+    return DA_OK;
+}
+
+struct Sizes {
+    wide q, k, v, out, grad, dense_q, dense_k;
+};
+Sizes sizes_of(const attn_problem* p) {
+    const int e = elem_bytes(p->dtype);
+    return {extent_bytes(p->q_stride, p->batch, p->queries, p->heads, p->head_dim, e),
+            extent_bytes(p->k_stride, p->batch, p->keys, p->key_heads, p->head_dim, e),
+            extent_bytes(p->v_stride, p->batch, p->keys, p->key_heads, p->head_dim, e),
+            extent_bytes(p->out_stride, p->batch, p->queries, p->heads, p->head_dim, e),
+            extent_bytes(p->grad_stride, p->batch, p->queries, p->heads, p->head_dim, e),
+            (wide)p->batch * p->queries * p->heads * p->head_dim * e,
+            (wide)p->batch * p->keys * p->key_heads * p->head_dim * e};
+}
+
+da_status check_inputs(const attn_problem* p, const void* q, const void* k, const void* v,
+                       const int32_t* kv_lens) {
+    if ((p->queries > 0 && !q) || (p->keys > 0 && (!k || !v)))
+        return report_error(DA_ERR_INVALID_ARG, "q / k / v is NULL");
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16))
+        return report_error(DA_ERR_INVALID_ARG, "q / k / v is not 16-byte aligned");
+    if (!aligned(kv_lens, 4)) return report_error(DA_ERR_INVALID_ARG, "kv_lens is not 4-byte aligned");
+    return DA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+da_status attn_forward_workspace_size(const attn_problem* p, size_t* bytes) {
+    if (!bytes) return report_error(DA_ERR_INVALID_ARG, "bytes is NULL");
+    const da_status st = check_problem(p);
+    if (st != DA_OK) return st;
+    da::AttnArgs a;
+    describe(p, a);
+    choose_forward(a);
+    *bytes = p->batch == 0 || p->queries == 0 ? 0 : (size_t)need_forward(a);
+    return DA_OK;
+}
+
+da_status attn_forward(const attn_problem* p, const void* q, const void* k, const void* v,
+                       const int32_t* kv_lens, const uint8_t* key_mask, void* out, float* lse,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    da_status st = check_problem(p);
+    if (st != DA_OK) return st;
+    if (p->batch == 0 || p->queries == 0) return DA_OK;
+    st = check_inputs(p, q, k, v, kv_lens);
+    if (st != DA_OK) return st;
+    if (!out) return report_error(DA_ERR_INVALID_ARG, "out is NULL");
+    if (!aligned(out, 16) || !aligned(lse, 4))
+        return report_error(DA_ERR_INVALID_ARG, "out is not 16-byte aligned, or lse not 4-byte");
+    const Sizes n = sizes_of(p);
+    const wide lse_bytes = (wide)p->batch * p->heads * p->queries * 4;
+    if (ranges_clash(out, n.out, q, n.q) || ranges_clash(out, n.out, k, n.k) || ranges_clash(out, n.out, v, n.v) ||
+        ranges_clash(out, n.out, lse, lse_bytes) || ranges_clash(lse, lse_bytes, q, n.q) ||
+        ranges_clash(lse, lse_bytes, k, n.k) || ranges_clash(lse, lse_bytes, v, n.v))
+        return report_error(DA_ERR_INVALID_ARG, "out or lse overlaps an input, or the other");
+    if (da::overlaps_itself(p->out_stride, p->batch, p->queries, p->heads, p->head_dim))
+        return report_error(DA_ERR_INVALID_ARG, "places of out overlap");
+    da::AttnArgs a;
+    describe(p, a);
+    choose_forward(a);
+    st = count_blocks(a);
+    if (st == DA_OK) st = check_workspace(need_forward(a), workspace, workspace_bytes);
+    if (st != DA_OK) return st;
+    a.q = q, a.k = k, a.v = v;
+    a.lens = kv_lens;
+    a.mask = key_mask;
+    a.out = out;
+    a.lse = lse;
+    if (a.splits > 1) {
+        a.part_stat = static_cast<float2*>(workspace);
+        a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + stat_bytes(a));
+    }
+    return da::report_hip(da::launch_attn_forward(a, static_cast<hipStream_t>(stream)),
+                          "attention forward launch");
+}
+
+da_status attn_backward_workspace_size(const attn_problem* p, size_t* bytes) {
+    if (!bytes) return report_error(DA_ERR_INVALID_ARG, "bytes is NULL");
+    const da_status st = check_problem(p);
+    if (st != DA_OK) return st;
+    da::AttnArgs a;
+    describe(p, a);
+    *bytes = (size_t)(2 * row_bytes(a));
+    return DA_OK;
+}
+
+da_status attn_backward(const attn_problem* p, const void* q, const void* k, const void* v,
+                        const void* out, const float* lse, const void* grad_out,
+                        const int32_t* kv_lens, const uint8_t* key_mask, void* grad_q, void* grad_k,
+                        void* grad_v, void* workspace, size_t workspace_bytes, void* stream) {
+    da_status st = check_problem(p);
+    if (st != DA_OK) return st;
+    st = check_strides("grad_out", p->grad_stride, p->batch, p->queries, p->heads, p->head_dim,
+                       elem_bytes(p->dtype));
+    if (st != DA_OK) return st;
+    if (p->batch == 0) return DA_OK;
+    st = check_inputs(p, q, k, v, kv_lens);
+    if (st != DA_OK) return st;
+    if (p->queries > 0 && (!out || !lse || !grad_out))
+        return report_error(DA_ERR_INVALID_ARG, "out / lse / grad_out is NULL");
+    if (p->keys > 0 && !grad_k != !grad_v)
+        return report_error(DA_ERR_INVALID_ARG, "one of grad_k and grad_v is NULL");
+    if (!aligned(out, 16) || !aligned(grad_out, 16) || !aligned(grad_q, 16) || !aligned(grad_k, 16) ||
+        !aligned(grad_v, 16) || !aligned(lse, 4))
+        return report_error(DA_ERR_INVALID_ARG,
+                            "out or a gradient is not 16-byte aligned, or lse not 4-byte");
+    const Sizes n = sizes_of(p);
+    const struct {
+        const void* at;
+        wide bytes;
+    } results[] = {{grad_q, n.dense_q}, {grad_k, n.dense_k}, {grad_v, n.dense_k}},
+      inputs[] = {{q, n.q}, {k, n.k}, {v, n.v}, {out, n.out}, {grad_out, n.grad},
+                  {lse, (wide)p->batch * p->heads * p->queries * 4}};
+    for (int i = 0; i < 3; ++i) {
+        for (const auto& x : inputs)
+            if (ranges_clash(results[i].at, results[i].bytes, x.at, x.bytes))
+                return report_error(DA_ERR_INVALID_ARG, "a gradient overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (ranges_clash(results[i].at, results[i].bytes, results[j].at, results[j].bytes))
+                return report_error(DA_ERR_INVALID_ARG, "two gradients overlap");
+    }
+    da::AttnArgs a, of_q, of_kv;
+    describe(p, a);
+    st = check_workspace(2 * row_bytes(a), workspace, workspace_bytes);
+    if (st != DA_OK) return st;
+    a.q = q, a.k = k, a.v = v;
+    a.lens = kv_lens;
+    a.mask = key_mask;
+    a.out = const_cast<void*>(out);
+    a.lse = const_cast<float*>(lse);
+    a.grad_out = grad_out;
+    a.grad_q = grad_q, a.grad_k = grad_k, a.grad_v = grad_v;
+    a.lse2 = static_cast<float*>(workspace);
+    a.delta = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + row_bytes(a));
+    of_q = of_kv = a;
+    choose_form(of_q, a.rows);
+    choose_form(of_kv, a.Nk);
+    st = count_blocks(of_q);
+    if (st == DA_OK) st = count_blocks(of_kv);
+    if (st != DA_OK) return st;
+    if ((wide)a.B * a.Nq * a.H * 8 >= wide(1) << 32)
+        return report_error(DA_ERR_UNSUPPORTED, "2^29 rows or more");
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    if (p->queries > 0 && (grad_q || (grad_k && p->keys > 0))) e = da::launch_attn_delta(a, s);
+    if (e == hipSuccess && grad_q && p->queries > 0) e = da::launch_attn_grad_q(of_q, s);
+    if (e == hipSuccess && grad_k && p->keys > 0) e = da::launch_attn_grad_kv(of_kv, s);
+    return da::report_hip(e, "attention backward launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,209 @@
+// Attention's gradients to the queries, and the sums that both gradient kernels need.  Contract
+// and formulas: include/attention.h; tiles and products: attn_device.h.
+//
+// As in the forward, columns are rows of queries and keys and values are streamed; a column's
+// lse and delta are a register each.  Three products to a tile: scores, dP, and keys times dS.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "attn_device.h"
+
+namespace da {
+namespace {
+
+template <typename T, int DP, bool DEEP>
+constexpr int kGradQWaves = DEEP || sizeof(T) == 4 ? 1 : 2;
+
+template <typename T, int DP, bool DEEP>
+__global__ __launch_bounds__(kAttnThreads, (kGradQWaves<T, DP, DEEP>))
+void attn_grad_q_kernel(AttnArgs a) {
+    constexpr int TILE = DEEP ? kAttnDeepTile : kAttnWideTile, NB = DEEP ? 1 : 2, ND = DP / 32;
+    using Tl = Tile<T, DP, TILE>;
+    constexpr bool TWICE = Tl::kPieces * 16 * 4 <= 128 * 1024;
+    __shared__ u32x4 k0[Tl::kPieces], v0[Tl::kPieces];
+    __shared__ u32x4 k1[TWICE ? Tl::kPieces : 1], v1[TWICE ? Tl::kPieces : 1];
+    const Spot spot = spot_of(a);
+    if (!spot.there) return;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int col = lane % 32, half = lane / 32;
+    const int b = spot.unit / a.Hk, hk = spot.unit % a.Hk;
+    const int keys = keys_of(a, b), tiles = (keys + TILE - 1) / TILE;
+
+    const int r = spot.tile * (DEEP ? kAttnDeep : kAttnWide) + (DEEP ? 0 : wave * 32) + col;
+    const int query = (uint32_t)r / (uint32_t)a.group, head = hk * a.group + (uint32_t)r % (uint32_t)a.group;
+    const bool there = r < a.rows;
+    const int64_t line = ((int64_t)b * a.Nq + query) * a.H + head;
+    u32x4 qc[Tl::kSteps], gc[Tl::kSteps];
+    load_column<T, DP>(static_cast<const char*>(a.q) + b * a.q_batch + query * a.q_token + head * a.q_head,
+                       there, a.D, half, qc);
+    load_column<T, DP>(static_cast<const char*>(a.grad_out) + b * a.g_batch + query * a.g_token +
+                           head * a.g_head,
+                       there, a.D, half, gc);
+    const int64_t stat = ((int64_t)b * a.H + head) * a.Nq + query;
+    const float lse2 = there ? a.lse2[stat] : kInf, delta = there ? a.delta[stat] : 0.0f;
+
+    const char* kp = static_cast<const char*>(a.k) + b * a.k_batch + hk * a.k_head;
+    const char* vp = static_cast<const char*>(a.v) + b * a.v_batch + hk * a.v_head;
+    const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.Nk : nullptr;
+    const Places<T, DP> at(lane);
+    const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
+    MaskBytes<Tl::kWords> bytes;
+
+    const auto fetch = [&](int j, const Visible<Tl::kWords>& vis, u32x4* ks, u32x4* vs) {
+        const int rows = min(keys - j * TILE, TILE);
+        const auto see = [&](int row) { return !mask || vis(row); };
+        filler.run(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, see);
+        filler.run(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, see);
+    };
+    const auto ahead = [&](int j) {
+        bytes.load(mask ? mask + (int64_t)j * TILE : nullptr, keys - j * TILE, lane);
+    };
+
+    f32x16 acc[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+    Lift<T, ND> lift;
+
+    const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible<Tl::kWords>& vis) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const int block = DEEP ? wave : n;
+            f32x16 s = mul_columns<T, DP>(at, ks, block, qc);
+            const f32x16 dp = mul_columns<T, DP>(at, vs, block, gc);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], a.scale2, -lse2)) * (dp[i] - delta);
+            const uint32_t see = vis.block(block);
+            if (see != ~0u) {
+                const uint32_t mine = see >> (4 * half);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[i] = mine & (1u << (8 * (i / 4) + i % 4)) ? s[i] : 0.0f;
+            }
+            lift.apply(s, acc);
+            mul_rows<T, DP, false>(at, ks, block, Weights<T, false>(s), acc);
+        }
+    };
+
+    if (tiles > 0) {
+        ahead(0);
+        Visible<Tl::kWords> here = bytes.visible(keys, lane);
+        if (tiles > 1) ahead(1);
+        fetch(0, here, k0, v0);
+        tile_barrier();
+        int j = 0;
+        const auto turn = [&](u32x4* ks, u32x4* vs, u32x4* kn, u32x4* vn) {
+            Visible<Tl::kWords> next = here;
+            if (j + 1 < tiles) {
+                next = bytes.visible(keys - (j + 1) * TILE, lane);
+                if (j + 2 < tiles) ahead(j + 2);
+                if constexpr (TWICE) fetch(j + 1, next, kn, vn);
+            }
+            step((LdsBytes)ks, (LdsBytes)vs, here);
+            tile_barrier();
+            if constexpr (!TWICE) {
+                if (j + 1 < tiles) fetch(j + 1, next, kn, vn);
+                tile_barrier();
+            }
+            here = next;
+            return ++j < tiles;
+        };
+        if constexpr (TWICE) {
+            while (turn(k0, v0, k1, v1) && turn(k1, v1, k0, v0)) {}
+        } else {
+            while (turn(k0, v0, k0, v0)) {}
+        }
+    }
+    float factor = a.scale * lift.down();
+    if constexpr (DEEP) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[d][i] *= factor;
+        factor = 1.0f;
+        add_waves<ND>(acc, reinterpret_cast<float*>(k0), wave, lane);
+        if (wave != 0) return;
+    }
+    if (there)
+        store_column<T, ND>(static_cast<T*>(a.grad_q) + line * a.D, a.D, half, acc, factor);
+}
+
+// ---- lse in base 2, and delta ------------------------------------------------------------
+//
+// Eight lanes to a row of out and grad_out, a run of 16-byte pieces in turn to each.
+template <typename T>
+__global__ __launch_bounds__(kAttnThreads) void attn_delta_kernel(AttnArgs a) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const int64_t line = ((int64_t)blockIdx.x * kAttnThreads + threadIdx.x) / 8;
+    const int part = threadIdx.x % 8;
+    if (line >= (int64_t)a.B * a.Nq * a.H) return;
+    const int64_t bq = line / a.H, b = bq / a.Nq, query = bq % a.Nq;
+    const int head = (int)(line % a.H);
+    const T* o = reinterpret_cast<const T*>(static_cast<const char*>(a.out) + b * a.o_batch +
+                                            query * a.o_token + head * a.o_head);
+    const T* g = reinterpret_cast<const T*>(static_cast<const char*>(a.grad_out) + b * a.g_batch +
+                                            query * a.g_token + head * a.g_head);
+    float sum = 0.0f;
+    for (int at = part * V; at < a.D; at += 8 * V) {
+        float x[V], y[V];
+        load_as(o + at, x);
+        load_as(g + at, y);
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum = fmaf(x[e], y[e], sum);
+    }
+#pragma unroll
+    for (int m = 1; m < 8; m *= 2) sum += __shfl_xor(sum, m);
+    if (part != 0) return;
+    const int64_t stat = (b * a.H + head) * a.Nq + query;
+    const float lse = a.lse[stat];
+    a.lse2[stat] = lse == -kInf ? kInf : lse / kLn2;
+    a.delta[stat] = sum;
+}
+
+template <typename T, int DP>
+void launch(const AttnArgs& a, hipStream_t stream) {
+    const uint32_t blocks = (uint32_t)(a.blocks + 7) / 8 * 8;
+    if (a.deep)
+        attn_grad_q_kernel<T, DP, true><<<blocks, kAttnThreads, 0, stream>>>(a);
+    else
+        attn_grad_q_kernel<T, DP, false><<<blocks, kAttnThreads, 0, stream>>>(a);
+}
+
+template <typename T>
+hipError_t launch_type(const AttnArgs& a, hipStream_t stream) {
+    if (a.D <= 32)
+        launch<T, 32>(a, stream);
+    else if (a.D <= 64)
+        launch<T, 64>(a, stream);
+    else if (a.D <= 96)
+        launch<T, 96>(a, stream);
+    else
+        launch<T, 128>(a, stream);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_grad_q(const AttnArgs& a, hipStream_t stream) {
+    if (a.dtype == DA_BF16) return launch_type<__bf16>(a, stream);
+    if (a.dtype == DA_F16) return launch_type<_Float16>(a, stream);
+    return launch_type<float>(a, stream);
+}
+
+hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream) {
+    const int64_t threads = (int64_t)a.B * a.Nq * a.H * 8;
+    const uint32_t blocks = (uint32_t)((threads + kAttnThreads - 1) / kAttnThreads);
+    if (a.dtype == DA_BF16)
+        attn_delta_kernel<__bf16><<<blocks, kAttnThreads, 0, stream>>>(a);
+    else if (a.dtype == DA_F16)
+        attn_delta_kernel<_Float16><<<blocks, kAttnThreads, 0, stream>>>(a);
+    else
+        attn_delta_kernel<float><<<blocks, kAttnThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace da

@@ -1,0 +1,57 @@
+// Internal launch description of the attention kernels (attn_forward.hip, attn_grad_q.hip,
+// attn_grad_kv.hip), filled by the host API (attn_api.cpp).  Not part of the public ABI.
+//
+// Rows are the queries of the heads that share a key head: row r of a (batch entry, key head)
+// is query r / group of its head r % group.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime_api.h>
+
+#include "attention.h"
+
+namespace da {
+
+constexpr int kAttnThreads = 256;   // four waves
+// A workgroup of the wide form has 32 columns (rows of the forward and of grad_q, keys of grad_k
+// and grad_v) to each wave, one of the deep form 32 in all, its waves taking the tile's parts.
+constexpr int kAttnWide = 128, kAttnDeep = 32;
+constexpr int kAttnWideTile = 64, kAttnDeepTile = 128;   // rows or keys streamed at a time
+
+struct AttnArgs {
+    const void *q, *k, *v;
+    const int32_t* lens;      // [B] or NULL
+    const uint8_t* mask;      // [B, Nk] or NULL
+    void* out;                // [B, Nq, H, D], strided
+    float* lse;               // [B, H, Nq] or NULL in the forward
+    const void* grad_out;
+    void *grad_q, *grad_k, *grad_v;   // dense
+    float* part;              // forward: [splits, B Hk, rows, D] results of a split's keys, not
+                              // divided by their sums
+    float2* part_stat;        // forward: [splits, B Hk, rows] (logarithm of base 2 that the
+                              // result is scaled by, sum)
+    float* lse2;              // backward: [B, H, Nq] lse in base 2, +infinity for an empty row
+    float* delta;             // backward: [B, H, Nq]
+    int64_t q_batch, q_token, q_head;   // strides in bytes
+    int64_t k_batch, k_token, k_head;
+    int64_t v_batch, v_token, v_head;
+    int64_t o_batch, o_token, o_head;
+    int64_t g_batch, g_token, g_head;   // of grad_out
+    int32_t B, Nq, Nk, H, Hk, D;
+    int32_t group, rows;      // H / Hk; Nq * group
+    int32_t col_tiles;        // tiles of columns
+    int32_t splits, split_keys;
+    int32_t blocks;           // workgroups with work; a launch has a multiple of 8
+    float scale, scale2;      // scale2: scale / log 2
+    int32_t dtype;
+    bool deep;
+};
+
+hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_grad_q(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_attn_grad_kv(const AttnArgs& a, hipStream_t stream);
+
+}  // namespace da

@@ -95,28 +95,43 @@ void describe(const attn_problem* p, da::AttnArgs& a) {
     a.dtype = p->dtype;
 }
 
-// The form for so many columns to a key head: wide where that gives every compute unit a workgroup,
-// else deep, four times as many; always deep where one of its workgroups has all columns.
-void choose_form(da::AttnArgs& a, int64_t columns) {
-    const int64_t units = (int64_t)a.B * a.Hk;
-    a.deep = columns <= da::kAttnDeep ||
-             units * ((columns + da::kAttnWide - 1) / da::kAttnWide) < 256;
-    const int64_t width = a.deep ? da::kAttnDeep : da::kAttnWide;
-    a.col_tiles = (int32_t)((columns + width - 1) / width);
-}
-
-// The forward's form; where even the deep one leaves compute units without work, the keys are
-// split over workgroups.
+// The forward's form: wide where that gives every compute unit a workgroup, else deep, four times as
+// many; always deep where one of its workgroups has all rows.  Where even the deep one leaves
+// compute units without work, the keys are split over workgroups.
 void choose_forward(da::AttnArgs& a) {
-    choose_form(a, a.rows);
-    const int64_t blocks = (int64_t)a.B * a.Hk * a.col_tiles;
-    const int64_t tiles = (a.Nk + da::kAttnDeepTile - 1) / da::kAttnDeepTile;
+    const int64_t units = (int64_t)a.B * a.Hk;
+    a.deep = a.rows <= da::kAttnDeep ||
+             units * ((a.rows + (int64_t)da::kAttnWide - 1) / da::kAttnWide) < 256;
+    const int64_t width = a.deep ? da::kAttnDeep : da::kAttnWide;
+    a.col_tiles = (int32_t)((a.rows + width - 1) / width);
+    const int64_t blocks = units * a.col_tiles;
+    const int64_t tiles = (a.Nk + (int64_t)da::kAttnDeepTile - 1) / da::kAttnDeepTile;
     if (a.deep && blocks < 256 && tiles > 1) {
         const int64_t splits = std::min(tiles, 512 / std::max<int64_t>(blocks, 1));
         const int64_t per = (tiles + splits - 1) / splits;
         a.split_keys = (int32_t)(per * da::kAttnDeepTile);
         a.splits = (int32_t)((tiles + per - 1) / per);
     }
+}
+
+// A gradient's form for so many columns to a key head and tiles that are streamed to them: split
+// over workgroups until every compute unit has `want`, but at least two tiles to a split.
+void choose_backward(da::AttnArgs& a, int64_t columns, int64_t tiles, int64_t want) {
+    a.col_tiles = (int32_t)((columns + da::kAttnWide - 1) / da::kAttnWide);
+    const int64_t blocks = (int64_t)a.B * a.Hk * a.col_tiles;
+    const int64_t splits = std::max<int64_t>(
+        1, std::min((tiles + 1) / 2, want * 256 / std::max<int64_t>(blocks, 1)));
+    const int64_t per = std::max<int64_t>(1, (tiles + splits - 1) / splits);
+    a.split_keys = (int32_t)per;
+    a.splits = (int32_t)std::max<int64_t>(1, (tiles + per - 1) / per);
+}
+void choose_grad_q(da::AttnArgs& a) {
+    const int64_t tiles = ((int64_t)a.Nk + da::kAttnWideTile - 1) / da::kAttnWideTile;
+    choose_backward(a, a.rows, tiles, a.dtype == DA_F32 ? 1 : 2);
+}
+void choose_grad_kv(da::AttnArgs& a) {
+    const int64_t tiles = ((int64_t)a.Nq + da::kAttnWideTile - 1) / da::kAttnWideTile * a.group;
+    choose_backward(a, a.Nk, tiles, a.dtype == DA_F32 || a.D > 64 ? 1 : 2);
 }
 
 // Counts the workgroups; a launch has fewer than 2^32 threads.
@@ -134,6 +149,12 @@ uint64_t stat_bytes(const da::AttnArgs& a) {
 uint64_t need_forward(const da::AttnArgs& a) {
     if (a.splits == 1) return 0;
     return stat_bytes(a) + part_bytes((uint64_t)a.splits * a.B * a.Hk * a.rows * a.D * sizeof(float));
+}
+uint64_t part_q_bytes(const da::AttnArgs& q) {
+    return q.splits == 1 ? 0 : part_bytes((uint64_t)q.splits * q.B * q.Nq * q.H * q.D * sizeof(float));
+}
+uint64_t part_k_bytes(const da::AttnArgs& kv) {
+    return kv.splits == 1 ? 0 : part_bytes((uint64_t)kv.splits * kv.B * kv.Nk * kv.Hk * kv.D * sizeof(float));
 }
 uint64_t row_bytes(const da::AttnArgs& a) { return part_bytes((uint64_t)a.B * a.H * a.Nq * sizeof(float)); }
 
@@ -231,7 +252,10 @@ da_status attn_backward_workspace_size(const attn_problem* p, size_t* bytes) {
     if (st != DA_OK) return st;
     da::AttnArgs a;
     describe(p, a);
-    *bytes = (size_t)(2 * row_bytes(a));
+    da::AttnArgs of_kv = a;
+    choose_grad_q(a);
+    choose_grad_kv(of_kv);
+    *bytes = (size_t)(2 * row_bytes(a) + part_q_bytes(a) + 2 * part_k_bytes(of_kv));
     return DA_OK;
 }
 
@@ -270,32 +294,42 @@ da_status attn_backward(const attn_problem* p, const void* q, const void* k, con
             if (ranges_clash(results[i].at, results[i].bytes, results[j].at, results[j].bytes))
                 return report_error(DA_ERR_INVALID_ARG, "two gradients overlap");
     }
-    da::AttnArgs a, of_q, of_kv;
-    describe(p, a);
-    st = check_workspace(2 * row_bytes(a), workspace, workspace_bytes);
-    if (st != DA_OK) return st;
-    a.q = q, a.k = k, a.v = v;
-    a.lens = kv_lens;
-    a.mask = key_mask;
-    a.out = const_cast<void*>(out);
-    a.lse = const_cast<float*>(lse);
-    a.grad_out = grad_out;
-    a.grad_q = grad_q, a.grad_k = grad_k, a.grad_v = grad_v;
-    a.lse2 = static_cast<float*>(workspace);
-    a.delta = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + row_bytes(a));
-    of_q = of_kv = a;
-    choose_form(of_q, a.rows);
-    choose_form(of_kv, a.Nk);
+    da::AttnArgs of_q;
+    describe(p, of_q);
+    of_q.q = q, of_q.k = k, of_q.v = v;
+    of_q.lens = kv_lens;
+    of_q.mask = key_mask;
+    of_q.out = const_cast<void*>(out);
+    of_q.lse = const_cast<float*>(lse);
+    of_q.grad_out = grad_out;
+    of_q.grad_q = grad_q, of_q.grad_k = grad_k, of_q.grad_v = grad_v;
+    unsigned char* base = static_cast<unsigned char*>(workspace);
+    of_q.lse2 = reinterpret_cast<float*>(base);
+    of_q.delta = reinterpret_cast<float*>(base + row_bytes(of_q));
+    da::AttnArgs of_kv = of_q;
+    choose_grad_q(of_q);
+    choose_grad_kv(of_kv);
     st = count_blocks(of_q);
     if (st == DA_OK) st = count_blocks(of_kv);
     if (st != DA_OK) return st;
-    if ((wide)a.B * a.Nq * a.H * 8 >= wide(1) << 32)
+    const wide numbers = (wide)of_q.B * of_q.Nq * of_q.H * of_q.D + 2 * (wide)of_q.B * of_q.Nk * of_q.Hk * of_q.D;
+    if ((wide)of_q.B * of_q.Nq * of_q.H * 8 >= wide(1) << 32 ||
+        ((of_q.splits > 1 || of_kv.splits > 1) && numbers / 8 >= wide(1) << 32))
         return report_error(DA_ERR_UNSUPPORTED, "2^29 rows or more");
+    const uint64_t need = 2 * row_bytes(of_q) + part_q_bytes(of_q) + 2 * part_k_bytes(of_kv);
+    st = check_workspace(need, workspace, workspace_bytes);
+    if (st != DA_OK) return st;
+    of_q.part = reinterpret_cast<float*>(base + 2 * row_bytes(of_q));
+    of_kv.part_k = reinterpret_cast<float*>(base + 2 * row_bytes(of_q) + part_q_bytes(of_q));
+    of_kv.part_v = of_kv.part_k + part_k_bytes(of_kv) / sizeof(float);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = hipSuccess;
-    if (p->queries > 0 && (grad_q || (grad_k && p->keys > 0))) e = da::launch_attn_delta(a, s);
+    if (p->queries > 0 && (grad_q || (grad_k && p->keys > 0))) e = da::launch_attn_delta(of_q, s);
     if (e == hipSuccess && grad_q && p->queries > 0) e = da::launch_attn_grad_q(of_q, s);
     if (e == hipSuccess && grad_k && p->keys > 0) e = da::launch_attn_grad_kv(of_kv, s);
+    if (p->queries == 0) of_q.splits = 1;
+    if (p->keys == 0) of_kv.splits = 1;
+    if (e == hipSuccess) e = da::launch_attn_grad_join(of_q, of_kv, s);
     return da::report_hip(e, "attention backward launch");
 }
 

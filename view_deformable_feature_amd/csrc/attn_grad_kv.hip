@@ -19,17 +19,15 @@ namespace {
 template <typename T>
 constexpr float kLiftLog2 = std::is_same<T, _Float16>::value ? 15.0f : 0.0f;
 
-template <typename T, int DP, bool DEEP>
-constexpr int kGradKvWaves = DEEP || sizeof(T) == 4 || DP > 64 ? 1 : 2;
+template <typename T, int DP>
+constexpr int kGradKvWaves = sizeof(T) == 4 || DP > 64 ? 1 : 2;
 
-template <typename T, int DP, bool DEEP>
-__global__ __launch_bounds__(kAttnThreads, (kGradKvWaves<T, DP, DEEP>))
+template <typename T, int DP>
+__global__ __launch_bounds__(kAttnThreads, (kGradKvWaves<T, DP>))
 void attn_grad_kv_kernel(AttnArgs a) {
-    constexpr int TILE = DEEP ? kAttnDeepTile : kAttnWideTile, NB = DEEP ? 1 : 2, ND = DP / 32;
+    constexpr int TILE = kAttnWideTile, NB = TILE / 32, ND = DP / 32;
     using Tl = Tile<T, DP, TILE>;
-    constexpr bool TWICE = Tl::kPieces * 16 * 4 <= 128 * 1024;
-    __shared__ u32x4 q0[Tl::kPieces], g0[Tl::kPieces];
-    __shared__ u32x4 q1[TWICE ? Tl::kPieces : 1], g1[TWICE ? Tl::kPieces : 1];
+    __shared__ u32x4 q0[Tl::kPieces], g0[Tl::kPieces], q1[Tl::kPieces], g1[Tl::kPieces];
     __shared__ __align__(16) float stat0[2 * TILE], stat1[2 * TILE];   // lse2, delta of a tile
     const Spot spot = spot_of(a);
     if (!spot.there) return;
@@ -37,11 +35,11 @@ void attn_grad_kv_kernel(AttnArgs a) {
     const int col = lane % 32, half = lane / 32;
     const int b = spot.unit / a.Hk, hk = spot.unit % a.Hk;
     const int keys = keys_of(a, b);
-    const int first = spot.tile * (DEEP ? kAttnDeep : kAttnWide);
-    const int per_head = (a.Nq + TILE - 1) / TILE;
-    const int tiles = first < keys ? per_head * a.group : 0;
+    const int first = spot.tile * kAttnWide;
+    const int per_head = (a.Nq + TILE - 1) / TILE, from = spot.split * a.split_keys;
+    const int tiles = first < keys ? min(per_head * a.group - from, a.split_keys) : 0;
 
-    const int key = first + (DEEP ? 0 : wave * 32) + col;
+    const int key = first + wave * 32 + col;
     const bool there = key < a.Nk;
     bool seen = key < keys;
     if (a.mask && seen) seen = a.mask[(int64_t)b * a.Nk + key] != 0;
@@ -59,7 +57,8 @@ void attn_grad_kv_kernel(AttnArgs a) {
     const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
     const auto all = [](int) { return true; };
 
-    int head = 0, row = 0;   // of the tile that is fetched next
+    // of the tile that is fetched next
+    int head = a.Nq ? from / per_head : 0, row = a.Nq ? from % per_head * TILE : 0;
     float mine = 0.0f;       // a thread's part of its statistics
     const auto fetch = [&](u32x4* qs, u32x4* gs) {
         const int rows = min(a.Nq - row, TILE);
@@ -90,27 +89,26 @@ void attn_grad_kv_kernel(AttnArgs a) {
     const auto step = [&](LdsBytes qs, LdsBytes gs, const float* stat) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            const int block = DEEP ? wave : n;
-            f32x16 p = mul_columns<T, DP>(at, qs, block, kc);
+            f32x16 p = mul_columns<T, DP>(at, qs, n, kc);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const f32x4 lse2 = *reinterpret_cast<const f32x4*>(stat + block * 32 + 8 * j + 4 * half);
+                const f32x4 lse2 = *reinterpret_cast<const f32x4*>(stat + n * 32 + 8 * j + 4 * half);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     p[4 * j + e] = __builtin_amdgcn_exp2f(
                         fmaf(p[4 * j + e], a.scale2, kLiftLog2<T> - lse2[e]));
             }
-            mul_rows<T, DP, false>(at, gs, block, Weights<T, false>(p), dv);
-            f32x16 ds = mul_columns<T, DP>(at, gs, block, vc);
+            mul_rows<T, DP, false>(at, gs, n, Weights<T, false>(p), dv);
+            f32x16 ds = mul_columns<T, DP>(at, gs, n, vc);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const f32x4 delta =
-                    *reinterpret_cast<const f32x4*>(stat + TILE + block * 32 + 8 * j + 4 * half);
+                    *reinterpret_cast<const f32x4*>(stat + TILE + n * 32 + 8 * j + 4 * half);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) ds[4 * j + e] = p[4 * j + e] * (ds[4 * j + e] - delta[e]);
             }
             lift.apply(ds, dk);
-            mul_rows<T, DP, false>(at, qs, block, Weights<T, false>(ds), dk);
+            mul_rows<T, DP, false>(at, qs, n, Weights<T, false>(ds), dk);
         }
     };
 
@@ -120,40 +118,16 @@ void attn_grad_kv_kernel(AttnArgs a) {
         tile_barrier();
         int j = 0;
         const auto turn = [&](u32x4* qs, u32x4* gs, float* st, u32x4* qn, u32x4* gn, float* sn) {
-            if constexpr (TWICE) {
-                if (j + 1 < tiles) fetch(qn, gn);
-            }
+            if (j + 1 < tiles) fetch(qn, gn);
             step((LdsBytes)qs, (LdsBytes)gs, st);
-            if constexpr (TWICE) {
-                if (j + 1 < tiles) keep(sn);
-            } else {
-                tile_barrier();
-                if (j + 1 < tiles) {
-                    fetch(qn, gn);
-                    keep(sn);
-                }
-            }
+            if (j + 1 < tiles) keep(sn);
             tile_barrier();
             return ++j < tiles;
         };
-        if constexpr (TWICE) {
-            while (turn(q0, g0, stat0, q1, g1, stat1) && turn(q1, g1, stat1, q0, g0, stat0)) {}
-        } else {
-            while (turn(q0, g0, stat0, q0, g0, stat0)) {}
-        }
+        while (turn(q0, g0, stat0, q1, g1, stat1) && turn(q1, g1, stat1, q0, g0, stat0)) {}
     }
     const float back = std::is_same<T, _Float16>::value ? 1.0f / 32768.0f : 1.0f;
-    float fk = a.scale * lift.down() * back, fv = back;
-    if constexpr (DEEP) {
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dk[d][i] *= fk;
-        fk = 1.0f;
-        add_waves<ND>(dk, reinterpret_cast<float*>(q0), wave, lane);
-        add_waves<ND>(dv, reinterpret_cast<float*>(q0), wave, lane);
-        if (wave != 0) return;
-    }
+    const float fk = a.scale * lift.down() * back, fv = back;
     if (!there) return;
     if (!seen) {
 #pragma unroll
@@ -162,6 +136,12 @@ void attn_grad_kv_kernel(AttnArgs a) {
             for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.0f;
     }
     const int64_t line = ((int64_t)b * a.Nk + key) * a.Hk + hk;
+    if (a.splits > 1) {
+        const int64_t at_line = (spot.split * (int64_t)a.B * a.Nk * a.Hk + line) * a.D;
+        store_column<float, ND>(a.part_k + at_line, a.D, half, dk, fk);
+        store_column<float, ND>(a.part_v + at_line, a.D, half, dv, fv);
+        return;
+    }
     store_column<T, ND>(static_cast<T*>(a.grad_k) + line * a.D, a.D, half, dk, fk);
     store_column<T, ND>(static_cast<T*>(a.grad_v) + line * a.D, a.D, half, dv, fv);
 }
@@ -169,10 +149,7 @@ void attn_grad_kv_kernel(AttnArgs a) {
 template <typename T, int DP>
 void launch(const AttnArgs& a, hipStream_t stream) {
     const uint32_t blocks = (uint32_t)(a.blocks + 7) / 8 * 8;
-    if (a.deep)
-        attn_grad_kv_kernel<T, DP, true><<<blocks, kAttnThreads, 0, stream>>>(a);
-    else
-        attn_grad_kv_kernel<T, DP, false><<<blocks, kAttnThreads, 0, stream>>>(a);
+    attn_grad_kv_kernel<T, DP><<<blocks, kAttnThreads, 0, stream>>>(a);
 }
 
 template <typename T>

@@ -13,25 +13,25 @@
 namespace da {
 namespace {
 
-template <typename T, int DP, bool DEEP>
-constexpr int kGradQWaves = DEEP || sizeof(T) == 4 ? 1 : 2;
+template <typename T, int DP>
+constexpr int kGradQWaves = sizeof(T) == 4 ? 1 : 2;
 
-template <typename T, int DP, bool DEEP>
-__global__ __launch_bounds__(kAttnThreads, (kGradQWaves<T, DP, DEEP>))
+template <typename T, int DP>
+__global__ __launch_bounds__(kAttnThreads, (kGradQWaves<T, DP>))
 void attn_grad_q_kernel(AttnArgs a) {
-    constexpr int TILE = DEEP ? kAttnDeepTile : kAttnWideTile, NB = DEEP ? 1 : 2, ND = DP / 32;
+    constexpr int TILE = kAttnWideTile, NB = TILE / 32, ND = DP / 32;
     using Tl = Tile<T, DP, TILE>;
-    constexpr bool TWICE = Tl::kPieces * 16 * 4 <= 128 * 1024;
-    __shared__ u32x4 k0[Tl::kPieces], v0[Tl::kPieces];
-    __shared__ u32x4 k1[TWICE ? Tl::kPieces : 1], v1[TWICE ? Tl::kPieces : 1];
+    __shared__ u32x4 k0[Tl::kPieces], v0[Tl::kPieces], k1[Tl::kPieces], v1[Tl::kPieces];
     const Spot spot = spot_of(a);
     if (!spot.there) return;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int col = lane % 32, half = lane / 32;
     const int b = spot.unit / a.Hk, hk = spot.unit % a.Hk;
-    const int keys = keys_of(a, b), tiles = (keys + TILE - 1) / TILE;
+    const int first = spot.split * a.split_keys * TILE;
+    const int keys = min(keys_of(a, b) - first, a.split_keys * TILE);   // of this split; may be none
+    const int tiles = keys > 0 ? (keys + TILE - 1) / TILE : 0;
 
-    const int r = spot.tile * (DEEP ? kAttnDeep : kAttnWide) + (DEEP ? 0 : wave * 32) + col;
+    const int r = spot.tile * kAttnWide + wave * 32 + col;
     const int query = (uint32_t)r / (uint32_t)a.group, head = hk * a.group + (uint32_t)r % (uint32_t)a.group;
     const bool there = r < a.rows;
     const int64_t line = ((int64_t)b * a.Nq + query) * a.H + head;
@@ -44,9 +44,9 @@ void attn_grad_q_kernel(AttnArgs a) {
     const int64_t stat = ((int64_t)b * a.H + head) * a.Nq + query;
     const float lse2 = there ? a.lse2[stat] : kInf, delta = there ? a.delta[stat] : 0.0f;
 
-    const char* kp = static_cast<const char*>(a.k) + b * a.k_batch + hk * a.k_head;
-    const char* vp = static_cast<const char*>(a.v) + b * a.v_batch + hk * a.v_head;
-    const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.Nk : nullptr;
+    const char* kp = static_cast<const char*>(a.k) + b * a.k_batch + hk * a.k_head + first * a.k_token;
+    const char* vp = static_cast<const char*>(a.v) + b * a.v_batch + hk * a.v_head + first * a.v_token;
+    const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.Nk + first : nullptr;
     const Places<T, DP> at(lane);
     const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
     MaskBytes<Tl::kWords> bytes;
@@ -71,13 +71,12 @@ void attn_grad_q_kernel(AttnArgs a) {
     const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible<Tl::kWords>& vis) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            const int block = DEEP ? wave : n;
-            f32x16 s = mul_columns<T, DP>(at, ks, block, qc);
-            const f32x16 dp = mul_columns<T, DP>(at, vs, block, gc);
+            f32x16 s = mul_columns<T, DP>(at, ks, n, qc);
+            const f32x16 dp = mul_columns<T, DP>(at, vs, n, gc);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], a.scale2, -lse2)) * (dp[i] - delta);
-            const uint32_t see = vis.block(block);
+            const uint32_t see = vis.block(n);
             if (see != ~0u) {
                 const uint32_t mine = see >> (4 * half);
 #pragma unroll
@@ -85,7 +84,7 @@ void attn_grad_q_kernel(AttnArgs a) {
                     s[i] = mine & (1u << (8 * (i / 4) + i % 4)) ? s[i] : 0.0f;
             }
             lift.apply(s, acc);
-            mul_rows<T, DP, false>(at, ks, block, Weights<T, false>(s), acc);
+            mul_rows<T, DP, false>(at, ks, n, Weights<T, false>(s), acc);
         }
     };
 
@@ -101,34 +100,21 @@ void attn_grad_q_kernel(AttnArgs a) {
             if (j + 1 < tiles) {
                 next = bytes.visible(keys - (j + 1) * TILE, lane);
                 if (j + 2 < tiles) ahead(j + 2);
-                if constexpr (TWICE) fetch(j + 1, next, kn, vn);
+                fetch(j + 1, next, kn, vn);
             }
             step((LdsBytes)ks, (LdsBytes)vs, here);
             tile_barrier();
-            if constexpr (!TWICE) {
-                if (j + 1 < tiles) fetch(j + 1, next, kn, vn);
-                tile_barrier();
-            }
             here = next;
             return ++j < tiles;
         };
-        if constexpr (TWICE) {
-            while (turn(k0, v0, k1, v1) && turn(k1, v1, k0, v0)) {}
-        } else {
-            while (turn(k0, v0, k0, v0)) {}
-        }
+        while (turn(k0, v0, k1, v1) && turn(k1, v1, k0, v0)) {}
     }
-    float factor = a.scale * lift.down();
-    if constexpr (DEEP) {
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[d][i] *= factor;
-        factor = 1.0f;
-        add_waves<ND>(acc, reinterpret_cast<float*>(k0), wave, lane);
-        if (wave != 0) return;
-    }
-    if (there)
+    if (!there) return;
+    const float factor = a.scale * lift.down();
+    if (a.splits > 1)
+        store_column<float, ND>(a.part + (spot.split * (int64_t)a.B * a.Nq * a.H + line) * a.D, a.D, half,
+                                acc, factor);
+    else
         store_column<T, ND>(static_cast<T*>(a.grad_q) + line * a.D, a.D, half, acc, factor);
 }
 
@@ -164,13 +150,42 @@ __global__ __launch_bounds__(kAttnThreads) void attn_delta_kernel(AttnArgs a) {
     a.delta[stat] = sum;
 }
 
+// ---- splits' gradients added up ----------------------------------------------------------
+//
+// Eight numbers to a thread, of grad_q, grad_k and grad_v in turn.
+struct JoinSide {
+    const float* part;
+    void* out;
+    int64_t numbers;   // of one split; a multiple of 8
+    int32_t splits;
+};
+struct JoinArgs {
+    JoinSide side[3];
+};
+
+template <typename T>
+__global__ __launch_bounds__(kAttnThreads) void attn_grad_join_kernel(JoinArgs a) {
+    int64_t at = ((int64_t)blockIdx.x * kAttnThreads + threadIdx.x) * 8;
+    int i = 0;
+    while (i < 2 && at >= a.side[i].numbers) at -= a.side[i++].numbers;
+    const JoinSide& t = a.side[i];
+    if (at >= t.numbers) return;
+    float sum[8];
+    load_as(t.part + at, sum);
+#pragma unroll 4
+    for (int s = 1; s < t.splits; ++s) {
+        float v[8];
+        load_as(t.part + s * t.numbers + at, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[e];
+    }
+    store_as(static_cast<T*>(t.out) + at, sum);
+}
+
 template <typename T, int DP>
 void launch(const AttnArgs& a, hipStream_t stream) {
     const uint32_t blocks = (uint32_t)(a.blocks + 7) / 8 * 8;
-    if (a.deep)
-        attn_grad_q_kernel<T, DP, true><<<blocks, kAttnThreads, 0, stream>>>(a);
-    else
-        attn_grad_q_kernel<T, DP, false><<<blocks, kAttnThreads, 0, stream>>>(a);
+    attn_grad_q_kernel<T, DP><<<blocks, kAttnThreads, 0, stream>>>(a);
 }
 
 template <typename T>
@@ -192,6 +207,27 @@ hipError_t launch_attn_grad_q(const AttnArgs& a, hipStream_t stream) {
     if (a.dtype == DA_BF16) return launch_type<__bf16>(a, stream);
     if (a.dtype == DA_F16) return launch_type<_Float16>(a, stream);
     return launch_type<float>(a, stream);
+}
+
+hipError_t launch_attn_grad_join(const AttnArgs& of_q, const AttnArgs& of_kv, hipStream_t stream) {
+    JoinArgs a = {};
+    if (of_q.grad_q && of_q.splits > 1)
+        a.side[0] = {of_q.part, of_q.grad_q, (int64_t)of_q.B * of_q.Nq * of_q.H * of_q.D, of_q.splits};
+    if (of_kv.grad_k && of_kv.splits > 1) {
+        const int64_t n = (int64_t)of_kv.B * of_kv.Nk * of_kv.Hk * of_kv.D;
+        a.side[1] = {of_kv.part_k, of_kv.grad_k, n, of_kv.splits};
+        a.side[2] = {of_kv.part_v, of_kv.grad_v, n, of_kv.splits};
+    }
+    const int64_t threads = (a.side[0].numbers + a.side[1].numbers + a.side[2].numbers) / 8;
+    if (threads == 0) return hipSuccess;
+    const uint32_t blocks = (uint32_t)((threads + kAttnThreads - 1) / kAttnThreads);
+    if (of_q.dtype == DA_BF16)
+        attn_grad_join_kernel<__bf16><<<blocks, kAttnThreads, 0, stream>>>(a);
+    else if (of_q.dtype == DA_F16)
+        attn_grad_join_kernel<_Float16><<<blocks, kAttnThreads, 0, stream>>>(a);
+    else
+        attn_grad_join_kernel<float><<<blocks, kAttnThreads, 0, stream>>>(a);
+    return hipGetLastError();
 }
 
 hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream) {

@@ -15,8 +15,8 @@
 namespace da {
 
 constexpr int kAttnThreads = 256;   // four waves
-// A workgroup of the wide form has 32 columns (rows of the forward and of grad_q, keys of grad_k
-// and grad_v) to each wave, one of the deep form 32 in all, its waves taking the tile's parts.
+// A workgroup has 32 columns (rows of the forward and of grad_q, keys of grad_k and grad_v) to each
+// wave; in the forward's deep form it has 32 in all, its waves taking the tile's parts.
 constexpr int kAttnWide = 128, kAttnDeep = 32;
 constexpr int kAttnWideTile = 64, kAttnDeepTile = 128;   // rows or keys streamed at a time
 
@@ -32,6 +32,8 @@ struct AttnArgs {
                               // divided by their sums
     float2* part_stat;        // forward: [splits, B Hk, rows] (logarithm of base 2 that the
                               // result is scaled by, sum)
+    float *part_k, *part_v;   // backward: [splits, B, Nk, Hk, D] (and part, [splits, B, Nq, H, D])
+                              // gradients from a split's rows (keys)
     float* lse2;              // backward: [B, H, Nq] lse in base 2, +infinity for an empty row
     float* delta;             // backward: [B, H, Nq]
     int64_t q_batch, q_token, q_head;   // strides in bytes
@@ -42,7 +44,8 @@ struct AttnArgs {
     int32_t B, Nq, Nk, H, Hk, D;
     int32_t group, rows;      // H / Hk; Nq * group
     int32_t col_tiles;        // tiles of columns
-    int32_t splits, split_keys;
+    int32_t splits;           // of what is streamed
+    int32_t split_keys;       // keys of a split (forward), or tiles of it (backward)
     int32_t blocks;           // workgroups with work; a launch has a multiple of 8
     float scale, scale2;      // scale2: scale / log 2
     int32_t dtype;
@@ -53,5 +56,7 @@ hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_grad_q(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_grad_kv(const AttnArgs& a, hipStream_t stream);
+// Splits' gradients added up: of_q's, of_kv's, where they have more than one.
+hipError_t launch_attn_grad_join(const AttnArgs& of_q, const AttnArgs& of_kv, hipStream_t stream);
 
 }  // namespace da

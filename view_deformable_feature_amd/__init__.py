@@ -2,7 +2,7 @@
 
 The computation lives in ``libdeformagg.so`` (HIP kernels behind a C ABI,
 declared in ``include/*.h``); ``api``, ``pack``, ``dcn``, ``norm``, ``int8``,
-``rotary`` and ``attention`` bind it to PyTorch tensors.
+``rope`` and ``attention`` bind it to PyTorch tensors.
 ``workloads`` draws seeded synthetic inputs.
 """
 from .api import (DeformableAggregationFunction, da_backward, da_backward_accumulate,  # noqa: F401
@@ -22,7 +22,7 @@ from .int8 import (i8_linear, i8_linear_workspace_size, i8_matmul,  # noqa: F401
                    i8_matmul_workspace_size, i8_norm_linear, i8_norm_linear_workspace_size,
                    i8_quantize_rows)
 
-from .rotary import (NormRotaryFunction, RotaryFunction, norm_rotary, rope_forward,  # noqa: F401
+from .rope import (NormRotaryFunction, RotaryFunction, norm_rotary, rope_forward,  # noqa: F401
                      rope_frequencies, rope_norm_backward, rope_norm_backward_workspace_size,
                      rope_norm_forward, rotary)
 

@@ -28,35 +28,33 @@ __all__ = ["attn_forward", "attn_backward", "attn_workspace_size", "attn_backwar
            "CrossAttentionFunction", "cross_attention"]
 
 
-@functools.lru_cache(maxsize=256)
-def _plan(func, q, k, q_stride, k_stride, v_stride, o_stride, g_stride, scale, dtype):
-    """(problem, workspace bytes) of shapes, strides and type; the library only reads the
-    problem."""
-    B, Nq, H, D = q
-    _, Nk, Hk, _ = k
-    three = ctypes.c_int64 * 3
-    prob = ctypes.byref(_lib.AttnProblem(
-        B, Nq, Nk, H, Hk, D, three(*q_stride), three(*k_stride), three(*v_stride),
-        three(*o_stride), three(*g_stride),
-        1 / math.sqrt(D) if scale is None and D > 0 else scale or 0.0, _DTYPES[dtype], 0, 0))
-    return prob, size(func + "_workspace_size", prob)
-
-
-def _strides(t, name):
-    """t's strides; those of dimensions of one place or none, which say nothing, as if what they
-    hold were dense."""
-    shape, strides = t.shape, t.stride()
-    if strides[3] != 1 and shape[3] > 1:
-        raise ValueError(f"the numbers of a head of {name} must be consecutive")
-    if min(shape[:3]) > 1:
-        return strides[:3]
-    dense = _dense(shape)
-    return tuple(s if n > 1 else d for n, s, d in zip(shape, strides, dense))
-
-
 def _dense(shape):
     D, H = shape[3], max(shape[2], 1)
     return D * H * max(shape[1], 1), D * H, D
+
+
+def _strides(shape, strides, name):
+    """The first three strides as the library takes them; those of dimensions of one place or none,
+    which say nothing, as if what they hold were dense."""
+    if strides[3] != 1 and shape[3] > 1:
+        raise ValueError(f"the numbers of a head of {name} must be consecutive")
+    three = ctypes.c_int64 * 3
+    return three(*(s if n > 1 else d for n, s, d in zip(shape, strides, _dense(shape))))
+
+
+@functools.lru_cache(maxsize=256)
+def _plan(func, q, k, q_stride, k_stride, v_stride, o_stride, g_stride, scale, dtype):
+    """(problem, workspace bytes) of shapes, strides (None: dense) and type; the library only reads
+    the problem."""
+    B, Nq, H, D = q
+    _, Nk, Hk, _ = k
+    dense = (*_dense(q), 1)
+    prob = ctypes.byref(_lib.AttnProblem(
+        B, Nq, Nk, H, Hk, D, _strides(q, q_stride, "q"), _strides(k, k_stride, "k"),
+        _strides(k, v_stride, "v"), _strides(q, o_stride or dense, "out"),
+        _strides(q, g_stride or dense, "grad_out"),
+        1 / math.sqrt(D) if scale is None and D > 0 else scale or 0.0, _DTYPES[dtype], 0, 0))
+    return prob, size(func + "_workspace_size", prob)
 
 
 def _planned(func, q, k, v, scale, out=None, grad_out=None):
@@ -65,17 +63,15 @@ def _planned(func, q, k, v, scale, out=None, grad_out=None):
             raise ValueError(f"{name} must be a [batch, tokens, heads, head_dim] tensor")
     if q.dtype not in _DTYPES:
         raise TypeError(f"dtypes must be among {_FLOATS}")
-    shape = q.shape
-    if k.shape != v.shape or k.shape[0] != shape[0] or k.shape[3] != shape[3]:
-        raise ValueError(f"q {tuple(shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit "
-                         "together")
+    shape, ks = q.shape, k.shape
+    if ks != v.shape or ks[0] != shape[0] or ks[3] != shape[3]:
+        raise ValueError(f"q {tuple(shape)}, k {tuple(ks)} and v {tuple(v.shape)} do not fit together")
     for name, t in (("out", out), ("grad_out", grad_out)):
         if t is not None and (not isinstance(t, torch.Tensor) or t.shape != shape):
             raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    dense = _dense(shape)
-    return _plan(func, shape, k.shape, _strides(q, "q"), _strides(k, "k"), _strides(v, "v"),
-                 dense if out is None else _strides(out, "out"),
-                 dense if grad_out is None else _strides(grad_out, "grad_out"),
+    return _plan(func, shape, ks, q.stride(), k.stride(), v.stride(),
+                 None if out is None else out.stride(),
+                 None if grad_out is None else grad_out.stride(),
                  None if scale is None else float(scale), q.dtype)
 
 
@@ -88,6 +84,13 @@ def _need_heads(t, name, dtype, dev):
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     return t.data_ptr()
+
+
+def _like(x):
+    """A new dense tensor of x's shape and type."""
+    if x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, device=x.device, dtype=x.dtype)
 
 
 def attn_workspace_size(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> int:
@@ -118,7 +121,7 @@ def attn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     dev, shape = q.device, q.shape
     pq, pk, pv, pl, pm = _inputs(q, k, v, kv_lens, key_mask)
     if out is None:
-        out = torch.empty(shape, device=dev, dtype=q.dtype)
+        out = _like(q)
     po = _need_heads(out, "out", q.dtype, dev)
     lse = torch.empty((shape[0], shape[2], shape[1]), device=dev, dtype=torch.float32)
     workspace = scratch(workspace, bytes_needed, dev)
@@ -142,9 +145,8 @@ def attn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.
     po = _need_heads(out, "out", dtype, dev)
     ps = need(lse, "lse", torch.float32, dev, (shape[0], shape[2], shape[1]))
     pg = _need_heads(grad_out, "grad_out", dtype, dev)
-    dq = torch.empty(shape, device=dev, dtype=dtype) if need_q else None
-    dk = torch.empty(k.shape, device=dev, dtype=dtype) if need_kv else None
-    dv = torch.empty(k.shape, device=dev, dtype=dtype) if need_kv else None
+    dq = _like(q) if need_q else None
+    dk, dv = (_like(k), _like(v)) if need_kv else (None, None)
     pdq = dq.data_ptr() if need_q else None
     pdk, pdv = (dk.data_ptr(), dv.data_ptr()) if need_kv else (None, None)
     workspace = scratch(workspace, bytes_needed, dev)
@@ -156,8 +158,8 @@ def attn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.
 def _fits(t):
     """t itself where the kernels take its strides and place, else a dense copy."""
     per = 16 // t.element_size()
-    if (t.dim() != 4 or t.shape[3] > 1 and t.stride(3) != 1 or t.data_ptr() % 16
-            or any(s % per for s in _strides(t, ""))):
+    if (t.dim() == 4 and (t.shape[3] > 1 and t.stride(3) != 1 or t.data_ptr() % 16
+                          or any(n > 1 and s % per for n, s in zip(t.shape[:3], t.stride())))):
         t = t.contiguous()
         if t.data_ptr() % 16:
             t = t.clone()

@@ -107,7 +107,8 @@ void choose_forward(da::AttnArgs& a) {
     const int64_t blocks = units * a.col_tiles;
     const int64_t tiles = (a.Nk + (int64_t)da::kAttnDeepTile - 1) / da::kAttnDeepTile;
     if (a.deep && blocks < 256 && tiles > 1) {
-        const int64_t splits = std::min(tiles, 512 / std::max<int64_t>(blocks, 1));
+        const int64_t splits =
+            std::min({tiles, 512 / std::max<int64_t>(blocks, 1), (int64_t)da::kAttnMostSplits});
         const int64_t per = (tiles + splits - 1) / splits;
         a.split_keys = (int32_t)(per * da::kAttnDeepTile);
         a.splits = (int32_t)((tiles + per - 1) / per);
@@ -324,8 +325,10 @@ da_status attn_backward(const attn_problem* p, const void* q, const void* k, con
     of_kv.part_v = of_kv.part_k + part_k_bytes(of_kv) / sizeof(float);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = hipSuccess;
-    if (p->queries > 0 && (grad_q || (grad_k && p->keys > 0))) e = da::launch_attn_delta(of_q, s);
-    if (e == hipSuccess && grad_q && p->queries > 0) e = da::launch_attn_grad_q(of_q, s);
+    if (p->queries > 0 && grad_q)
+        e = da::launch_attn_grad_q(of_q, s);
+    else if (p->queries > 0 && grad_k && p->keys > 0)
+        e = da::launch_attn_delta(of_q, s);
     if (e == hipSuccess && grad_k && p->keys > 0) e = da::launch_attn_grad_kv(of_kv, s);
     if (p->queries == 0) of_q.splits = 1;
     if (p->keys == 0) of_kv.splits = 1;

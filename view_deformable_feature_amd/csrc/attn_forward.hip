@@ -193,41 +193,50 @@ void attn_forward_kernel(AttnArgs a) {
 
 // ---- splits of keys joined ---------------------------------------------------------------
 //
-// A thread has four numbers of a row; rows of 32 numbers, or fewer, to eight threads and so
-// on.
+// `threads` threads to a row, a power of two: the splits' statistics go through LDS, then each
+// four numbers of each split are a thread's, whose sums meet in LDS.  All reads of a row are on
+// their way at once, since a launch of so little work is bound by their latency (one wave to a
+// row, split after split, took 7 us for 12 splits of 8 rows of 64 numbers).
 template <typename T>
-__global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a) {
-    const int per = a.D / 4;
-    const int64_t n = (int64_t)blockIdx.x * kAttnThreads + threadIdx.x;
-    const int64_t line = n / per, units = (int64_t)a.B * a.Hk;
-    const int at = (int)(n % per) * 4;
-    if (line >= units * a.rows) return;
-    const int unit = (int)(line / a.rows), r = (int)(line % a.rows);
+__global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int threads) {
+    __shared__ float2 stat[kAttnThreads];
+    __shared__ f32x4 meet[kAttnThreads];
+    const int64_t units = (int64_t)a.B * a.Hk, lines = units * a.rows;
+    const int t = threadIdx.x % threads, base = threadIdx.x - t;
+    const int64_t line = (int64_t)blockIdx.x * (kAttnThreads / threads) + threadIdx.x / threads;
+    const bool there = line < lines;
+    const int unit = there ? (int)(line / a.rows) : 0, r = there ? (int)(line % a.rows) : 0;
     const int b = unit / a.Hk, hk = unit % a.Hk;
-    const int splits = (keys_of(a, b) + a.split_keys - 1) / a.split_keys;   // that have keys
-    const int64_t step = units * a.rows;
-    float most = -kInf;
-    for (int s = 0; s < splits; ++s) {
-        const float2 t = a.part_stat[s * step + line];
-        if (t.y != 0.0f) most = fmaxf(most, t.x);
-    }
+    const int splits = there ? (keys_of(a, b) + a.split_keys - 1) / a.split_keys : 0;   // with keys
+    float2 mine = make_float2(-kInf, 0.0f);
+    if (t < splits) mine = a.part_stat[t * lines + line];
+    if (mine.y == 0.0f) mine.x = -kInf;
+    stat[threadIdx.x] = mine;
+    // 4 numbers to a thread, threads / vectors of them side by side
+    const int vectors = a.D / 4, abreast = threads / vectors, at = t % vectors * 4;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    __syncthreads();
+    float most = -kInf, sum = 0.0f;
+    for (int s = 0; s < splits; ++s) most = fmaxf(most, stat[base + s].x);
     most = most == -kInf ? 0.0f : most;
-    float sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s) {
-        const float2 t = a.part_stat[s * step + line];
-        const float f = t.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(t.x - most);
-        float p[4];
-        load_as(a.part + (s * step + line) * a.D + at, p);
-        sum = fmaf(t.y, f, sum);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = fmaf(p[e], f, v[e]);
+    const auto weight = [&](float2 p) { return p.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(p.x - most); };
+    for (int s = 0; s < splits; ++s) sum = fmaf(stat[base + s].y, weight(stat[base + s]), sum);
+    if (t < abreast * vectors) {
+#pragma unroll 8
+        for (int s = t / vectors; s < splits; s += abreast) {
+            const f32x4 p = *reinterpret_cast<const f32x4*>(a.part + (s * lines + line) * a.D + at);
+            v += p * weight(stat[base + s]);
+        }
     }
+    meet[threadIdx.x] = v;
+    __syncthreads();
+    if (!there || t >= vectors) return;
+    for (int i = 1; i < abreast; ++i) v += meet[threadIdx.x + i * vectors];
     const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] *= inverse;
+    const float result[4] = {v[0] * inverse, v[1] * inverse, v[2] * inverse, v[3] * inverse};
     const int query = (uint32_t)r / (uint32_t)a.group, head = hk * a.group + (uint32_t)r % (uint32_t)a.group;
     char* out = static_cast<char*>(a.out) + b * a.o_batch + query * a.o_token + head * a.o_head;
-    store_as(reinterpret_cast<T*>(out) + at, v);
+    store_as(reinterpret_cast<T*>(out) + at, result);
     if (a.lse && at == 0)
         a.lse[((int64_t)b * a.H + head) * a.Nq + query] =
             sum == 0.0f ? -kInf : fmaf(most, kLn2, logf(sum));
@@ -254,9 +263,10 @@ hipError_t launch_type(const AttnArgs& a, hipStream_t stream) {
         launch<T, 128>(a, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t threads = (int64_t)a.B * a.Hk * a.rows * (a.D / 4);
-    attn_join_kernel<T><<<(uint32_t)((threads + kAttnThreads - 1) / kAttnThreads), kAttnThreads, 0,
-                          stream>>>(a);
+    int threads = 8;
+    while (threads < kAttnThreads && threads < a.splits * (a.D / 4)) threads *= 2;
+    const int64_t rows = (int64_t)a.B * a.Hk * a.rows, per = kAttnThreads / threads;
+    attn_join_kernel<T><<<(uint32_t)((rows + per - 1) / per), kAttnThreads, 0, stream>>>(a, threads);
     return hipGetLastError();
 }
 

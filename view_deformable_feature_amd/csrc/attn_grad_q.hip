@@ -1,4 +1,4 @@
-// Attention's gradients to the queries, and the sums that both gradient kernels need.  Contract
+// Attention's gradients to the queries, and the sums that the other gradients need as well.  Contract
 // and formulas: include/attention.h; tiles and products: attn_device.h.
 //
 // As in the forward, columns are rows of queries and keys and values are streamed; a column's
@@ -41,8 +41,25 @@ void attn_grad_q_kernel(AttnArgs a) {
     load_column<T, DP>(static_cast<const char*>(a.grad_out) + b * a.g_batch + query * a.g_token +
                            head * a.g_head,
                        there, a.D, half, gc);
-    const int64_t stat = ((int64_t)b * a.H + head) * a.Nq + query;
-    const float lse2 = there ? a.lse2[stat] : kInf, delta = there ? a.delta[stat] : 0.0f;
+    float lse2 = kInf, delta = 0.0f;
+    {
+        u32x4 oc[Tl::kSteps];
+        load_column<T, DP>(static_cast<const char*>(a.out) + b * a.o_batch + query * a.o_token +
+                               head * a.o_head,
+                           there, a.D, half, oc);
+#pragma unroll
+        for (int t = 0; t < Tl::kSteps; ++t) delta = dot_pieces<T>(oc[t], gc[t], delta);
+        delta = column_sum(delta);
+        const int64_t stat = ((int64_t)b * a.H + head) * a.Nq + query;
+        if (there) {
+            const float lse = a.lse[stat];
+            lse2 = lse == -kInf ? kInf : lse / kLn2;
+            if (spot.split == 0 && half == 0) {   // for the other gradients
+                a.lse2[stat] = lse2;
+                a.delta[stat] = delta;
+            }
+        }
+    }
 
     const char* kp = static_cast<const char*>(a.k) + b * a.k_batch + hk * a.k_head + first * a.k_token;
     const char* vp = static_cast<const char*>(a.v) + b * a.v_batch + hk * a.v_head + first * a.v_token;
@@ -118,7 +135,7 @@ void attn_grad_q_kernel(AttnArgs a) {
         store_column<T, ND>(static_cast<T*>(a.grad_q) + line * a.D, a.D, half, acc, factor);
 }
 
-// ---- lse in base 2, and delta ------------------------------------------------------------
+// ---- lse in base 2, and delta, where the queries' gradients are not wanted ---------------
 //
 // Eight lanes to a row of out and grad_out, a run of 16-byte pieces in turn to each.
 template <typename T>

@@ -19,6 +19,7 @@ constexpr int kAttnThreads = 256;   // four waves
 // wave; in the forward's deep form it has 32 in all, its waves taking the tile's parts.
 constexpr int kAttnWide = 128, kAttnDeep = 32;
 constexpr int kAttnWideTile = 64, kAttnDeepTile = 128;   // rows or keys streamed at a time
+constexpr int kAttnMostSplits = 256;   // of a forward's keys: a thread of the join to each
 
 struct AttnArgs {
     const void *q, *k, *v;

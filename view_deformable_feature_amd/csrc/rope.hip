@@ -3,9 +3,10 @@
 //
 // A head's numbers go by units of two vectors, a and b, that lie so that a pair never leaves
 // its lane: in the half layout the vectors j and j + R / 2 V of the rotated part, in the
-// interleaved one neighbours.  A power of two of lanes has a head, a lane keeps its units
-// while it walks over a token's heads, and so forms their angles once for all of them: an angle
-// costs some 40 instructions, eight heads' worth of the rest.
+// interleaved one neighbours.  A power of two of lanes has a head.  A workgroup has some tokens and
+// forms their turns first, once each, in LDS: one costs some 30 instructions, a third of them in
+// binary64, as much as two numbers' way through the rest.  Then groups of lanes walk over the
+// tokens' heads, several abreast, the next ones' numbers on the way while these are turned.
 // Bound by memory: every number is read once and written once.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -92,17 +93,15 @@ struct Units {
             if (n >= r.units || b[u] >= r.D) b[u] = -1;
         }
     }
-    __device__ __forceinline__ void turns(const RopeArgs& r, int lane, double position) {
+    // from the token's turns
+    __device__ __forceinline__ void load(const RopeArgs& r, int lane, const float2* turns) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                c[u][e] = s[u][e] = 0.0f;
-                if (e < left[u]) {
-                    turn_of(position * r.freqs[(lane + u * r.lanes) * V + e], c[u][e], s[u][e]);
-                    c[u][e] *= r.magnitude;
-                    s[u][e] *= r.magnitude * r.sign;
-                }
+                const float2 t = e < left[u] ? turns[(lane + u * r.lanes) * V + e] : make_float2(1.0f, 0.0f);
+                c[u][e] = t.x;
+                s[u][e] = t.y;
             }
     }
     // x = [a's V, b's V] turned; SIGN -1 the other way.  Numbers past R stay what they are, whatever
@@ -133,66 +132,98 @@ __device__ __forceinline__ float head_sum(float v, int lanes) {
     return v;
 }
 
-// What a thread has to do: `lanes` lanes have an item, a token and a slice of its heads.
-struct Item {
-    int64_t b, n;
-    int head;
-    __device__ __forceinline__ Item(const RopeSide& t, int64_t item) {
-        const int64_t token = item / t.slices;
-        head = (int)(item % t.slices);
-        b = token / t.N;
-        n = token % t.N;
+// The turns of a workgroup's tokens from `first` on, R / 2 to each.
+__device__ __forceinline__ void form_turns(const RopeArgs& r, const RopeSide& t, int64_t first, int count,
+                                           float2* turns) {
+    const int pairs = r.R / 2, all = count * pairs;
+    for (int i = threadIdx.x; i < all; i += kRopeThreads) {
+        const int64_t token = first + i / pairs;
+        if (token >= t.tokens) break;
+        const double position = position_of(t, token / t.N, token % t.N);
+        float c, s;
+        turn_of(position * r.freqs[i % pairs], c, s);
+        turns[i] = make_float2(c * r.magnitude, s * r.magnitude * r.sign);
+    }
+}
+
+// A workgroup's share: its groups of lanes have `abreast` heads of `count` tokens.
+struct Share {
+    int lane, head, token, count;
+    __device__ __forceinline__ Share(const RopeArgs& r, const RopeSide& t) {
+        const int group = threadIdx.x / r.lanes;
+        lane = threadIdx.x % r.lanes;
+        head = group % t.abreast;
+        token = group / t.abreast;
+        count = kRopeThreads / r.lanes / t.abreast;
     }
 };
 
-template <typename T, int V, int U, bool NORM>
-__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs r) {
-    const int which = blockIdx.x >= (uint32_t)r.side[0].blocks;
-    const RopeSide& t = r.side[which];
-    const int64_t thread =
-        (int64_t)(blockIdx.x - (which ? r.side[0].blocks : 0)) * kRopeThreads + threadIdx.x;
-    const int lane = (int)(thread % r.lanes);
-    const int64_t item = thread / r.lanes;
-    if (item >= t.items) return;   // whole heads
-    const Item it(t, item);
-    Units<V, U> units(r, lane);
-    const bool interleaved = r.layout == ROPE_LAYOUT_INTERLEAVED;
-    const T* x = static_cast<const T*>(t.x) + it.b * t.x_batch + it.n * t.x_token;
-    T* y = static_cast<T*>(t.y) + it.b * t.y_batch + it.n * t.y_token;
-    Piece<T, V> in[U][2], next[U][2];
-    const auto fetch = [&](int head, Piece<T, V> (&to)[U][2]) {
+template <typename T, int V, int U>
+struct Vectors {
+    Piece<T, V> v[U][2];
+    __device__ __forceinline__ void load(const Units<V, U>& units, const T* p) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            to[u][0].zero();
-            to[u][1].zero();
-            if (units.a[u] >= 0) to[u][0].load(x + head * t.x_head + units.a[u]);
-            if (units.b[u] >= 0) to[u][1].load(x + head * t.x_head + units.b[u]);
+            v[u][0].zero();
+            v[u][1].zero();
+            if (units.a[u] >= 0) v[u][0].load(p + units.a[u]);
+            if (units.b[u] >= 0) v[u][1].load(p + units.b[u]);
         }
-    };
-    fetch(it.head, in);
-    float w[U][2 * V];
-    if constexpr (NORM) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                w[u][e] = t.weight && units.a[u] >= 0 ? t.weight[units.a[u] + e] : 1.0f;
-                w[u][e + V] = t.weight && units.b[u] >= 0 ? t.weight[units.b[u] + e] : 1.0f;
-            }
     }
-    units.turns(r, lane, position_of(t, it.b, it.n));
-    for (int head = it.head; head < t.H; head += t.slices) {
-        const bool more = head + t.slices < t.H;
-        if (more) fetch(head + t.slices, next);
+    __device__ __forceinline__ void unpack(int u, float (&x)[2 * V]) const {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            x[e] = (float)v[u][0].v[e];
+            x[e + V] = (float)v[u][1].v[e];
+        }
+    }
+};
+template <int V, int U>
+__device__ __forceinline__ void load_weights(const Units<V, U>& units, const float* weight,
+                                             float (&w)[U][2 * V]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            w[u][e] = weight && units.a[u] >= 0 ? weight[units.a[u] + e] : 1.0f;
+            w[u][e + V] = weight && units.b[u] >= 0 ? weight[units.b[u] + e] : 1.0f;
+        }
+}
+
+template <typename T, int V, int U, bool NORM>
+__global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs r) {
+    __shared__ float2 turns[kRopeThreads * V * U];   // lanes * V * U >= R / 2 to a token
+    const int which = blockIdx.x >= (uint32_t)r.side[0].blocks;
+    const RopeSide& t = r.side[which];
+    const Share at(r, t);
+    const int64_t first = (int64_t)(blockIdx.x - (which ? r.side[0].blocks : 0)) * at.count;
+    const int64_t token = first + at.token;
+    const bool there = token < t.tokens && at.head < t.H;   // for whole heads alike
+    Units<V, U> units(r, at.lane);
+    const int64_t b = there ? token / t.N : 0, n = there ? token % t.N : 0;
+    const T* x = static_cast<const T*>(t.x) + b * t.x_batch + n * t.x_token;
+    T* y = static_cast<T*>(t.y) + b * t.y_batch + n * t.y_token;
+    Vectors<T, V, U> in, next;
+    if (there) in.load(units, x + at.head * t.x_head);
+    float w[U][2 * V];
+    if constexpr (NORM) load_weights(units, t.weight, w);
+    form_turns(r, t, first, at.count, turns);
+    __syncthreads();
+    if (!there) return;
+    units.load(r, at.lane, turns + at.token * (r.R / 2));
+    const bool interleaved = r.layout == ROPE_LAYOUT_INTERLEAVED;
+    for (int head = at.head; head < t.H; head += t.abreast) {
+        const bool more = head + t.abreast < t.H;
+        if (more) next.load(units, x + (head + t.abreast) * t.x_head);
         float v[U][2 * V], sum = 0.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            in.unpack(u, v[u]);
+            if constexpr (NORM) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                v[u][e] = (float)in[u][0].v[e];
-                v[u][e + V] = (float)in[u][1].v[e];
-                if constexpr (NORM) sum = fmaf(v[u][e], v[u][e], fmaf(v[u][e + V], v[u][e + V], sum));
+                for (int e = 0; e < 2 * V; ++e) sum = fmaf(v[u][e], v[u][e], sum);
             }
+        }
         if constexpr (NORM) {
             const float f = rsqrtf(head_sum(sum, r.lanes) / (float)r.D + r.eps);
 #pragma unroll
@@ -207,67 +238,58 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs r) {
             if (units.a[u] >= 0) store_piece<T, V>(to + units.a[u], v[u]);
             if (units.b[u] >= 0) store_piece<T, V>(to + units.b[u], v[u] + V);
         }
-        if (more) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) in[u][i] = next[u][i];
-        }
+        if (more) in = next;
     }
 }
 
-// The gradients.  Workgroups walk over the items, so that a lane's sums for the weights' gradient
+// The gradients.  Workgroups walk over the tokens, so that a lane's sums for the weights' gradient
 // stay in registers; they meet in the workgroup through LDS, in an order of their own, and the
 // workgroups' sums in rope_weight_kernel.
 template <typename T, int V, int U>
 __global__ __launch_bounds__(kRopeThreads) void rope_backward_kernel(RopeArgs r) {
-    __shared__ float meet[kRopeThreads * U * 2 * V];
+    __shared__ float meet[kRopeThreads * U * 2 * V];   // turns, then the sums
+    float2* turns = reinterpret_cast<float2*>(meet);
     const int which = blockIdx.x >= (uint32_t)r.side[0].blocks;
     const RopeSide& t = r.side[which];
     const int block = blockIdx.x - (which ? r.side[0].blocks : 0);
-    const int lane = threadIdx.x % r.lanes, per = kRopeThreads / r.lanes;
-    Units<V, U> units(r, lane);
+    const Share at(r, t);
+    Units<V, U> units(r, at.lane);
     const bool interleaved = r.layout == ROPE_LAYOUT_INTERLEAVED;
     float w[U][2 * V], gw[U][2 * V];
+    load_weights(units, t.weight, w);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            w[u][e] = t.weight && units.a[u] >= 0 ? t.weight[units.a[u] + e] : 1.0f;
-            w[u][e + V] = t.weight && units.b[u] >= 0 ? t.weight[units.b[u] + e] : 1.0f;
-            gw[u][e] = gw[u][e + V] = 0.0f;
+        for (int e = 0; e < 2 * V; ++e) gw[u][e] = 0.0f;
+    for (int64_t first = (int64_t)block * at.count; first < t.tokens;
+         first += (int64_t)t.blocks * at.count) {
+        const int64_t token = first + at.token;
+        const bool there = token < t.tokens && at.head < t.H;
+        const int64_t b = there ? token / t.N : 0, n = there ? token % t.N : 0;
+        const T* x = static_cast<const T*>(t.x) + b * t.x_batch + n * t.x_token;
+        const T* g = static_cast<const T*>(t.y) + b * t.y_batch + n * t.y_token;
+        T* dx = static_cast<T*>(t.dx) + (there ? token : 0) * t.H * r.D;
+        Vectors<T, V, U> px, pg, nx, ng;
+        if (there) {
+            px.load(units, x + at.head * t.x_head);
+            pg.load(units, g + at.head * t.y_head);
         }
-    for (int64_t item = (int64_t)block * per + threadIdx.x / r.lanes; item < t.items;
-         item += (int64_t)t.blocks * per) {
-        const Item it(t, item);
-        const T* x = static_cast<const T*>(t.x) + it.b * t.x_batch + it.n * t.x_token;
-        const T* g = static_cast<const T*>(t.y) + it.b * t.y_batch + it.n * t.y_token;
-        T* dx = static_cast<T*>(t.dx) + (it.b * t.N + it.n) * t.H * r.D;
-        units.turns(r, lane, position_of(t, it.b, it.n));
-        for (int head = it.head; head < t.H; head += t.slices) {
-            Piece<T, V> px[U][2], pg[U][2];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                px[u][0].zero(), px[u][1].zero(), pg[u][0].zero(), pg[u][1].zero();
-                if (units.a[u] >= 0) {
-                    px[u][0].load(x + head * t.x_head + units.a[u]);
-                    pg[u][0].load(g + head * t.y_head + units.a[u]);
-                }
-                if (units.b[u] >= 0) {
-                    px[u][1].load(x + head * t.x_head + units.b[u]);
-                    pg[u][1].load(g + head * t.y_head + units.b[u]);
-                }
+        __syncthreads();
+        form_turns(r, t, first, at.count, turns);
+        __syncthreads();
+        if (!there) continue;
+        units.load(r, at.lane, turns + at.token * (r.R / 2));
+        for (int head = at.head; head < t.H; head += t.abreast) {
+            const bool more = head + t.abreast < t.H;
+            if (more) {
+                nx.load(units, x + (head + t.abreast) * t.x_head);
+                ng.load(units, g + (head + t.abreast) * t.y_head);
             }
             float v[U][2 * V], d[U][2 * V], squares = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    v[u][e] = (float)px[u][0].v[e];
-                    v[u][e + V] = (float)px[u][1].v[e];
-                    d[u][e] = (float)pg[u][0].v[e];
-                    d[u][e + V] = (float)pg[u][1].v[e];
-                }
+                px.unpack(u, v[u]);
+                pg.unpack(u, d[u]);
                 units.template rotate<-1>(interleaved, u, d[u]);
 #pragma unroll
                 for (int e = 0; e < 2 * V; ++e) {
@@ -293,9 +315,14 @@ __global__ __launch_bounds__(kRopeThreads) void rope_backward_kernel(RopeArgs r)
                     if (units.b[u] >= 0) store_piece<T, V>(to + units.b[u], d[u] + V);
                 }
             }
+            if (more) {
+                px = nx;
+                pg = ng;
+            }
         }
     }
     if (!t.grad_weight) return;
+    __syncthreads();
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -303,38 +330,45 @@ __global__ __launch_bounds__(kRopeThreads) void rope_backward_kernel(RopeArgs r)
             meet[(u * 2 * V + e) * kRopeThreads + threadIdx.x] = gw[u][e];
     __syncthreads();
     // thread k adds up number (u, e) of lane l over the workgroup's heads
+    const int per = kRopeThreads / r.lanes;
     for (int k = threadIdx.x; k < U * 2 * V * r.lanes; k += kRopeThreads) {
         const int l = k % r.lanes, ue = k / r.lanes;
         const Units<V, U> of(r, l);
-        int at = -1;
+        int place = -1;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                if (ue == u * 2 * V + e && of.a[u] >= 0) at = of.a[u] + e;
-                if (ue == u * 2 * V + e + V && of.b[u] >= 0) at = of.b[u] + e;
+                if (ue == u * 2 * V + e && of.a[u] >= 0) place = of.a[u] + e;
+                if (ue == u * 2 * V + e + V && of.b[u] >= 0) place = of.b[u] + e;
             }
-        if (at < 0) continue;
+        if (place < 0) continue;
         double sum = 0.0;
         for (int p = 0; p < per; ++p) sum += (double)meet[ue * kRopeThreads + p * r.lanes + l];
-        t.part[(int64_t)block * r.D + at] = (float)sum;
+        t.part[(int64_t)block * r.D + place] = (float)sum;
     }
 }
 
-// The workgroups' sums joined in binary64: 16 numbers of a head to a workgroup, 16 threads to each.
+// The workgroups' sums joined in binary64: 8 numbers of a head to a workgroup, 32 threads to each.
+constexpr int kJoinNumbers = 8;
 __global__ __launch_bounds__(kRopeThreads) void rope_weight_kernel(RopeArgs r) {
+    constexpr int kRows = kRopeThreads / kJoinNumbers;
     __shared__ double meet[kRopeThreads];
-    const int tiles = (r.D + 15) / 16;
+    const int tiles = (r.D + kJoinNumbers - 1) / kJoinNumbers;
     const RopeSide& t = r.side[blockIdx.x / tiles];
     if (!t.grad_weight) return;
-    const int at = blockIdx.x % tiles * 16 + threadIdx.x % 16;
+    const int at = blockIdx.x % tiles * kJoinNumbers + threadIdx.x % kJoinNumbers;
     double sum = 0.0;
-    if (at < r.D)
-        for (int k = threadIdx.x / 16; k < t.blocks; k += 16) sum += (double)t.part[(int64_t)k * r.D + at];
+    if (at < r.D) {
+#pragma unroll 16
+        for (int k = threadIdx.x / kJoinNumbers; k < t.blocks; k += kRows)
+            sum += (double)t.part[(int64_t)k * r.D + at];
+    }
     meet[threadIdx.x] = sum;
     __syncthreads();
-    if (threadIdx.x >= 16 || at >= r.D) return;
-    for (int k = 1; k < 16; ++k) sum += meet[k * 16 + threadIdx.x];
+    if (threadIdx.x >= kJoinNumbers || at >= r.D) return;
+#pragma unroll
+    for (int k = 1; k < kRows; ++k) sum += meet[k * kJoinNumbers + threadIdx.x];
     t.grad_weight[at] = (float)sum;
 }
 
@@ -396,7 +430,7 @@ hipError_t launch_rope_norm_backward(const RopeArgs& a, int vec, int per_lane, h
     bool weights = false;
     for (int i = 0; i < a.sides; ++i) weights = weights || a.side[i].grad_weight;
     if (e != hipSuccess || !weights) return e;
-    rope_weight_kernel<<<(uint32_t)(a.sides * ((a.D + 15) / 16)), kRopeThreads, 0, stream>>>(a);
+    rope_weight_kernel<<<(uint32_t)(a.sides * ((a.D + kJoinNumbers - 1) / kJoinNumbers)), kRopeThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -72,6 +72,9 @@ da_status check_tensor(const rope_problem* p, const rope_tensor* t) {
 
 int pos_bytes(int32_t t) { return t == ROPE_POS_I64 ? 8 : 4; }
 
+constexpr int64_t kWantedBlocks = 1024;     // workgroups that a launch should have
+constexpr int64_t kBackwardBlocks = 512;    // that a backward launch has at most
+
 bool empty(const rope_tensor* t) { return !t || t->batch == 0 || t->tokens == 0; }
 
 // The largest vector, at most 16 bytes, that the sizes, strides and addresses allow.
@@ -109,41 +112,30 @@ int lay_out(const rope_problem* p, int vec, da::RopeArgs& a) {
     return per_lane <= 1 ? 1 : per_lane <= 2 ? 2 : 4;
 }
 
-// A token's heads in slices: as few as give `groups` groups of lanes something to do.
-void slice(const rope_tensor* t, int64_t groups, da::RopeSide& s) {
-    s.B = (int32_t)t->batch;
+// A side's tensor and its workgroups: heads abreast so that a group of lanes has four or more of a
+// token's to walk over, but up to all of them side by side where that leaves fewer than `want`
+// workgroups.  A launch has fewer than 2^32 threads; the backward's workgroups walk over the tokens.
+da_status share_out(const rope_tensor* t, const da::RopeArgs& a, bool backward, da::RopeSide& s) {
+    s.tokens = t->batch * t->tokens;
     s.N = (int32_t)t->tokens;
     s.H = (int32_t)t->heads;
     s.pos_type = t->pos_type;
     s.pos_batch = t->pos_stride;
     s.x_batch = t->x_stride[0], s.x_token = t->x_stride[1], s.x_head = t->x_stride[2];
     s.y_batch = t->y_stride[0], s.y_token = t->y_stride[1], s.y_head = t->y_stride[2];
-    const int64_t tokens = t->batch * t->tokens;
-    const int64_t want = tokens ? (groups + tokens - 1) / tokens : 1;
-    const int64_t steps = std::max<int64_t>(1, t->heads / std::min(want, t->heads));   // heads of a slice
-    s.slices = (int32_t)((t->heads + steps - 1) / steps);
-    s.items = tokens * s.slices;
-}
-
-constexpr int64_t kForwardThreads = int64_t(256) * 1024;   // lanes that a forward launch should have
-constexpr int64_t kBackwardBlocks = 1024;
-
-da_status count_blocks(da::RopeArgs& a, bool backward) {
-    wide all = 0;
-    for (int i = 0; i < a.sides; ++i) {
-        da::RopeSide& s = a.side[i];
-        const wide blocks = ((wide)s.items * a.lanes + da::kRopeThreads - 1) / da::kRopeThreads;
-        if (backward) {
-            s.blocks = (int32_t)std::min<wide>(blocks, kBackwardBlocks);
-        } else {
-            if (blocks >= (wide(1) << 32) / da::kRopeThreads)
-                return report_error(DA_ERR_UNSUPPORTED, "2^32 threads of workgroups or more");
-            s.blocks = (int32_t)blocks;
-        }
-        all += s.blocks;
-    }
-    if (all >= (wide(1) << 32) / da::kRopeThreads)
-        return report_error(DA_ERR_UNSUPPORTED, "2^32 threads of workgroups or more");
+    const int64_t groups = da::kRopeThreads / a.lanes;
+    s.abreast = 1;
+    const auto blocks = [&] {
+        const int64_t tokens = groups / s.abreast;
+        return (s.tokens + tokens - 1) / tokens;
+    };
+    while (s.abreast * 2 <= std::min(groups, t->heads) &&
+           (s.abreast * 8 <= t->heads || blocks() < kWantedBlocks))
+        s.abreast *= 2;
+    const int64_t n = blocks();
+    if (!backward && n >= (int64_t(1) << 32) / da::kRopeThreads / 2)
+        return report_error(DA_ERR_UNSUPPORTED, "2^31 threads of workgroups or more");
+    s.blocks = (int32_t)(backward ? std::min(n, kBackwardBlocks) : n);
     return DA_OK;
 }
 
@@ -254,9 +246,10 @@ da_status set_up(const rope_problem* p, const Given (&given)[2], const double* f
     int at = 0;
     for (const Given& g : given) {
         if (!g.t || (empty(g.t) && !(backward && g.grad_weight))) continue;
-        slice(g.t, (backward ? kBackwardBlocks * da::kRopeThreads : kForwardThreads) / a.lanes, a.side[at++]);
+        const da_status shared = share_out(g.t, a, backward, a.side[at++]);
+        if (shared != DA_OK) return shared;
     }
-    return count_blocks(a, backward);
+    return DA_OK;
 }
 
 // Workgroups' sums of one side: as many as there may be, since the vectors are not known yet.

@@ -27,10 +27,10 @@ struct RopeSide {
     int64_t x_batch, x_token, x_head;   // strides in elements
     int64_t y_batch, y_token, y_head;
     int64_t pos_batch;
-    int64_t items;            // tokens of all batch entries, times slices
-    int32_t B, N, H;
+    int64_t tokens;           // of all batch entries
+    int32_t N, H;
     int32_t pos_type;
-    int32_t slices;           // of a token's heads: item's head is its slice, and every slices-th after
+    int32_t abreast;          // heads of a token that a workgroup has side by side
     int32_t blocks;           // workgroups
 };
 

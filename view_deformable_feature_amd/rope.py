@@ -21,9 +21,9 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from ._call import call, maybe, need, scratch, size
+from ._call import call, need, scratch, size
 from .api import _DTYPES, _FLOATS
-from .attention import _need_heads, _strides
+from .attention import _like, _need_heads, _strides
 
 __all__ = ["rope_frequencies", "rope_forward", "rope_norm_forward", "rope_norm_backward",
            "rope_norm_backward_workspace_size", "RotaryFunction", "NormRotaryFunction", "rotary",
@@ -90,10 +90,11 @@ def _problem(D, rotated, eps, magnitude, layout, dtype, flags):
 
 
 @functools.lru_cache(maxsize=512)
-def _tensor(shape, x_stride, y_stride, pos_type, pos_stride):
-    three = ctypes.c_int64 * 3
-    return ctypes.byref(_lib.RopeTensor(*shape[:3], three(*x_stride), three(*y_stride), pos_stride,
-                                        pos_type, 0))
+def _tensor(shape, x_stride, y_stride, pos_type, batched, name):
+    """A tensor's description for the library, which only reads it."""
+    return ctypes.byref(_lib.RopeTensor(
+        *shape[:3], _strides(shape, x_stride, name), _strides(shape, y_stride, name + "'s result"),
+        shape[1] if batched else 0, pos_type, 0))
 
 
 @functools.lru_cache(maxsize=256)
@@ -111,27 +112,42 @@ def _check_heads(x, name):
 def _frequencies(freqs, dev):
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
         raise ValueError("freqs must be a [R / 2] float64 tensor")
+    if freqs.dtype is torch.float64 and freqs.device == dev and freqs.is_contiguous():
+        return freqs.data_ptr()
     return need(freqs, "freqs", torch.float64, dev, freqs.shape)
 
 
+def _weight(w, name, dev, D):
+    if w is None:
+        return None
+    if (isinstance(w, torch.Tensor) and w.dtype is torch.float32 and w.device == dev and w.dim() == 1
+            and w.shape[0] == D and w.is_contiguous()):
+        return w.data_ptr()
+    return need(w, name, torch.float32, dev, (D,))
+
+
 def _place(positions, name, shape, dev):
-    """(address, type, stride of the batch) of positions."""
+    """(address, type, whether each batch entry has its own) of positions."""
     if positions is None:
-        return None, _lib.ROPE_POS_INDEX, 0
-    if not isinstance(positions, torch.Tensor) or positions.dtype not in _POSITIONS:
+        return None, _lib.ROPE_POS_INDEX, False
+    kind = _POSITIONS.get(positions.dtype) if isinstance(positions, torch.Tensor) else None
+    if kind is None:
         raise TypeError(f"{name} must be a tensor of {tuple(_POSITIONS)}")
-    batched = positions.dim() == 2
-    if positions.dim() not in (1, 2):
+    at = positions.shape
+    batched = len(at) == 2
+    if len(at) not in (1, 2):
         raise ValueError(f"{name} must be [N] or [B, N]")
-    p = need(positions, name, positions.dtype, dev, shape[:2] if batched else shape[1:2])
-    return p, _POSITIONS[positions.dtype], shape[1] if batched else 0
+    if (at[-1] == shape[1] and (not batched or at[0] == shape[0]) and positions.device == dev
+            and positions.is_contiguous()):
+        return positions.data_ptr(), kind, batched
+    return need(positions, name, positions.dtype, dev, shape[:2] if batched else shape[1:2]), kind, batched
 
 
 def _result(out, name, x):
-    """out, or a new dense tensor, and its strides; x's shape and type."""
+    """out, or a new dense tensor; x's shape and type."""
     if out is None:
-        out = torch.empty(x.shape, device=x.device, dtype=x.dtype)
-    elif not isinstance(out, torch.Tensor) or out.shape != x.shape:
+        return _like(x)
+    if not isinstance(out, torch.Tensor) or out.shape != x.shape:
         raise ValueError(f"{name} must have the shape {tuple(x.shape)}")
     _need_heads(out, name, x.dtype, x.device)
     return out
@@ -146,11 +162,11 @@ def rope_forward(x: torch.Tensor, freqs: torch.Tensor, positions: Optional[torch
     dev, shape = x.device, x.shape
     px = _need_heads(x, "x", x.dtype, dev)
     pf = _frequencies(freqs, dev)
-    pp, kind, step = _place(positions, "positions", shape, dev)
+    pp, kind, batched = _place(positions, "positions", shape, dev)
     out = _result(out, "out", x)
     prob = _problem(shape[3], 2 * freqs.shape[0], 0.0, float(magnitude), layout, x.dtype,
                     _lib.ROPE_FLAG_INVERSE if inverse else 0)
-    t = _tensor(shape, _strides(x, "x"), _strides(out, "out"), kind, step)
+    t = _tensor(shape, x.stride(), out.stride(), kind, batched, "x")
     call("rope_forward", dev, prob, t, px, pp, pf, out.data_ptr())
     return out
 
@@ -185,10 +201,11 @@ def rope_norm_forward(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Opti
             outs.append(None)
             continue
         px = _need_heads(x, name, q.dtype, dev)
-        pw = maybe(w, name + "_weight", torch.float32, dev, x.shape[3:])
-        pp, kind, step = _place(pos, name + "_positions", x.shape, dev)
+        shape = x.shape
+        pw = _weight(w, name + "_weight", dev, shape[3])
+        pp, kind, batched = _place(pos, name + "_positions", shape, dev)
         out = _result(out, name + "_out", x)
-        args += [_tensor(x.shape, _strides(x, name), _strides(out, name + "_out"), kind, step), px, pp, pw, out.data_ptr()]
+        args += [_tensor(shape, x.stride(), out.stride(), kind, batched, name), px, pp, pw, out.data_ptr()]
         outs.append(out)
     call("rope_norm_forward", dev, prob, *args, pf)
     return tuple(outs)
@@ -203,9 +220,9 @@ def _backward_plan(q, k, gq, gk, freqs, q_positions, k_positions, eps, layout, m
         if x is None:
             tensors.append((None, None))
             continue
-        pp, kind, step = _place(pos, name + "_positions", x.shape, q.device)
-        tensors.append((_tensor(x.shape, _strides(x, name),
-                                _strides(x if g is None else g, f"grad_{name}_out"), kind, step), pp))
+        pp, kind, batched = _place(pos, name + "_positions", x.shape, q.device)
+        tensors.append((_tensor(x.shape, x.stride(), (x if g is None else g).stride(), kind, batched,
+                                name), pp))
     return prob, tensors, _backward_size(prob, tensors[0][0], tensors[1][0])
 
 
@@ -241,8 +258,8 @@ def rope_norm_backward(q: torch.Tensor, k: Optional[torch.Tensor], grad_q_out: t
             continue
         px = _need_heads(x, name, q.dtype, dev)
         pg = _need_heads(g, f"grad_{name}_out", q.dtype, dev)
-        pw = maybe(w, name + "_weight", torch.float32, dev, x.shape[3:])
-        grads.append(torch.empty(x.shape, device=dev, dtype=x.dtype))
+        pw = _weight(w, name + "_weight", dev, x.shape[3])
+        grads.append(_like(x))
         weights.append(torch.empty(x.shape[3:], device=dev, dtype=torch.float32) if need_weights else None)
         args += [t, px, pp, pw, pg, grads[-1].data_ptr(),
                  weights[-1].data_ptr() if need_weights else None]

@@ -74,7 +74,7 @@ DA_API da_status attn_forward_workspace_size(const attn_problem* problem, size_t
  *   workspace  device scratch of attn_forward_workspace_size() bytes, 256-byte aligned (may
  *              be NULL when that is 0); contents on entry do not matter.
  * Errors: DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (head_dim, strides of a token of 2^24 bytes or
- * more, 2^31 rows or keys, a launch of 2^32 threads or more), DA_ERR_HIP.
+ * more, 2^31 rows, 2^30 keys, a launch of 2^32 threads or more), DA_ERR_HIP.
  */
 DA_API da_status attn_forward(const attn_problem* problem, const void* q, const void* k,
                               const void* v, const int32_t* kv_lens, const uint8_t* key_mask,

@@ -70,7 +70,7 @@ ATTN_BAD = [
     (dict(reserved=1), 1, "reserved"),
     (dict(head_dim=20), 2, "multiple of 8"),
     (dict(head_dim=136), 2, "up to 128"),
-    (dict(keys=1 << 31), 2, "2^31"),
+    (dict(keys=1 << 30), 2, "2^30"),
     (dict(queries=1 << 30), 2, "2^31"),
     (dict(batch=1 << 30), 2, "2^31"),
     (dict(heads=1 << 20, key_heads=1 << 20), 2, "2^24"),

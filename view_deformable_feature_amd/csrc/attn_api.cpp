@@ -56,11 +56,11 @@ da_status check_problem(const attn_problem* p) {
     if (p->head_dim % 8 != 0 || p->head_dim > 128)
         return report_error(DA_ERR_UNSUPPORTED, "head_dim is not a multiple of 8 up to 128");
     const int e = elem_bytes(p->dtype);
-    if (p->batch >= k2to31 || p->queries >= k2to31 || p->keys >= k2to31 - 256 || p->heads >= k2to31 ||
+    if (p->batch >= k2to31 || p->queries >= k2to31 || p->keys >= (int64_t(1) << 30) || p->heads >= k2to31 ||
         (wide)p->queries * (p->heads / p->key_heads) >= k2to31 - 256 ||
         (wide)p->batch * p->key_heads >= k2to31 || (wide)p->heads * p->head_dim * e >= (1 << 24))
         return report_error(DA_ERR_UNSUPPORTED,
-                            "2^31 rows, keys or key heads, or heads of 2^24 bytes a token");
+                            "2^31 rows or key heads, 2^30 keys, or heads of 2^24 bytes a token");
     if ((wide)p->batch * p->queries * p->heads >= (wide)1 << 45 ||
         (wide)p->batch * p->keys * p->key_heads >= (wide)1 << 45)
         return report_error(DA_ERR_UNSUPPORTED, "2^45 rows or keys");
@@ -95,24 +95,29 @@ void describe(const attn_problem* p, da::AttnArgs& a) {
     a.dtype = p->dtype;
 }
 
-// The forward's form: wide where that gives every compute unit a workgroup, else deep, four times as
-// many; always deep where one of its workgroups has all rows.  Where even the deep one leaves
-// compute units without work, the keys are split over workgroups.
+constexpr int64_t kShortSteps = 8;      // of a workgroup over the keys that are not worth a second launch
+constexpr int64_t kSplitBlocks = 512;   // workgroups that splits may make
+
+// The forward's form: wide where that gives every compute unit a workgroup, else 32 rows to one,
+// four times as many; always so where one of those has all rows.  Where even these leave compute
+// units without work, the keys are split over workgroups.
 void choose_forward(da::AttnArgs& a) {
     const int64_t units = (int64_t)a.B * a.Hk;
-    a.deep = a.rows <= da::kAttnDeep ||
-             units * ((a.rows + (int64_t)da::kAttnWide - 1) / da::kAttnWide) < 256;
-    const int64_t width = a.deep ? da::kAttnDeep : da::kAttnWide;
+    a.few = a.rows <= da::kAttnFew ||
+            units * ((a.rows + (int64_t)da::kAttnWide - 1) / da::kAttnWide) < 256;
+    const int64_t width = a.few ? da::kAttnFew : da::kAttnWide;
     a.col_tiles = (int32_t)((a.rows + width - 1) / width);
     const int64_t blocks = units * a.col_tiles;
-    const int64_t tiles = (a.Nk + (int64_t)da::kAttnDeepTile - 1) / da::kAttnDeepTile;
-    if (a.deep && blocks < 256 && tiles > 1) {
-        const int64_t splits =
-            std::min({tiles, 512 / std::max<int64_t>(blocks, 1), (int64_t)da::kAttnMostSplits});
-        const int64_t per = (tiles + splits - 1) / splits;
-        a.split_keys = (int32_t)(per * da::kAttnDeepTile);
-        a.splits = (int32_t)((tiles + per - 1) / per);
-    }
+    if (!a.few || blocks >= 256) return;
+    const int64_t per_step = (int64_t)da::kAttnFew * da::attn_few_waves(a);
+    const int64_t steps = (a.Nk + per_step - 1) / per_step;
+    if (steps <= kShortSteps) return;
+    const int64_t splits =
+        std::min({steps / 2, kSplitBlocks / std::max<int64_t>(blocks, 1), (int64_t)da::kAttnMostSplits});
+    if (splits <= 1) return;
+    const int64_t per = (steps + splits - 1) / splits;
+    a.split_keys = (int32_t)(per * per_step);
+    a.splits = (int32_t)((steps + per - 1) / per);
 }
 
 // A gradient's form for so many columns to a key head and tiles that are streamed to them: split
@@ -127,11 +132,11 @@ void choose_backward(da::AttnArgs& a, int64_t columns, int64_t tiles, int64_t wa
     a.splits = (int32_t)std::max<int64_t>(1, (tiles + per - 1) / per);
 }
 void choose_grad_q(da::AttnArgs& a) {
-    const int64_t tiles = ((int64_t)a.Nk + da::kAttnWideTile - 1) / da::kAttnWideTile;
+    const int64_t tiles = ((int64_t)a.Nk + da::kAttnTile - 1) / da::kAttnTile;
     choose_backward(a, a.rows, tiles, a.dtype == DA_F32 ? 1 : 2);
 }
 void choose_grad_kv(da::AttnArgs& a) {
-    const int64_t tiles = ((int64_t)a.Nq + da::kAttnWideTile - 1) / da::kAttnWideTile * a.group;
+    const int64_t tiles = ((int64_t)a.Nq + da::kAttnTile - 1) / da::kAttnTile * a.group;
     choose_backward(a, a.Nk, tiles, a.dtype == DA_F32 || a.D > 64 ? 1 : 2);
 }
 

@@ -72,16 +72,17 @@ __device__ __forceinline__ float column_sum(float v) {
 // A tile of ROWS rows of DP numbers, in pieces of 16 bytes.  A row's pieces are turned by an
 // exclusive or that depends on the row, so that neither 16 rows' equal pieces (rows times
 // columns) nor 64 bytes of four rows in a row (the transposing read) meet in the banks.
-template <typename T, int DP, int ROWS>
+// THREADS fill it together.
+template <typename T, int DP, int ROWS, int THREADS = kAttnThreads>
 struct Tile {
     static constexpr int kUsed = DP * (int)sizeof(T) / 16;
     static constexpr int kRow = kUsed <= 4 ? 4 : kUsed <= 8 ? 8 : kUsed <= 16 ? 16 : 32;
     static constexpr int kPieces = ROWS * kRow;
     static constexpr int kBytesRow = kRow * 16;
-    static constexpr int kFetches = kPieces / kAttnThreads;
+    static constexpr int kThreads = THREADS;
+    static constexpr int kFetches = kPieces / THREADS;
     static constexpr int kSteps = DP * (int)sizeof(T) / 32;   // pieces of a lane half
-    static constexpr int kRowsFetch = kAttnThreads / kRow;
-    static constexpr int kWords = ROWS / 64;
+    static constexpr int kRowsFetch = THREADS / kRow;
 
     static __host__ __device__ constexpr int turn(int row) {
         return kRow >= 16 ? ((row & 3) << 2) | ((row >> 2) & 3)
@@ -211,6 +212,13 @@ __device__ __forceinline__ void load_column(const char* p, bool there, int D, in
     }
 }
 
+// Which of up to 64 keys are visible, a bit each, from their number and their bytes of a mask; the
+// bytes are read a tile ahead, a key to a lane.
+struct Visible {
+    uint64_t bits;
+    __device__ __forceinline__ bool operator()(int row) const { return (bits >> row) & 1; }
+    __device__ __forceinline__ uint32_t block(int b) const { return (uint32_t)(bits >> (b * 32)); }
+};
 // Fills a tile in LDS straight from memory: a filling instruction puts lane l's 16 bytes at
 // place l of a run of 1 KB, so the turned order is in the addresses that the lanes fetch
 // from.  Rows past `rows`, numbers past D and rows that `see` leaves out become zeros.
@@ -220,9 +228,21 @@ struct Filler {
     uint32_t pieces;       // of a row, D numbers
     __device__ __forceinline__ Filler(int thread, int row_bytes)
         : row(thread / Tl::kRow), piece(thread % Tl::kRow), pieces(row_bytes / 16) {}
-    template <typename See>
+    // rows without a mask
     __device__ __forceinline__ void run(const char* base, int rows, uint32_t stride, u32x4* tile,
-                                        int wave, See&& see) const {
+                                        int wave) const {
+        fill(base, rows, stride, tile, wave, [](int) { return true; });
+    }
+    __device__ __forceinline__ void run(const char* base, int rows, uint32_t stride, u32x4* tile,
+                                        int wave, const Visible& vis, bool masked) const {
+        if (masked)
+            fill(base, rows, stride, tile, wave, vis);
+        else
+            run(base, rows, stride, tile, wave);
+    }
+    template <typename See>
+    __device__ __forceinline__ void fill(const char* base, int rows, uint32_t stride, u32x4* tile,
+                                         int wave, See&& see) const {
         // whole numbers in scalar registers, or every fetch becomes a loop over a lane's values
         rows = __builtin_amdgcn_readfirstlane(rows);
         const uint64_t place = reinterpret_cast<uint64_t>(base);
@@ -238,7 +258,7 @@ struct Filler {
             const uint32_t p = piece ^ Tl::turn(at);
             const uint32_t off = p < pieces && see(at) ? at * stride + p * 16 : 0x80000000u;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                r, (__attribute__((address_space(3))) void*)(tile + i * kAttnThreads + wave * 64), 16,
+                r, (__attribute__((address_space(3))) void*)(tile + i * Tl::kThreads + wave * 64), 16,
                 off, 0, 0, 0);
         }
     }
@@ -251,38 +271,26 @@ __device__ __forceinline__ void tile_barrier() {
     __syncthreads();
 }
 
-// Which rows of a tile of keys are visible, a bit each.
-template <int WORDS>
-struct Visible {
-    uint64_t word[WORDS];
-    __device__ __forceinline__ bool operator()(int row) const {
-        const uint64_t w = WORDS == 2 && row >= 64 ? word[WORDS - 1] : word[0];
-        return (w >> (row & 63)) & 1;
-    }
-    __device__ __forceinline__ uint32_t block(int b) const {
-        const uint64_t w = WORDS == 2 && b >= 2 ? word[WORDS - 1] : word[0];
-        return (uint32_t)(w >> (b % 2 * 32));
-    }
-};
-// The bytes of a tile's mask, a row to a lane and word, read a tile ahead; keys is the number of
-// keys from the tile's first on.
-template <int WORDS>
-struct MaskBytes {
-    uint32_t byte[WORDS];
-    __device__ __forceinline__ void load(const uint8_t* mask, int keys, int lane) {
+// The wave's own fills of LDS have arrived and its reads are done.
+__device__ __forceinline__ void own_fills() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t mask_byte(const uint8_t* mask, int keys, int lane) {
+    uint32_t byte = 1;
+    if (mask && lane < keys) byte = mask[lane];
+    return byte;
+}
+__device__ __forceinline__ Visible visible(uint32_t byte, int keys, int lane) {
+    return {__ballot(byte && lane < keys)};
+}
+// Scores (or dS) of a block of keys, `other` where the key is not visible
+__device__ __forceinline__ void hide(f32x16& s, uint32_t see, int half, float other) {
+    if (see == ~0u) return;
+    const uint32_t mine = see >> (4 * half);
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-            byte[w] = 1;
-            if (mask && w * 64 + lane < keys) byte[w] = mask[w * 64 + lane];
-        }
-    }
-    __device__ __forceinline__ Visible<WORDS> visible(int keys, int lane) const {
-        Visible<WORDS> v;
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) v.word[w] = __ballot(byte[w] && w * 64 + lane < keys);
-        return v;
-    }
-};
+    for (int i = 0; i < 16; ++i) s[i] = mine & (1u << (8 * (i / 4) + i % 4)) ? s[i] : other;
+}
 
 // The workgroup's place: (batch entry, key head), tile of columns, split of keys.  Workgroups go
 // to the eight XCDs in turn, and those of a key head stay on one, whose L2 then has its states:
@@ -311,32 +319,6 @@ __device__ __forceinline__ Spot spot_of(const AttnArgs& a) {
 // The number of keys of a batch entry.
 __device__ __forceinline__ int keys_of(const AttnArgs& a, int b) {
     return a.lens ? min(max(a.lens[b], 0), a.Nk) : a.Nk;
-}
-
-// Adds up the four waves' accumulators of the deep form in the first one; `meet` has room for
-// two of them.  All threads of the workgroup.
-template <int ND>
-__device__ __forceinline__ void add_waves(f32x16 (&acc)[ND], float* meet, int wave, int lane) {
-    const auto put = [&](int slot) {
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) meet[((slot * ND + d) * 16 + i) * 64 + lane] = acc[d][i];
-    };
-    const auto add = [&](int slot) {
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[d][i] += meet[((slot * ND + d) * 16 + i) * 64 + lane];
-    };
-    __syncthreads();
-    if (wave >= 2) put(wave - 2);
-    __syncthreads();
-    if (wave < 2) add(wave);
-    __syncthreads();
-    if (wave == 1) put(0);
-    __syncthreads();
-    if (wave == 0) add(0);
 }
 
 // A lane's part of its column's result, numbers 32 d + 8 j + 4 (l / 32) + 0 .. 3 each times

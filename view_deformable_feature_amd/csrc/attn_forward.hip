@@ -22,82 +22,22 @@ template <typename T>
 constexpr float kLiftLog2 = std::is_same<T, _Float16>::value ? 7.0f : 0.0f;
 constexpr float kGrowth = 8.0f;
 
-// Waves to a SIMD that the registers leave room for.
-template <typename T, int DP, bool DEEP>
-constexpr int kForwardWaves = DEEP || sizeof(T) == 4 ? 1 : 2;
-
-template <typename T, int DP, bool DEEP>
-__global__ __launch_bounds__(kAttnThreads, (kForwardWaves<T, DP, DEEP>))
-void attn_forward_kernel(AttnArgs a) {
-    constexpr int TILE = DEEP ? kAttnDeepTile : kAttnWideTile, NB = DEEP ? 1 : 2, ND = DP / 32;
-    using Tl = Tile<T, DP, TILE>;
-    constexpr bool TWICE = Tl::kPieces * 16 * 4 <= 128 * 1024;   // room for the next tile
-    // arrays of their own: the compiler then sees that what is filled is not what is read
-    __shared__ u32x4 k0[Tl::kPieces], v0[Tl::kPieces];
-    __shared__ u32x4 k1[TWICE ? Tl::kPieces : 1], v1[TWICE ? Tl::kPieces : 1];
-    const Spot spot = spot_of(a);
-    if (!spot.there) return;
-    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int col = lane % 32, half = lane / 32;
-    const int b = spot.unit / a.Hk, hk = spot.unit % a.Hk;
-    const int all = keys_of(a, b);
-    const int first = spot.split * a.split_keys;
-    const int keys = min(all - first, a.split_keys);   // of this workgroup; may be none
-    const int tiles = keys > 0 ? (keys + TILE - 1) / TILE : 0;
-
-    const int r = spot.tile * (DEEP ? kAttnDeep : kAttnWide) + (DEEP ? 0 : wave * 32) + col;
-    const int query = (uint32_t)r / (uint32_t)a.group, head = hk * a.group + (uint32_t)r % (uint32_t)a.group;
-    const bool there = r < a.rows;
-    u32x4 qc[Tl::kSteps];
-    load_column<T, DP>(static_cast<const char*>(a.q) + b * a.q_batch + query * a.q_token + head * a.q_head,
-                       there, a.D, half, qc);
-
-    const char* kp = static_cast<const char*>(a.k) + b * a.k_batch + hk * a.k_head + first * a.k_token;
-    const char* vp = static_cast<const char*>(a.v) + b * a.v_batch + hk * a.v_head + first * a.v_token;
-    const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.Nk + first : nullptr;
-    const Places<T, DP> at(lane);
-    const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
-    MaskBytes<Tl::kWords> bytes;
-
-    const auto fetch = [&](int j, const Visible<Tl::kWords>& vis, u32x4* ks, u32x4* vs) {
-        const int rows = min(keys - j * TILE, TILE);
-        const auto see = [&](int row) { return !mask || vis(row); };
-        filler.run(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, see);
-        filler.run(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, see);
-    };
-    const auto ahead = [&](int j) {   // the mask of tile j
-        bytes.load(mask ? mask + j * TILE : nullptr, keys - j * TILE, lane);
-    };
-
-    f32x16 acc[ND];
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
-    float top = -kInf, shift = 0.0f, sum = 0.0f;   // the maximum; what exponents are less by
-    const float growth = kGrowth / a.scale2;
-
-    const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible<Tl::kWords>& vis) {
-        f32x16 s[NB];
+// A column's running maximum and sum, and what exponents are less by.
+struct Running {
+    float top = -kInf, shift = 0.0f, sum = 0.0f;
+    // Scores of NB blocks become weights, 2^(s scale2 - shift), after the results so far are scaled
+    // to a new maximum where one has grown.
+    template <typename T, int NB, int ND>
+    __device__ __forceinline__ void weigh(f32x16 (&s)[NB], f32x16 (&acc)[ND], float scale2, float growth) {
         float big = -kInf;
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const int block = DEEP ? wave : n;
-            s[n] = mul_columns<T, DP>(at, ks, block, qc);
-            const uint32_t see = vis.block(block);
-            if (see != ~0u) {
-                const uint32_t mine = see >> (4 * half);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[n][i] = mine & (1u << (8 * (i / 4) + i % 4)) ? s[n][i] : -kInf;
-            }
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int i = 0; i < 16; ++i) big = fmaxf(big, s[n][i]);
-        }
         big = column_max(big);
         if (__any(big > top + growth)) {
             const float now = fmaxf(top, big);
-            const float to = now == -kInf ? 0.0f : fmaf(now, a.scale2, -kLiftLog2<T>);
+            const float to = now == -kInf ? 0.0f : fmaf(now, scale2, -kLiftLog2<T>);
             const float change = top == -kInf ? 0.0f : __builtin_amdgcn_exp2f(shift - to);
             top = now;
             shift = to;
@@ -112,83 +52,254 @@ void attn_forward_kernel(AttnArgs a) {
             float part[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], a.scale2, -shift));
+                s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], scale2, -shift));
                 part[i % 2] += s[n][i];
             }
             sum += part[0] + part[1];
-            mul_rows<T, DP, DEEP>(at, vs, DEEP ? wave : n, Weights<T, DEEP>(s[n]), acc);
         }
+    }
+};
+
+template <int ND>
+__device__ __forceinline__ void clear(f32x16 (&acc)[ND]) {
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+}
+
+__device__ __forceinline__ float lse_of(float shift, float sum) {
+    return sum == 0.0f ? -kInf : fmaf(shift, kLn2, logf(sum));
+}
+
+// Waves to a SIMD that the registers leave room for.
+template <typename T>
+constexpr int kForwardWaves = sizeof(T) == 4 ? 1 : 2;
+
+template <typename T, int DP>
+__global__ __launch_bounds__(kAttnThreads, kForwardWaves<T>) void attn_forward_kernel(AttnArgs a) {
+    constexpr int TILE = kAttnTile, NB = TILE / 32, ND = DP / 32;
+    using Tl = Tile<T, DP, TILE>;
+    // arrays of their own: the compiler then sees that what is filled is not what is read
+    __shared__ u32x4 k0[Tl::kPieces], v0[Tl::kPieces], k1[Tl::kPieces], v1[Tl::kPieces];
+    const Spot spot = spot_of(a);
+    if (!spot.there) return;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int col = lane % 32, half = lane / 32;
+    const int b = spot.unit / a.Hk, hk = spot.unit % a.Hk;
+    const int keys = keys_of(a, b), tiles = (keys + TILE - 1) / TILE;
+
+    const int r = spot.tile * kAttnWide + wave * 32 + col;
+    const int query = (uint32_t)r / (uint32_t)a.group, head = hk * a.group + (uint32_t)r % (uint32_t)a.group;
+    const bool there = r < a.rows;
+    u32x4 qc[Tl::kSteps];
+    load_column<T, DP>(static_cast<const char*>(a.q) + b * a.q_batch + query * a.q_token + head * a.q_head,
+                       there, a.D, half, qc);
+
+    const char* kp = static_cast<const char*>(a.k) + b * a.k_batch + hk * a.k_head;
+    const char* vp = static_cast<const char*>(a.v) + b * a.v_batch + hk * a.v_head;
+    const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.Nk : nullptr;
+    const Places<T, DP> at(lane);
+    const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
+    uint32_t byte = 1;
+
+    const auto fetch = [&](int j, const Visible& vis, u32x4* ks, u32x4* vs) {
+        const int rows = min(keys - j * TILE, TILE);
+        filler.run(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, vis, mask);
+        filler.run(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, vis, mask);
+    };
+    const auto ahead = [&](int j) {   // the mask of tile j
+        byte = mask_byte(mask ? mask + (int64_t)j * TILE : nullptr, keys - j * TILE, lane);
+    };
+
+    f32x16 acc[ND];
+    clear(acc);
+    Running run;
+    const float growth = kGrowth / a.scale2;
+    const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible& vis) {
+        f32x16 s[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            s[n] = mul_columns<T, DP>(at, ks, n, qc);
+            hide(s[n], vis.block(n), half, -kInf);
+        }
+        run.weigh<T>(s, acc, a.scale2, growth);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+            mul_rows<T, DP, false>(at, vs, n, Weights<T, false>(s[n]), acc);
     };
 
     if (tiles > 0) {
         ahead(0);
-        Visible<Tl::kWords> here = bytes.visible(keys, lane);
+        Visible here = visible(byte, keys, lane);
         if (tiles > 1) ahead(1);
         fetch(0, here, k0, v0);
         tile_barrier();
         int j = 0;
         // tile j from (ks, vs) while tile j + 1 fills (kn, vn)
         const auto turn = [&](u32x4* ks, u32x4* vs, u32x4* kn, u32x4* vn) {
-            Visible<Tl::kWords> next = here;
+            Visible next = here;
             if (j + 1 < tiles) {
-                next = bytes.visible(keys - (j + 1) * TILE, lane);
+                next = visible(byte, keys - (j + 1) * TILE, lane);
+                if (j + 2 < tiles) ahead(j + 2);
+                fetch(j + 1, next, kn, vn);
+            }
+            step((LdsBytes)ks, (LdsBytes)vs, here);
+            tile_barrier();
+            here = next;
+            return ++j < tiles;
+        };
+        while (turn(k0, v0, k1, v1) && turn(k1, v1, k0, v0)) {}
+    }
+
+    const float sum = column_sum(run.sum);
+    if (!there) return;
+    char* out = static_cast<char*>(a.out) + b * a.o_batch + query * a.o_token + head * a.o_head;
+    store_column<T, ND>(reinterpret_cast<T*>(out), a.D, half, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
+    if (a.lse && half == 0) a.lse[((int64_t)b * a.H + head) * a.Nq + query] = lse_of(run.shift, sum);
+}
+
+// ---- few rows ----------------------------------------------------------------------------
+//
+// All waves have the same 32 rows, and every so many blocks of 32 keys are a wave's, in tiles of its
+// own, so that no wave waits for another until their results meet at the end.  Bound by the
+// states' way from memory (one token on long caches), or by latency.
+template <typename T, int DP>
+__global__ __launch_bounds__(64 * attn_few_waves(DP * (int)sizeof(T)))
+void attn_few_kernel(AttnArgs a) {
+    constexpr int WAVES = attn_few_waves(DP * (int)sizeof(T)), ND = DP / 32;
+    constexpr bool LOW = sizeof(T) == 2;
+    using Tl = Tile<T, DP, 32, 64>;
+    constexpr bool TWICE = WAVES * Tl::kPieces * 16 * 4 <= 128 * 1024;   // room for the next tile
+    constexpr int kMore = TWICE ? WAVES * Tl::kPieces : 1;
+    __shared__ u32x4 k0[WAVES * Tl::kPieces], v0[WAVES * Tl::kPieces], k1[kMore], v1[kMore];
+    __shared__ float2 stat[WAVES * 32];
+    const Spot spot = spot_of(a);
+    if (!spot.there) return;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int col = lane % 32, half = lane / 32;
+    const int b = spot.unit / a.Hk, hk = spot.unit % a.Hk;
+    const int first = spot.split * a.split_keys + wave * 32;
+    const int keys = min(keys_of(a, b), (spot.split + 1) * a.split_keys) - first;   // from the wave's first
+    const int tiles = keys > 0 ? (keys + WAVES * 32 - 1) / (WAVES * 32) : 0;
+
+    const int r0 = spot.tile * kAttnFew, r = r0 + col;
+    const bool there = r < a.rows;
+    u32x4 qc[Tl::kSteps];
+    {
+        const int query = (uint32_t)r / (uint32_t)a.group;
+        const int head = hk * a.group + (uint32_t)r % (uint32_t)a.group;
+        load_column<T, DP>(static_cast<const char*>(a.q) + b * a.q_batch + query * a.q_token +
+                               head * a.q_head,
+                           there, a.D, half, qc);
+    }
+    const char* kp = static_cast<const char*>(a.k) + b * a.k_batch + hk * a.k_head + first * a.k_token;
+    const char* vp = static_cast<const char*>(a.v) + b * a.v_batch + hk * a.v_head + first * a.v_token;
+    const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.Nk + first : nullptr;
+    const Places<T, DP> at(lane);
+    const Filler<Tl> filler(lane, a.D * (int)sizeof(T));
+    uint32_t byte = 1;
+
+    const auto left = [&](int j) { return min(keys - j * WAVES * 32, 32); };
+    const auto fetch = [&](int j, const Visible& vis, u32x4* ks, u32x4* vs) {
+        const int64_t row = (int64_t)j * WAVES * 32;
+        filler.run(kp + row * a.k_token, left(j), (uint32_t)a.k_token, ks, 0, vis, mask);
+        filler.run(vp + row * a.v_token, left(j), (uint32_t)a.v_token, vs, 0, vis, mask);
+    };
+    const auto ahead = [&](int j) {
+        byte = mask_byte(mask ? mask + (int64_t)j * WAVES * 32 : nullptr, left(j), lane);
+    };
+
+    f32x16 acc[ND];
+    clear(acc);
+    Running run;
+    const float growth = kGrowth / a.scale2;
+    const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible& vis) {
+        f32x16 s[1] = {mul_columns<T, DP>(at, ks, 0, qc)};
+        hide(s[0], vis.block(0), half, -kInf);
+        run.weigh<T>(s, acc, a.scale2, growth);
+        mul_rows<T, DP, LOW>(at, vs, 0, Weights<T, LOW>(s[0]), acc);
+    };
+
+    if (tiles > 0) {
+        u32x4 *ka = k0 + wave * Tl::kPieces, *va = v0 + wave * Tl::kPieces;
+        u32x4 *kb = TWICE ? k1 + wave * Tl::kPieces : ka, *vb = TWICE ? v1 + wave * Tl::kPieces : va;
+        ahead(0);
+        Visible here = visible(byte, left(0), lane);
+        if (tiles > 1) ahead(1);
+        fetch(0, here, ka, va);
+        own_fills();
+        int j = 0;
+        const auto turn = [&](u32x4* ks, u32x4* vs, u32x4* kn, u32x4* vn) {
+            Visible next = here;
+            if (j + 1 < tiles) {
+                next = visible(byte, left(j + 1), lane);
                 if (j + 2 < tiles) ahead(j + 2);
                 if constexpr (TWICE) fetch(j + 1, next, kn, vn);
             }
             step((LdsBytes)ks, (LdsBytes)vs, here);
-            tile_barrier();
             if constexpr (!TWICE) {
+                own_fills();   // and its reads: the tile is filled again
                 if (j + 1 < tiles) fetch(j + 1, next, kn, vn);
-                tile_barrier();
             }
+            own_fills();
             here = next;
             return ++j < tiles;
         };
-        if constexpr (TWICE) {
-            while (turn(k0, v0, k1, v1) && turn(k1, v1, k0, v0)) {}
-        } else {
-            while (turn(k0, v0, k0, v0)) {}
-        }
+        while (turn(ka, va, kb, vb) && turn(kb, vb, ka, va)) {}
     }
 
-    sum = column_sum(sum);
-    if constexpr (DEEP) {
-        // the waves' parts meet at their largest exponent
-        float2* stat = reinterpret_cast<float2*>(k0);
-        __syncthreads();
-        if (half == 0) stat[wave * 32 + col] = make_float2(top == -kInf ? -kInf : shift, sum);
-        __syncthreads();
-        float most = -kInf, total = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) most = fmaxf(most, stat[w * 32 + col].x);
-        most = most == -kInf ? 0.0f : most;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float2 s = stat[w * 32 + col];
-            total += s.y == 0.0f ? 0.0f : s.y * __builtin_amdgcn_exp2f(s.x - most);
-        }
-        const float factor = top == -kInf ? 0.0f : __builtin_amdgcn_exp2f(shift - most);
+    // The waves' parts meet at their largest exponent.  A wave's place has DP numbers to a column, in
+    // fours, turned by the column so that 32 columns' equal fours spread over the banks.
+    const float part = column_sum(run.sum);
+    __syncthreads();
+    if (half == 0) stat[wave * 32 + col] = make_float2(run.top == -kInf ? -kInf : run.shift, part);
+    constexpr int kFours = DP / 4, kPlace = 32 * kFours;   // of 16 bytes
+    constexpr int kHere = WAVES * Tl::kPieces / kPlace;    // waves that k0 has room for
+    static_assert(2 * kHere >= WAVES, "k0 and v0 hold every wave's part");
+    const auto place = [&](int w) {
+        return reinterpret_cast<f32x4*>(w < kHere ? k0 : v0) + (w < kHere ? w : w - kHere) * kPlace;
+    };
+    if (there) {
+        f32x4* to = place(wave) + col * kFours;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[d][i] *= factor;
-        sum = total;
-        shift = most;
-        add_waves<ND>(acc, reinterpret_cast<float*>(k0), wave, lane);
-        if (wave != 0) return;
+            for (int j = 0; j < 4; ++j)
+                to[(d * 8 + j * 2 + half) ^ (col & 7)] =
+                    f32x4{acc[d][4 * j], acc[d][4 * j + 1], acc[d][4 * j + 2], acc[d][4 * j + 3]};
     }
-    if (!there) return;
-    if (a.splits > 1) {
-        const int64_t at_row = ((int64_t)spot.split * a.B * a.Hk + spot.unit) * a.rows + r;
-        if (half == 0) a.part_stat[at_row] = make_float2(shift, sum);
-        store_column<float, ND>(a.part + at_row * a.D, a.D, half, acc, 1.0f);
-        return;
+    __syncthreads();
+    const int rows = min(a.rows - r0, kAttnFew), vectors = a.D / 4;
+    for (int n = threadIdx.x; n < rows * vectors; n += 64 * WAVES) {
+        const int c = n / vectors, v = n % vectors;
+        float most = -kInf, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) most = fmaxf(most, stat[w * 32 + c].x);
+        most = most == -kInf ? 0.0f : most;
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float2 s = stat[w * 32 + c];
+            const float f = s.x == -kInf ? 0.0f : __builtin_amdgcn_exp2f(s.x - most);
+            sum = fmaf(s.y, f, sum);
+            x += place(w)[c * kFours + (v ^ (c & 7))] * f;
+        }
+        const int row = r0 + c;
+        if (a.splits > 1) {
+            const int64_t line = ((int64_t)spot.split * a.B * a.Hk + spot.unit) * a.rows + row;
+            if (v == 0) a.part_stat[line] = make_float2(most, sum);
+            *reinterpret_cast<f32x4*>(a.part + line * a.D + v * 4) = x;
+            continue;
+        }
+        const int query = (uint32_t)row / (uint32_t)a.group;
+        const int head = hk * a.group + (uint32_t)row % (uint32_t)a.group;
+        const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float result[4] = {x[0] * inverse, x[1] * inverse, x[2] * inverse, x[3] * inverse};
+        char* out = static_cast<char*>(a.out) + b * a.o_batch + query * a.o_token + head * a.o_head;
+        store_as(reinterpret_cast<T*>(out) + v * 4, result);
+        if (a.lse && v == 0) a.lse[((int64_t)b * a.H + head) * a.Nq + query] = lse_of(most, sum);
     }
-    char* out = static_cast<char*>(a.out) + b * a.o_batch + query * a.o_token + head * a.o_head;
-    store_column<T, ND>(reinterpret_cast<T*>(out), a.D, half, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
-    if (a.lse && half == 0)
-        a.lse[((int64_t)b * a.H + head) * a.Nq + query] =
-            sum == 0.0f ? -kInf : fmaf(shift, kLn2, logf(sum));
 }
 
 // ---- splits of keys joined ---------------------------------------------------------------
@@ -238,17 +349,17 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
     char* out = static_cast<char*>(a.out) + b * a.o_batch + query * a.o_token + head * a.o_head;
     store_as(reinterpret_cast<T*>(out) + at, result);
     if (a.lse && at == 0)
-        a.lse[((int64_t)b * a.H + head) * a.Nq + query] =
-            sum == 0.0f ? -kInf : fmaf(most, kLn2, logf(sum));
+        a.lse[((int64_t)b * a.H + head) * a.Nq + query] = lse_of(most, sum);
 }
 
 template <typename T, int DP>
 void launch(const AttnArgs& a, hipStream_t stream) {
     const uint32_t blocks = (uint32_t)(a.blocks + 7) / 8 * 8;
-    if (a.deep)
-        attn_forward_kernel<T, DP, true><<<blocks, kAttnThreads, 0, stream>>>(a);
+    if (a.few)
+        attn_few_kernel<T, DP>
+            <<<blocks, 64 * attn_few_waves(DP * (int)sizeof(T)), 0, stream>>>(a);
     else
-        attn_forward_kernel<T, DP, false><<<blocks, kAttnThreads, 0, stream>>>(a);
+        attn_forward_kernel<T, DP><<<blocks, kAttnThreads, 0, stream>>>(a);
 }
 
 template <typename T>

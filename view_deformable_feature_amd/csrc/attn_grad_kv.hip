@@ -25,7 +25,7 @@ constexpr int kGradKvWaves = sizeof(T) == 4 || DP > 64 ? 1 : 2;
 template <typename T, int DP>
 __global__ __launch_bounds__(kAttnThreads, (kGradKvWaves<T, DP>))
 void attn_grad_kv_kernel(AttnArgs a) {
-    constexpr int TILE = kAttnWideTile, NB = TILE / 32, ND = DP / 32;
+    constexpr int TILE = kAttnTile, NB = TILE / 32, ND = DP / 32;
     using Tl = Tile<T, DP, TILE>;
     __shared__ u32x4 q0[Tl::kPieces], g0[Tl::kPieces], q1[Tl::kPieces], g1[Tl::kPieces];
     __shared__ __align__(16) float stat0[2 * TILE], stat1[2 * TILE];   // lse2, delta of a tile
@@ -55,15 +55,14 @@ void attn_grad_kv_kernel(AttnArgs a) {
     const int64_t stats = ((int64_t)b * a.H + hk * a.group) * a.Nq;
     const Places<T, DP> at(lane);
     const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
-    const auto all = [](int) { return true; };
 
     // of the tile that is fetched next
     int head = a.Nq ? from / per_head : 0, row = a.Nq ? from % per_head * TILE : 0;
     float mine = 0.0f;       // a thread's part of its statistics
     const auto fetch = [&](u32x4* qs, u32x4* gs) {
         const int rows = min(a.Nq - row, TILE);
-        filler.run(qp + head * a.q_head + row * a.q_token, rows, (uint32_t)a.q_token, qs, wave, all);
-        filler.run(gp + head * a.g_head + row * a.g_token, rows, (uint32_t)a.g_token, gs, wave, all);
+        filler.run(qp + head * a.q_head + row * a.q_token, rows, (uint32_t)a.q_token, qs, wave);
+        filler.run(gp + head * a.g_head + row * a.g_token, rows, (uint32_t)a.g_token, gs, wave);
         const int t = threadIdx.x % TILE;
         // past the last row p is 0
         mine = threadIdx.x < TILE ? kInf : 0.0f;

@@ -19,7 +19,7 @@ constexpr int kGradQWaves = sizeof(T) == 4 ? 1 : 2;
 template <typename T, int DP>
 __global__ __launch_bounds__(kAttnThreads, (kGradQWaves<T, DP>))
 void attn_grad_q_kernel(AttnArgs a) {
-    constexpr int TILE = kAttnWideTile, NB = TILE / 32, ND = DP / 32;
+    constexpr int TILE = kAttnTile, NB = TILE / 32, ND = DP / 32;
     using Tl = Tile<T, DP, TILE>;
     __shared__ u32x4 k0[Tl::kPieces], v0[Tl::kPieces], k1[Tl::kPieces], v1[Tl::kPieces];
     const Spot spot = spot_of(a);
@@ -66,16 +66,15 @@ void attn_grad_q_kernel(AttnArgs a) {
     const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.Nk + first : nullptr;
     const Places<T, DP> at(lane);
     const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
-    MaskBytes<Tl::kWords> bytes;
+    uint32_t byte = 1;
 
-    const auto fetch = [&](int j, const Visible<Tl::kWords>& vis, u32x4* ks, u32x4* vs) {
+    const auto fetch = [&](int j, const Visible& vis, u32x4* ks, u32x4* vs) {
         const int rows = min(keys - j * TILE, TILE);
-        const auto see = [&](int row) { return !mask || vis(row); };
-        filler.run(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, see);
-        filler.run(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, see);
+        filler.run(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, vis, mask);
+        filler.run(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, vis, mask);
     };
     const auto ahead = [&](int j) {
-        bytes.load(mask ? mask + (int64_t)j * TILE : nullptr, keys - j * TILE, lane);
+        byte = mask_byte(mask ? mask + (int64_t)j * TILE : nullptr, keys - j * TILE, lane);
     };
 
     f32x16 acc[ND];
@@ -85,7 +84,7 @@ void attn_grad_q_kernel(AttnArgs a) {
         for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
     Lift<T, ND> lift;
 
-    const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible<Tl::kWords>& vis) {
+    const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible& vis) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             f32x16 s = mul_columns<T, DP>(at, ks, n, qc);
@@ -93,13 +92,7 @@ void attn_grad_q_kernel(AttnArgs a) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], a.scale2, -lse2)) * (dp[i] - delta);
-            const uint32_t see = vis.block(n);
-            if (see != ~0u) {
-                const uint32_t mine = see >> (4 * half);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[i] = mine & (1u << (8 * (i / 4) + i % 4)) ? s[i] : 0.0f;
-            }
+            hide(s, vis.block(n), half, 0.0f);
             lift.apply(s, acc);
             mul_rows<T, DP, false>(at, ks, n, Weights<T, false>(s), acc);
         }
@@ -107,15 +100,15 @@ void attn_grad_q_kernel(AttnArgs a) {
 
     if (tiles > 0) {
         ahead(0);
-        Visible<Tl::kWords> here = bytes.visible(keys, lane);
+        Visible here = visible(byte, keys, lane);
         if (tiles > 1) ahead(1);
         fetch(0, here, k0, v0);
         tile_barrier();
         int j = 0;
         const auto turn = [&](u32x4* ks, u32x4* vs, u32x4* kn, u32x4* vn) {
-            Visible<Tl::kWords> next = here;
+            Visible next = here;
             if (j + 1 < tiles) {
-                next = bytes.visible(keys - (j + 1) * TILE, lane);
+                next = visible(byte, keys - (j + 1) * TILE, lane);
                 if (j + 2 < tiles) ahead(j + 2);
                 fetch(j + 1, next, kn, vn);
             }

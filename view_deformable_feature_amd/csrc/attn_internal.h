@@ -16,9 +16,10 @@ namespace da {
 
 constexpr int kAttnThreads = 256;   // four waves
 // A workgroup has 32 columns (rows of the forward and of grad_q, keys of grad_k and grad_v) to each
-// wave; in the forward's deep form it has 32 in all, its waves taking the tile's parts.
-constexpr int kAttnWide = 128, kAttnDeep = 32;
-constexpr int kAttnWideTile = 64, kAttnDeepTile = 128;   // rows or keys streamed at a time
+// wave.  Where that leaves the forward too few workgroups, one has 32 rows in all and its waves
+// share the keys, 32 at a time to each.
+constexpr int kAttnWide = 128, kAttnFew = 32;
+constexpr int kAttnTile = 64;      // rows or keys streamed at a time, kAttnFew to each wave of the other
 constexpr int kAttnMostSplits = 256;   // of a forward's keys: a thread of the join to each
 
 struct AttnArgs {
@@ -50,8 +51,16 @@ struct AttnArgs {
     int32_t blocks;           // workgroups with work; a launch has a multiple of 8
     float scale, scale2;      // scale2: scale / log 2
     int32_t dtype;
-    bool deep;
+    bool few;
 };
+
+// Waves of a workgroup with few rows.  They have tiles of their own, two of 32 keys and values each
+// where 128 KB hold them; eight where that leaves room for them, else four.
+constexpr int attn_few_waves(int head_bytes) { return head_bytes <= 128 ? 8 : 4; }
+inline int attn_few_waves(const AttnArgs& a) {
+    const int wide = a.D <= 32 ? 32 : a.D <= 64 ? 64 : 128;
+    return attn_few_waves(wide * (a.dtype == DA_F32 ? 4 : 2));
+}
 
 hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream);

@@ -137,7 +137,7 @@ void choose_grad_q(da::AttnArgs& a) {
 }
 void choose_grad_kv(da::AttnArgs& a) {
     const int64_t tiles = ((int64_t)a.Nq + da::kAttnTile - 1) / da::kAttnTile * a.group;
-    choose_backward(a, a.Nk, tiles, a.dtype == DA_F32 || a.D > 64 ? 1 : 2);
+    choose_backward(a, a.Nk, tiles, a.dtype == DA_F32 ? 1 : 2);
 }
 
 // Counts the workgroups; a launch has fewer than 2^32 threads.

@@ -221,28 +221,16 @@ struct Visible {
 };
 // Fills a tile in LDS straight from memory: a filling instruction puts lane l's 16 bytes at
 // place l of a run of 1 KB, so the turned order is in the addresses that the lanes fetch
-// from.  Rows past `rows`, numbers past D and rows that `see` leaves out become zeros.
+// from.  Rows past `rows`, numbers past D and, with a mask, rows that are not visible become zeros.
 template <class Tl>
 struct Filler {
     int row, piece;        // of the first fetch, the piece as it is turned there
     uint32_t pieces;       // of a row, D numbers
     __device__ __forceinline__ Filler(int thread, int row_bytes)
         : row(thread / Tl::kRow), piece(thread % Tl::kRow), pieces(row_bytes / 16) {}
-    // rows without a mask
+    template <bool MASK>
     __device__ __forceinline__ void run(const char* base, int rows, uint32_t stride, u32x4* tile,
-                                        int wave) const {
-        fill(base, rows, stride, tile, wave, [](int) { return true; });
-    }
-    __device__ __forceinline__ void run(const char* base, int rows, uint32_t stride, u32x4* tile,
-                                        int wave, const Visible& vis, bool masked) const {
-        if (masked)
-            fill(base, rows, stride, tile, wave, vis);
-        else
-            run(base, rows, stride, tile, wave);
-    }
-    template <typename See>
-    __device__ __forceinline__ void fill(const char* base, int rows, uint32_t stride, u32x4* tile,
-                                         int wave, See&& see) const {
+                                        int wave, const Visible& vis) const {
         // whole numbers in scalar registers, or every fetch becomes a loop over a lane's values
         rows = __builtin_amdgcn_readfirstlane(rows);
         const uint64_t place = reinterpret_cast<uint64_t>(base);
@@ -256,7 +244,8 @@ struct Filler {
         for (int i = 0; i < Tl::kFetches; ++i) {
             const int at = row + i * Tl::kRowsFetch;
             const uint32_t p = piece ^ Tl::turn(at);
-            const uint32_t off = p < pieces && see(at) ? at * stride + p * 16 : 0x80000000u;
+            const bool there = p < pieces && (!MASK || vis(at));
+            const uint32_t off = there ? at * stride + p * 16 : 0x80000000u;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 r, (__attribute__((address_space(3))) void*)(tile + i * Tl::kThreads + wave * 64), 16,
                 off, 0, 0, 0);
@@ -277,8 +266,8 @@ __device__ __forceinline__ void own_fills() {
 }
 
 __device__ __forceinline__ uint32_t mask_byte(const uint8_t* mask, int keys, int lane) {
-    uint32_t byte = 1;
-    if (mask && lane < keys) byte = mask[lane];
+    uint32_t byte = 0;
+    if (lane < keys) byte = mask[lane];
     return byte;
 }
 __device__ __forceinline__ Visible visible(uint32_t byte, int keys, int lane) {

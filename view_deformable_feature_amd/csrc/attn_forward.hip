@@ -76,7 +76,7 @@ __device__ __forceinline__ float lse_of(float shift, float sum) {
 template <typename T>
 constexpr int kForwardWaves = sizeof(T) == 4 ? 1 : 2;
 
-template <typename T, int DP>
+template <typename T, int DP, bool MASK>
 __global__ __launch_bounds__(kAttnThreads, kForwardWaves<T>) void attn_forward_kernel(AttnArgs a) {
     constexpr int TILE = kAttnTile, NB = TILE / 32, ND = DP / 32;
     using Tl = Tile<T, DP, TILE>;
@@ -98,18 +98,19 @@ __global__ __launch_bounds__(kAttnThreads, kForwardWaves<T>) void attn_forward_k
 
     const char* kp = static_cast<const char*>(a.k) + b * a.k_batch + hk * a.k_head;
     const char* vp = static_cast<const char*>(a.v) + b * a.v_batch + hk * a.v_head;
-    const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.Nk : nullptr;
+    const uint8_t* mask = MASK ? a.mask + (int64_t)b * a.Nk : nullptr;
     const Places<T, DP> at(lane);
     const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
-    uint32_t byte = 1;
+    uint32_t byte = 1;   // of the tile that is fetched next
 
-    const auto fetch = [&](int j, const Visible& vis, u32x4* ks, u32x4* vs) {
+    // Fetches tile j, or zeros past the last, and reads the mask of the one after it.
+    const auto fetch = [&](int j, u32x4* ks, u32x4* vs) {
         const int rows = min(keys - j * TILE, TILE);
-        filler.run(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, vis, mask);
-        filler.run(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, vis, mask);
-    };
-    const auto ahead = [&](int j) {   // the mask of tile j
-        byte = mask_byte(mask ? mask + (int64_t)j * TILE : nullptr, keys - j * TILE, lane);
+        const Visible vis = visible(byte, rows, lane);
+        filler.template run<MASK>(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, vis);
+        filler.template run<MASK>(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, vis);
+        if constexpr (MASK) byte = mask_byte(mask + (int64_t)(j + 1) * TILE, keys - (j + 1) * TILE, lane);
+        return vis;
     };
 
     f32x16 acc[ND];
@@ -129,27 +130,21 @@ __global__ __launch_bounds__(kAttnThreads, kForwardWaves<T>) void attn_forward_k
             mul_rows<T, DP, false>(at, vs, n, Weights<T, false>(s[n]), acc);
     };
 
+    // A tile is worked on while the next one fills the other half of LDS.  The loop has no branches of
+    // its own, so that the results stay in their registers.
     if (tiles > 0) {
-        ahead(0);
-        Visible here = visible(byte, keys, lane);
-        if (tiles > 1) ahead(1);
-        fetch(0, here, k0, v0);
+        if constexpr (MASK) byte = mask_byte(mask, keys, lane);
+        Visible here = fetch(0, k0, v0);
         tile_barrier();
-        int j = 0;
-        // tile j from (ks, vs) while tile j + 1 fills (kn, vn)
-        const auto turn = [&](u32x4* ks, u32x4* vs, u32x4* kn, u32x4* vn) {
-            Visible next = here;
-            if (j + 1 < tiles) {
-                next = visible(byte, keys - (j + 1) * TILE, lane);
-                if (j + 2 < tiles) ahead(j + 2);
-                fetch(j + 1, next, kn, vn);
-            }
-            step((LdsBytes)ks, (LdsBytes)vs, here);
+        for (int j = 0; j + 1 < tiles; j += 2) {
+            Visible next = fetch(j + 1, k1, v1);
+            step((LdsBytes)k0, (LdsBytes)v0, here);
             tile_barrier();
-            here = next;
-            return ++j < tiles;
-        };
-        while (turn(k0, v0, k1, v1) && turn(k1, v1, k0, v0)) {}
+            here = fetch(j + 2, k0, v0);
+            step((LdsBytes)k1, (LdsBytes)v1, next);
+            tile_barrier();
+        }
+        if (tiles % 2) step((LdsBytes)k0, (LdsBytes)v0, here);
     }
 
     const float sum = column_sum(run.sum);
@@ -203,11 +198,16 @@ void attn_few_kernel(AttnArgs a) {
     const auto left = [&](int j) { return min(keys - j * WAVES * 32, 32); };
     const auto fetch = [&](int j, const Visible& vis, u32x4* ks, u32x4* vs) {
         const int64_t row = (int64_t)j * WAVES * 32;
-        filler.run(kp + row * a.k_token, left(j), (uint32_t)a.k_token, ks, 0, vis, mask);
-        filler.run(vp + row * a.v_token, left(j), (uint32_t)a.v_token, vs, 0, vis, mask);
+        if (mask) {
+            filler.template run<true>(kp + row * a.k_token, left(j), (uint32_t)a.k_token, ks, 0, vis);
+            filler.template run<true>(vp + row * a.v_token, left(j), (uint32_t)a.v_token, vs, 0, vis);
+        } else {
+            filler.template run<false>(kp + row * a.k_token, left(j), (uint32_t)a.k_token, ks, 0, vis);
+            filler.template run<false>(vp + row * a.v_token, left(j), (uint32_t)a.v_token, vs, 0, vis);
+        }
     };
     const auto ahead = [&](int j) {
-        byte = mask_byte(mask ? mask + (int64_t)j * WAVES * 32 : nullptr, left(j), lane);
+        if (mask) byte = mask_byte(mask + (int64_t)j * WAVES * 32, left(j), lane);
     };
 
     f32x16 acc[ND];
@@ -358,8 +358,10 @@ void launch(const AttnArgs& a, hipStream_t stream) {
     if (a.few)
         attn_few_kernel<T, DP>
             <<<blocks, 64 * attn_few_waves(DP * (int)sizeof(T)), 0, stream>>>(a);
+    else if (a.mask)
+        attn_forward_kernel<T, DP, true><<<blocks, kAttnThreads, 0, stream>>>(a);
     else
-        attn_forward_kernel<T, DP><<<blocks, kAttnThreads, 0, stream>>>(a);
+        attn_forward_kernel<T, DP, false><<<blocks, kAttnThreads, 0, stream>>>(a);
 }
 
 template <typename T>

@@ -20,10 +20,10 @@ template <typename T>
 constexpr float kLiftLog2 = std::is_same<T, _Float16>::value ? 15.0f : 0.0f;
 
 template <typename T, int DP>
-constexpr int kGradKvWaves = sizeof(T) == 4 || DP > 64 ? 1 : 2;
+constexpr int kGradKvWaves = sizeof(T) == 4 ? 1 : 2;
 
 template <typename T, int DP>
-__global__ __launch_bounds__(kAttnThreads, (kGradKvWaves<T, DP>))
+__global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(kGradKvWaves<T, DP>, kGradKvWaves<T, DP>)))
 void attn_grad_kv_kernel(AttnArgs a) {
     constexpr int TILE = kAttnTile, NB = TILE / 32, ND = DP / 32;
     using Tl = Tile<T, DP, TILE>;
@@ -59,10 +59,12 @@ void attn_grad_kv_kernel(AttnArgs a) {
     // of the tile that is fetched next
     int head = a.Nq ? from / per_head : 0, row = a.Nq ? from % per_head * TILE : 0;
     float mine = 0.0f;       // a thread's part of its statistics
+    const Visible none = {0};
+    // Fetches the next tile, or zeros past the last.
     const auto fetch = [&](u32x4* qs, u32x4* gs) {
-        const int rows = min(a.Nq - row, TILE);
-        filler.run(qp + head * a.q_head + row * a.q_token, rows, (uint32_t)a.q_token, qs, wave);
-        filler.run(gp + head * a.g_head + row * a.g_token, rows, (uint32_t)a.g_token, gs, wave);
+        const int rows = head < a.group ? min(a.Nq - row, TILE) : 0;
+        filler.template run<false>(qp + head * a.q_head + row * a.q_token, rows, (uint32_t)a.q_token, qs, wave, none);
+        filler.template run<false>(gp + head * a.g_head + row * a.g_token, rows, (uint32_t)a.g_token, gs, wave, none);
         const int t = threadIdx.x % TILE;
         // past the last row p is 0
         mine = threadIdx.x < TILE ? kInf : 0.0f;
@@ -111,19 +113,23 @@ void attn_grad_kv_kernel(AttnArgs a) {
         }
     };
 
+    // A tile is worked on while the next one fills the other half of LDS.  The loop has no branches of
+    // its own, so that the results stay in their registers.
     if (tiles > 0) {
         fetch(q0, g0);
         keep(stat0);
         tile_barrier();
-        int j = 0;
-        const auto turn = [&](u32x4* qs, u32x4* gs, float* st, u32x4* qn, u32x4* gn, float* sn) {
-            if (j + 1 < tiles) fetch(qn, gn);
-            step((LdsBytes)qs, (LdsBytes)gs, st);
-            if (j + 1 < tiles) keep(sn);
+        for (int j = 0; j + 1 < tiles; j += 2) {
+            fetch(q1, g1);
+            step((LdsBytes)q0, (LdsBytes)g0, stat0);
+            keep(stat1);
             tile_barrier();
-            return ++j < tiles;
-        };
-        while (turn(q0, g0, stat0, q1, g1, stat1) && turn(q1, g1, stat1, q0, g0, stat0)) {}
+            fetch(q0, g0);
+            step((LdsBytes)q1, (LdsBytes)g1, stat1);
+            keep(stat0);
+            tile_barrier();
+        }
+        if (tiles % 2) step((LdsBytes)q0, (LdsBytes)g0, stat0);
     }
     const float back = std::is_same<T, _Float16>::value ? 1.0f / 32768.0f : 1.0f;
     const float fk = a.scale * lift.down() * back, fv = back;

@@ -16,7 +16,7 @@ namespace {
 template <typename T, int DP>
 constexpr int kGradQWaves = sizeof(T) == 4 ? 1 : 2;
 
-template <typename T, int DP>
+template <typename T, int DP, bool MASK>
 __global__ __launch_bounds__(kAttnThreads, (kGradQWaves<T, DP>))
 void attn_grad_q_kernel(AttnArgs a) {
     constexpr int TILE = kAttnTile, NB = TILE / 32, ND = DP / 32;
@@ -63,18 +63,19 @@ void attn_grad_q_kernel(AttnArgs a) {
 
     const char* kp = static_cast<const char*>(a.k) + b * a.k_batch + hk * a.k_head + first * a.k_token;
     const char* vp = static_cast<const char*>(a.v) + b * a.v_batch + hk * a.v_head + first * a.v_token;
-    const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.Nk + first : nullptr;
+    const uint8_t* mask = MASK ? a.mask + (int64_t)b * a.Nk + first : nullptr;
     const Places<T, DP> at(lane);
     const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
-    uint32_t byte = 1;
+    uint32_t byte = 1;   // of the tile that is fetched next
 
-    const auto fetch = [&](int j, const Visible& vis, u32x4* ks, u32x4* vs) {
+    // Fetches tile j, or zeros past the last, and reads the mask of the one after it.
+    const auto fetch = [&](int j, u32x4* ks, u32x4* vs) {
         const int rows = min(keys - j * TILE, TILE);
-        filler.run(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, vis, mask);
-        filler.run(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, vis, mask);
-    };
-    const auto ahead = [&](int j) {
-        byte = mask_byte(mask ? mask + (int64_t)j * TILE : nullptr, keys - j * TILE, lane);
+        const Visible vis = visible(byte, rows, lane);
+        filler.template run<MASK>(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, vis);
+        filler.template run<MASK>(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, vis);
+        if constexpr (MASK) byte = mask_byte(mask + (int64_t)(j + 1) * TILE, keys - (j + 1) * TILE, lane);
+        return vis;
     };
 
     f32x16 acc[ND];
@@ -98,27 +99,23 @@ void attn_grad_q_kernel(AttnArgs a) {
         }
     };
 
+    // A tile is worked on while the next one fills the other half of LDS.  The loop has no branches of
+    // its own, so that the results stay in their registers.
     if (tiles > 0) {
-        ahead(0);
-        Visible here = visible(byte, keys, lane);
-        if (tiles > 1) ahead(1);
-        fetch(0, here, k0, v0);
+        if constexpr (MASK) byte = mask_byte(mask, keys, lane);
+        Visible here = fetch(0, k0, v0);
         tile_barrier();
-        int j = 0;
-        const auto turn = [&](u32x4* ks, u32x4* vs, u32x4* kn, u32x4* vn) {
-            Visible next = here;
-            if (j + 1 < tiles) {
-                next = visible(byte, keys - (j + 1) * TILE, lane);
-                if (j + 2 < tiles) ahead(j + 2);
-                fetch(j + 1, next, kn, vn);
-            }
-            step((LdsBytes)ks, (LdsBytes)vs, here);
+        for (int j = 0; j + 1 < tiles; j += 2) {
+            Visible next = fetch(j + 1, k1, v1);
+            step((LdsBytes)k0, (LdsBytes)v0, here);
             tile_barrier();
-            here = next;
-            return ++j < tiles;
-        };
-        while (turn(k0, v0, k1, v1) && turn(k1, v1, k0, v0)) {}
+            here = fetch(j + 2, k0, v0);
+            step((LdsBytes)k1, (LdsBytes)v1, next);
+            tile_barrier();
+        }
+        if (tiles % 2) step((LdsBytes)k0, (LdsBytes)v0, here);
     }
+
     if (!there) return;
     const float factor = a.scale * lift.down();
     if (a.splits > 1)
@@ -195,7 +192,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_grad_join_kernel(JoinArgs a
 template <typename T, int DP>
 void launch(const AttnArgs& a, hipStream_t stream) {
     const uint32_t blocks = (uint32_t)(a.blocks + 7) / 8 * 8;
-    attn_grad_q_kernel<T, DP><<<blocks, kAttnThreads, 0, stream>>>(a);
+    if (a.mask)
+        attn_grad_q_kernel<T, DP, true><<<blocks, kAttnThreads, 0, stream>>>(a);
+    else
+        attn_grad_q_kernel<T, DP, false><<<blocks, kAttnThreads, 0, stream>>>(a);
 }
 
 template <typename T>

@@ -20,8 +20,7 @@ PROBE_SOURCE = os.path.join(PKG_DIR, "csrc", "bw_probe.hip")
 SOURCES = [os.path.join(CSRC, f)
            for f in ("da_forward.hip", "da_backward.hip", "da_pack.hip", "da_api.cpp", "dcn.hip",
                      "dcn_api.cpp", "da_noalloc.hip", "gn.hip", "gn_api.cpp", "i8.hip",
-                     "i8_api.cpp", "attn_forward.hip", "attn_grad_q.hip", "attn_grad_kv.hip",
-                     "attn_api.cpp", "rope.hip", "rope_api.cpp")]
+                     "i8_api.cpp", "attn_forward.hip", "attn_grad.hip", "attn_api.cpp", "rope.hip", "rope_api.cpp")]
 HEADERS = [os.path.join(INCLUDE, f) for f in ("deformagg.h", "dcn.h", "group_norm.h", "int8.h",
                                                 "attention.h", "rotary.h")] + [
     os.path.join(CSRC, f) for f in ("da_internal.h", "da_device.h", "da_pack.h", "dcn_internal.h",

@@ -318,6 +318,8 @@ da_status attn_backward(const attn_problem* p, const void* q, const void* k, con
     st = count_blocks(of_q);
     if (st == DA_OK) st = count_blocks(of_kv);
     if (st != DA_OK) return st;
+    if ((wide)of_q.blocks + of_kv.blocks + 16 >= (wide(1) << 32) / da::kAttnThreads)
+        return report_error(DA_ERR_UNSUPPORTED, "2^32 threads of workgroups or more");
     const wide numbers = (wide)of_q.B * of_q.Nq * of_q.H * of_q.D + 2 * (wide)of_q.B * of_q.Nk * of_q.Hk * of_q.D;
     if ((wide)of_q.B * of_q.Nq * of_q.H * 8 >= wide(1) << 32 ||
         ((of_q.splits > 1 || of_kv.splits > 1) && numbers / 8 >= wide(1) << 32))
@@ -330,13 +332,11 @@ da_status attn_backward(const attn_problem* p, const void* q, const void* k, con
     of_kv.part_v = of_kv.part_k + part_k_bytes(of_kv) / sizeof(float);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = hipSuccess;
-    if (p->queries > 0 && grad_q)
-        e = da::launch_attn_grad_q(of_q, s);
-    else if (p->queries > 0 && grad_k && p->keys > 0)
-        e = da::launch_attn_delta(of_q, s);
-    if (e == hipSuccess && grad_k && p->keys > 0) e = da::launch_attn_grad_kv(of_kv, s);
-    if (p->queries == 0) of_q.splits = 1;
-    if (p->keys == 0) of_kv.splits = 1;
+    if (p->queries == 0 || !grad_q) of_q.blocks = 0;
+    if (p->keys == 0 || !grad_k) of_kv.blocks = 0;
+    if (of_q.blocks == 0 && of_kv.blocks == 0) return DA_OK;
+    if (p->queries > 0) e = da::launch_attn_delta(of_q, s);
+    if (e == hipSuccess) e = da::launch_attn_grad(of_q, of_kv, s);
     if (e == hipSuccess) e = da::launch_attn_grad_join(of_q, of_kv, s);
     return da::report_hip(e, "attention backward launch");
 }

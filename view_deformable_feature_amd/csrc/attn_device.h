@@ -274,11 +274,15 @@ __device__ __forceinline__ Visible visible(uint32_t byte, int keys, int lane) {
     return {__ballot(byte && lane < keys)};
 }
 // Scores (or dS) of a block of keys, `other` where the key is not visible
-__device__ __forceinline__ void hide(f32x16& s, uint32_t see, int half, float other) {
+__device__ __forceinline__ void hide(f32x16& s, uint32_t see, float other) {
     if (see == ~0u) return;
-    const uint32_t mine = see >> (4 * half);
+    // a row's bit, for the lanes of either half, as a mask of lanes in scalar registers
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = mine & (1u << (8 * (i / 4) + i % 4)) ? s[i] : other;
+    for (int i = 0; i < 16; ++i) {
+        const int at = 8 * (i / 4) + i % 4;
+        const uint32_t low = see & (1u << at) ? ~0u : 0u, high = see & (1u << (at + 4)) ? ~0u : 0u;
+        s[i] = __builtin_amdgcn_inverse_ballot_w64((uint64_t)high << 32 | low) ? s[i] : other;
+    }
 }
 
 // The workgroup's place: (batch entry, key head), tile of columns, split of keys.  Workgroups go
@@ -289,15 +293,15 @@ struct Spot {
     int unit, tile, split;
     bool there;
 };
-__device__ __forceinline__ Spot spot_of(const AttnArgs& a) {
-    const uint32_t n = blockIdx.x, per = (uint32_t)(a.col_tiles * a.splits);
+__device__ __forceinline__ Spot spot_of(const AttnArgs& a, uint32_t n, uint32_t blocks) {
+    const uint32_t per = (uint32_t)(a.col_tiles * a.splits);
     uint32_t unit, rest;
     bool there = true;
     if ((uint32_t)(a.B * a.Hk) % 8 == 0) {
         unit = n % 8 + n / 8 / per * 8;
         rest = n / 8 % per;
     } else {
-        const uint32_t line = n % 8 * (gridDim.x / 8) + n / 8;
+        const uint32_t line = n % 8 * (blocks / 8) + n / 8;
         there = line < (uint32_t)a.blocks;
         unit = line / per;
         rest = line % per;

@@ -82,7 +82,7 @@ __global__ __launch_bounds__(kAttnThreads, kForwardWaves<T>) void attn_forward_k
     using Tl = Tile<T, DP, TILE>;
     // arrays of their own: the compiler then sees that what is filled is not what is read
     __shared__ u32x4 k0[Tl::kPieces], v0[Tl::kPieces], k1[Tl::kPieces], v1[Tl::kPieces];
-    const Spot spot = spot_of(a);
+    const Spot spot = spot_of(a, blockIdx.x, gridDim.x);
     if (!spot.there) return;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int col = lane % 32, half = lane / 32;
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(kAttnThreads, kForwardWaves<T>) void attn_forward_k
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             s[n] = mul_columns<T, DP>(at, ks, n, qc);
-            hide(s[n], vis.block(n), half, -kInf);
+            hide(s[n], vis.block(n), -kInf);
         }
         run.weigh<T>(s, acc, a.scale2, growth);
 #pragma unroll
@@ -169,7 +169,7 @@ void attn_few_kernel(AttnArgs a) {
     constexpr int kMore = TWICE ? WAVES * Tl::kPieces : 1;
     __shared__ u32x4 k0[WAVES * Tl::kPieces], v0[WAVES * Tl::kPieces], k1[kMore], v1[kMore];
     __shared__ float2 stat[WAVES * 32];
-    const Spot spot = spot_of(a);
+    const Spot spot = spot_of(a, blockIdx.x, gridDim.x);
     if (!spot.there) return;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int col = lane % 32, half = lane / 32;
@@ -216,7 +216,7 @@ void attn_few_kernel(AttnArgs a) {
     const float growth = kGrowth / a.scale2;
     const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible& vis) {
         f32x16 s[1] = {mul_columns<T, DP>(at, ks, 0, qc)};
-        hide(s[0], vis.block(0), half, -kInf);
+        hide(s[0], vis.block(0), -kInf);
         run.weigh<T>(s, acc, a.scale2, growth);
         mul_rows<T, DP, LOW>(at, vs, 0, Weights<T, LOW>(s[0]), acc);
     };

@@ -1,5 +1,4 @@
-// Internal launch description of the attention kernels (attn_forward.hip, attn_grad_q.hip,
-// attn_grad_kv.hip), filled by the host API (attn_api.cpp).  Not part of the public ABI.
+// Internal launch description of the attention kernels (attn_forward.hip, attn_grad.hip), filled by the host API (attn_api.cpp).  Not part of the public ABI.
 //
 // Rows are the queries of the heads that share a key head: row r of a (batch entry, key head)
 // is query r / group of its head r % group.
@@ -48,7 +47,7 @@ struct AttnArgs {
     int32_t col_tiles;        // tiles of columns
     int32_t splits;           // of what is streamed
     int32_t split_keys;       // keys of a split (forward), or tiles of it (backward)
-    int32_t blocks;           // workgroups with work; a launch has a multiple of 8
+    int32_t blocks;           // workgroups with work; a launch has a multiple of 8 of each kind
     float scale, scale2;      // scale2: scale / log 2
     int32_t dtype;
     bool few;
@@ -64,8 +63,8 @@ inline int attn_few_waves(const AttnArgs& a) {
 
 hipError_t launch_attn_forward(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream);
-hipError_t launch_attn_grad_q(const AttnArgs& a, hipStream_t stream);
-hipError_t launch_attn_grad_kv(const AttnArgs& a, hipStream_t stream);
+// Both kinds of gradients, after delta; one without blocks is left out.
+hipError_t launch_attn_grad(const AttnArgs& of_q, const AttnArgs& of_kv, hipStream_t stream);
 // Splits' gradients added up: of_q's, of_kv's, where they have more than one.
 hipError_t launch_attn_grad_join(const AttnArgs& of_q, const AttnArgs& of_kv, hipStream_t stream);
 

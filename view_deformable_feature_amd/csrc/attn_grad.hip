@@ -32,7 +32,10 @@ template <typename T>
 constexpr float kLiftLog2 = std::is_same<T, _Float16>::value ? 15.0f : 0.0f;
 
 template <typename T, int DP>
-constexpr int kGradWaves = sizeof(T) * DP > 256 ? 1 : 2;   // to a SIMD, whose registers they share
+constexpr int kGradWaves = sizeof(T) * DP > 256   ? 1   // to a SIMD, whose registers they share
+                           : sizeof(T) * DP > 128 ? 2
+                           : sizeof(T) * DP > 64  ? 3
+                                                  : 4;
 
 constexpr int TILE = kAttnTile, NB = TILE / 32;
 

@@ -126,9 +126,26 @@ struct Units {
     }
 };
 
-// The sum over the lanes of a head.
+// The sum over the lanes of a head, a power of two: pairs, fours, eights (which then read their
+// mirror image) and sixteens by data-parallel primitives, then halves of the wave exchanged.  Every
+// lane has the same sum, bit for bit.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
 __device__ __forceinline__ float head_sum(float v, int lanes) {
-    for (int m = 1; m < lanes; m *= 2) v += __shfl_xor(v, m);
+    if (lanes > 1) v += moved<0xb1>(v);    // quad_perm 1 0 3 2
+    if (lanes > 2) v += moved<0x4e>(v);    // quad_perm 2 3 0 1
+    if (lanes > 4) v += moved<0x141>(v);   // row_half_mirror
+    if (lanes > 8) v += moved<0x140>(v);   // row_mirror
+    if (lanes > 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if (lanes > 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
     return v;
 }
 

@@ -81,7 +81,7 @@ typedef struct {
  *   x, positions (as pos_type says), y   device, element aligned.  y may be x itself with the
  *                                        same strides; it must not overlap x otherwise.
  *   freqs                                device double [R / 2] (may be NULL when R is 0).
- * Errors: DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (head_dim, 2^31 tokens or heads, a launch of 2^32
+ * Errors: DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (head_dim, 2^31 tokens or heads, a launch of 2^31
  * threads or more), DA_ERR_HIP.
  */
 DA_API da_status rope_forward(const rope_problem* problem, const rope_tensor* tensor, const void* x,

@@ -42,7 +42,9 @@ __device__ __forceinline__ void turn_of(double angle, float& c, float& s) {
     s = quadrant & 2 ? -b : b;
 }
 
-__device__ __forceinline__ double position_of(const RopeSide& t, int64_t b, int64_t n) {
+// Of all tokens' `token`-th.
+__device__ __forceinline__ double position_of(const RopeSide& t, uint32_t token) {
+    const uint32_t b = token / (uint32_t)t.N, n = token - b * (uint32_t)t.N;
     const int64_t at = b * t.pos_batch + n;
     switch (t.pos_type) {
         case ROPE_POS_I32: return (double)static_cast<const int32_t*>(t.positions)[at];
@@ -107,20 +109,27 @@ struct Units {
     // x = [a's V, b's V] turned; SIGN -1 the other way.  Numbers past R stay what they are, whatever
     // their neighbours hold.
     template <int SIGN>
-    __device__ __forceinline__ void rotate(bool interleaved, int u, float (&x)[2 * V]) const {
+    __device__ __forceinline__ void rotate(const RopeArgs& r, int u, float (&x)[2 * V]) const {
+        if (r.R == r.D)
+            rotate_some<SIGN, true>(r.layout == ROPE_LAYOUT_INTERLEAVED, u, x);
+        else
+            rotate_some<SIGN, false>(r.layout == ROPE_LAYOUT_INTERLEAVED, u, x);
+    }
+    template <int SIGN, bool ALL>
+    __device__ __forceinline__ void rotate_some(bool interleaved, int u, float (&x)[2 * V]) const {
         if (V > 1 && interleaved) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float p = x[2 * e], q = x[2 * e + 1], t = SIGN * s[u][e];
-                x[2 * e] = e < left[u] ? p * c[u][e] - q * t : p;
-                x[2 * e + 1] = e < left[u] ? q * c[u][e] + p * t : q;
+                x[2 * e] = ALL || e < left[u] ? p * c[u][e] - q * t : p;
+                x[2 * e + 1] = ALL || e < left[u] ? q * c[u][e] + p * t : q;
             }
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float p = x[e], q = x[e + V], t = SIGN * s[u][e];
-                x[e] = e < left[u] ? p * c[u][e] - q * t : p;
-                x[e + V] = e < left[u] ? q * c[u][e] + p * t : q;
+                x[e] = ALL || e < left[u] ? p * c[u][e] - q * t : p;
+                x[e + V] = ALL || e < left[u] ? q * c[u][e] + p * t : q;
             }
         }
     }
@@ -150,15 +159,14 @@ __device__ __forceinline__ float head_sum(float v, int lanes) {
 }
 
 // The turns of a workgroup's tokens from `first` on, R / 2 to each.
-__device__ __forceinline__ void form_turns(const RopeArgs& r, const RopeSide& t, int64_t first, int count,
+__device__ __forceinline__ void form_turns(const RopeArgs& r, const RopeSide& t, uint32_t first, int count,
                                            float2* turns) {
-    const int pairs = r.R / 2, all = count * pairs;
-    for (int i = threadIdx.x; i < all; i += kRopeThreads) {
-        const int64_t token = first + i / pairs;
-        if (token >= t.tokens) break;
-        const double position = position_of(t, token / t.N, token % t.N);
+    const uint32_t pairs = r.R / 2, all = count * pairs;
+    for (uint32_t i = threadIdx.x; i < all; i += kRopeThreads) {
+        const uint32_t token = first + i / pairs;
+        if (token >= (uint32_t)t.tokens) break;
         float c, s;
-        turn_of(position * r.freqs[i % pairs], c, s);
+        turn_of(position_of(t, token) * r.freqs[i % pairs], c, s);
         turns[i] = make_float2(c * r.magnitude, s * r.magnitude * r.sign);
     }
 }
@@ -199,12 +207,12 @@ template <int V, int U>
 __device__ __forceinline__ void load_weights(const Units<V, U>& units, const float* weight,
                                              float (&w)[U][2 * V]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            w[u][e] = weight && units.a[u] >= 0 ? weight[units.a[u] + e] : 1.0f;
-            w[u][e + V] = weight && units.b[u] >= 0 ? weight[units.b[u] + e] : 1.0f;
-        }
+        for (int e = 0; e < 2 * V; ++e) w[u][e] = 1.0f;
+        if (weight && units.a[u] >= 0) __builtin_memcpy(w[u], weight + units.a[u], 4 * V);
+        if (weight && units.b[u] >= 0) __builtin_memcpy(w[u] + V, weight + units.b[u], 4 * V);
+    }
 }
 
 template <typename T, int V, int U, bool NORM>
@@ -213,14 +221,14 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs r) {
     const int which = blockIdx.x >= (uint32_t)r.side[0].blocks;
     const RopeSide& t = r.side[which];
     const Share at(r, t);
-    const int64_t first = (int64_t)(blockIdx.x - (which ? r.side[0].blocks : 0)) * at.count;
-    const int64_t token = first + at.token;
-    const bool there = token < t.tokens && at.head < t.H;   // for whole heads alike
+    const uint32_t first = (blockIdx.x - (which ? r.side[0].blocks : 0)) * at.count;
+    const uint32_t token = first + at.token;
+    const bool there = token < (uint32_t)t.tokens && at.head < t.H;   // for whole heads alike
     Units<V, U> units(r, at.lane);
-    const int64_t b = there ? token / t.N : 0, n = there ? token % t.N : 0;
+    const uint32_t b = there ? token / (uint32_t)t.N : 0, n = there ? token - b * (uint32_t)t.N : 0;
     const T* x = static_cast<const T*>(t.x) + b * t.x_batch + n * t.x_token;
     T* y = static_cast<T*>(t.y) + b * t.y_batch + n * t.y_token;
-    Vectors<T, V, U> in, next;
+    Vectors<T, V, U> in;
     if (there) in.load(units, x + at.head * t.x_head);
     float w[U][2 * V];
     if constexpr (NORM) load_weights(units, t.weight, w);
@@ -228,10 +236,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs r) {
     __syncthreads();
     if (!there) return;
     units.load(r, at.lane, turns + at.token * (r.R / 2));
-    const bool interleaved = r.layout == ROPE_LAYOUT_INTERLEAVED;
     for (int head = at.head; head < t.H; head += t.abreast) {
         const bool more = head + t.abreast < t.H;
-        if (more) next.load(units, x + (head + t.abreast) * t.x_head);
         float v[U][2 * V], sum = 0.0f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -250,12 +256,12 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs r) {
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            units.template rotate<1>(interleaved, u, v[u]);
+            units.template rotate<1>(r, u, v[u]);
             T* to = y + head * t.y_head;
             if (units.a[u] >= 0) store_piece<T, V>(to + units.a[u], v[u]);
             if (units.b[u] >= 0) store_piece<T, V>(to + units.b[u], v[u] + V);
         }
-        if (more) in = next;
+        if (more) in.load(units, x + (head + t.abreast) * t.x_head);
     }
 }
 
@@ -271,22 +277,20 @@ __global__ __launch_bounds__(kRopeThreads) void rope_backward_kernel(RopeArgs r)
     const int block = blockIdx.x - (which ? r.side[0].blocks : 0);
     const Share at(r, t);
     Units<V, U> units(r, at.lane);
-    const bool interleaved = r.layout == ROPE_LAYOUT_INTERLEAVED;
     float w[U][2 * V], gw[U][2 * V];
     load_weights(units, t.weight, w);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < 2 * V; ++e) gw[u][e] = 0.0f;
-    for (int64_t first = (int64_t)block * at.count; first < t.tokens;
-         first += (int64_t)t.blocks * at.count) {
-        const int64_t token = first + at.token;
-        const bool there = token < t.tokens && at.head < t.H;
-        const int64_t b = there ? token / t.N : 0, n = there ? token % t.N : 0;
+    for (uint32_t first = block * at.count; first < (uint32_t)t.tokens; first += t.blocks * at.count) {
+        const uint32_t token = first + at.token;
+        const bool there = token < (uint32_t)t.tokens && at.head < t.H;
+        const uint32_t b = there ? token / (uint32_t)t.N : 0, n = there ? token - b * (uint32_t)t.N : 0;
         const T* x = static_cast<const T*>(t.x) + b * t.x_batch + n * t.x_token;
         const T* g = static_cast<const T*>(t.y) + b * t.y_batch + n * t.y_token;
-        T* dx = static_cast<T*>(t.dx) + (there ? token : 0) * t.H * r.D;
-        Vectors<T, V, U> px, pg, nx, ng;
+        T* dx = static_cast<T*>(t.dx) + (int64_t)(there ? token : 0) * t.H * r.D;
+        Vectors<T, V, U> px, pg;
         if (there) {
             px.load(units, x + at.head * t.x_head);
             pg.load(units, g + at.head * t.y_head);
@@ -298,16 +302,12 @@ __global__ __launch_bounds__(kRopeThreads) void rope_backward_kernel(RopeArgs r)
         units.load(r, at.lane, turns + at.token * (r.R / 2));
         for (int head = at.head; head < t.H; head += t.abreast) {
             const bool more = head + t.abreast < t.H;
-            if (more) {
-                nx.load(units, x + (head + t.abreast) * t.x_head);
-                ng.load(units, g + (head + t.abreast) * t.y_head);
-            }
             float v[U][2 * V], d[U][2 * V], squares = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 px.unpack(u, v[u]);
                 pg.unpack(u, d[u]);
-                units.template rotate<-1>(interleaved, u, d[u]);
+                units.template rotate<-1>(r, u, d[u]);
 #pragma unroll
                 for (int e = 0; e < 2 * V; ++e) {
                     squares = fmaf(v[u][e], v[u][e], squares);
@@ -333,8 +333,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_backward_kernel(RopeArgs r)
                 }
             }
             if (more) {
-                px = nx;
-                pg = ng;
+                px.load(units, x + (head + t.abreast) * t.x_head);
+                pg.load(units, g + (head + t.abreast) * t.y_head);
             }
         }
     }

@@ -59,8 +59,9 @@ da_status check_tensor(const rope_problem* p, const rope_tensor* t) {
             return report_error(DA_ERR_INVALID_ARG, "a stride is negative or past 2^56");
     if (t->pos_stride < 0 || t->pos_stride > (int64_t(1) << 40))
         return report_error(DA_ERR_INVALID_ARG, "pos_stride is negative or past 2^40");
-    if (t->batch >= k2to31 || t->tokens >= k2to31 || t->heads >= k2to31)
-        return report_error(DA_ERR_UNSUPPORTED, "2^31 batch entries, tokens or heads");
+    if (t->batch >= k2to31 || t->tokens >= k2to31 || t->heads >= k2to31 ||
+        (wide)t->batch * t->tokens >= k2to31 - 1024)
+        return report_error(DA_ERR_UNSUPPORTED, "2^31 tokens of all batch entries, or heads");
     if ((wide)t->batch * t->tokens * t->heads * p->head_dim >= (wide)1 << 56)
         return report_error(DA_ERR_UNSUPPORTED, "2^56 numbers");
     const int e = elem_bytes(p->dtype);
@@ -72,7 +73,7 @@ da_status check_tensor(const rope_problem* p, const rope_tensor* t) {
 
 int pos_bytes(int32_t t) { return t == ROPE_POS_I64 ? 8 : 4; }
 
-constexpr int64_t kWantedBlocks = 1024;     // workgroups that a launch should have
+constexpr int64_t kWantedBlocks = 512;      // workgroups that a launch should have
 constexpr int64_t kBackwardBlocks = 512;    // that a backward launch has at most
 
 bool empty(const rope_tensor* t) { return !t || t->batch == 0 || t->tokens == 0; }

@@ -190,45 +190,59 @@ def rope_norm_forward(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Opti
     launch; k may be None, and of other batch, tokens and heads than q.  ``q_out`` and ``k_out`` may
     be q and k themselves."""
     _sides(q, k)
-    dev = q.device
+    dev, dtype, shape = q.device, q.dtype, q.shape
     pf = _frequencies(freqs, dev)
-    prob = _problem(q.shape[3], 2 * freqs.shape[0], float(eps), float(magnitude), layout, q.dtype, 0)
-    args, outs = [], []
-    for name, x, w, pos, out in (("q", q, q_weight, q_positions, q_out),
-                                 ("k", k, k_weight, k_positions, k_out)):
-        if x is None:
-            args += [None] * 5
-            outs.append(None)
-            continue
-        px = _need_heads(x, name, q.dtype, dev)
-        shape = x.shape
-        pw = _weight(w, name + "_weight", dev, shape[3])
-        pp, kind, batched = _place(pos, name + "_positions", shape, dev)
-        out = _result(out, name + "_out", x)
-        args += [_tensor(shape, x.stride(), out.stride(), kind, batched, name), px, pp, pw, out.data_ptr()]
-        outs.append(out)
-    call("rope_norm_forward", dev, prob, *args, pf)
-    return tuple(outs)
-
-
-def _backward_plan(q, k, gq, gk, freqs, q_positions, k_positions, eps, layout, magnitude):
-    """(problem, tensors, workspace bytes)."""
-    _sides(q, k)
-    prob = _problem(q.shape[3], 2 * freqs.shape[0], float(eps), float(magnitude), layout, q.dtype, 0)
-    tensors = []
-    for name, x, g, pos in (("q", q, gq, q_positions), ("k", k, gk, k_positions)):
-        if x is None:
-            tensors.append((None, None))
-            continue
-        pp, kind, batched = _place(pos, name + "_positions", x.shape, q.device)
-        tensors.append((_tensor(x.shape, x.stride(), (x if g is None else g).stride(), kind, batched,
-                                name), pp))
-    return prob, tensors, _backward_size(prob, tensors[0][0], tensors[1][0])
+    prob = _problem(shape[3], 2 * freqs.shape[0], float(eps), float(magnitude), layout, dtype, 0)
+    pq = _need_heads(q, "q", dtype, dev)
+    pw = _weight(q_weight, "q_weight", dev, shape[3])
+    pp, kind, batched = _place(q_positions, "q_positions", shape, dev)
+    q_out = _result(q_out, "q_out", q)
+    tq = _tensor(shape, q.stride(), q_out.stride(), kind, batched, "q")
+    if k is None:
+        call("rope_norm_forward", dev, prob, tq, pq, pp, pw, q_out.data_ptr(), None, None, None, None,
+             None, pf)
+        return q_out, None
+    shape = k.shape
+    pk = _need_heads(k, "k", dtype, dev)
+    pkw = _weight(k_weight, "k_weight", dev, shape[3])
+    pkp, kind, batched = _place(k_positions, "k_positions", shape, dev)
+    k_out = _result(k_out, "k_out", k)
+    tk = _tensor(shape, k.stride(), k_out.stride(), kind, batched, "k")
+    call("rope_norm_forward", dev, prob, tq, pq, pp, pw, q_out.data_ptr(), tk, pk, pkp, pkw,
+         k_out.data_ptr(), pf)
+    return q_out, k_out
 
 
 def rope_norm_backward_workspace_size(q: torch.Tensor, k: Optional[torch.Tensor]) -> int:
     """Bytes of ``workspace`` that ``rope_norm_backward`` uses."""
-    return _backward_plan(q, k, None, None, torch.empty(0), None, None, 0.0, "half", 1.0)[2]
+    _sides(q, k)
+    prob = _problem(q.shape[3], 0, 0.0, 1.0, "half", q.dtype, 0)
+    tq, tk = (None if x is None else _tensor(x.shape, x.stride(), x.stride(), 0, False, name)
+              for name, x in (("q", q), ("k", k)))
+    return _backward_size(prob, tq, tk)
+
+
+_OF_Q = ("q", "q_weight", "q_positions", "grad_q_out")
+_OF_K = ("k", "k_weight", "k_positions", "grad_k_out")
+
+
+def _backward_side(x, g, w, positions, need_weights, names, dev):
+    """(tensor's description, gradient, weight's gradient, addresses) of q or k."""
+    name, of_weight, of_positions, of_grad = names
+    shape, dtype = x.shape, x.dtype
+    if not isinstance(g, torch.Tensor) or g.shape != shape:
+        raise ValueError(f"{of_grad} must have {name}'s shape")
+    px = _need_heads(x, name, dtype, dev)
+    pg = _need_heads(g, of_grad, dtype, dev)
+    pw = _weight(w, of_weight, dev, shape[3])
+    pp, kind, batched = _place(positions, of_positions, shape, dev)
+    dx = _like(x)
+    dw = None
+    if need_weights:
+        dw = (torch.empty(shape[3], device=dev, dtype=torch.float32) if w is None
+              else torch.empty_like(w))
+    t = _tensor(shape, x.stride(), g.stride(), kind, batched, name)
+    return t, dx, dw, (px, pp, pw, pg, dx.data_ptr(), dw.data_ptr() if need_weights else None)
 
 
 def rope_norm_backward(q: torch.Tensor, k: Optional[torch.Tensor], grad_q_out: torch.Tensor,
@@ -241,32 +255,19 @@ def rope_norm_backward(q: torch.Tensor, k: Optional[torch.Tensor], grad_q_out: t
     """(grad_q, grad_k of the inputs' type, dense; grad_q_weight, grad_k_weight [D] float32), from
     what ``rope_norm_forward`` was given and the gradients of its results.  ``need_weights`` false
     leaves out the weights' part (None in its place)."""
-    for name, x, g in (("q", q, grad_q_out), ("k", k, grad_k_out)):
-        if x is not None and (not isinstance(g, torch.Tensor) or g.shape != x.shape):
-            raise ValueError(f"grad_{name}_out must have {name}'s shape")
+    _sides(q, k)
     dev = q.device
     pf = _frequencies(freqs, dev)
-    prob, tensors, bytes_needed = _backward_plan(q, k, grad_q_out, grad_k_out, freqs, q_positions,
-                                                 k_positions, eps, layout, magnitude)
-    args, grads, weights = [], [], []
-    for name, x, g, w, (t, pp) in (("q", q, grad_q_out, q_weight, tensors[0]),
-                                   ("k", k, grad_k_out, k_weight, tensors[1])):
-        if x is None:
-            args += [None] * 7
-            grads.append(None)
-            weights.append(None)
-            continue
-        px = _need_heads(x, name, q.dtype, dev)
-        pg = _need_heads(g, f"grad_{name}_out", q.dtype, dev)
-        pw = _weight(w, name + "_weight", dev, x.shape[3])
-        grads.append(_like(x))
-        weights.append(torch.empty(x.shape[3:], device=dev, dtype=torch.float32) if need_weights else None)
-        args += [t, px, pp, pw, pg, grads[-1].data_ptr(),
-                 weights[-1].data_ptr() if need_weights else None]
-    workspace = scratch(workspace, bytes_needed if need_weights else 0, dev)
+    prob = _problem(q.shape[3], 2 * freqs.shape[0], float(eps), float(magnitude), layout, q.dtype, 0)
+    tq, dq, dqw, of_q = _backward_side(q, grad_q_out, q_weight, q_positions, need_weights, _OF_Q, dev)
+    if k is None:
+        tk, dk, dkw, of_k = None, None, None, (None,) * 6
+    else:
+        tk, dk, dkw, of_k = _backward_side(k, grad_k_out, k_weight, k_positions, need_weights, _OF_K, dev)
+    workspace = scratch(workspace, _backward_size(prob, tq, tk) if need_weights else 0, dev)
     pws, nws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    call("rope_norm_backward", dev, prob, *args, pf, pws, nws)
-    return (*grads, *weights)
+    call("rope_norm_backward", dev, prob, tq, *of_q, tk, *of_k, pf, pws, nws)
+    return dq, dk, dqw, dkw
 
 
 def _consecutive(t):

@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "attention.h"
 #include "attn_internal.h"
@@ -95,49 +96,77 @@ void describe(const attn_problem* p, da::AttnArgs& a) {
     a.dtype = p->dtype;
 }
 
-constexpr int64_t kShortSteps = 8;      // of a workgroup over the keys that are not worth a second launch
-constexpr int64_t kSplitBlocks = 512;   // workgroups that splits may make
-
-// The forward's form: wide where that gives every compute unit a workgroup, else 32 rows to one,
-// four times as many; always so where one of those has all rows.  Where even these leave compute
-// units without work, the keys are split over workgroups.
+// The forward's form and the splits of its keys: of a few candidates the one whose time this counts
+// least, in microseconds.  A workgroup takes so long for a tile of 64 keys (wide) or for its waves'
+// 32 keys each (few rows), longer where several have to share a compute unit (16 heads of 48 on
+// 3 x 1329 rows, binary16: wide 44, by 32 rows 73); splits cost a launch that joins them, and their
+// results' way.  Measured, 8 heads of 64 numbers, bfloat16:
+// 128 rows on 8192 keys wide in 1, 8 and 32 splits 89, 22 and 20 us, by 32 rows 35, 16 and 28; 300
+// rows on 4096 keys wide in 1, 4, 8 and 16 splits 48, 21, 19 and 23, by 32 rows in 1, 3 and 8 21, 17
+// and 26; 16 x 875 rows of two entries on 684 keys wide 14, by 32 rows 29; one row on 1500 keys in
+// 1 and 6 splits 11.4 and 10.7 on the GPU, 11 and 15 with the second launch's host time.
 void choose_forward(da::AttnArgs& a) {
     const int64_t units = (int64_t)a.B * a.Hk;
-    a.few = a.rows <= da::kAttnFew ||
-            units * ((a.rows + (int64_t)da::kAttnWide - 1) / da::kAttnWide) < 256;
-    const int64_t width = a.few ? da::kAttnFew : da::kAttnWide;
-    a.col_tiles = (int32_t)((a.rows + width - 1) / width);
-    const int64_t blocks = units * a.col_tiles;
-    if (!a.few || blocks >= 256) return;
-    const int64_t per_step = (int64_t)da::kAttnFew * da::attn_few_waves(a);
-    const int64_t steps = (a.Nk + per_step - 1) / per_step;
-    if (steps <= kShortSteps) return;
-    const int64_t splits =
-        std::min({steps / 2, kSplitBlocks / std::max<int64_t>(blocks, 1), (int64_t)da::kAttnMostSplits});
-    if (splits <= 1) return;
-    const int64_t per = (steps + splits - 1) / splits;
-    a.split_keys = (int32_t)(per * per_step);
-    a.splits = (int32_t)((steps + per - 1) / per);
+    const int D = a.D <= 32 ? 32 : a.D <= 64 ? 64 : a.D <= 96 ? 96 : 128, waves = da::attn_few_waves(a);
+    const bool f32 = a.dtype == DA_F32;
+    const double step_time[2] = {f32 ? 0.35 + 0.058 * D : 0.45 + 0.004 * D,
+                                 f32 ? 0.009 * D * waves : 0.7 + 0.0036 * D};
+    double best = 1e30;
+    for (int few = a.rows <= da::kAttnFew; few < 2; ++few) {
+        const int64_t width = few ? da::kAttnFew : da::kAttnWide;
+        const int64_t tiles = (a.rows + width - 1) / width, blocks = std::max<int64_t>(units * tiles, 1);
+        const int64_t keys = few ? (int64_t)da::kAttnFew * waves : da::kAttnTile;   // of a step
+        const int64_t steps = std::max<int64_t>((a.Nk + keys - 1) / keys, 1);
+        for (int64_t most : {int64_t(1), 256 / blocks, 512 / blocks}) {
+            const int64_t splits = std::min({most, steps, (int64_t)da::kAttnMostSplits});
+            if (splits < 1) continue;
+            const int64_t per = (steps + splits - 1) / splits, made = (steps + per - 1) / per;
+            // 32 rows to a workgroup: one to a compute unit, and four times the states' way
+            const int64_t all = blocks * made, rounds = (all + 255) / 256;
+            const double load = !few ? std::max(1.0, (double)all / 256)
+                                     : rounds == 1 ? 1.0 : (double)rounds * (f32 ? 1.2 : 1.8);
+            double time = load * (double)per * step_time[few];
+            if (made > 1) time += 6.0 + 2e-6 * (double)(made * units * a.rows) * a.D;
+            if (time >= best) continue;
+            best = time;
+            a.few = few;
+            a.col_tiles = (int32_t)tiles;
+            a.splits = (int32_t)made;
+            a.split_keys = (int32_t)(made > 1 ? per * keys : std::max(a.Nk, 1));
+        }
+    }
+    // long shares are halved, so that entries of different lengths spread over the compute units
+    const int64_t keys = a.few ? (int64_t)da::kAttnFew * waves : da::kAttnTile, per = a.split_keys / keys;
+    if (a.splits > 1 && per >= 32 && a.splits * 2 <= da::kAttnMostSplits) {
+        a.split_keys = (int32_t)((per + 1) / 2 * keys);
+        a.splits = (int32_t)((a.Nk + (int64_t)a.split_keys - 1) / a.split_keys);
+    }
 }
 
-// A gradient's form for so many columns to a key head and tiles that are streamed to them: split
-// over workgroups until every compute unit has `want`, but at least two tiles to a split.
-void choose_backward(da::AttnArgs& a, int64_t columns, int64_t tiles, int64_t want) {
+// The splits of what is streamed to so many columns of a key head: up to 128 workgroups in all, 256
+// where each keeps 8 tiles, 512 where it keeps 32.  Measured, 64 numbers, bfloat16, both kinds
+// together: 900 queries on 600 keys of 8 heads (64 and 40 workgroups of 10 and 15 tiles) without
+// splits, up to 128, 256 and 512 workgroups 37, 28, 31 and 33 us; 2048 on 2048 of 8 heads (128 of 32)
+// 70, 70, 62 and 60; 293 on 6304 of 2 heads (6 of 99, 100 of 5) 86, 24, 45 and 50.
+void choose_backward(da::AttnArgs& a, int64_t columns, int64_t tiles) {
     a.col_tiles = (int32_t)((columns + da::kAttnWide - 1) / da::kAttnWide);
-    const int64_t blocks = (int64_t)a.B * a.Hk * a.col_tiles;
-    const int64_t splits = std::max<int64_t>(
-        1, std::min((tiles + 1) / 2, want * 256 / std::max<int64_t>(blocks, 1)));
-    const int64_t per = std::max<int64_t>(1, (tiles + splits - 1) / splits);
+    const int64_t blocks = std::max<int64_t>((int64_t)a.B * a.Hk * a.col_tiles, 1);
+    tiles = std::max<int64_t>(tiles, 1);
+    int64_t per = tiles;
+    for (const auto& t : {std::pair<int, int>{128, 1}, {256, 8}, {512, 32}}) {
+        const int64_t splits = std::min(tiles, t.first / blocks);
+        if (splits < 1) continue;
+        const int64_t share = (tiles + splits - 1) / splits;
+        if (share >= t.second) per = share;
+    }
     a.split_keys = (int32_t)per;
-    a.splits = (int32_t)std::max<int64_t>(1, (tiles + per - 1) / per);
+    a.splits = (int32_t)((tiles + per - 1) / per);
 }
 void choose_grad_q(da::AttnArgs& a) {
-    const int64_t tiles = ((int64_t)a.Nk + da::kAttnTile - 1) / da::kAttnTile;
-    choose_backward(a, a.rows, tiles, a.dtype == DA_F32 ? 1 : 2);
+    choose_backward(a, a.rows, ((int64_t)a.Nk + da::kAttnTile - 1) / da::kAttnTile);
 }
 void choose_grad_kv(da::AttnArgs& a) {
-    const int64_t tiles = ((int64_t)a.Nq + da::kAttnTile - 1) / da::kAttnTile * a.group;
-    choose_backward(a, a.Nk, tiles, a.dtype == DA_F32 ? 1 : 2);
+    choose_backward(a, a.Nk, ((int64_t)a.Nq + da::kAttnTile - 1) / da::kAttnTile * a.group);
 }
 
 // Counts the workgroups; a launch has fewer than 2^32 threads.
@@ -322,7 +351,7 @@ da_status attn_backward(const attn_problem* p, const void* q, const void* k, con
         return report_error(DA_ERR_UNSUPPORTED, "2^32 threads of workgroups or more");
     const wide numbers = (wide)of_q.B * of_q.Nq * of_q.H * of_q.D + 2 * (wide)of_q.B * of_q.Nk * of_q.Hk * of_q.D;
     if ((wide)of_q.B * of_q.Nq * of_q.H * 8 >= wide(1) << 32 ||
-        ((of_q.splits > 1 || of_kv.splits > 1) && numbers / 8 >= wide(1) << 32))
+        ((of_q.splits > 1 || of_kv.splits > 1) && numbers * 4 >= wide(1) << 32))
         return report_error(DA_ERR_UNSUPPORTED, "2^29 rows or more");
     const uint64_t need = 2 * row_bytes(of_q) + part_q_bytes(of_q) + 2 * part_k_bytes(of_kv);
     st = check_workspace(need, workspace, workspace_bytes);

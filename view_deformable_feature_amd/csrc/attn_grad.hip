@@ -2,7 +2,8 @@
 // attn_device.h.
 //
 // Two kinds of workgroups, both in one launch, so that the one's fill the compute units that the
-// other's leave (6 x 900 queries on up to 1201 keys, 8 heads of 64, binary16: LAUNCHES).
+// other's leave (6 x 900 queries on up to 1201 keys, 8 heads of 64, binary16: 42 and 42 us apart, 78
+// in one; with three waves to a SIMD, which heads of 64 numbers have room for, 64).
 //
 // The queries' gradients: as in the forward, columns are rows of queries and keys and values are
 // streamed; a column's lse and delta are a register each.  Three products to a tile: scores, dP, and
@@ -15,7 +16,10 @@
 //
 // Two waves to a SIMD, and the loops have no branches of their own: with branches the accumulators
 // moved between registers at each of them, and heads of 128 numbers had room for one wave
-// (1 x 4096 on 4096, 16 heads of 128 on 4, bfloat16: 694 us, 475 so).
+// (1 x 4096 on 4096, 16 heads of 128 on 4, bfloat16: 694 us, 475 so).  Bound by the matrix
+// instructions, at 720 Tflop/s of five products' worth, with the scores' and dP's products formed
+// twice, once by either kind: at 1010 of the seven that run.  What the scores' exponentials and the
+// roundings of p and dS cost lies in their shadow only in part.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -310,7 +314,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_delta_kernel(AttnArgs a) {
 
 // ---- splits' gradients added up ----------------------------------------------------------
 //
-// Eight numbers to a thread, of grad_q, grad_k and grad_v in turn.
+// Eight numbers of grad_q, grad_k and grad_v in turn to `threads` threads, a power of two up to
+// 32, which have every so many splits each and meet in the wave: with one thread to all of 50
+// splits the launch was bound by its reads' latency.
 struct JoinSide {
     const float* part;
     void* out;
@@ -322,22 +328,25 @@ struct JoinArgs {
 };
 
 template <typename T>
-__global__ __launch_bounds__(kAttnThreads) void attn_grad_join_kernel(JoinArgs a) {
-    int64_t at = ((int64_t)blockIdx.x * kAttnThreads + threadIdx.x) * 8;
+__global__ __launch_bounds__(kAttnThreads) void attn_grad_join_kernel(JoinArgs a, int threads) {
+    int64_t at = ((int64_t)blockIdx.x * kAttnThreads + threadIdx.x) / threads * 8;
+    const int first = threadIdx.x % threads;
     int i = 0;
     while (i < 2 && at >= a.side[i].numbers) at -= a.side[i++].numbers;
     const JoinSide& t = a.side[i];
     if (at >= t.numbers) return;
-    float sum[8];
-    load_as(t.part + at, sum);
+    float sum[8] = {};
 #pragma unroll 4
-    for (int s = 1; s < t.splits; ++s) {
+    for (int s = first; s < t.splits; s += threads) {
         float v[8];
         load_as(t.part + s * t.numbers + at, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += v[e];
     }
-    store_as(static_cast<T*>(t.out) + at, sum);
+    for (int m = 1; m < threads; m *= 2)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor(sum[e], m);
+    if (first == 0) store_as(static_cast<T*>(t.out) + at, sum);
 }
 
 template <typename T, int DP>
@@ -379,15 +388,18 @@ hipError_t launch_attn_grad_join(const AttnArgs& of_q, const AttnArgs& of_kv, hi
         a.side[1] = {of_kv.part_k, of_kv.grad_k, n, of_kv.splits};
         a.side[2] = {of_kv.part_v, of_kv.grad_v, n, of_kv.splits};
     }
-    const int64_t threads = (a.side[0].numbers + a.side[1].numbers + a.side[2].numbers) / 8;
-    if (threads == 0) return hipSuccess;
-    const uint32_t blocks = (uint32_t)((threads + kAttnThreads - 1) / kAttnThreads);
+    const int64_t eights = (a.side[0].numbers + a.side[1].numbers + a.side[2].numbers) / 8;
+    if (eights == 0) return hipSuccess;
+    const int most = std::max(a.side[0].numbers ? a.side[0].splits : 1, a.side[1].numbers ? a.side[1].splits : 1);
+    int threads = 1;
+    while (threads < 32 && threads * 4 < most) threads *= 2;
+    const uint32_t blocks = (uint32_t)((eights * threads + kAttnThreads - 1) / kAttnThreads);
     if (of_q.dtype == DA_BF16)
-        attn_grad_join_kernel<__bf16><<<blocks, kAttnThreads, 0, stream>>>(a);
+        attn_grad_join_kernel<__bf16><<<blocks, kAttnThreads, 0, stream>>>(a, threads);
     else if (of_q.dtype == DA_F16)
-        attn_grad_join_kernel<_Float16><<<blocks, kAttnThreads, 0, stream>>>(a);
+        attn_grad_join_kernel<_Float16><<<blocks, kAttnThreads, 0, stream>>>(a, threads);
     else
-        attn_grad_join_kernel<float><<<blocks, kAttnThreads, 0, stream>>>(a);
+        attn_grad_join_kernel<float><<<blocks, kAttnThreads, 0, stream>>>(a, threads);
     return hipGetLastError();
 }
 

@@ -222,15 +222,17 @@ da_status set_up(const rope_problem* p, const Given (&given)[2], const double* f
             // heads of one packed tensor lie between each other: only equal strides tell them apart
             const auto between = [&](const int64_t (&s)[3], const void* at, const int64_t (&so)[3],
                                      const void* ato) {
-                if (s[1] != so[1] || s[1] == 0) return false;
-                if ((g.t->batch > 1 || o.t->batch > 1) &&
+                // one token to an entry: the entries lie as tokens do otherwise
+                const int in = g.t->tokens > 1 || o.t->tokens > 1;
+                if (s[in] != so[in] || s[in] == 0) return false;
+                if (in == 1 && (g.t->batch > 1 || o.t->batch > 1) &&
                     (s[0] != so[0] || (wide)s[0] < (wide)s[1] * std::max(g.t->tokens, o.t->tokens)))
                     return false;
                 const wide span = ((wide)(g.t->heads - 1) * s[2] + p->head_dim) * e;
                 const wide spano = ((wide)(o.t->heads - 1) * so[2] + p->head_dim) * e;
                 const wide d = (wide)reinterpret_cast<uintptr_t>(ato) - (wide)reinterpret_cast<uintptr_t>(at);
-                return d >= 0 ? d >= span && d + spano <= (wide)s[1] * e
-                              : -d >= spano && -d + span <= (wide)s[1] * e;
+                return d >= 0 ? d >= span && d + spano <= (wide)s[in] * e
+                              : -d >= spano && -d + span <= (wide)s[in] * e;
             };
             const auto meets = [&](const int64_t (&so)[3], const void* ato) {
                 return ranges_clash(to, n, ato, size(o, so)) &&

@@ -205,10 +205,13 @@ def rope_norm_forward(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Opti
     shape = k.shape
     pk = _need_heads(k, "k", dtype, dev)
     pkw = _weight(k_weight, "k_weight", dev, shape[3])
-    pkp, kind, batched = _place(k_positions, "k_positions", shape, dev)
+    if k_positions is not q_positions or shape[:2] != q.shape[:2]:
+        pp_k, kind, batched = _place(k_positions, "k_positions", shape, dev)
+    else:
+        pp_k = pp
     k_out = _result(k_out, "k_out", k)
     tk = _tensor(shape, k.stride(), k_out.stride(), kind, batched, "k")
-    call("rope_norm_forward", dev, prob, tq, pq, pp, pw, q_out.data_ptr(), tk, pk, pkp, pkw,
+    call("rope_norm_forward", dev, prob, tq, pq, pp, pw, q_out.data_ptr(), tk, pk, pp_k, pkw,
          k_out.data_ptr(), pf)
     return q_out, k_out
 

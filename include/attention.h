@@ -38,7 +38,7 @@ extern "C" {
 #endif
 
 /* Problem description.  batch, queries and keys may be 0; heads, key_heads >= 1; heads %
- * key_heads == 0; head_dim a multiple of 8, at most 128; scale finite and > 0.  Strides count
+ * key_heads == 0; head_dim a multiple of 8, at most 128; scale > 0, at most 2^126.  Strides count
  * elements, of a batch entry, a token and a head; a head's numbers are consecutive.  They are
  * >= 0 and multiples of 16 bytes (an input's batch stride may be 0: the same states for all). */
 typedef struct {

@@ -37,6 +37,9 @@ SHAPES = {
     "wide_96": (2, 129, 130, 64, 64, 88),
     "wide_128": (2, 140, 190, 64, 64, 128),
     "wide_shared": (2, 70, 100, 256, 64, 56),
+    "wide_split_64": (2, 200, 1000, 20, 20, 64),  # ... with its keys split over workgroups
+    "wide_split_96": (1, 220, 1700, 40, 40, 88),
+    "wide_split_128": (5, 230, 1500, 9, 9, 128),
     "units_of_eight": (8, 100, 96, 8, 8, 32),
     "units_of_seven": (7, 50, 96, 1, 1, 64),
 }
@@ -74,7 +77,7 @@ def test_shapes(name, dtype):
 
 
 @pytest.mark.parametrize("name", ["one_query", "shared_heads", "odd", "past_tile_edges", "many_keys",
-                                  "wide_64", "wide_128", "units_of_seven"])
+                                  "wide_64", "wide_128", "wide_split_96", "units_of_seven"])
 @pytest.mark.parametrize("lens, mask", [(True, False), (False, True), (True, True)],
                          ids=["lens", "mask", "both"])
 @TYPES
@@ -185,6 +188,19 @@ def test_small_and_large_gradients_in_binary16():
 def test_scale(scale):
     for dtype in (F32, BF16):
         _check(*_inputs((2, 40, 90, 2, 2, 24), dtype, 97), scale=scale)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -140, 2.0 ** -120, 2.0 ** 126])
+@pytest.mark.parametrize("Nq", [3, 300])
+def test_scales_at_the_ends_of_their_range(scale, Nq):
+    """Scores that are all equal however large the products, the mean of the values; and scores that
+    overflow unless the products are small."""
+    q, k, v, _, _, _ = _inputs((2, Nq, 90, 3, 3, 32), F32, 71)
+    if scale > 1:
+        q, k = q * 2.0 ** -65, k * 2.0 ** -64
+    out, lse = vdf.attn_forward(q, k, v, None, None, scale)
+    torch.cuda.synchronize()
+    Attention(q, k, v, None, None, scale).check_forward(out, lse)
 
 
 def test_nothing_is_written_past_the_end():

@@ -66,6 +66,7 @@ ATTN_BAD = [
     (dict(scale=-1.0), 1, "scale"),
     (dict(scale=float("nan")), 1, "scale"),
     (dict(scale=float("inf")), 1, "scale"),
+    (dict(scale=2.0 ** 127), 1, "scale"),
     (dict(flags=1), 1, "flags"),
     (dict(reserved=1), 1, "reserved"),
     (dict(head_dim=20), 2, "multiple of 8"),

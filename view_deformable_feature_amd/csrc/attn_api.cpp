@@ -52,8 +52,8 @@ da_status check_problem(const attn_problem* p) {
                             (long long)p->heads, (long long)p->key_heads);
     if (p->dtype != DA_F32 && p->dtype != DA_BF16 && p->dtype != DA_F16)
         return report_error(DA_ERR_INVALID_ARG, "dtype %d is not a da_dtype", (int)p->dtype);
-    if (!isfinite(p->scale) || !(p->scale > 0.0f))
-        return report_error(DA_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (!(p->scale > 0.0f) || !(p->scale <= 0x1p126f))   // times 1 / log 2 it is finite
+        return report_error(DA_ERR_INVALID_ARG, "scale must be > 0 and at most 2^126");
     if (p->head_dim % 8 != 0 || p->head_dim > 128)
         return report_error(DA_ERR_UNSUPPORTED, "head_dim is not a multiple of 8 up to 128");
     const int e = elem_bytes(p->dtype);

@@ -12,6 +12,7 @@
 // products.  Bound by the matrix instructions: 2 x 4096 rows on 8192 keys, 16 heads of 128, bfloat16,
 // 505 us, 1090 Tflop/s, where a product of 8192^3 runs at 1363; the clock falls to about 1.75 GHz
 // under this load.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(kAttnThreads, kForwardWaves<T>) void attn_forward_k
     f32x16 acc[ND];
     clear(acc);
     Running run;
-    const float growth = kGrowth / a.scale2;
+    const float growth = fminf(kGrowth / a.scale2, FLT_MAX);   // finite: added to -infinity
     const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible& vis) {
         f32x16 s[NB];
 #pragma unroll
@@ -229,7 +230,7 @@ void attn_few_kernel(AttnArgs a) {
     f32x16 acc[ND];
     clear(acc);
     Running run;
-    const float growth = kGrowth / a.scale2;
+    const float growth = fminf(kGrowth / a.scale2, FLT_MAX);   // finite: added to -infinity
     const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible& vis) {
         f32x16 s[1] = {mul_columns<T, DP>(at, ks, 0, qc)};
         hide(s[0], vis.block(0), -kInf);

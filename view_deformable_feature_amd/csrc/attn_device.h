@@ -186,13 +186,18 @@ __device__ __forceinline__ void mul_rows(const Places<T, DP>& at, LdsBytes tile,
     }
 }
 
-// The block's rows times the columns in registers.
+__device__ __forceinline__ f32x16 all_equal(float v) {
+    f32x16 x;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = v;
+    return x;
+}
+
+// The block's rows times the columns in registers, added to acc.
 template <typename T, int DP>
 __device__ __forceinline__ f32x16 mul_columns(const Places<T, DP>& at, LdsBytes tile, int block,
-                                              const u32x4 (&cols)[Tile<T, DP, 64>::kSteps]) {
-    f32x16 acc;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+                                              const u32x4 (&cols)[Tile<T, DP, 64>::kSteps],
+                                              f32x16 acc = all_equal(0.0f)) {
 #pragma unroll
     for (int t = 0; t < Tile<T, DP, 64>::kSteps; ++t)
         acc = mul_pieces<T>(at.row_piece(tile, block, t), cols[t], acc);

@@ -3,7 +3,7 @@
 //
 // Two kinds of workgroups, both in one launch, so that the one's fill the compute units that the
 // other's leave (6 x 900 queries on up to 1201 keys, 8 heads of 64, binary16: 42 and 42 us apart, 78
-// in one; with three waves to a SIMD, which heads of 64 numbers have room for, 64).
+// in one; with three waves to a SIMD, which heads of 64 numbers have room for, 62).
 //
 // The queries' gradients: as in the forward, columns are rows of queries and keys and values are
 // streamed; a column's lse and delta are a register each.  Three products to a tile: scores, dP, and
@@ -41,12 +41,34 @@ constexpr int kGradWaves = sizeof(T) * DP > 256   ? 1   // to a SIMD, whose regi
                            : sizeof(T) * DP > 64  ? 3
                                                   : 4;
 
+// In 16-bit types dP's product begins with -delta, which saves a subtraction for each score; its
+// roundings, of delta's size too then, are far below those of dS (4 x 2048 on 2048, 16 heads of 64,
+// bfloat16: 266 us, 255 so).  In binary32 they would not be, and for the keys of wide heads the
+// registers do not reach.
+template <typename T, int DP>
+constexpr bool kKeysFromDelta = sizeof(T) == 2 && DP <= 96;
+
 constexpr int TILE = kAttnTile, NB = TILE / 32;
+
+// A lane's 16 of a tile's statistics, by the rows of a block's results, in fours.
+__device__ __forceinline__ f32x4 stats_at(const float* stat, int block, int four, int half) {
+    return *reinterpret_cast<const f32x4*>(stat + block * 32 + 8 * four + 4 * half);
+}
+__device__ __forceinline__ f32x16 stats_of(const float* stat, int block, int half) {
+    f32x16 x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const f32x4 four = stats_at(stat, block, j, half);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * j + e] = four[e];
+    }
+    return x;
+}
 
 // A workgroup's part of LDS: two tiles of two tensors.
 struct Shared {
     u32x4 *a0, *b0, *a1, *b1;
-    float *stat0, *stat1;   // lse2 and delta of a tile's rows
+    float *stat0, *stat1;   // of a tile's rows, what exponents are more by, and -delta
 };
 
 template <typename T, int DP, bool MASK>
@@ -103,10 +125,16 @@ __device__ __forceinline__ void grad_q(const AttnArgs& a, int block, int blocks,
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             f32x16 s = mul_columns<T, DP>(at, ks, n, qc);
-            const f32x16 dp = mul_columns<T, DP>(at, vs, n, gc);
+            f32x16 dp;
+            if constexpr (sizeof(T) == 2) {
+                dp = mul_columns<T, DP>(at, vs, n, gc, all_equal(-delta));
+            } else {
+                dp = mul_columns<T, DP>(at, vs, n, gc);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], a.scale2, -lse2)) * (dp[i] - delta);
+                for (int i = 0; i < 16; ++i) dp[i] -= delta;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], a.scale2, -lse2)) * dp[i];
             hide(s, vis.block(n), 0.0f);
             lift.apply(s, acc);
             mul_rows<T, DP, false>(at, ks, n, Weights<T, false>(s), acc);
@@ -181,9 +209,11 @@ __device__ __forceinline__ void grad_kv(const AttnArgs& a, int block, int blocks
         filler.template run<false>(gp + head * a.g_head + row * a.g_token, rows, (uint32_t)a.g_token, gs, wave, none);
         const int at_row = threadIdx.x % TILE;
         // past the last row p is 0
-        mine = threadIdx.x < TILE ? kInf : 0.0f;
-        if (threadIdx.x < 2 * TILE && at_row < rows)
+        mine = threadIdx.x < TILE ? -kInf : 0.0f;
+        if (threadIdx.x < 2 * TILE && at_row < rows) {
             mine = (threadIdx.x < TILE ? a.lse2 : a.delta)[stats + (int64_t)head * a.Nq + row + at_row];
+            mine = (threadIdx.x < TILE ? kLiftLog2<T> : 0.0f) - mine;
+        }
         row += TILE;
         if (row >= a.Nq) {
             row = 0;
@@ -207,20 +237,25 @@ __device__ __forceinline__ void grad_kv(const AttnArgs& a, int block, int blocks
             f32x16 p = mul_columns<T, DP>(at, qs, n, kc);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const f32x4 lse2 = *reinterpret_cast<const f32x4*>(stat + n * 32 + 8 * j + 4 * half);
+                const f32x4 more = stats_at(stat, n, j, half);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    p[4 * j + e] = __builtin_amdgcn_exp2f(
-                        fmaf(p[4 * j + e], a.scale2, kLiftLog2<T> - lse2[e]));
+                    p[4 * j + e] = __builtin_amdgcn_exp2f(fmaf(p[4 * j + e], a.scale2, more[e]));
             }
             mul_rows<T, DP, false>(at, gs, n, Weights<T, false>(p), dv);
-            f32x16 ds = mul_columns<T, DP>(at, gs, n, vc);
+            f32x16 ds;
+            if constexpr (kKeysFromDelta<T, DP>) {
+                ds = mul_columns<T, DP>(at, gs, n, vc, stats_of(stat + TILE, n, half));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x4 delta =
-                    *reinterpret_cast<const f32x4*>(stat + TILE + n * 32 + 8 * j + 4 * half);
+                for (int i = 0; i < 16; ++i) ds[i] *= p[i];
+            } else {
+                ds = mul_columns<T, DP>(at, gs, n, vc);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ds[4 * j + e] = p[4 * j + e] * (ds[4 * j + e] - delta[e]);
+                for (int j = 0; j < 4; ++j) {
+                    const f32x4 less = stats_at(stat + TILE, n, j, half);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ds[4 * j + e] = p[4 * j + e] * (ds[4 * j + e] + less[e]);
+                }
             }
             lift.apply(ds, dk);
             mul_rows<T, DP, false>(at, qs, n, Weights<T, false>(ds), dk);

@@ -13,7 +13,8 @@
  * Numbers from R on stay as they are.  With ROPE_FLAG_INVERSE the sign of s changes: the
  * rotation's transpose, which is its gradient.  Frequencies are binary64, and so are the
  * angles up to their place within a turn, so that far positions keep their digits; a position
- * is any number (an index, or a coordinate).
+ * is any number (an index, or a coordinate).  An angle of 2^52 and more, or none at all, makes its
+ * pairs NaN.
  *
  * The head norm comes before the rotation: with
  *

@@ -221,8 +221,10 @@ def test_nothing_is_written_past_the_end():
     assert (ws[n:] == 0x5a).all()
 
 
-def test_parts_of_the_gradients():
-    q, k, v, go, kv, m = _inputs((2, 30, 90, 4, 2, 32), BF16, 99, True, True)
+@pytest.mark.parametrize("shape", [(2, 30, 90, 4, 2, 32), (1, 40, 6000, 2, 2, 64), (1, 5000, 40, 2, 1, 24)],
+                         ids=["small", "queries_split", "keys_split"])
+def test_parts_of_the_gradients(shape):
+    q, k, v, go, kv, m = _inputs(shape, BF16, 99, True, True)
     out, lse = vdf.attn_forward(q, k, v, kv, m)
     dq, dk, dv = vdf.attn_backward(q, k, v, out, lse, go, kv, m)
     a = vdf.attn_backward(q, k, v, out, lse, go, kv, m, need_kv=False)

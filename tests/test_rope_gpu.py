@@ -129,6 +129,22 @@ def test_positions_that_are_no_numbers():
     assert y[0, [0, 3]].isfinite().all()
 
 
+def test_angles_without_a_place_in_a_turn():
+    """Pairs whose angles pass 2^52 are NaN, slower ones of the same token and the largest below are
+    not: a position of 2^51 at frequencies 1, 2 and 2^-20."""
+    x = _heads((1, 3, 2, 6, 6), F32, torch.Generator().manual_seed(243))
+    f = torch.tensor([1.0, 2.0, 2.0 ** -20], dtype=torch.float64, device="cuda")
+    pos = torch.tensor([2.0 ** 51, 3.0, -2.0 ** 51], device="cuda")
+    y = vdf.rope_forward(x, f, pos, "interleaved")
+    torch.cuda.synchronize()
+    assert y[0, ::2, :, 2:4].isnan().all()
+    assert y[0, ::2, :, [0, 1, 4, 5]].isfinite().all() and y[0, 1].isfinite().all()
+    want, mag = rotate(x, f, pos.cpu(), "interleaved")
+    keep = torch.ones_like(want, dtype=torch.bool)
+    keep[0, ::2, :, 2:4] = False
+    check("y", y.cpu()[keep], want[keep], (8 * U * mag)[keep])
+
+
 @LAYOUTS
 @TYPES
 def test_what_is_not_rotated_stays(layout, dtype):

@@ -27,7 +27,8 @@ namespace {
 // result.  Off by about a unit in the last place of binary32.
 __device__ __forceinline__ void turn_of(double angle, float& c, float& s) {
     const double q = rint(angle * 0.63661977236758134);   // 2 / pi
-    const double rest = fma(-q, 6.123233995736766e-17, fma(-q, 1.5707963267948966, angle));
+    double rest = fma(-q, 6.123233995736766e-17, fma(-q, 1.5707963267948966, angle));
+    if (!(fabs(angle) < 0x1p52)) rest = __builtin_nan("");   // no place within a turn
     const int quadrant = (int)(q - 4.0 * rint(q * 0.25));
     const float y = (float)rest, z = y * y;
     float sp = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);

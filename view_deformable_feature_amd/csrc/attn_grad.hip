@@ -209,19 +209,18 @@ __device__ __forceinline__ void grad_kv(const AttnArgs& a, int block, int blocks
         filler.template run<false>(gp + head * a.g_head + row * a.g_token, rows, (uint32_t)a.g_token, gs, wave, none);
         const int at_row = threadIdx.x % TILE;
         // past the last row p is 0
-        mine = threadIdx.x < TILE ? -kInf : 0.0f;
-        if (threadIdx.x < 2 * TILE && at_row < rows) {
+        mine = threadIdx.x < TILE ? kInf : 0.0f;
+        if (threadIdx.x < 2 * TILE && at_row < rows)
             mine = (threadIdx.x < TILE ? a.lse2 : a.delta)[stats + (int64_t)head * a.Nq + row + at_row];
-            mine = (threadIdx.x < TILE ? kLiftLog2<T> : 0.0f) - mine;
-        }
         row += TILE;
         if (row >= a.Nq) {
             row = 0;
             ++head;
         }
     };
+    // At the end of a step, when they have arrived: what is done with them waits for the fills too.
     const auto keep = [&](float* stat) {
-        if (threadIdx.x < 2 * TILE) stat[threadIdx.x] = mine;
+        if (threadIdx.x < 2 * TILE) stat[threadIdx.x] = (threadIdx.x < TILE ? kLiftLog2<T> : 0.0f) - mine;
     };
 
     f32x16 dk[ND], dv[ND];

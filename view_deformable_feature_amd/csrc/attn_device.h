@@ -18,6 +18,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "act_device.h"
 #include "attn_internal.h"
 
@@ -263,6 +265,33 @@ struct Filler {
 __device__ __forceinline__ void tile_barrier() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __syncthreads();
+}
+
+// Walks over `tiles` tiles with two buffers: a tile is worked on while the next one fills the other.
+// fetch(i) starts the next tile's fills of buffer i, keep(i) puts down what else of it came by
+// registers, step(i) works on it; i is a constant, so that what is filled and what is read are
+// arrays of their own.  The loop has no branches of its own, so that results stay in their registers,
+// and fetches past the end, where fetch gives zeros.  (Three buffers gained nothing with heads of 64
+// numbers, for which there is room: 6 x 900 on up to 1201 keys, gradients, 62 us, 63 so.)
+template <class Fetch, class Step, class Keep>
+__device__ __forceinline__ void walk(int tiles, Fetch fetch, Step step, Keep keep) {
+    constexpr std::integral_constant<int, 0> first{};
+    constexpr std::integral_constant<int, 1> second{};
+    if (tiles <= 0) return;
+    fetch(first);
+    keep(first);
+    tile_barrier();
+    for (int j = 0; j + 1 < tiles; j += 2) {
+        fetch(second);
+        step(first);
+        keep(second);
+        tile_barrier();
+        fetch(first);
+        step(second);
+        keep(first);
+        tile_barrier();
+    }
+    if (tiles % 2) step(first);
 }
 
 // The wave's own fills of LDS have arrived and its reads are done.

@@ -112,21 +112,27 @@ __global__ __launch_bounds__(kAttnThreads, kForwardWaves<T>) void attn_forward_k
     const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
     uint32_t byte = 1;   // of the tile that is fetched next
 
-    // Fetches tile j, or zeros past the last, and reads the mask of the one after it.
-    const auto fetch = [&](int j, u32x4* ks, u32x4* vs) {
-        const int rows = min(keys - j * TILE, TILE);
+    u32x4 *const kt[2] = {k0, k1}, *const vt[2] = {v0, v1};
+    Visible visible_keys[2];
+    int tile = 0;
+    // Fetches the next tile, or zeros past the last, and reads the mask of the one after it.
+    const auto fetch = [&](auto i) {
+        const int rows = min(keys - tile * TILE, TILE);
         const Visible vis = visible(byte, rows, lane);
-        filler.template run<MASK>(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, vis);
-        filler.template run<MASK>(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, vis);
-        if constexpr (MASK) byte = mask_byte(mask + (int64_t)(j + 1) * TILE, keys - (j + 1) * TILE, lane);
-        return vis;
+        if constexpr (MASK) byte = mask_byte(mask + (int64_t)(tile + 1) * TILE, keys - (tile + 1) * TILE, lane);
+        filler.template run<MASK>(kp + (int64_t)tile * TILE * a.k_token, rows, (uint32_t)a.k_token, kt[i], wave, vis);
+        filler.template run<MASK>(vp + (int64_t)tile * TILE * a.v_token, rows, (uint32_t)a.v_token, vt[i], wave, vis);
+        visible_keys[i] = vis;
+        ++tile;
     };
 
     f32x16 acc[ND];
     clear(acc);
     Running run;
     const float growth = fminf(kGrowth / a.scale2, FLT_MAX);   // finite: added to -infinity
-    const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible& vis) {
+    const auto step = [&](auto buffer) {
+        const LdsBytes ks = (LdsBytes)kt[buffer], vs = (LdsBytes)vt[buffer];
+        const Visible vis = visible_keys[buffer];
         f32x16 s[NB];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -139,22 +145,8 @@ __global__ __launch_bounds__(kAttnThreads, kForwardWaves<T>) void attn_forward_k
             mul_rows<T, DP, false>(at, vs, n, Weights<T, false>(s[n]), acc);
     };
 
-    // A tile is worked on while the next one fills the other half of LDS.  The loop has no branches of
-    // its own, so that the results stay in their registers.
-    if (tiles > 0) {
-        if constexpr (MASK) byte = mask_byte(mask, keys, lane);
-        Visible here = fetch(0, k0, v0);
-        tile_barrier();
-        for (int j = 0; j + 1 < tiles; j += 2) {
-            Visible next = fetch(j + 1, k1, v1);
-            step((LdsBytes)k0, (LdsBytes)v0, here);
-            tile_barrier();
-            here = fetch(j + 2, k0, v0);
-            step((LdsBytes)k1, (LdsBytes)v1, next);
-            tile_barrier();
-        }
-        if (tiles % 2) step((LdsBytes)k0, (LdsBytes)v0, here);
-    }
+    if constexpr (MASK) byte = mask_byte(mask, keys, lane);
+    walk(tiles, fetch, step, [](auto) {});
 
     const float sum = column_sum(run.sum);
     if (!there) return;

@@ -16,9 +16,9 @@
 //
 // Two waves to a SIMD, and the loops have no branches of their own: with branches the accumulators
 // moved between registers at each of them, and heads of 128 numbers had room for one wave
-// (1 x 4096 on 4096, 16 heads of 128 on 4, bfloat16: 694 us, 475 so).  Bound by the matrix
-// instructions, at 720 Tflop/s of five products' worth, with the scores' and dP's products formed
-// twice, once by either kind: at 1010 of the seven that run.  What the scores' exponentials and the
+// (1 x 4096 on 4096, 16 heads of 128 on 4, bfloat16: 694 us, 475 so, 455 now).  Bound by the matrix
+// instructions, at 755 Tflop/s of five products' worth, with the scores' and dP's products formed
+// twice, once by either kind: at 1060 of the seven that run.  What the scores' exponentials and the
 // roundings of p and dS cost lies in their shadow only in part.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -65,10 +65,11 @@ __device__ __forceinline__ f32x16 stats_of(const float* stat, int block, int hal
     return x;
 }
 
-// A workgroup's part of LDS: two tiles of two tensors.
+// A workgroup's part of LDS, by the buffer: tiles of two tensors, and of the second one's rows what
+// exponents are more by, and -delta.
 struct Shared {
-    u32x4 *a0, *b0, *a1, *b1;
-    float *stat0, *stat1;   // of a tile's rows, what exponents are more by, and -delta
+    u32x4 *a[2], *b[2];
+    float* stat[2];
 };
 
 template <typename T, int DP, bool MASK>
@@ -104,14 +105,17 @@ __device__ __forceinline__ void grad_q(const AttnArgs& a, int block, int blocks,
     const Filler<Tl> filler(threadIdx.x, a.D * (int)sizeof(T));
     uint32_t byte = 1;   // of the tile that is fetched next
 
-    // Fetches tile j, or zeros past the last, and reads the mask of the one after it.
-    const auto fetch = [&](int j, u32x4* ks, u32x4* vs) {
-        const int rows = min(keys - j * TILE, TILE);
+    // Fetches the next tile, or zeros past the last, and reads the mask of the one after it.
+    Visible visible_keys[2];
+    int tile = 0;
+    const auto fetch = [&](auto i) {
+        const int rows = min(keys - tile * TILE, TILE);
         const Visible vis = visible(byte, rows, lane);
-        filler.template run<MASK>(kp + (int64_t)j * TILE * a.k_token, rows, (uint32_t)a.k_token, ks, wave, vis);
-        filler.template run<MASK>(vp + (int64_t)j * TILE * a.v_token, rows, (uint32_t)a.v_token, vs, wave, vis);
-        if constexpr (MASK) byte = mask_byte(mask + (int64_t)(j + 1) * TILE, keys - (j + 1) * TILE, lane);
-        return vis;
+        if constexpr (MASK) byte = mask_byte(mask + (int64_t)(tile + 1) * TILE, keys - (tile + 1) * TILE, lane);
+        filler.template run<MASK>(kp + (int64_t)tile * TILE * a.k_token, rows, (uint32_t)a.k_token, t.a[i], wave, vis);
+        filler.template run<MASK>(vp + (int64_t)tile * TILE * a.v_token, rows, (uint32_t)a.v_token, t.b[i], wave, vis);
+        visible_keys[i] = vis;
+        ++tile;
     };
 
     f32x16 acc[ND];
@@ -121,7 +125,9 @@ __device__ __forceinline__ void grad_q(const AttnArgs& a, int block, int blocks,
         for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
     Lift<T, ND> lift;
 
-    const auto step = [&](LdsBytes ks, LdsBytes vs, const Visible& vis) {
+    const auto step = [&](auto buffer) {
+        const LdsBytes ks = (LdsBytes)t.a[buffer], vs = (LdsBytes)t.b[buffer];
+        const Visible vis = visible_keys[buffer];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             f32x16 s = mul_columns<T, DP>(at, ks, n, qc);
@@ -141,22 +147,8 @@ __device__ __forceinline__ void grad_q(const AttnArgs& a, int block, int blocks,
         }
     };
 
-    // A tile is worked on while the next one fills the other half of LDS.  The loop has no branches of
-    // its own, so that the results stay in their registers.
-    if (tiles > 0) {
-        if constexpr (MASK) byte = mask_byte(mask, keys, lane);
-        Visible here = fetch(0, t.a0, t.b0);
-        tile_barrier();
-        for (int j = 0; j + 1 < tiles; j += 2) {
-            Visible next = fetch(j + 1, t.a1, t.b1);
-            step((LdsBytes)t.a0, (LdsBytes)t.b0, here);
-            tile_barrier();
-            here = fetch(j + 2, t.a0, t.b0);
-            step((LdsBytes)t.a1, (LdsBytes)t.b1, next);
-            tile_barrier();
-        }
-        if (tiles % 2) step((LdsBytes)t.a0, (LdsBytes)t.b0, here);
-    }
+    if constexpr (MASK) byte = mask_byte(mask, keys, lane);
+    walk(tiles, fetch, step, [](auto) {});
 
     if (!there) return;
     const float factor = a.scale * lift.down();
@@ -203,15 +195,15 @@ __device__ __forceinline__ void grad_kv(const AttnArgs& a, int block, int blocks
     float mine = 0.0f;       // a thread's part of its statistics
     const Visible none = {0};
     // Fetches the next tile, or zeros past the last.
-    const auto fetch = [&](u32x4* qs, u32x4* gs) {
+    const auto fetch = [&](auto i) {
         const int rows = head < a.group ? min(a.Nq - row, TILE) : 0;
-        filler.template run<false>(qp + head * a.q_head + row * a.q_token, rows, (uint32_t)a.q_token, qs, wave, none);
-        filler.template run<false>(gp + head * a.g_head + row * a.g_token, rows, (uint32_t)a.g_token, gs, wave, none);
         const int at_row = threadIdx.x % TILE;
         // past the last row p is 0
         mine = threadIdx.x < TILE ? kInf : 0.0f;
         if (threadIdx.x < 2 * TILE && at_row < rows)
             mine = (threadIdx.x < TILE ? a.lse2 : a.delta)[stats + (int64_t)head * a.Nq + row + at_row];
+        filler.template run<false>(qp + head * a.q_head + row * a.q_token, rows, (uint32_t)a.q_token, t.a[i], wave, none);
+        filler.template run<false>(gp + head * a.g_head + row * a.g_token, rows, (uint32_t)a.g_token, t.b[i], wave, none);
         row += TILE;
         if (row >= a.Nq) {
             row = 0;
@@ -219,8 +211,8 @@ __device__ __forceinline__ void grad_kv(const AttnArgs& a, int block, int blocks
         }
     };
     // At the end of a step, when they have arrived: what is done with them waits for the fills too.
-    const auto keep = [&](float* stat) {
-        if (threadIdx.x < 2 * TILE) stat[threadIdx.x] = (threadIdx.x < TILE ? kLiftLog2<T> : 0.0f) - mine;
+    const auto keep = [&](auto i) {
+        if (threadIdx.x < 2 * TILE) t.stat[i][threadIdx.x] = (threadIdx.x < TILE ? kLiftLog2<T> : 0.0f) - mine;
     };
 
     f32x16 dk[ND], dv[ND];
@@ -230,7 +222,9 @@ __device__ __forceinline__ void grad_kv(const AttnArgs& a, int block, int blocks
         for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.0f;
     Lift<T, ND> lift;
 
-    const auto step = [&](LdsBytes qs, LdsBytes gs, const float* stat) {
+    const auto step = [&](auto buffer) {
+        const LdsBytes qs = (LdsBytes)t.a[buffer], gs = (LdsBytes)t.b[buffer];
+        const float* stat = t.stat[buffer];
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             f32x16 p = mul_columns<T, DP>(at, qs, n, kc);
@@ -261,24 +255,8 @@ __device__ __forceinline__ void grad_kv(const AttnArgs& a, int block, int blocks
         }
     };
 
-    // A tile is worked on while the next one fills the other half of LDS.  The loop has no branches of
-    // its own, so that the results stay in their registers.
-    if (tiles > 0) {
-        fetch(t.a0, t.b0);
-        keep(t.stat0);
-        tile_barrier();
-        for (int j = 0; j + 1 < tiles; j += 2) {
-            fetch(t.a1, t.b1);
-            step((LdsBytes)t.a0, (LdsBytes)t.b0, t.stat0);
-            keep(t.stat1);
-            tile_barrier();
-            fetch(t.a0, t.b0);
-            step((LdsBytes)t.a1, (LdsBytes)t.b1, t.stat1);
-            keep(t.stat0);
-            tile_barrier();
-        }
-        if (tiles % 2) step((LdsBytes)t.a0, (LdsBytes)t.b0, t.stat0);
-    }
+    walk(tiles, fetch, step, keep);
+
     const float back = std::is_same<T, _Float16>::value ? 1.0f / 32768.0f : 1.0f;
     const float fk = a.scale * lift.down() * back, fv = back;
     if (!there) return;
@@ -307,7 +285,7 @@ void attn_grad_kernel(AttnArgs of_q, AttnArgs of_kv, int q_blocks) {
     // arrays of their own: the compiler then sees that what is filled is not what is read
     __shared__ u32x4 a0[Tl::kPieces], b0[Tl::kPieces], a1[Tl::kPieces], b1[Tl::kPieces];
     __shared__ __align__(16) float stat0[2 * TILE], stat1[2 * TILE];
-    const Shared t = {a0, b0, a1, b1, stat0, stat1};
+    const Shared t = {{a0, a1}, {b0, b1}, {stat0, stat1}};
     if ((int)blockIdx.x < q_blocks)
         grad_q<T, DP, MASK>(of_q, blockIdx.x, q_blocks, t);
     else

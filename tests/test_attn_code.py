@@ -37,13 +37,15 @@ def _product(line):
 
 
 def test_buffer_resources_are_scalar(kernels):
-    """A resource built of a vector register would make each access a loop over its values, which
-    reads them four at a time, in every fill of a tile."""
+    """A resource that may differ between lanes would make each access a loop over its values, which
+    compares them with the first lane's and masks the others, in every fill of a tile.  What is
+    taken from the first lane by the source itself stands by itself, three words to a tensor's
+    tile in each of the copies of the loop's body."""
     for name, code in kernels.items():
-        fills = [k for k, i in enumerate(code) if _fills(i)]
-        for k in fills:
-            assert not any(i.startswith("v_readfirstlane") for i in code[max(k - 3, 0):k]), (name, code[k - 3:k + 1])
-        assert sum(i.startswith("v_readfirstlane") for i in code) < 16, name
+        for k in (k for k, i in enumerate(code) if _fills(i)):
+            before = code[max(k - 12, 0):k]
+            assert not any(i.startswith("v_cmp_eq_u64") for i in before), (name, before)
+        assert sum(i.startswith("v_readfirstlane") for i in code) < 32, name
 
 
 def test_barriers_wait_for_fills(kernels):

@@ -102,6 +102,16 @@ def _backward_size(*args):
     return size("rope_norm_backward_workspace_size", *args)
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_plan(q, q_stride, qo_stride, q_place, k, k_stride, ko_stride, k_place, R, eps, magnitude,
+               layout, dtype):
+    """(problem, q's description, k's) of shapes, strides and (type of positions, batched), in one
+    look: a call of a few microseconds is bound by the host."""
+    return (_problem(q[3], R, eps, magnitude, layout, dtype, 0),
+            _tensor(q, q_stride, qo_stride, *q_place, "q"),
+            None if k is None else _tensor(k, k_stride, ko_stride, *k_place, "k"))
+
+
 def _check_heads(x, name):
     if not isinstance(x, torch.Tensor) or x.dim() != 4:
         raise ValueError(f"{name} must be a [batch, tokens, heads, head_dim] tensor")
@@ -192,26 +202,29 @@ def rope_norm_forward(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Opti
     _sides(q, k)
     dev, dtype, shape = q.device, q.dtype, q.shape
     pf = _frequencies(freqs, dev)
-    prob = _problem(shape[3], 2 * freqs.shape[0], float(eps), float(magnitude), layout, dtype, 0)
     pq = _need_heads(q, "q", dtype, dev)
     pw = _weight(q_weight, "q_weight", dev, shape[3])
-    pp, kind, batched = _place(q_positions, "q_positions", shape, dev)
+    pp, *place = _place(q_positions, "q_positions", shape, dev)
+    place = tuple(place)
     q_out = _result(q_out, "q_out", q)
-    tq = _tensor(shape, q.stride(), q_out.stride(), kind, batched, "q")
     if k is None:
+        prob, tq, _ = _norm_plan(shape, q.stride(), q_out.stride(), place, None, None, None, None,
+                                 2 * freqs.shape[0], float(eps), float(magnitude), layout, dtype)
         call("rope_norm_forward", dev, prob, tq, pq, pp, pw, q_out.data_ptr(), None, None, None, None,
              None, pf)
         return q_out, None
-    shape = k.shape
+    ks = k.shape
     pk = _need_heads(k, "k", dtype, dev)
-    pkw = _weight(k_weight, "k_weight", dev, shape[3])
-    if k_positions is not q_positions or shape[:2] != q.shape[:2]:
-        pp_k, kind, batched = _place(k_positions, "k_positions", shape, dev)
+    pkw = _weight(k_weight, "k_weight", dev, ks[3])
+    if k_positions is q_positions and ks[:2] == shape[:2]:
+        pkp, k_place = pp, place
     else:
-        pp_k = pp
+        pkp, *k_place = _place(k_positions, "k_positions", ks, dev)
+        k_place = tuple(k_place)
     k_out = _result(k_out, "k_out", k)
-    tk = _tensor(shape, k.stride(), k_out.stride(), kind, batched, "k")
-    call("rope_norm_forward", dev, prob, tq, pq, pp, pw, q_out.data_ptr(), tk, pk, pp_k, pkw,
+    prob, tq, tk = _norm_plan(shape, q.stride(), q_out.stride(), place, ks, k.stride(), k_out.stride(),
+                              k_place, 2 * freqs.shape[0], float(eps), float(magnitude), layout, dtype)
+    call("rope_norm_forward", dev, prob, tq, pq, pp, pw, q_out.data_ptr(), tk, pk, pkp, pkw,
          k_out.data_ptr(), pf)
     return q_out, k_out
 

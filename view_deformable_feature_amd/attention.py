@@ -4,9 +4,9 @@
 Queries are [B, Nq, H, D], keys and values [B, Nk, Hk, D] with H a multiple of Hk: the layout
 that a projection's output has once its last dimension is seen as heads, so views of one
 projection for queries, keys and values go in as they are (their heads' numbers have to be
-consecutive, their strides multiples of 16 bytes; so for results that are given).  ``kv_lens`` [B] int32 says how many keys
-of each batch entry count, ``key_mask`` [B, Nk] bool which of them; a query that sees no key
-gets 0 and an lse of -inf.
+consecutive, their strides multiples of 16 bytes; so for results that are given).  ``kv_lens`` [B]
+int32 says how many keys of each batch entry count, ``key_mask`` [B, Nk] bool which of them; a query
+that sees no key gets 0 and an lse of -inf.
 
 Only metadata checks and pointer passing happen here; every step runs in the HIP
 kernels of libdeformagg.

@@ -1,4 +1,5 @@
-// Internal launch description of the attention kernels (attn_forward.hip, attn_grad.hip), filled by the host API (attn_api.cpp).  Not part of the public ABI.
+// Internal launch description of the attention kernels (attn_forward.hip, attn_grad.hip), filled by
+// the host API (attn_api.cpp).  Not part of the public ABI.
 //
 // Rows are the queries of the heads that share a key head: row r of a (batch entry, key head)
 // is query r / group of its head r % group.

@@ -16,11 +16,12 @@
  * batch entry as its serving form.
  *
  * Products of 16-bit types are exact and add up in binary32; scores, maxima, sums and results
- * under way are binary32, and a 16-bit result is rounded once to nearest even.  In 16 bits the
- * weights are rounded to q's type (bfloat16, binary16) before they multiply v, and in the
- * gradients so are p and p (dP - delta): a share of at most half a step of each term, the same as
- * the rounding of the result.  With at most 32 rows (queries times heads to a key head) weights
- * are carried in twice the digits.
+ * under way are binary32, and a 16-bit result is rounded once to nearest even.  Weights come from
+ * the scores' differences, so that large scores (within binary32 before `scale`) give weights as
+ * small ones do.  In 16 bits the weights are rounded to q's type (bfloat16, binary16) before they
+ * multiply v, and in the gradients so are p and p (dP - delta): a share of at most half a step of
+ * each term, the same as the rounding of the result.  With at most 32 rows (queries times heads to
+ * a key head) weights are carried in twice the digits.
  *
  * Conventions of the library (see deformagg.h): the caller owns every buffer, calls
  * are asynchronous on `stream` and may be captured into a HIP graph, every check runs

@@ -184,6 +184,103 @@ def test_small_and_large_gradients_in_binary16():
     _check(q, (k / 64).to(F16), (v * 100).to(F16), (go * 200).to(F16))
 
 
+# Queries 256 2^n and, in their second place, 1; keys with as much in the first place and a step of their
+# own in the second: scores of 2^n, exact in binary32, that differ by whole steps.
+def _far_inputs(shape, dtype, level, seed, step=1.0):
+    """(q, k, v, scores [B, H, Nq, Nk] in 64 bits) of scores about 2^level at a scale of 1."""
+    B, Nq, Nk, H, Hk, D = shape
+    gen = torch.Generator().manual_seed(seed)
+    q = torch.zeros((B, Nq, H, D))
+    k = torch.zeros((B, Nk, Hk, D))
+    q[..., 0] = 2.0 ** (level // 2)
+    k[..., 0] = 2.0 ** (level - level // 2)
+    q[..., 1] = 1
+    k[..., 1] = torch.randint(0, 9, (B, Nk, Hk), generator=gen) * step
+    v = torch.randn((B, Nk, Hk, D), generator=gen).to(dtype)
+    s = q.double().transpose(1, 2) @ k.double().repeat_interleave(H // Hk, 2).permute(0, 2, 3, 1)
+    return q.to(dtype).cuda(), k.to(dtype).cuda(), v.cuda(), s
+
+
+def _far_levels():
+    """Up to where binary16 reaches, 2^15 times 2^15; steps of a unit of the scores' last place in
+    binary32, 1 at least."""
+    for dtype, most in ((F32, 60), (BF16, 60), (F16, 30)):
+        for level in (12, 19, 21, 25, 30, 60):
+            if level <= most:
+                yield pytest.param(dtype, level, max(1.0, 2.0 ** (level - 23)),
+                                   id=f"{str(dtype)[6:]}-{level}")
+
+
+@pytest.mark.parametrize("dtype, level, step", _far_levels())
+@pytest.mark.parametrize("shape", [(2, 3, 90, 4, 2, 32), (1, 2, 9000, 3, 3, 64), (2, 140, 190, 64, 64, 128),
+                                   (2, 200, 1000, 20, 20, 64), (1, 1, 1, 1, 1, 8)],
+                         ids=["few", "few_split", "wide", "wide_split", "one_key"])
+@pytest.mark.parametrize("sign", [1, -1], ids=["up", "down"])
+def test_far_scores(dtype, level, step, shape, sign):
+    """Scores of 2^12 to 2^60, by whole steps apart: the weights are those of the differences, d.
+    Scores are exact here, so what is off is the scale in base 2 (u), the difference's product (u) and
+    the exponential (2 u): a weight by (2 d + 3) u of itself, d p at most p (d + 1); in 16 bits by its
+    rounding h too, or with 32 rows to a key head by h^2 (binary16: 2^-31 of v); the sums by (n + 32) u."""
+    say(f"[attn] far {dtype} 2^{level} {shape} {sign}")
+    q, k, v, s = _far_inputs(shape, dtype, level, 301, step)
+    q = q * sign
+    s = s * sign
+    out, lse = vdf.attn_forward(q, k, v, scale=1.0)
+    torch.cuda.synchronize()
+    B, Nq, Nk, H, Hk, D = shape
+    d = s.amax(-1, keepdim=True) - s
+    p = torch.exp(-d) / torch.exp(-d).sum(-1, keepdim=True)
+    x = v.cpu().double().repeat_interleave(H // Hk, 2).transpose(1, 2)
+    want = p @ x
+    u, h = 2.0 ** -24, 0.0 if dtype == F32 else 2.0 ** {BF16: -8, F16: -11}[dtype]
+    hw = h * h if Nq * (H // Hk) <= 32 else h
+    off = p * ((4 * d + 6 + 2 * (Nk + 32)) * u + hw)
+    tol = off @ x.abs() + (2.0 ** -31 if dtype == F16 else 0.0) * x.abs().sum(2, keepdim=True)
+    check("out", out.transpose(1, 2), want, tol * (1 + h) + h * want.abs() + 2.0 ** -126)
+    top = s.amax(-1) + torch.exp(-d).sum(-1).log()
+    check("lse", lse, top, top.abs() * 6 * u + (Nk + 32) * u)
+
+
+@pytest.mark.parametrize("Nq", [3, 300])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_that_pass_binary32_once_scaled(Nq, sign):
+    """Products of 8 to 90 at a scale of 2^126: the largest alone has weight, lse is infinite."""
+    q, k, v, _, _, _ = _inputs((2, Nq, 83, 4, 4, 32), F32, 303)
+    q[:], k[:] = 0, 0
+    q[..., 0] = sign
+    k[..., 0] = torch.arange(8, 91, device="cuda")[:, None]
+    out, lse = vdf.attn_forward(q, k, v, scale=2.0 ** 126)
+    torch.cuda.synchronize()
+    assert torch.equal(out, v[:, 82 if sign > 0 else 0][:, None].expand(out.shape))
+    assert (lse == sign * math.inf).all()
+
+
+@TYPES
+def test_far_scores_beside_near_ones(dtype):
+    """Rows of scores past 2^20, of ordinary ones and of a growing one in one tile of rows, keys that
+    grow along the tiles; and an entry whose keys are all invisible."""
+    B, Nq, Nk, D = 2, 150, 700, 32
+    for H, rows in ((60, Nq), (2, 5)):
+        q, k, v, _, _, _ = _inputs((B, rows, Nk, H, H, D), dtype, 302)
+        q[..., 0] = 0
+        q[:, ::3, :, 0] = 2.0 ** 14
+        q[:, ::3, :, 1:] = 0
+        k[..., 0] = (torch.arange(Nk, device="cuda") // 50 * 8 + 2.0 ** 12)[:, None].to(dtype)
+        kv = torch.tensor([Nk, 0], dtype=torch.int32, device="cuda")
+        out, lse = vdf.attn_forward(q, k, v, kv, scale=0.5)
+        torch.cuda.synchronize()
+        ref = Attention(q[:, 1::3], k, v, kv, scale=0.5)
+        ref.check_forward(out[:, 1::3], lse[..., 1::3])
+        # the steps are far apart: the last one's keys share the weight
+        first = 650 if dtype != BF16 else int((k[0, :, 0, 0] == k[0, -1, 0, 0]).nonzero()[0])
+        n = Nk - first
+        mean = v[0, first:].double().mean(0).cpu()
+        h = {F32: 0.0, BF16: 2.0 ** -8, F16: 2.0 ** -11}[dtype]
+        tol = v[0, first:].double().abs().mean(0).cpu() * ((2 * n + 70) * 2.0 ** -24) + h * mean.abs() + 2.0 ** -30
+        check("far", out[0, ::3], mean.expand(out[0, ::3].shape), tol)
+        assert (out[1] == 0).all() and (lse[1] == -math.inf).all()
+
+
 @pytest.mark.parametrize("scale", [0.01, 0.5, 3.0])
 def test_scale(scale):
     for dtype in (F32, BF16):

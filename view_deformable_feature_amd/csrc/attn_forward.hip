@@ -5,7 +5,8 @@
 // of a tile's scores s (keys by queries) a column keeps its maximum m and
 // sum l, its weights are 2^(s scale / log 2 - m), and the result, [numbers, queries], is scaled
 // again only when a maximum grows by more than 2^8, which is rare after the first tiles and
-// costs no digits in binary32.
+// costs no digits in binary32.  Where m is so large that its own rounding would count in the
+// weights, scores are taken less the largest one before they are scaled (kFar, below).
 //
 // Many rows: four waves of 32 columns and tiles of 64 keys, the next tile on its way while one is
 // used; two workgroups to a compute unit, so that one wave's exponentials run beside another's
@@ -29,11 +30,19 @@ template <typename T>
 constexpr float kLiftLog2 = std::is_same<T, _Float16>::value ? 7.0f : 0.0f;
 constexpr float kGrowth = 8.0f;
 
+// Maxima from here on, in base 2, are far: m, rounded to binary32, is off by up to 2^-4 there and
+// by 2^7 at 2^32, where weights would be infinite or 0.  A wave that meets one takes its scores less
+// their column's largest from then on, which is exact where it matters; the others pay a
+// comparison when a maximum grows and a branch for each tile (one token on 1500 keys 9.8 -> 10.1
+// us, 2 x 4096 rows on 8192 keys 503 -> 507).
+constexpr float kFar = 0x1p20f;
+
 // A column's running maximum and sum, and what exponents are less by.
 struct Running {
     float top = -kInf, shift = 0.0f, sum = 0.0f;
-    // Scores of NB blocks become weights, 2^(s scale2 - shift), after the results so far are scaled
-    // to a new maximum where one has grown.
+    bool far = false;    // of the wave; shift is then -kLiftLog2 alone
+    // Scores of NB blocks become weights, 2^(s scale2 - shift), far ones 2^((s - top) scale2 - shift),
+    // after the results so far are scaled to a new maximum where one has grown.
     template <typename T, int NB, int ND>
     __device__ __forceinline__ void weigh(f32x16 (&s)[NB], f32x16 (&acc)[ND], float scale2, float growth) {
         float big = -kInf;
@@ -42,10 +51,16 @@ struct Running {
 #pragma unroll
             for (int i = 0; i < 16; ++i) big = fmaxf(big, s[n][i]);
         big = column_max(big);
-        if (__any(big > top + growth)) {
+        // (a unit of a far maximum's last place may be more than `growth`)
+        if (__any(big > top + (far ? 0.0f : growth))) {
             const float now = fmaxf(top, big);
-            const float to = now == -kInf ? 0.0f : fmaf(now, scale2, -kLiftLog2<T>);
-            const float change = top == -kInf ? 0.0f : __builtin_amdgcn_exp2f(shift - to);
+            float to = now == -kInf ? 0.0f : fmaf(now, scale2, -kLiftLog2<T>), less = shift - to;
+            if (__builtin_expect(far || __any(fabsf(to) >= kFar), false)) {
+                less = far ? (top - now) * scale2 : kLiftLog2<T> - fmaf(now, scale2, -shift);
+                to = now == -kInf ? 0.0f : -kLiftLog2<T>;
+                far = true;
+            }
+            const float change = top == -kInf ? 0.0f : __builtin_amdgcn_exp2f(less);
             top = now;
             shift = to;
             sum *= change;
@@ -53,6 +68,13 @@ struct Running {
             for (int d = 0; d < ND; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[d][i] *= change;
+        }
+        if (__builtin_expect(far, false)) {
+            const float base = top == -kInf ? 0.0f : top;
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[n][i] -= base;
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -65,6 +87,48 @@ struct Running {
             sum += part[0] + part[1];
         }
     }
+    // What is kept of a column whose weights add up to `all` and that others' parts join.
+    __device__ __forceinline__ float2 part(float all) const {
+        if (top == -kInf) return make_float2(-kInf, all);
+        return far ? make_float2(top, -all) : make_float2(shift, all);
+    }
+};
+
+// Parts of a column that meet, each (shift, sum) or, of a far one, (top, -sum): the largest of what
+// they are less by, or, if one is far, their largest score, and what each counts for.
+template <typename T>
+struct Meet {
+    float most = -kInf;
+    bool far = false;
+    // `at(n)` is the n-th part of `count`
+    template <class At>
+    __device__ __forceinline__ Meet(int count, At at, float scale2) {
+        float least = 0.0f;
+#pragma unroll
+        for (int n = 0; n < count; ++n) {
+            most = fmaxf(most, at(n).x);
+            least = fminf(least, at(n).y);
+        }
+        if (__builtin_expect(least < 0.0f, false)) {
+            far = true;
+            most = -kInf;
+            for (int n = 0; n < count; ++n) {
+                const float2 p = at(n);
+                const float score = p.y < 0.0f || p.x == -kInf ? p.x : (p.x + kLiftLog2<T>) / scale2;
+                most = fmaxf(most, p.y < 0.0f ? score : fminf(score, FLT_MAX));
+            }
+        }
+        most = most == -kInf ? 0.0f : most;
+    }
+    __device__ __forceinline__ float share(float2 p, float scale2) const {
+        if (p.x == -kInf) return 0.0f;
+        float e = p.x - most;
+        if (__builtin_expect(far, false)) e = p.y < 0.0f ? e * scale2 : kLiftLog2<T> - fmaf(most, scale2, -p.x);
+        return __builtin_amdgcn_exp2f(e);
+    }
+    __device__ __forceinline__ float lse(float sum, float scale2) const {
+        return sum == 0.0f ? -kInf : fmaf(far ? fmaf(most, scale2, -kLiftLog2<T>) : most, kLn2, logf(sum));
+    }
 };
 
 template <int ND>
@@ -73,10 +137,6 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[ND]) {
     for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
-}
-
-__device__ __forceinline__ float lse_of(float shift, float sum) {
-    return sum == 0.0f ? -kInf : fmaf(shift, kLn2, logf(sum));
 }
 
 // Waves to a SIMD that the registers leave room for.
@@ -152,13 +212,16 @@ __global__ __launch_bounds__(kAttnThreads, kForwardWaves<T>) void attn_forward_k
     if (!there) return;
     if (a.splits > 1) {
         const int64_t line = ((int64_t)spot.split * a.B * a.Hk + spot.unit) * a.rows + r;
-        if (half == 0) a.part_stat[line] = make_float2(run.shift, sum);
+        if (half == 0) a.part_stat[line] = run.part(sum);
         store_column<float, ND>(a.part + line * a.D, a.D, half, acc, 1.0f);
         return;
     }
     char* out = static_cast<char*>(a.out) + b * a.o_batch + query * a.o_token + head * a.o_head;
     store_column<T, ND>(reinterpret_cast<T*>(out), a.D, half, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
-    if (a.lse && half == 0) a.lse[((int64_t)b * a.H + head) * a.Nq + query] = lse_of(run.shift, sum);
+    if (a.lse && half == 0) {
+        const float less = run.far ? fmaf(run.top, a.scale2, -kLiftLog2<T>) : run.shift;
+        a.lse[((int64_t)b * a.H + head) * a.Nq + query] = sum == 0.0f ? -kInf : fmaf(less, kLn2, logf(sum));
+    }
 }
 
 // ---- few rows ----------------------------------------------------------------------------
@@ -258,11 +321,11 @@ void attn_few_kernel(AttnArgs a) {
         while (turn(ka, va, kb, vb) && turn(kb, vb, ka, va)) {}
     }
 
-    // The waves' parts meet at their largest exponent.  A wave's place has DP numbers to a column, in
+    // The waves' parts meet.  A wave's place has DP numbers to a column, in
     // fours, turned by the column so that 32 columns' equal fours spread over the banks.
     const float part = column_sum(run.sum);
     __syncthreads();
-    if (half == 0) stat[wave * 32 + col] = make_float2(run.top == -kInf ? -kInf : run.shift, part);
+    if (half == 0) stat[wave * 32 + col] = run.part(part);
     constexpr int kFours = DP / 4, kPlace = 32 * kFours;   // of 16 bytes
     constexpr int kHere = WAVES * Tl::kPieces / kPlace;    // waves that k0 has room for
     static_assert(2 * kHere >= WAVES, "k0 and v0 hold every wave's part");
@@ -282,22 +345,20 @@ void attn_few_kernel(AttnArgs a) {
     const int rows = min(a.rows - r0, kAttnFew), vectors = a.D / 4;
     for (int n = threadIdx.x; n < rows * vectors; n += 64 * WAVES) {
         const int c = n / vectors, v = n % vectors;
-        float most = -kInf, sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) most = fmaxf(most, stat[w * 32 + c].x);
-        most = most == -kInf ? 0.0f : most;
+        const Meet<T> meet(WAVES, [&](int w) { return stat[w * 32 + c]; }, a.scale2);
+        float sum = 0.0f;
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             const float2 s = stat[w * 32 + c];
-            const float f = s.x == -kInf ? 0.0f : __builtin_amdgcn_exp2f(s.x - most);
-            sum = fmaf(s.y, f, sum);
+            const float f = meet.share(s, a.scale2);
+            sum = fmaf(fabsf(s.y), f, sum);
             x += place(w)[c * kFours + (v ^ (c & 7))] * f;
         }
         const int row = r0 + c;
         if (a.splits > 1) {
             const int64_t line = ((int64_t)spot.split * a.B * a.Hk + spot.unit) * a.rows + row;
-            if (v == 0) a.part_stat[line] = make_float2(most, sum);
+            if (v == 0) a.part_stat[line] = make_float2(meet.most, meet.far ? -sum : sum);
             *reinterpret_cast<f32x4*>(a.part + line * a.D + v * 4) = x;
             continue;
         }
@@ -307,7 +368,7 @@ void attn_few_kernel(AttnArgs a) {
         const float result[4] = {x[0] * inverse, x[1] * inverse, x[2] * inverse, x[3] * inverse};
         char* out = static_cast<char*>(a.out) + b * a.o_batch + query * a.o_token + head * a.o_head;
         store_as(reinterpret_cast<T*>(out) + v * 4, result);
-        if (a.lse && v == 0) a.lse[((int64_t)b * a.H + head) * a.Nq + query] = lse_of(most, sum);
+        if (a.lse && v == 0) a.lse[((int64_t)b * a.H + head) * a.Nq + query] = meet.lse(sum, a.scale2);
     }
 }
 
@@ -320,7 +381,7 @@ void attn_few_kernel(AttnArgs a) {
 template <typename T>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int threads) {
     __shared__ float2 stat[kAttnThreads];
-    __shared__ f32x4 meet[kAttnThreads];
+    __shared__ f32x4 fours[kAttnThreads];
     const int64_t units = (int64_t)a.B * a.Hk, lines = units * a.rows;
     const int t = threadIdx.x % threads, base = threadIdx.x - t;
     const int64_t line = (int64_t)blockIdx.x * (kAttnThreads / threads) + threadIdx.x / threads;
@@ -336,29 +397,28 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
     const int vectors = a.D / 4, abreast = threads / vectors, at = t % vectors * 4;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     __syncthreads();
-    float most = -kInf, sum = 0.0f;
-    for (int s = 0; s < splits; ++s) most = fmaxf(most, stat[base + s].x);
-    most = most == -kInf ? 0.0f : most;
-    const auto weight = [&](float2 p) { return p.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(p.x - most); };
-    for (int s = 0; s < splits; ++s) sum = fmaf(stat[base + s].y, weight(stat[base + s]), sum);
+    const Meet<T> meet(splits, [&](int s) { return stat[base + s]; }, a.scale2);
+    const auto share = [&](int s) { return meet.share(stat[base + s], a.scale2); };
+    float sum = 0.0f;
+    for (int s = 0; s < splits; ++s) sum = fmaf(fabsf(stat[base + s].y), share(s), sum);
     if (t < abreast * vectors) {
 #pragma unroll 8
         for (int s = t / vectors; s < splits; s += abreast) {
             const f32x4 p = *reinterpret_cast<const f32x4*>(a.part + (s * lines + line) * a.D + at);
-            v += p * weight(stat[base + s]);
+            v += p * share(s);
         }
     }
-    meet[threadIdx.x] = v;
+    fours[threadIdx.x] = v;
     __syncthreads();
     if (!there || t >= vectors) return;
-    for (int i = 1; i < abreast; ++i) v += meet[threadIdx.x + i * vectors];
+    for (int i = 1; i < abreast; ++i) v += fours[threadIdx.x + i * vectors];
     const float inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
     const float result[4] = {v[0] * inverse, v[1] * inverse, v[2] * inverse, v[3] * inverse};
     const int query = (uint32_t)r / (uint32_t)a.group, head = hk * a.group + (uint32_t)r % (uint32_t)a.group;
     char* out = static_cast<char*>(a.out) + b * a.o_batch + query * a.o_token + head * a.o_head;
     store_as(reinterpret_cast<T*>(out) + at, result);
     if (a.lse && at == 0)
-        a.lse[((int64_t)b * a.H + head) * a.Nq + query] = lse_of(most, sum);
+        a.lse[((int64_t)b * a.H + head) * a.Nq + query] = meet.lse(sum, a.scale2);
 }
 
 template <typename T, int DP>

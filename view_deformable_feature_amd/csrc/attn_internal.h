@@ -33,7 +33,7 @@ struct AttnArgs {
     float* part;              // forward: [splits, B Hk, rows, D] results of a split's keys, not
                               // divided by their sums
     float2* part_stat;        // forward: [splits, B Hk, rows] (logarithm of base 2 that the
-                              // result is scaled by, sum)
+                              // result is scaled by, sum), or (largest score, -sum) of far ones
     float *part_k, *part_v;   // backward: [splits, B, Nk, Hk, D] (and part, [splits, B, Nq, H, D])
                               // gradients from a split's rows (keys)
     float* lse2;              // backward: [B, H, Nq] lse in base 2, +infinity for an empty row

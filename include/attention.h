@@ -95,7 +95,9 @@ DA_API da_status attn_backward_workspace_size(const attn_problem* problem, size_
  *   grad_k  = scale * sum over i and the heads of the key head of dS_j q[i],
  *   grad_v  = sum over i and the heads of the key head of p_j grad_out[i].
  *
- * Gradients of invisible keys and of queries without a visible key are 0.
+ * Gradients of invisible keys and of queries without a visible key are 0.  p is formed from lse,
+ * which has the digits of binary32: it is off by a share of up to |lse| 2^-22, and where |lse|
+ * passes 2^21 no more is known of it than that it is at most 1.
  *   out, lse   as attn_forward wrote them.
  *   grad_out   device [B, Nq, H, D] with grad_stride, 16-byte aligned.
  *   grad_q     device [B, Nq, H, D]; grad_k, grad_v device [B, Nk, Hk, D]; dense, 16-byte

@@ -241,6 +241,47 @@ def test_far_scores(dtype, level, step, shape, sign):
     check("lse", lse, top, top.abs() * 6 * u + (Nk + 32) * u)
 
 
+@pytest.mark.parametrize("dtype, level", [(F32, 15), (F32, 20), (F32, 23), (F32, 27), (F32, 34), (F32, 60),
+                                          (BF16, 20), (BF16, 34), (BF16, 60), (F16, 20), (F16, 23),
+                                          (F16, 26), (F16, 29)])
+@pytest.mark.parametrize("Nk", [1, 70])
+def test_gradients_of_far_scores(dtype, level, Nk):
+    """One key that takes all the weight, scores of +-2^level and up to twice as much.  p comes from
+    lse, which is rounded three times on its way to base 2: p is off by a share of at most
+    2^(3 u |lse| / log 2) - 1 and 8 u, above 2^22 it is only known to be within 1.  So are the terms of
+    grad_v, and with dP and delta the same but for their roundings grad_q and grad_k are next to nothing."""
+    say(f"[attn] gradients far {dtype} 2^{level} {Nk}")
+    B, Nq, H, D = 2, 90, 3, 16
+    gen = torch.Generator().manual_seed(304)
+    q, k, v, go, _, _ = _inputs((B, Nq, Nk, H, H, D), dtype, 305)
+    q[:], k[:] = 0, 0
+    x = (1 + torch.rand((B, Nq, H), generator=gen)) * 2.0 ** (level // 2)
+    q[..., 0] = (x * torch.where(torch.rand((B, Nq, H), generator=gen) < 0.5, -1.0, 1.0)).to(dtype).cuda()
+    k[..., 0] = 2.0 ** (level - level // 2) / 4          # of invisible keys beside one
+    k[:, -1, :, 0] = 2.0 ** (level - level // 2)
+    m = torch.zeros((B, Nk), dtype=torch.bool, device="cuda")
+    m[:, -1] = True
+    out, lse = vdf.attn_forward(q, k, v, None, m, 1.0)
+    dq, dk, dv = vdf.attn_backward(q, k, v, out, lse, go, None, m, 1.0)
+    torch.cuda.synchronize()
+    u, h = 2.0 ** -24, 0.0 if dtype == F32 else 2.0 ** {BF16: -8, F16: -11}[dtype]
+    # the key's weight, which need not be a power of two, times v, its inverse, and their product: 3 u
+    # (16 bits: the weight's rounding, h, and the result's)
+    x = v[:, -1:].cpu().double().expand(out.shape)
+    check("out", out, x, x.abs() * (3 * u + 2 * h))
+    g = go.cpu().double()
+    base2 = lse.cpu().double().abs().transpose(1, 2)[..., None] / math.log(2)
+    share = torch.exp2(3 * u * base2) - 1 + 8 * u
+    share = torch.where(base2 < 2.0 ** 22, share, 1.0)
+    tol = (g.abs() * (share + h + (Nq + 32) * u)).sum(1)
+    want = g.sum(1)
+    check("grad_v", dv[:, -1], want, tol * (1 + h) + h * want.abs() + 2.0 ** -24)
+    assert all(t.isfinite().all() for t in (dq, dk, dv)) and (dk[:, :-1] == 0).all() and (dv[:, :-1] == 0).all()
+    # dP - delta: two sums of D products
+    less = 2 * (D + 8) * u * (g.abs() * v[:, -1:].cpu().double().abs()).sum(-1, keepdim=True) * 2 * (1 + h)
+    check("grad_q", dq, torch.zeros_like(g), less * k[:, -1:].cpu().double().abs() + 2.0 ** -24)
+
+
 @pytest.mark.parametrize("Nq", [3, 300])
 @pytest.mark.parametrize("sign", [1, -1])
 def test_scores_that_pass_binary32_once_scaled(Nq, sign):

@@ -295,6 +295,13 @@ void attn_grad_kernel(AttnArgs of_q, AttnArgs of_kv, int q_blocks) {
 // ---- lse in base 2, and delta ------------------------------------------------------------
 //
 // Eight lanes to a row of out and grad_out, a run of 16-byte pieces in turn to each.
+//
+// On its way from the scores lse is rounded three times, here the last one, by u = 2^-24 of itself
+// each, so that a p that is 1 comes out as 2^(+-3 u |lse2|).  From 2^22 on that could pass what
+// binary16 holds, and later be infinite: there lse2 is raised by 4 u of itself (one more for this
+// rounding), and no p passes 1.
+constexpr float kFarLse = 0x1p22f;
+
 template <typename T>
 __global__ __launch_bounds__(kAttnThreads) void attn_delta_kernel(AttnArgs a) {
     constexpr int V = 16 / (int)sizeof(T);
@@ -320,7 +327,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_delta_kernel(AttnArgs a) {
     if (part != 0) return;
     const int64_t stat = (b * a.H + head) * a.Nq + query;
     const float lse = a.lse[stat];
-    a.lse2[stat] = lse == -kInf ? kInf : lse / kLn2;
+    float lse2 = lse / kLn2;
+    if (fabsf(lse2) >= kFarLse) lse2 += fabsf(lse2) * 0x1p-22f;
+    a.lse2[stat] = lse == -kInf ? kInf : lse2;
     a.delta[stat] = sum;
 }
 

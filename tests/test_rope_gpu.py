@@ -309,6 +309,29 @@ def test_autograd(dtype, wdtype, layout):
     check("x.grad", x.grad, want, rounded(8 * U * mag, want, dtype))
 
 
+@pytest.mark.parametrize("need", ["all", "weights", "k_weight"])
+def test_autograd_without_keys(need):
+    """k None, its weight a leaf all the same, as a module that holds both passes it: its gradient is
+    none, the others are those of the queries alone."""
+    gen = torch.Generator().manual_seed(244)
+    shape = (2, 25, 4, 32, 16)
+    q, g = _heads(shape, F32, gen), _heads(shape, F32, gen)
+    w, wk = ((torch.rand(32, generator=gen) + 0.5).cuda().requires_grad_(need != "k_weight" or n == 1)
+             for n in range(2))
+    q.requires_grad_(need == "all" or need == "k_weight")
+    f = _freqs(16)
+    y, none = vdf.norm_rotary(q, None, w, wk, f, None, None, EPS)
+    assert none is None
+    y.backward(g)
+    torch.cuda.synchronize()
+    (dx, tx), (dw, tw) = norm_rotate_grad(q, w, g, f, None, "half", EPS)
+    assert wk.grad is None
+    if q.requires_grad:
+        check("q.grad", q.grad, dx, tx)
+    if w.requires_grad:
+        check("w.grad", w.grad, dw, tw)
+
+
 def test_gradient_against_differences():
     """Along the gradient, the norm's own forward: a step of h = 2^-8 of unit length moves a row of
     root mean square near 1 by a third derivative of a few times the gradient's size."""

@@ -333,7 +333,7 @@ class NormRotaryFunction(torch.autograd.Function):
                                               *ctx.conf, need_weights=needs[2] or needs[3])
         return (dq if needs[0] else None, dk if needs[1] else None,
                 dqw.to(ctx.weight_dtypes[0]) if needs[2] else None,
-                dkw.to(ctx.weight_dtypes[1]) if needs[3] else None,
+                dkw.to(ctx.weight_dtypes[1]) if needs[3] and dkw is not None else None,
                 None, None, None, None, None, None)
 
 

@@ -82,7 +82,8 @@ DA_API da_status attn_forward(const attn_problem* problem, const void* q, const 
                               void* out, float* lse, void* workspace, size_t workspace_bytes,
                               void* stream);
 
-/* attn_backward_workspace_size -- bytes of device workspace attn_backward needs. */
+/* attn_backward_workspace_size -- bytes of device workspace attn_backward needs.  Refuses the
+ * problems that attn_backward does. */
 DA_API da_status attn_backward_workspace_size(const attn_problem* problem, size_t* bytes);
 
 /*
@@ -106,7 +107,8 @@ DA_API da_status attn_backward_workspace_size(const attn_problem* problem, size_
  *              part is written on its own: their sum is the gradient of the shared states.
  *   workspace  device scratch of attn_backward_workspace_size() bytes, 256-byte aligned;
  *              contents on entry do not matter.
- * Errors as attn_forward.
+ * Errors as attn_forward; the launch has a workgroup of 256 threads for each 128 rows, and for each
+ * 128 keys, of a batch entry's key head, and for each split of few.
  */
 DA_API da_status attn_backward(const attn_problem* problem, const void* q, const void* k,
                                const void* v, const void* out, const float* lse,

@@ -514,6 +514,29 @@ def test_long_cache():
         ref.check_forward(out[:, :, h:h + 1], lse[:, h:h + 1])
 
 
+def test_gradients_of_more_rows_than_threads():
+    """2^29 and 160 rows of 8 numbers, all but the first and last tokens' queries and gradients 0: their
+    gradients, and the keys', which are those of these tokens."""
+    Nq, Nk, H, D, n = (1 << 24) + 5, 70, 32, 8, 40
+    gen = torch.Generator().manual_seed(110)
+    q, go = (torch.zeros((1, Nq, H, D), dtype=BF16, device="cuda") for _ in range(2))
+    for t in (q, go):
+        t[:, :n] = torch.randn((1, n, H, D), generator=gen).to(BF16).cuda()
+        t[:, -n:] = torch.randn((1, n, H, D), generator=gen).to(BF16).cuda()
+    k, v = (torch.randn((1, Nk, H, D), generator=gen).to(BF16).cuda() for _ in range(2))
+    out, lse = vdf.attn_forward(q, k, v)
+    grads = vdf.attn_backward(q, k, v, out, lse, go)
+    torch.cuda.synchronize()
+
+    def ends(t, dim=1):
+        return torch.cat([t.narrow(dim, 0, n), t.narrow(dim, Nq - n, n)], dim)
+
+    ref = Attention(ends(q), k, v)
+    ref.check_forward(ends(out), ends(lse, 2))
+    ref.check_backward((ends(grads[0]), *grads[1:]), ends(go))
+    assert not grads[0][:, n:-n].any()
+
+
 def test_one_device_at_a_time():
     q, k, v, _, kv, m = _inputs((2, 3, 9, 2, 1, 16), F32, 108, True, True)
     with pytest.raises(ValueError, match="GPU"):

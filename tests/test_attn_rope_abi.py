@@ -156,6 +156,33 @@ def test_attention_workspaces(lib):
     assert lib.attn_backward(ref(_attn(batch=0)), *[None] * 12, 0, None) == 0
 
 
+BIG = [dict(batch=1, queries=1 << 20, keys=600, heads=8, key_heads=8, head_dim=128, dtype=1),
+       dict(batch=1, queries=1 << 20, keys=600, heads=8, key_heads=1, head_dim=128, dtype=1),
+       dict(batch=1, queries=5, keys=5 << 20, heads=1, key_heads=1, head_dim=128, dtype=0),
+       dict(batch=1, queries=1 << 25, keys=7, heads=32, key_heads=32, head_dim=8, dtype=2)]
+
+
+@pytest.mark.parametrize("kw", BIG)
+def test_attention_gradients_of_what_the_forward_takes(lib, kw):
+    """Many rows or keys, one side split: neither the query nor the call refuses the sizes (both are
+    asked with a workspace of nothing, which is)."""
+    far, n = 1 << 55, ctypes.c_size_t(0)
+    p = _attn(**kw, **{s + "_stride": _dense(8, kw["key_heads" if s in "kv" else "heads"], kw["head_dim"])
+                       for s in ("q", "k", "v", "out", "grad")})
+    assert lib.attn_forward_workspace_size(ref(p), ref(n)) == 0
+    assert lib.attn_backward_workspace_size(ref(p), ref(n)) == 0 and n.value > 0
+    assert _bwd(lib, p, gq=far, gk=2 * far, gv=3 * far, n=0) == 1
+    assert f"{n.value} needed" in _msg(lib)
+
+
+def test_attention_workspace_query_refuses_what_the_call_does(lib):
+    p = _attn(batch=1 << 15, queries=1 << 22, heads=1, key_heads=1, keys=8, head_dim=8,
+              **{n + "_stride": _dense(8 if n in "kv" else 1 << 22, 1, 8)
+                 for n in ("q", "k", "v", "out", "grad")})
+    assert lib.attn_backward_workspace_size(ref(p), ref(ctypes.c_size_t(0))) == 2
+    assert "workgroups" in _msg(lib)
+
+
 def _rope(**kw):
     d = dict(head_dim=32, rotated=16, eps=1e-6, magnitude=1.0, layout=0, dtype=0, flags=0, reserved=0)
     d.update(kw)

@@ -178,6 +178,19 @@ da_status count_blocks(da::AttnArgs& a) {
     return DA_OK;
 }
 
+// Both kinds of gradients' splits and workgroups, of one launch.  What their joins and delta's launch
+// take sets no limit of its own: sides that are split have at most 256 workgroups' columns, and
+// delta's workgroups walk over the rows.
+da_status plan_backward(da::AttnArgs& of_q, da::AttnArgs& of_kv) {
+    choose_grad_q(of_q);
+    choose_grad_kv(of_kv);
+    da_status st = count_blocks(of_q);
+    if (st == DA_OK) st = count_blocks(of_kv);
+    if (st == DA_OK && (wide)of_q.blocks + of_kv.blocks + 16 >= (wide(1) << 32) / da::kAttnThreads)
+        st = report_error(DA_ERR_UNSUPPORTED, "2^32 threads of workgroups or more");
+    return st;
+}
+
 uint64_t stat_bytes(const da::AttnArgs& a) {
     return part_bytes((uint64_t)a.splits * a.B * a.Hk * a.rows * sizeof(float2));
 }
@@ -283,13 +296,13 @@ da_status attn_forward(const attn_problem* p, const void* q, const void* k, cons
 
 da_status attn_backward_workspace_size(const attn_problem* p, size_t* bytes) {
     if (!bytes) return report_error(DA_ERR_INVALID_ARG, "bytes is NULL");
-    const da_status st = check_problem(p);
+    da_status st = check_problem(p);
     if (st != DA_OK) return st;
     da::AttnArgs a;
     describe(p, a);
     da::AttnArgs of_kv = a;
-    choose_grad_q(a);
-    choose_grad_kv(of_kv);
+    st = plan_backward(a, of_kv);
+    if (st != DA_OK) return st;
     *bytes = (size_t)(2 * row_bytes(a) + part_q_bytes(a) + 2 * part_k_bytes(of_kv));
     return DA_OK;
 }
@@ -342,17 +355,8 @@ da_status attn_backward(const attn_problem* p, const void* q, const void* k, con
     of_q.lse2 = reinterpret_cast<float*>(base);
     of_q.delta = reinterpret_cast<float*>(base + row_bytes(of_q));
     da::AttnArgs of_kv = of_q;
-    choose_grad_q(of_q);
-    choose_grad_kv(of_kv);
-    st = count_blocks(of_q);
-    if (st == DA_OK) st = count_blocks(of_kv);
+    st = plan_backward(of_q, of_kv);
     if (st != DA_OK) return st;
-    if ((wide)of_q.blocks + of_kv.blocks + 16 >= (wide(1) << 32) / da::kAttnThreads)
-        return report_error(DA_ERR_UNSUPPORTED, "2^32 threads of workgroups or more");
-    const wide numbers = (wide)of_q.B * of_q.Nq * of_q.H * of_q.D + 2 * (wide)of_q.B * of_q.Nk * of_q.Hk * of_q.D;
-    if ((wide)of_q.B * of_q.Nq * of_q.H * 8 >= wide(1) << 32 ||
-        ((of_q.splits > 1 || of_kv.splits > 1) && numbers * 4 >= wide(1) << 32))
-        return report_error(DA_ERR_UNSUPPORTED, "2^29 rows or more");
     const uint64_t need = 2 * row_bytes(of_q) + part_q_bytes(of_q) + 2 * part_k_bytes(of_kv);
     st = check_workspace(need, workspace, workspace_bytes);
     if (st != DA_OK) return st;

@@ -294,7 +294,8 @@ void attn_grad_kernel(AttnArgs of_q, AttnArgs of_kv, int q_blocks) {
 
 // ---- lse in base 2, and delta ------------------------------------------------------------
 //
-// Eight lanes to a row of out and grad_out, a run of 16-byte pieces in turn to each.
+// Eight lanes to a row of out and grad_out, a run of 16-byte pieces in turn to each.  Workgroups walk
+// over the rows where there are more than a launch has threads for.
 //
 // On its way from the scores lse is rounded three times, here the last one, by u = 2^-24 of itself
 // each, so that a p that is 1 comes out as 2^(+-3 u |lse2|).  From 2^22 on that could pass what
@@ -304,33 +305,35 @@ constexpr float kFarLse = 0x1p22f;
 
 template <typename T>
 __global__ __launch_bounds__(kAttnThreads) void attn_delta_kernel(AttnArgs a) {
-    constexpr int V = 16 / (int)sizeof(T);
-    const int64_t line = ((int64_t)blockIdx.x * kAttnThreads + threadIdx.x) / 8;
+    constexpr int V = 16 / (int)sizeof(T), kRows = kAttnThreads / 8;
     const int part = threadIdx.x % 8;
-    if (line >= (int64_t)a.B * a.Nq * a.H) return;
-    const int64_t bq = line / a.H, b = bq / a.Nq, query = bq % a.Nq;
-    const int head = (int)(line % a.H);
-    const T* o = reinterpret_cast<const T*>(static_cast<const char*>(a.out) + b * a.o_batch +
-                                            query * a.o_token + head * a.o_head);
-    const T* g = reinterpret_cast<const T*>(static_cast<const char*>(a.grad_out) + b * a.g_batch +
-                                            query * a.g_token + head * a.g_head);
-    float sum = 0.0f;
-    for (int at = part * V; at < a.D; at += 8 * V) {
-        float x[V], y[V];
-        load_as(o + at, x);
-        load_as(g + at, y);
+    const int64_t lines = (int64_t)a.B * a.Nq * a.H;
+    for (int64_t line = (int64_t)blockIdx.x * kRows + threadIdx.x / 8; line < lines;
+         line += (int64_t)gridDim.x * kRows) {
+        const int64_t bq = line / a.H, b = bq / a.Nq, query = bq % a.Nq;
+        const int head = (int)(line % a.H);
+        const T* o = reinterpret_cast<const T*>(static_cast<const char*>(a.out) + b * a.o_batch +
+                                                query * a.o_token + head * a.o_head);
+        const T* g = reinterpret_cast<const T*>(static_cast<const char*>(a.grad_out) + b * a.g_batch +
+                                                query * a.g_token + head * a.g_head);
+        float sum = 0.0f;
+        for (int at = part * V; at < a.D; at += 8 * V) {
+            float x[V], y[V];
+            load_as(o + at, x);
+            load_as(g + at, y);
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum = fmaf(x[e], y[e], sum);
+            for (int e = 0; e < V; ++e) sum = fmaf(x[e], y[e], sum);
+        }
+#pragma unroll
+        for (int m = 1; m < 8; m *= 2) sum += __shfl_xor(sum, m);
+        if (part != 0) continue;
+        const int64_t stat = (b * a.H + head) * a.Nq + query;
+        const float lse = a.lse[stat];
+        float lse2 = lse / kLn2;
+        if (fabsf(lse2) >= kFarLse) lse2 += fabsf(lse2) * 0x1p-22f;
+        a.lse2[stat] = lse == -kInf ? kInf : lse2;
+        a.delta[stat] = sum;
     }
-#pragma unroll
-    for (int m = 1; m < 8; m *= 2) sum += __shfl_xor(sum, m);
-    if (part != 0) return;
-    const int64_t stat = (b * a.H + head) * a.Nq + query;
-    const float lse = a.lse[stat];
-    float lse2 = lse / kLn2;
-    if (fabsf(lse2) >= kFarLse) lse2 += fabsf(lse2) * 0x1p-22f;
-    a.lse2[stat] = lse == -kInf ? kInf : lse2;
-    a.delta[stat] = sum;
 }
 
 // ---- splits' gradients added up ----------------------------------------------------------
@@ -426,7 +429,7 @@ hipError_t launch_attn_grad_join(const AttnArgs& of_q, const AttnArgs& of_kv, hi
 
 hipError_t launch_attn_delta(const AttnArgs& a, hipStream_t stream) {
     const int64_t threads = (int64_t)a.B * a.Nq * a.H * 8;
-    const uint32_t blocks = (uint32_t)((threads + kAttnThreads - 1) / kAttnThreads);
+    const uint32_t blocks = (uint32_t)std::min<int64_t>((threads + kAttnThreads - 1) / kAttnThreads, 1 << 22);
     if (a.dtype == DA_BF16)
         attn_delta_kernel<__bf16><<<blocks, kAttnThreads, 0, stream>>>(a);
     else if (a.dtype == DA_F16)

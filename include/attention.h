@@ -61,7 +61,8 @@ typedef struct {
 } attn_problem;
 
 /* attn_forward_workspace_size -- bytes of device workspace attn_forward needs (0 where one
- * workgroup sees all keys of its queries).  Host only. */
+ * workgroup sees all keys of its queries).  Host only; refuses the problems that attn_forward
+ * does. */
 DA_API da_status attn_forward_workspace_size(const attn_problem* problem, size_t* bytes);
 
 /*
@@ -75,7 +76,9 @@ DA_API da_status attn_forward_workspace_size(const attn_problem* problem, size_t
  *   workspace  device scratch of attn_forward_workspace_size() bytes, 256-byte aligned (may
  *              be NULL when that is 0); contents on entry do not matter.
  * Errors: DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (head_dim, strides of a token of 2^24 bytes or
- * more, 2^31 rows, 2^30 keys, a launch of 2^32 threads or more), DA_ERR_HIP.
+ * more, 2^31 rows, 2^30 keys, a launch of 2^32 threads or more: 2^24 tiles of 128 rows of a key head,
+ * or, with 32 rows or fewer, 2^23 key heads of all batch entries, 2^24 of more than 128 bytes),
+ * DA_ERR_HIP.
  */
 DA_API da_status attn_forward(const attn_problem* problem, const void* q, const void* k,
                               const void* v, const int32_t* kv_lens, const uint8_t* key_mask,

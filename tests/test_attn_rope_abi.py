@@ -175,6 +175,19 @@ def test_attention_gradients_of_what_the_forward_takes(lib, kw):
     assert f"{n.value} needed" in _msg(lib)
 
 
+@pytest.mark.parametrize("kw", [dict(batch=1 << 23, heads=1, key_heads=1), dict(batch=1 << 20, heads=24, key_heads=12),
+                                dict(batch=1 << 24, heads=1, key_heads=1, head_dim=128),
+                                dict(batch=1 << 23, heads=4, key_heads=1, queries=8, dtype=0)])
+def test_attention_of_few_rows_rejects_launches_past_32_bits(lib, kw):
+    """The form for few rows has 512 threads to a workgroup in heads of up to 128 bytes, 256 in others."""
+    kw = dict(dict(queries=1, keys=3, head_dim=8, dtype=1), **kw)
+    far, n = 1 << 55, ctypes.c_size_t(0)
+    p = _attn(**kw, **{s + "_stride": _dense(8, kw["key_heads" if s in "kv" else "heads"], kw["head_dim"])
+                       for s in ("q", "k", "v", "out", "grad")})
+    assert lib.attn_forward_workspace_size(ref(p), ref(n)) == 2 and "workgroups" in _msg(lib)
+    assert _fwd(lib, p, out=far, lse=2 * far) == 2 and "workgroups" in _msg(lib)
+
+
 def test_attention_workspace_query_refuses_what_the_call_does(lib):
     p = _attn(batch=1 << 15, queries=1 << 22, heads=1, key_heads=1, keys=8, head_dim=8,
               **{n + "_stride": _dense(8 if n in "kv" else 1 << 22, 1, 8)

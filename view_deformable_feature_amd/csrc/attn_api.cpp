@@ -172,7 +172,8 @@ void choose_grad_kv(da::AttnArgs& a) {
 // Counts the workgroups; a launch has fewer than 2^32 threads.
 da_status count_blocks(da::AttnArgs& a) {
     const wide blocks = (wide)a.B * a.Hk * a.col_tiles * a.splits;
-    if (blocks + 8 >= (wide(1) << 32) / da::kAttnThreads)
+    const int threads = a.few ? 64 * da::attn_few_waves(a) : da::kAttnThreads;
+    if (blocks + 8 >= (wide(1) << 32) / threads)
         return report_error(DA_ERR_UNSUPPORTED, "2^32 threads of workgroups or more");
     a.blocks = (int32_t)blocks;
     return DA_OK;
@@ -247,12 +248,16 @@ extern "C" {
 
 da_status attn_forward_workspace_size(const attn_problem* p, size_t* bytes) {
     if (!bytes) return report_error(DA_ERR_INVALID_ARG, "bytes is NULL");
-    const da_status st = check_problem(p);
+    da_status st = check_problem(p);
     if (st != DA_OK) return st;
     da::AttnArgs a;
     describe(p, a);
     choose_forward(a);
-    *bytes = p->batch == 0 || p->queries == 0 ? 0 : (size_t)need_forward(a);
+    *bytes = 0;
+    if (p->batch == 0 || p->queries == 0) return DA_OK;
+    st = count_blocks(a);
+    if (st != DA_OK) return st;
+    *bytes = (size_t)need_forward(a);
     return DA_OK;
 }
 

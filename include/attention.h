@@ -71,7 +71,8 @@ DA_API da_status attn_forward_workspace_size(const attn_problem* problem, size_t
  *   kv_lens    device int32 [B], or NULL for Nk; below 0 counts as 0, above Nk as Nk.
  *   key_mask   device, one byte for each of [B, Nk], or NULL for all visible.
  *   out        device [B, Nq, H, D] with out_stride, 16-byte aligned, fully overwritten; its
- *              places must not overlap each other, nor q, k or v.
+ *              places must not overlap each other, nor q, k or v (it may lie between their
+ *              heads in one packed buffer).
  *   lse        device float [B, H, Nq], dense, fully overwritten, for attn_backward; or NULL.
  *   workspace  device scratch of attn_forward_workspace_size() bytes, 256-byte aligned (may
  *              be NULL when that is 0); contents on entry do not matter.
@@ -106,8 +107,9 @@ DA_API da_status attn_backward_workspace_size(const attn_problem* problem, size_
  *   grad_out   device [B, Nq, H, D] with grad_stride, 16-byte aligned.
  *   grad_q     device [B, Nq, H, D]; grad_k, grad_v device [B, Nk, Hk, D]; dense, 16-byte
  *              aligned, fully overwritten; grad_q may be NULL, grad_k and grad_v both may.  They
- *              must not overlap an input or each other.  With a batch stride of 0 each entry's
- *              part is written on its own: their sum is the gradient of the shared states.
+ *              must not overlap an input, from its first number to its last, or each other.
+ *              With a batch stride of 0 each entry's part is written on its own: their sum is
+ *              the gradient of the shared states.
  *   workspace  device scratch of attn_backward_workspace_size() bytes, 256-byte aligned;
  *              contents on entry do not matter.
  * Errors as attn_forward; the launch has a workgroup of 256 threads for each 128 rows, and for each

@@ -80,7 +80,8 @@ typedef struct {
 /*
  * rope_forward -- the rotation of one tensor.
  *   x, positions (as pos_type says), y   device, element aligned.  y may be x itself with the
- *                                        same strides; it must not overlap x otherwise.
+ *                                        same strides, or lie between x's heads in one packed
+ *                                        buffer; it must not overlap x otherwise.
  *   freqs                                device double [R / 2] (may be NULL when R is 0).
  * Errors: DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED (head_dim, 2^31 tokens or heads, a launch of 2^31
  * threads or more), DA_ERR_HIP.
@@ -115,7 +116,7 @@ DA_API da_status rope_norm_backward_workspace_size(const rope_problem* problem,
  *   grad_q_out, ..     device, with y_stride.
  *   grad_q, grad_k     device [B, N, H, D], dense, element aligned, fully overwritten, or NULL.
  *                      They may be the gradients that come in, where those are dense, and must
- *                      not overlap an input otherwise.
+ *                      not overlap an input, from its first number to its last, otherwise.
  *   grad_q_weight, ..  device float [D], fully overwritten, or NULL; sums join in binary64.
  *   workspace          device scratch of rope_norm_backward_workspace_size() bytes, 256-byte
  *                      aligned (may be NULL when that is 0); contents on entry do not matter.

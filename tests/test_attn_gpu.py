@@ -165,6 +165,29 @@ def test_results_and_gradients_with_strides(dtype):
     assert (buf[..., 48:] == 7).all()
 
 
+@pytest.mark.parametrize("N", [3, 140])
+@TYPES
+def test_out_in_the_buffer_of_the_projection(dtype, N):
+    """out beside q, k and v in one buffer, tokens or heads first: what is there stays."""
+    gen = torch.Generator().manual_seed(111)
+    B, H, Hk, D = 2, 4, 2, 32
+    parts = [H, Hk, Hk, H]
+    for heads_first in (False, True):
+        shape = (B, sum(parts), N, D) if heads_first else (B, N, sum(parts), D)
+        packed = torch.randn(shape, generator=gen).to(dtype).cuda()
+        before = packed.clone()
+        q, k, v, room = (t.transpose(1, 2) if heads_first else t
+                         for t in packed.split(parts, 1 if heads_first else 2))
+        want, _ = vdf.attn_forward(q, k, v)
+        out, lse = vdf.attn_forward(q, k, v, out=room)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and out.data_ptr() == room.data_ptr()
+        Attention(q, k, v).check_forward(out, lse)
+        rest = H + 2 * Hk
+        assert torch.equal(packed[:, :rest] if heads_first else packed[:, :, :rest],
+                           before[:, :rest] if heads_first else before[:, :, :rest])
+
+
 @TYPES
 def test_large_scores(dtype):
     """Scores of hundreds: one key takes all the weight; growing along the keys, so that the

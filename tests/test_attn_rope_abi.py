@@ -138,6 +138,62 @@ def test_attention_rejects_pointers(lib):
     assert lib.attn_backward_workspace_size(ref(p), None) == 1
 
 
+def _places(at, B, N, H, D, strides):
+    """The addresses of a tensor's binary32 numbers, by fours."""
+    return {at + 4 * (b * strides[0] + n * strides[1] + h * strides[2] + d)
+            for b in range(B) for n in range(N) for h in range(H) for d in range(0, D, 4)}
+
+
+def _out_beside_q(lib, q, out, Nq, H, D, B=2):
+    """What the call says of q and out, (distance in bytes, strides) each; keys enough to want a
+    workspace, which it does not get."""
+    p = _attn(batch=B, queries=Nq, keys=40000, heads=H, key_heads=1, head_dim=D,
+              q_stride=(ctypes.c_int64 * 3)(*q[1]), out_stride=(ctypes.c_int64 * 3)(*out[1]),
+              k_stride=_dense(40000, 1, D), v_stride=_dense(40000, 1, D))
+    assert _fwd(lib, p, q=FAR + q[0], out=FAR + out[0], lse=FARTHEST, n=0) == 1
+    return _msg(lib)
+
+
+@pytest.mark.parametrize("B", [1, 2])
+def test_out_among_the_heads_of_one_buffer(lib, B):
+    """Places of a packed tensor: token by token beside q's heads (the same buffer holds k and v, or not),
+    batch entries first or tokens first, heads first."""
+    N, H, D = 7, 3, 16
+    row = 8 * D
+    for strides, step in (((N * row, row, D), H * D), ((row, B * row, D), H * D),
+                          ((2 * H * N * D, D, N * D), H * N * D), ((N * 2 * H * D, 2 * H * D, 2 * D), D)):
+        for q, out in ((0, step), (step, 0)):
+            assert "workspace" in _out_beside_q(lib, (4 * q, strides), (4 * out, strides), N, H, D, B)
+    strides = (N * row, row, D)
+    for off in (-4, 4, 16, H * D - 4, -H * D + 4, row - 4):
+        assert "overlaps" in _out_beside_q(lib, (0, strides), (4 * off, strides), N, H, D, B)
+    assert "overlaps" in _out_beside_q(lib, (0, strides), (4 * H * D, (N * row, row - D, D)), N, H, D, B)
+
+
+def test_out_is_refused_wherever_it_shares_a_place(lib):
+    """Random strides and distances against the sets of places themselves."""
+    import random
+    rng, shared, taken = random.Random(7), 0, 0
+    for _ in range(6000):
+        B, N, H, D = rng.choice([1, 2]), rng.choice([1, 2, 3]), rng.choice([1, 2]), 8
+        few = [8 * rng.randint(0, 9) if rng.random() < 0.7 else 4 * rng.randint(0, 40) for _ in range(6)]
+        q = few[:3]
+        out = q if rng.random() < 0.6 else few[3:]
+        if rng.random() < 0.5:
+            rng.shuffle(q)
+        at = 4 * 4 * rng.randint(-40, 40)
+        mine = _places(at, B, N, H, D, out)
+        msg = _out_beside_q(lib, (0, q), (at, out), N, H, D, B)
+        if "places of out" in msg:
+            continue
+        if mine & _places(0, B, N, H, D, q):
+            shared += 1
+            assert "overlaps" in msg, (B, N, H, q, out, at)
+        else:
+            taken += "workspace" in msg
+    assert shared > 300 and taken > 300, (shared, taken)
+
+
 def test_attention_workspaces(lib):
     n = ctypes.c_size_t(0)
     p = _attn(queries=1, keys=40000)            # few rows: keys are split

@@ -196,6 +196,25 @@ def test_views_and_in_place(dtype):
         vdf.rope_norm_forward(q, k, w, wk, f, q_out=k, k_out=q)
 
 
+@TYPES
+def test_result_beside_its_input_in_one_buffer(dtype):
+    """The second part of a packed tensor is the first one rotated, tokens or heads first."""
+    gen = torch.Generator().manual_seed(245)
+    B, N, H, D = 2, 21, 4, 32
+    f = _freqs(D)
+    for dim in (2, 1):
+        packed = torch.randn((B, N, 2 * H, D) if dim == 2 else (B, 2 * H, N, D), generator=gen).to(dtype).cuda()
+        before = packed.clone()
+        x, y = (t if dim == 2 else t.transpose(1, 2) for t in packed.split(H, dim))
+        vdf.rope_forward(x, f, out=y)
+        torch.cuda.synchronize()
+        want, mag = rotate(x, f, None, "half")
+        check("y", y, want, rounded(8 * U * mag, want, dtype))
+        assert torch.equal(packed.split(H, dim)[0], before.split(H, dim)[0])
+        with pytest.raises(vdf._lib.DAError, match="overlaps"):
+            vdf.rope_forward(x[..., :16], f[:8], out=x[..., 8:24])
+
+
 def test_magnitude_and_scaled_frequencies():
     gen = torch.Generator().manual_seed(234)
     x = _heads((2, 40, 3, 64, 64), F32, gen)

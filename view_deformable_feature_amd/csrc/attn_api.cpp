@@ -15,6 +15,7 @@
 namespace {
 
 using da::extent_bytes;
+using da::may_meet;
 using da::ranges_clash;
 using da::report_error;
 
@@ -274,7 +275,11 @@ da_status attn_forward(const attn_problem* p, const void* q, const void* k, cons
         return report_error(DA_ERR_INVALID_ARG, "out is not 16-byte aligned, or lse not 4-byte");
     const Sizes n = sizes_of(p);
     const wide lse_bytes = (wide)p->batch * p->heads * p->queries * 4;
-    if (ranges_clash(out, n.out, q, n.q) || ranges_clash(out, n.out, k, n.k) || ranges_clash(out, n.out, v, n.v) ||
+    const int e = elem_bytes(p->dtype);
+    const da::Heads to = {out, {p->batch, p->queries, p->heads}, p->out_stride, p->head_dim, e};
+    if (may_meet(to, {q, {p->batch, p->queries, p->heads}, p->q_stride, p->head_dim, e}) ||
+        may_meet(to, {k, {p->batch, p->keys, p->key_heads}, p->k_stride, p->head_dim, e}) ||
+        may_meet(to, {v, {p->batch, p->keys, p->key_heads}, p->v_stride, p->head_dim, e}) ||
         ranges_clash(out, n.out, lse, lse_bytes) || ranges_clash(lse, lse_bytes, q, n.q) ||
         ranges_clash(lse, lse_bytes, k, n.k) || ranges_clash(lse, lse_bytes, v, n.v))
         return report_error(DA_ERR_INVALID_ARG, "out or lse overlaps an input, or the other");

@@ -151,6 +151,10 @@ struct Given {
     float* grad_weight;
 };
 
+da::Heads of(const rope_problem* p, const rope_tensor* t, const void* at, const int64_t (&stride)[3]) {
+    return {at, {t->batch, t->tokens, t->heads}, stride, p->head_dim, elem_bytes(p->dtype)};
+}
+
 da_status check_given(const rope_problem* p, const Given& g, const double* freqs, bool backward) {
     const int e = elem_bytes(p->dtype);
     if (!g.x || !g.y) return report_error(DA_ERR_INVALID_ARG, "%s or its other tensor is NULL", g.name);
@@ -166,7 +170,7 @@ da_status check_given(const rope_problem* p, const Given& g, const double* freqs
         if (da::overlaps_itself(g.t->y_stride, g.t->batch, g.t->tokens, g.t->heads, p->head_dim))
             return report_error(DA_ERR_INVALID_ARG, "places of the result of %s overlap", g.name);
         const bool same = g.x == g.y && !memcmp(g.t->x_stride, g.t->y_stride, sizeof g.t->x_stride);
-        if (!same && ranges_clash(g.x, nx, g.y, ny))
+        if (!same && da::may_meet(of(p, g.t, g.x, g.t->x_stride), of(p, g.t, g.y, g.t->y_stride)))
             return report_error(DA_ERR_INVALID_ARG, "the result of %s overlaps it without being it", g.name);
         return DA_OK;
     }
@@ -210,36 +214,17 @@ da_status set_up(const rope_problem* p, const Given (&given)[2], const double* f
     // results of one side over what the other reads or writes
     if (!empty(given[0].t) && !empty(given[1].t)) {
         const int e = elem_bytes(p->dtype);
-        const auto size = [&](const Given& g, const int64_t (&stride)[3]) {
-            return extent(stride, g.t, p->head_dim, e);
-        };
         for (int i = 0; i < 2; ++i) {
             const Given &g = given[i], &o = given[1 - i];
-            const void* to = backward ? g.dx : g.y;
-            const wide n = backward ? (wide)g.t->batch * g.t->tokens * g.t->heads * p->head_dim * e
-                                    : size(g, g.t->y_stride);
-            const wide no = backward ? (wide)o.t->batch * o.t->tokens * o.t->heads * p->head_dim * e : 0;
-            // heads of one packed tensor lie between each other: only equal strides tell them apart
-            const auto between = [&](const int64_t (&s)[3], const void* at, const int64_t (&so)[3],
-                                     const void* ato) {
-                // one token to an entry: the entries lie as tokens do otherwise
-                const int in = g.t->tokens > 1 || o.t->tokens > 1;
-                if (s[in] != so[in] || s[in] == 0) return false;
-                if (in == 1 && (g.t->batch > 1 || o.t->batch > 1) &&
-                    (s[0] != so[0] || (wide)s[0] < (wide)s[1] * std::max(g.t->tokens, o.t->tokens)))
-                    return false;
-                const wide span = ((wide)(g.t->heads - 1) * s[2] + p->head_dim) * e;
-                const wide spano = ((wide)(o.t->heads - 1) * so[2] + p->head_dim) * e;
-                const wide d = (wide)reinterpret_cast<uintptr_t>(ato) - (wide)reinterpret_cast<uintptr_t>(at);
-                return d >= 0 ? d >= span && d + spano <= (wide)s[in] * e
-                              : -d >= spano && -d + span <= (wide)s[in] * e;
+            const auto bytes = [&](const Given& x) { return (wide)x.t->batch * x.t->tokens * x.t->heads * p->head_dim * e; };
+            // a forward result may lie between the other's heads; the backward's are dense
+            const auto meets = [&](const int64_t (&stride)[3], const void* at) {
+                const da::Heads other = of(p, o.t, at, stride);
+                return backward ? ranges_clash(g.dx, bytes(g), at, other.bytes())
+                                : da::may_meet(of(p, g.t, g.y, g.t->y_stride), other);
             };
-            const auto meets = [&](const int64_t (&so)[3], const void* ato) {
-                return ranges_clash(to, n, ato, size(o, so)) &&
-                       (backward || !between(g.t->y_stride, to, so, ato));
-            };
-            if (meets(o.t->x_stride, o.x) || (!backward && meets(o.t->y_stride, o.y)) ||
-                (backward && (ranges_clash(to, n, o.dx, no) || meets(o.t->y_stride, o.y))))
+            if (meets(o.t->x_stride, o.x) || meets(o.t->y_stride, o.y) ||
+                (backward && ranges_clash(g.dx, bytes(g), o.dx, bytes(o))))
                 return report_error(DA_ERR_INVALID_ARG, "a result of %s overlaps a tensor of %s", g.name, o.name);
         }
     }

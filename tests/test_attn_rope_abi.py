@@ -439,3 +439,17 @@ def test_frequencies():
     assert ((blend <= plain) & (blend >= plain / 16 * (1 - 1e-15))).all() and (blend.diff() < 0).all()
     assert vdf.rope_frequencies(0, device="cpu")[0].shape == (0,)
     assert vdf.rope_frequencies(2, scaling="base", factor=2.0, device="cpu")[0].tolist() == [1.0]
+
+
+@pytest.mark.parametrize("trained", [3, 6, 20, 100, 512, 4096, 1 << 20])
+@pytest.mark.parametrize("rotated, base", [(2, 10000.0), (64, 10000.0), (128, 500000.0)])
+@pytest.mark.parametrize("fast, slow", [(32.0, 1.0), (4.0, 0.5), (40.0, 2.0)])
+def test_blended_frequencies_at_both_ends(trained, rotated, base, fast, slow):
+    """Pairs that turn at least `fast` times within what was trained stay, those that turn at most `slow`
+    times are divided, however short that is; no pair leaves the two."""
+    plain = base ** (-torch.arange(0, rotated, 2, dtype=torch.float64) / rotated)
+    f, _ = vdf.rope_frequencies(rotated, base, "blend", 16.0, trained, fast, slow, device="cpu")
+    turns = trained * plain / (2 * torch.pi)
+    assert torch.allclose(f[turns >= fast * 1.0001], plain[turns >= fast * 1.0001], rtol=1e-15)
+    assert torch.allclose(f[turns <= slow * 0.9999], plain[turns <= slow * 0.9999] / 16, rtol=1e-15)
+    assert ((f <= plain * (1 + 1e-15)) & (f >= plain / 16 * (1 - 1e-15))).all()

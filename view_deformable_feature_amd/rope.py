@@ -46,7 +46,8 @@ def rope_frequencies(rotated: int, base: float = 10000.0, scaling: str = "none",
       last is divided by ``factor``;
     * "blend": pairs that turn at least ``fast`` times within ``trained`` positions stay, those that
       turn at most ``slow`` times are divided by ``factor``, between the two even over the pairs'
-      numbers; magnitude 1 + log(factor) / 10.
+      numbers; magnitude 1 + log(factor) / 10.  The published method is YaRN's, with its bounds of
+      the two pairs' numbers (whole ones, 0 and ``rotated`` - 1), which trained weights count on.
     """
     if rotated < 0 or rotated % 2:
         raise ValueError(f"rotated must be even and >= 0, got {rotated}")
@@ -71,6 +72,8 @@ def rope_frequencies(rotated: int, base: float = 10000.0, scaling: str = "none",
         low = max(math.floor(number(fast)), 0)
         high = min(math.ceil(number(slow)), rotated - 1)
         stretched = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+        if number(slow) <= 0:   # no pair turns more often
+            stretched = torch.ones_like(i)
         freqs = freqs * (1 - stretched) + freqs / factor * stretched
         magnitude = 1 + 0.1 * math.log(factor)
     return freqs.to(device), magnitude

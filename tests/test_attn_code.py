@@ -46,6 +46,17 @@ def test_buffer_resources_are_scalar(kernels):
         assert sum(i.startswith("v_readfirstlane") for i in code) < 32, name
 
 
+def test_every_kernel_is_looked_at(kernels):
+    """The names by which the tests pick their kernels are those of all that there are: three types by
+    four sizes of a head, with and without a mask, and the small ones of each type."""
+    count = {}
+    for name in kernels:
+        kind = re.match(r"attn_[a-z_]+_kernel", name).group(0)
+        count[kind] = count.get(kind, 0) + 1
+    assert count in ({"attn_forward_kernel": 24, "attn_few_kernel": 12, "attn_join_kernel": 3},
+                     {"attn_grad_kernel": 24, "attn_delta_kernel": 3, "attn_grad_join_kernel": 3})
+
+
 def test_barriers_wait_for_fills(kernels):
     """Between a fill of LDS and the next barrier stands a wait for all that is on its way, which
     the barrier itself is none for."""

@@ -1,5 +1,6 @@
-// Activations and 16-byte vector access shared by the group norm (gn.hip) and the
-// 8-bit products (i8.hip).  Device code.
+// Activations, shared by the group norm (gn.hip) and the 8-bit products (i8.hip), and 16-byte
+// vector access, which the attention (attn_device.h) and the rotation (rope.hip) use too.  Device
+// code.
 #pragma once
 
 #include <hip/hip_runtime.h>

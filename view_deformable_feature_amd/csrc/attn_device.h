@@ -50,17 +50,6 @@ __device__ __forceinline__ f32x16 mul_pieces(u32x4 a, u32x4 b, f32x16 acc) {
     }
 }
 
-// sum + the products of two pieces' numbers
-template <typename T>
-__device__ __forceinline__ float dot_pieces(u32x4 a, u32x4 b, float sum) {
-    constexpr int V = 16 / (int)sizeof(T);
-    typedef T vec __attribute__((ext_vector_type(V)));
-    const vec x = __builtin_bit_cast(vec, a), y = __builtin_bit_cast(vec, b);
-#pragma unroll
-    for (int e = 0; e < V; ++e) sum = fmaf((float)x[e], (float)y[e], sum);
-    return sum;
-}
-
 // The largest of a value over the two lanes of a column; its sum.
 __device__ __forceinline__ float column_max(float v) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);

@@ -12,8 +12,6 @@
 namespace da {
 
 constexpr int kRopeThreads = 256;
-// Units (pairs of vectors) of a head that one lane may have.
-constexpr int kRopeMostUnits = 4;
 
 // One tensor of a launch.
 struct RopeSide {

@@ -118,6 +118,45 @@ def test_turns_are_exact_to_a_unit():
     check("sin", y[0, :, 0, 1], torch.sin(t), 3 * U * torch.sin(t).abs() + slack + 2.0 ** -30)
 
 
+def test_turns_at_their_own_size():
+    """Cosines and sines of angles from 2^-20 to 2^47, and next to quarter turns, where one of the two is
+    small, by their own size.  The rest is exact to far below u = 2^-24 and rounds once to binary32 (its
+    share of a sine is at most u, of a cosine pi / 4 u); the first term left out is 2^-27.7 of the result;
+    the last multiply-add of a sine rounds by u, what it adds to y is at most a ninth of it and off by
+    3 u: 2.5 u; the cosine's adds at most 0.41 of the result, off by 3 u too: 3.1 u and 0.1."""
+    gen = torch.Generator().manual_seed(246)
+    t = torch.exp2(torch.rand(6000, generator=gen) * 67 - 20) * (torch.randint(0, 2, (6000,), generator=gen) * 2 - 1)
+    near = (torch.arange(1, 2000).double() * math.pi / 2).float()
+    t = torch.cat([t, near, near * 4096, -near])
+    x = torch.zeros((1, len(t), 2, 2), device="cuda")
+    x[..., 0, 0], x[..., 1, 1] = 1, 1
+    y = vdf.rope_forward(x, torch.ones(1, dtype=torch.float64, device="cuda"), t.cuda())
+    torch.cuda.synchronize()
+    c, s = (torch.tensor([f(v) for v in t.double().tolist()], dtype=torch.float64) for f in (math.cos, math.sin))
+    tol = 3.2 * U
+    check("cos", y[0, :, 0, 0], c, tol * c.abs())
+    check("sin", y[0, :, 0, 1], s, tol * s.abs())
+    check("-sin", y[0, :, 1, 0], -s, tol * s.abs())
+    check("cos", y[0, :, 1, 1], c, tol * c.abs())
+
+
+@LAYOUTS
+def test_rotation_by_its_own_terms(layout):
+    """y_a = x_a c - x_b s and y_b within their terms' own roundings: a turn's, 3.2 u of either, a product's
+    and a multiply-add's, u each: 5.2 u of |x_a c| + |x_b s|, whatever the sizes beside each other."""
+    gen = torch.Generator().manual_seed(247)
+    x = torch.randn((2, 300, 3, 64), generator=gen) * torch.exp2(torch.randint(-12, 13, (2, 300, 3, 64), generator=gen))
+    pos = torch.randint(0, 1 << 30, (2, 300), generator=gen)
+    f = _freqs(64)
+    y = vdf.rope_forward(x.cuda(), f, pos.cuda(), layout).cpu().double()
+    t = pos.double()[..., None, None] * f.cpu()
+    c, s, d = torch.cos(t), torch.sin(t), x.double()
+    a, b = (d[..., ::2], d[..., 1::2]) if layout == "interleaved" else (d[..., :32], d[..., 32:])
+    ya, yb = (y[..., ::2], y[..., 1::2]) if layout == "interleaved" else (y[..., :32], y[..., 32:])
+    check("y_a", ya, a * c - b * s, 5.2 * U * ((a * c).abs() + (b * s).abs()))
+    check("y_b", yb, b * c + a * s, 5.2 * U * ((b * c).abs() + (a * s).abs()))
+
+
 def test_positions_that_are_no_numbers():
     """An infinite or NaN position makes its own token's rotated numbers NaN, no others."""
     gen = torch.Generator().manual_seed(231)

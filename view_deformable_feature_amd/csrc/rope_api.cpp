@@ -73,8 +73,8 @@ da_status check_tensor(const rope_problem* p, const rope_tensor* t) {
 
 int pos_bytes(int32_t t) { return t == ROPE_POS_I64 ? 8 : 4; }
 
-constexpr int64_t kWantedBlocks = 512;      // workgroups that a launch should have
-constexpr int64_t kBackwardBlocks = 512;    // that a backward launch has at most
+constexpr int64_t kWantedBlocks = 512;      // workgroups that each tensor of a launch should have
+constexpr int64_t kBackwardBlocks = 512;    // that each of a backward launch has at most
 
 bool empty(const rope_tensor* t) { return !t || t->batch == 0 || t->tokens == 0; }
 

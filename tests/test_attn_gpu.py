@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import view_deformable_feature_amd as vdf
-from attention_reference import BF16, F16, F32, Attention, check
+from attention_reference import BF16, F16, F32, HALF, U, Attention, check
 from gpu_helpers import say
 
 pytestmark = pytest.mark.gpu
@@ -262,6 +262,33 @@ def test_far_scores(dtype, level, step, shape, sign):
     check("out", out.transpose(1, 2), want, tol * (1 + h) + h * want.abs() + 2.0 ** -126)
     top = s.amax(-1) + torch.exp(-d).sum(-1).log()
     check("lse", lse, top, top.abs() * 6 * u + (Nk + 32) * u)
+
+
+@pytest.mark.parametrize("shape", [(2, 3, 900, 4, 2, 32), (1, 2, 9000, 3, 3, 64), (2, 140, 190, 64, 64, 128),
+                                   (2, 200, 1000, 20, 20, 64)], ids=["few", "few_split", "wide", "wide_split"])
+@pytest.mark.parametrize("sign", [1, -1], ids=["up", "down"])
+@TYPES
+def test_one_far_score_among_near_ones(dtype, sign, shape):
+    """A key in the midst whose score is +-2^25: what its wave, its tile and its split keep meets what
+    others do.  It takes all the weight (of the weight, its inverse and the product 3 u), or none, and the
+    others share it as if it were invisible."""
+    q, k, v, _, _, _ = _inputs(shape, dtype, 306)
+    at = shape[2] * 2 // 3
+    q[..., 0] = 2.0 ** 13
+    k[..., 0] = 0
+    k[:, at] = 0
+    k[:, at, :, 0] = sign * 2.0 ** 13
+    out, lse = vdf.attn_forward(q, k, v, scale=0.5)
+    torch.cuda.synchronize()
+    if sign > 0:
+        x = v[:, at:at + 1].cpu().double().repeat_interleave(shape[3] // shape[4], 2).expand(out.shape)
+        check("out", out, x, x.abs() * (3 * U + (0 if dtype == F32 else 2 * HALF[dtype])))
+        check("lse", lse, torch.full(lse.shape, 2.0 ** 25, dtype=torch.float64), torch.tensor(4.0).double())
+        return
+    m = torch.ones(k.shape[:2], dtype=torch.bool, device="cuda")
+    m[:, at] = False
+    q[..., 0] = 0          # as the other keys see it
+    Attention(q, k, v, None, m, 0.5).check_forward(out, lse)
 
 
 @pytest.mark.parametrize("dtype, level", [(F32, 15), (F32, 20), (F32, 23), (F32, 27), (F32, 34), (F32, 60),

@@ -20,8 +20,8 @@
  *
  *   r = 1 / sqrt(average of x^2 over the D numbers + eps),   n = x r weight[d],
  *
- * n takes x's place.  Sums and numbers under way are binary32, a 16-bit result is rounded once to
- * nearest even.
+ * n takes x's place.  Sums and numbers under way, x^2 among them, are binary32, a 16-bit result is
+ * rounded once to nearest even.
  *
  * Conventions of the library (see deformagg.h): the caller owns every buffer, calls
  * are asynchronous on `stream` and may be captured into a HIP graph, every check runs

@@ -11,8 +11,8 @@
 // Many rows: four waves of 32 columns and tiles of 64 keys, the next tile on its way while one is
 // used; two workgroups to a compute unit, so that one wave's exponentials run beside another's
 // products.  Bound by the matrix instructions: 2 x 4096 rows on 8192 keys, 16 heads of 128, bfloat16,
-// 505 us, 1090 Tflop/s, where a product of 8192^3 runs at 1363; the clock falls to about 1.75 GHz
-// under this load.
+// 507 us, 1085 Tflop/s, where a product of 8192^3 runs at 1363; the clock falls to about 1.75 GHz
+// under this load (on another card further: 544).
 #include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -16,9 +16,9 @@
 //
 // Two waves to a SIMD, and the loops have no branches of their own: with branches the accumulators
 // moved between registers at each of them, and heads of 128 numbers had room for one wave
-// (1 x 4096 on 4096, 16 heads of 128 on 4, bfloat16: 694 us, 475 so, 455 now).  Bound by the matrix
-// instructions, at 755 Tflop/s of five products' worth, with the scores' and dP's products formed
-// twice, once by either kind: at 1060 of the seven that run.  What the scores' exponentials and the
+// (1 x 4096 on 4096, 16 heads of 128 on 4, bfloat16: 694 us, 475 so, 450 to 463 now by the card).
+// Bound by the matrix instructions, at 743 to 763 Tflop/s of five products' worth, with the scores'
+// and dP's products formed twice, once by either kind: at 1040 to 1070 of the seven that run.  What the scores' exponentials and the
 // roundings of p and dS cost lies in their shadow only in part.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -26,7 +26,7 @@ namespace {
 // nearest is known to 2^-52.5 of the angle, so that the rest is at most pi / 4 and as much.  It goes
 // by the two series, whose first terms left out are 2^-28.5 and 2^-32.5 of the result at pi / 4 and
 // still 2^-27.7 and 2^-31.5 for angles of 2^48: with the roundings to binary32 on the way it is off
-// by at most 3 times 2^-24 of the result.  Towards 2^52, where neighbouring angles are half a radian
+// by at most 3.2 times 2^-24 of the result.  Towards 2^52, where neighbouring angles are half a radian
 // apart, the rest reaches 1.5 and the series are off by up to 2^-18.
 __device__ __forceinline__ void turn_of(double angle, float& c, float& s) {
     const double q = rint(angle * 0.63661977236758134);   // 2 / pi
